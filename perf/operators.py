@@ -312,7 +312,7 @@ def _sample(s):
 def _handle(n_q, n_kv, dim, page, fmt):
     """One handle (it owns the scratch) for each geometry, as a program that serves one model keeps it."""
     import block_drafter_pos_gb300 as bd
-    return bd.dflash2_paged_create(bd.make_paged_config(n_q, n_kv, dim, page, fmt, max_requests=64, max_tokens=40960))
+    return bd.dflash2_paged_create(bd.make_paged_config(n_q, n_kv, dim, page, fmt, max_requests=64))
 
 
 def _cache(s):
