@@ -7,5 +7,7 @@ from .binding import (  # noqa: F401
     dflash2_head_topk_noalloc, dflash2_debug_set_pipeline_error, dflash2_debug_noalloc_inject_error,
     dflash2_launch_count, dflash2_set_lmhead_events, dflash2_lmhead_bytes, dflash2_set_projection_events,
     dflash2_projection_launches, dflash2_projection_bytes, lib, make_config, upload_weights,
+    dflash2_paged_create, dflash2_paged_destroy, dflash2_paged_write, dflash2_paged_read, dflash2_paged_attention,
+    dflash2_sample, make_paged_config, paged_cache,
 )
 from .builder import build, LIB  # noqa: F401

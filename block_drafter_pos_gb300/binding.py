@@ -50,6 +50,42 @@ class StepArgs(ctypes.Structure):
         "emitted", "n_emitted", "width")]
 
 
+class PagedConfig(ctypes.Structure):
+    """dflash2_paged_config: the geometry of one target layer's paged cache."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_q_heads", "n_kv_heads", "head_dim", "page_size", "kv_format",
+                                               "max_requests")]
+
+
+class PagedCache(ctypes.Structure):
+    """dflash2_paged_cache: one layer's pools and the call's page table."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride", "scale_page_stride",
+                                       "scale_token_stride", "scale_head_stride", "table_stride")] + [
+        ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    """dflash2_rows: [tokens][heads][head_dim] rows."""
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    """dflash2_paged_attention_args."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_req", "n_tokens", "max_new", "max_len", "causal", "window")] + [
+        ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("token_begin", ctypes.c_void_p),
+        ("kv_len", ctypes.c_void_p), ("q", Rows), ("out", Rows), ("tree_mask", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class SampleArgs(ctypes.Structure):
+    """dflash2_sample_args."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_rows", "vocab", "logits_type", "reserved")] + [
+        ("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p", "uniform", "token", "prob",
+                                        "kept")] + [("kept_stride", ctypes.c_int64), ("status", ctypes.c_void_p)]
+
+
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("embed", "lm_head", "hidden_norm", "final_norm")] + [
         (n, Matrix) for n in ("fc", "sel_proj", "cb_a", "cb_b")] + [("layers", LayerWeights * MAX_LAYERS)]
@@ -101,6 +137,16 @@ def lib() -> ctypes.CDLL:
         L.dflash2_step.restype = i32
         L.dflash2_step_graphs_clear.argtypes = [vp]
         L.dflash2_step_graphs_clear.restype = i32
+        L.dflash2_paged_create.argtypes = [ctypes.POINTER(PagedConfig), ctypes.POINTER(vp)]
+        L.dflash2_paged_destroy.argtypes = [vp]
+        for f in ("dflash2_paged_write", "dflash2_paged_read"):
+            getattr(L, f).argtypes = [vp, ctypes.POINTER(PagedCache), i32, i32, vp, vp, ctypes.POINTER(Rows),
+                                      ctypes.POINTER(Rows), vp, vp]
+        L.dflash2_paged_attention.argtypes = [vp, ctypes.POINTER(PagedCache), ctypes.POINTER(PagedAttentionArgs), vp]
+        L.dflash2_sample.argtypes = [ctypes.POINTER(SampleArgs), vp]
+        for f in ("dflash2_paged_create", "dflash2_paged_destroy", "dflash2_paged_write", "dflash2_paged_read",
+                  "dflash2_paged_attention", "dflash2_sample"):
+            getattr(L, f).restype = i32
         L.dflash2_status_string.argtypes = [i32]
         L.dflash2_status_string.restype = ctypes.c_char_p
         for f in ("dflash2_create", "dflash2_destroy", "dflash2_draft_block", "dflash2_select", "dflash2_verify",
@@ -275,6 +321,168 @@ def dflash2_projection_bytes(h) -> int:
 
 def dflash2_lmhead_bytes(h, n_req) -> int:
     return int(lib().dflash2_lmhead_bytes(h, n_req))
+
+
+# ----------------------------------------------------------------------------- the target's side of a step
+
+KV_BF16, KV_F16, KV_INT8, KV_E4M3 = 0, 1, 2, 3
+T_BF16, T_F16, T_F32 = 0, 1, 2
+_KV_NAMES = {"bf16": KV_BF16, "fp16": KV_F16, "int8": KV_INT8, "e4m3": KV_E4M3}
+_dtype_ids = None
+_paged_cfg: Dict[int, PagedConfig] = {}      # geometry of each live handle, for the checks below
+
+
+def _dtypes():
+    global _dtype_ids
+    if _dtype_ids is None:
+        import torch
+        _dtype_ids = ({torch.bfloat16: T_BF16, torch.float16: T_F16, torch.float32: T_F32},
+                      {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.int8: KV_INT8,
+                       torch.float8_e4m3fn: KV_E4M3}, torch.int32, torch.float32, torch.int64)
+    return _dtype_ids
+
+
+def _inval(what: str, why: str):
+    return Dflash2Error(E_INVAL, f"{what}: {why}")
+
+
+def _vector(what, name, t, dtype, n, none_ok=True):
+    """A contiguous 1-D device tensor of n elements (or more than one row: n counts elements)."""
+    if t is None:
+        if none_ok:
+            return None
+        raise _inval(what, f"{name} is missing")
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise _inval(what, f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
+    return t.data_ptr()
+
+
+def _rows(what, name, t, heads, dim) -> Rows:
+    sh, st = t.shape, t.stride()
+    ty = _dtypes()[0].get(t.dtype)
+    if ty is None or len(sh) != 3 or sh[1] != heads or sh[2] != dim or not t.is_cuda:
+        raise _inval(what, f"{name} must be a bf16, fp16 or fp32 CUDA tensor [tokens, {heads}, {dim}]")
+    if st[2] != 1:
+        raise _inval(what, f"{name}: the last dimension must be contiguous")
+    return Rows(t.data_ptr(), st[0], st[1], ty, 0)
+
+
+def make_paged_config(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, kv_format: str,
+                      max_requests: int) -> PagedConfig:
+    """kv_format: "bf16", "fp16", "int8" or "e4m3"."""
+    return PagedConfig(n_q_heads, n_kv_heads, head_dim, page_size, _KV_NAMES[kv_format], max_requests)
+
+
+def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedCache:
+    """The cache structure of pools k, v [pages, page_size, n_kv_heads, head_dim] (any order of
+    the first three dimensions, the same for both), scales [pages, page_size, n_kv_heads]
+    (8-bit pools) and page_table int32 [requests, pages of a request].  It keeps the
+    tensors alive."""
+    what = "paged_cache"
+    fmt = _dtypes()[1].get(k.dtype)
+    if fmt is None or k.dim() != 4 or k.dtype != v.dtype or k.shape != v.shape or k.stride() != v.stride():
+        raise _inval(what, "k and v must be pools of one type, shape and layout")
+    if k.stride(3) != 1 or not k.is_cuda or not v.is_cuda:
+        raise _inval(what, "the pools must be CUDA tensors with contiguous channels")
+    if page_table.dtype != _dtypes()[2] or page_table.dim() != 2 or not page_table.is_cuda or page_table.stride(1) != 1:
+        raise _inval(what, "page_table must be an int32 CUDA tensor [requests, pages] with contiguous rows")
+    c = PagedCache()
+    c.k, c.v, c.page_table = k.data_ptr(), v.data_ptr(), page_table.data_ptr()
+    c.page_stride, c.token_stride, c.head_stride = k.stride()[:3]
+    if fmt in (KV_INT8, KV_E4M3):
+        f32 = _dtypes()[3]
+        if k_scale is None or v_scale is None or k_scale.dtype != f32 or v_scale.dtype != f32 or \
+                k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3] or k_scale.stride() != v_scale.stride() or \
+                not k_scale.is_cuda or not v_scale.is_cuda:
+            raise _inval(what, "8-bit pools need float32 scales [pages, page_size, heads] of one layout")
+        c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        c.scale_page_stride, c.scale_token_stride, c.scale_head_stride = k_scale.stride()
+    c.n_pages = k.shape[0]
+    c.max_pages, c.table_stride = page_table.shape[1], max(page_table.stride(0), page_table.shape[1])
+    c.n_req, c.fmt, c.shape = page_table.shape[0], fmt, tuple(k.shape[1:])
+    c._keep = (k, v, page_table, k_scale, v_scale)
+    return c
+
+
+def dflash2_paged_create(cfg: PagedConfig) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().dflash2_paged_create(ctypes.byref(cfg), ctypes.byref(h)), "dflash2_paged_create")
+    _paged_cfg[h.value] = cfg
+    return h.value
+
+
+def dflash2_paged_destroy(h: int):
+    _check(lib().dflash2_paged_destroy(h), "dflash2_paged_destroy")
+    _paged_cfg.pop(h, None)
+
+
+def _paged_check(what, h, cache, token_begin, kv_len, status):
+    """The handle's geometry against the cache's; returns (geometry, number of requests)."""
+    g = _paged_cfg.get(h)
+    if g is None:
+        raise _inval(what, "not a paged handle")
+    if cache.fmt != g.kv_format or cache.shape != (g.page_size, g.n_kv_heads, g.head_dim):
+        raise _inval(what, "the pools are not of the handle's format, page size or heads")
+    n = kv_len.numel()
+    if n > cache.n_req:
+        raise _inval(what, "the page table has fewer rows than there are requests")
+    i32 = _dtypes()[2]
+    return g, n, _vector(what, "token_begin", token_begin, i32, n + 1, False), \
+        _vector(what, "kv_len", kv_len, i32, n, False), _vector(what, "status", status, i32, n)
+
+
+def _paged_move(what, call, h, cache, k, v, token_begin, kv_len, status, stream):
+    g, n, begin, length, st = _paged_check(what, h, cache, token_begin, kv_len, status)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise _inval(what, "k and v must have one shape and type")
+    rk, rv = _rows(what, "k", k, g.n_kv_heads, g.head_dim), _rows(what, "v", v, g.n_kv_heads, g.head_dim)
+    _check(call(h, cache, n, k.shape[0], begin, length, rk, rv, st, _stream(stream)), what)
+
+
+def dflash2_paged_write(h, cache, k, v, token_begin, kv_len, status=None, stream=None):
+    """Writes the new tokens' keys and values [tokens, n_kv_heads, head_dim] into their positions."""
+    _paged_move("dflash2_paged_write", lib().dflash2_paged_write, h, cache, k, v, token_begin, kv_len, status, stream)
+
+
+def dflash2_paged_read(h, cache, k, v, token_begin, kv_len, status=None, stream=None):
+    """Reads the same positions back into k and v."""
+    _paged_move("dflash2_paged_read", lib().dflash2_paged_read, h, cache, k, v, token_begin, kv_len, status, stream)
+
+
+def dflash2_paged_attention(h, cache, q, out, token_begin, kv_len, max_new, max_len, scale, causal=True, window=0,
+                            tree_mask=None, lse=None, status=None, stream=None):
+    """Attention of the new tokens q [tokens, n_q_heads, head_dim] over their requests' caches, into out.
+    tree_mask: int64 [tokens] (the bits of a uint64)."""
+    what = "dflash2_paged_attention"
+    g, n, begin, length, st = _paged_check(what, h, cache, token_begin, kv_len, status)
+    rq, ro = _rows(what, "q", q, g.n_q_heads, g.head_dim), _rows(what, "out", out, g.n_q_heads, g.head_dim)
+    tokens = q.shape[0]
+    if out.shape[0] != tokens:
+        raise _inval(what, "q and out must have the same rows")
+    a = PagedAttentionArgs(n, tokens, max_new, max_len, 1 if causal else 0, window, scale, 0, begin, length, rq, ro,
+                           _vector(what, "tree_mask", tree_mask, _dtypes()[4], tokens),
+                           _vector(what, "lse", lse, _dtypes()[3], tokens * g.n_q_heads), st)
+    _check(lib().dflash2_paged_attention(h, cache, a, _stream(stream)), what)
+
+
+def dflash2_sample(logits, temperature, top_k, top_p, min_p, uniform, token, prob=None, kept=None, status=None,
+                   stream=None):
+    """Truncated sampling of the rows of logits [rows, vocab]; top_k, top_p and min_p may be None."""
+    what = "dflash2_sample"
+    ty = _dtypes()[0].get(logits.dtype)
+    if ty is None or logits.dim() != 2 or logits.stride(1) != 1 or not logits.is_cuda:
+        raise _inval(what, "logits must be a bf16, fp16 or fp32 CUDA tensor [rows, vocab] with contiguous rows")
+    n, v = logits.shape
+    i32, f32 = _dtypes()[2:4]
+    if kept is not None and (kept.dtype != f32 or kept.shape != logits.shape or kept.stride(1) != 1 or not kept.is_cuda):
+        raise _inval(what, "kept must be a float32 CUDA tensor of the logits' shape with contiguous rows")
+    a = SampleArgs(n, v, ty, 0, logits.data_ptr(), logits.stride(0),
+                   _vector(what, "temperature", temperature, f32, n, False), _vector(what, "top_k", top_k, i32, n),
+                   _vector(what, "top_p", top_p, f32, n), _vector(what, "min_p", min_p, f32, n),
+                   _vector(what, "uniform", uniform, f32, n, False), _vector(what, "token", token, i32, n, False),
+                   _vector(what, "prob", prob, f32, n), _p(kept), kept.stride(0) if kept is not None else 0,
+                   _vector(what, "status", status, i32, n))
+    _check(lib().dflash2_sample(a, _stream(stream)), what)
 
 
 # ----------------------------------------------------------------------------- convenience

@@ -1,0 +1,789 @@
+// Attention of new tokens over a paged cache: the kernel for few query rows per KV head
+// (decoding, verify blocks, small trees), whose bound is the cache's bytes.
+//
+// out = softmax(scale q K^T) V in one pass over the keys: per row a running maximum m and
+// sum l in base 2, o <- o 2^(m - m') + sum 2^(z - m') v.
+//
+//  * A KV head's query rows (new tokens x group) share every key read: rows = 16, 32 or 64
+//    of the MMA's M per unit.
+//  * The launch's key tiles are dealt to the CTAs in contiguous equal runs (paged.h), so
+//    ragged batches and single long requests fill the machine alike; a unit cut between
+//    CTAs leaves fp32 partials, joined by the combine kernel in CTA order (no atomics).
+//  * Tiles of 64 keys come by 16-byte cp.async, zero-filled past the visible range; the
+//    page table is read one tile ahead of the copies, so its latency is off the path, and
+//    a tile may cross any number of pages.
+//  * Four warps: rows / 16 row groups x key groups of the tile, each with its own running
+//    state, joined through shared memory when the unit (or the run) ends.
+//  * 16-bit caches feed mma.sync through ldmatrix.  8-bit codes are exact in fp16, so both
+//    products run on fp16 codes: the keys' scale multiplies the score, and the values'
+//    scale the weight, relative to the largest scale seen (so the fp16 weight cannot
+//    overflow and loses at most 2^-25 of the largest); the queries are rounded to fp16
+//    after an exact power-of-two shift of their row.  A lane loads the codes as 16-byte
+//    pieces and the contraction order (keys) and the output columns (values) are permuted
+//    to match, so no code passes through shared memory twice.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "paged_sched.cuh"
+
+namespace df2 {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kBN = kPagedBn;
+
+DF2_DEV uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+DF2_DEV void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DF2_DEV void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DF2_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DF2_DEV void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+DF2_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+DF2_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+DF2_DEV uint4 lds16(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+DF2_DEV uint2 lds8(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
+}
+DF2_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF>
+DF2_DEV void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF) mma_bf16(d, a[0], a[1], a[2], a[3], b0, b1);
+  else mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+template <bool BF>
+DF2_DEV uint32_t pack2(float lo, float hi) {
+  if constexpr (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <bool BF>
+DF2_DEV float2 unpack2(uint32_t w) {
+  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Two 16-bit values with zeros in the place of infinities and NaN.
+template <bool BF>
+DF2_DEV uint32_t finite2(uint32_t w) {
+  constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
+  if ((w & ex) == ex) w &= 0xFFFF0000u;
+  if (((w >> 16) & ex) == ex) w &= 0x0000FFFFu;
+  return w;
+}
+
+// Two codes (bytes 0, 1 or 2, 3 of w) as exact fp16 values.
+template <int FMT, int HI>
+DF2_DEV uint32_t codes2(uint32_t w) {
+  if constexpr (FMT == kKvInt8) {
+    return codes_to_half2(w ^ 0x80808080u, HI ? 0x4342u : 0x4140u);
+  } else {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+  }
+}
+
+// FMT: cache format; QBF: queries and output in bf16 (else fp16); MT: 16-row tiles per unit.
+template <int D, int FMT, int MT>
+struct Geo {
+  static constexpr bool kQuant = FMT == kKvInt8 || FMT == kKvE4m3;
+  static constexpr int kRowBytes = D * (kQuant ? 1 : 2);
+  static constexpr int kChunks = kRowBytes / 16;       // 16-byte pieces of a key
+  static constexpr int kSide = kBN * kRowBytes;        // keys (or values) of a tile
+  static constexpr int kScales = kQuant ? 2 * kBN * 4 : 0;
+  static constexpr int kStage = 2 * kSide + kScales;
+  static constexpr int kStages = 3;
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kKG = 4 / MT;                   // key groups
+  static constexpr int kWK = kBN / kKG;                // keys of a warp
+  static constexpr int kNT = D / 8;                    // output column tiles
+  static constexpr int kMergeCols = kNT / 4;           // column tiles joined at a time
+  static constexpr int kMerge = (kKG - 1) * MT * kMergeCols * 4 * 32 * 4;
+  static constexpr int kStat = 4 * 32 * 16;
+  static constexpr int kOff = (kStages + 1) * kBN * 8 + (kStages + 1) * 8 + 64;
+  static constexpr int kFixed = kStages * kStage + kMerge + kStat + kOff;
+};
+
+template <int D, int FMT, int MT, bool QBF>
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
+  using G = Geo<D, FMT, MT>;
+  constexpr bool kQuant = G::kQuant;
+  constexpr bool kBF = kQuant ? false : QBF;  // operand type of both products
+  constexpr int S = G::kStages, KG = G::kKG, WK = G::kWK, NT = G::kNT;
+  constexpr int kSteps = D / 16;
+  extern __shared__ __align__(128) char sm[];
+  const uint32_t ring = smem_addr(sm);
+  float* const merge = reinterpret_cast<float*>(sm + S * G::kStage);
+  float4* const stat = reinterpret_cast<float4*>(sm + S * G::kStage + G::kMerge);
+  long long* const offs = reinterpret_cast<long long*>(sm + S * G::kStage + G::kMerge + G::kStat);  // [S + 1][kBN]
+  int* const badp = reinterpret_cast<int*>(offs + (S + 1) * kBN);                                    // [S + 1][2]
+  long long* const tmp = reinterpret_cast<long long*>(badp + (S + 1) * 2);
+  long long* const pre = tmp + 8;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int rg = wid % MT, kg = wid / MT;
+
+  const long long T = paged_scan<kThreads>(a, pre, tmp);
+  // (no empty runs: a cut unit's CTAs are then consecutive)
+  const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
+  if (tid == 0) a.desc[4 * c] = -1;
+  if (c >= C) return;
+  const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
+
+  // ---- the page rows of a tile: threads 0 .. 63, one key each
+  PagedCursor oc;
+  oc.start(a, pre, t_begin, t_end);
+  long long my_off = -1, my_soff = 0;
+  int my_bad = 0;
+  auto look_up = [&]() {  // offsets of tile oc into registers; advances oc
+    my_off = -1;
+    my_bad = 0;
+    if (!oc.valid()) return;
+    if (tid < kBN) {
+      const int key = (oc.u.t0 + oc.i) * kBN + tid;
+      if (key >= oc.u.lo && key < oc.u.hi) {
+        const int pi = key / a.c.page_size, row = key - pi * a.c.page_size;
+        const int page = __ldg(a.c.table + oc.r * a.c.table_stride + pi);
+        if (!paged_row(a.c, page, row, oc.h, &my_off, &my_soff)) {
+          my_bad = 1;
+          if (a.rq.status) a.rq.status[oc.r] = 1;
+        }
+      }
+    }
+    oc.next(a);
+  };
+  // quantised: the scales' copies are issued with the look-up, one group ahead of the codes
+  auto put = [&](int j) {  // into slot j of the offsets' ring
+    const int s = j % (S + 1);
+    if (tid < kBN) {
+      offs[s * kBN + tid] = my_off;
+      const int any = __any_sync(0xffffffffu, my_bad);
+      if (lane == 0) badp[2 * s + wid] = any;
+    }
+  };
+  long long soff_next = 0;
+  bool sval_next = false;
+  auto issue = [&](int j) {  // the copies of tile j of the run
+    const uint32_t dst = ring + (j % S) * G::kStage;
+    const long long* o = offs + (j % (S + 1)) * kBN;
+    constexpr int kRowsPer = kThreads / G::kChunks;
+    const int ch = tid % G::kChunks;
+#pragma unroll
+    for (int i = 0; i < kBN / kRowsPer; ++i) {
+      const int row = tid / G::kChunks + i * kRowsPer;
+      const long long off = o[row];
+      const int bytes = off >= 0 ? 16 : 0;
+      const long long byte = (off >= 0 ? off * (kQuant ? 1 : 2) : 0) + ch * 16;
+      int ck, cv;
+      if constexpr (kQuant) {
+        ck = D == 128 ? ch ^ ((row & 1) << 2) : ch;
+        cv = D == 128 ? ch ^ (row & 6) : ch ^ ((row >> 1) & 3);
+      } else {
+        ck = cv = ch ^ (row & 7);
+      }
+      cp_async16(dst + row * G::kRowBytes + ck * 16, a.c.k + byte, bytes);
+      cp_async16(dst + G::kSide + row * G::kRowBytes + cv * 16, a.c.v + byte, bytes);
+    }
+    if constexpr (kQuant) {
+      if (tid < kBN) {
+        cp_async4(dst + 2 * G::kSide + tid * 4, a.c.k_scale + soff_next, sval_next ? 4 : 0);
+        cp_async4(dst + 2 * G::kSide + kBN * 4 + tid * 4, a.c.v_scale + soff_next, sval_next ? 4 : 0);
+      }
+    }
+  };
+
+  const int n_tiles = static_cast<int>(t_end - t_begin);
+  // prologue: tiles 0 .. S - 2 in flight, the offsets of tile S - 1 looked up
+#pragma unroll
+  for (int j = 0; j < S - 1; ++j) {
+    look_up();
+    put(j);
+    soff_next = my_soff;
+    sval_next = my_off >= 0;
+    __syncthreads();
+    if (j < n_tiles) issue(j);
+    cp_commit();
+  }
+  look_up();
+  put(S - 1);
+  soff_next = my_soff;
+  sval_next = my_off >= 0;
+
+  PagedCursor cc;
+  cc.start(a, pre, t_begin, t_end);
+  uint32_t qf[kSteps][4];
+  float o[NT][4];
+  float m0 = 0, m1 = 0, l0 = 0, l1 = 0, sc0 = 0, sc1 = 0, vref = 0, vinv = 0;
+  int hi0 = 0, hi1 = 0, lo0 = 0, lo1 = 0, base = 0;       // visible keys of this thread's two rows
+  int hi_min = 0, lo_max = 0;                             // keys in [lo_max, hi_min) are visible to every row
+  bool mixed_rows = false;
+  unsigned long long w0 = 0, w1 = 0;
+  bool fresh = true;
+
+  for (int j = 0; j < n_tiles; ++j) {
+    if (fresh) {
+      fresh = false;
+      const int rows = cc.n * a.s.group;
+      const int ra = cc.qt * G::kRows + rg * 16 + g, rb = ra + 8;
+      base = cc.len - cc.n;
+      const int ia = ra / a.s.group, ib = rb / a.s.group;
+      const bool va = ra < rows, vb = rb < rows;
+      hi0 = va ? (a.s.causal == 1 ? min(cc.len, base + ia + 1) : cc.len) : 0;
+      hi1 = vb ? (a.s.causal == 1 ? min(cc.len, base + ib + 1) : cc.len) : 0;
+      lo0 = a.s.window > 0 ? base + ia - a.s.window + 1 : 0;
+      lo1 = a.s.window > 0 ? base + ib - a.s.window + 1 : 0;
+      if (a.s.causal == 2) {
+        w0 = va ? __ldg(a.tree + cc.b0 + ia) : 0ull;
+        w1 = vb ? __ldg(a.tree + cc.b0 + ib) : 0ull;
+      }
+      const int i_first = cc.qt * G::kRows / a.s.group;
+      const int i_last = (min((cc.qt + 1) * G::kRows, rows) - 1) / a.s.group;
+      hi_min = a.s.causal == 1 ? min(cc.len, base + i_first + 1) : (a.s.causal == 2 ? min(cc.len, base) : cc.len);
+      lo_max = a.s.window > 0 ? base + i_last - a.s.window + 1 : 0;
+      mixed_rows = i_last > i_first || a.s.causal == 2;
+      const char* pa = a.q.p + ((cc.b0 + ia) * a.q.token_stride + (cc.h * a.s.group + ra % a.s.group) * a.q.head_stride) * 2;
+      const char* pb = a.q.p + ((cc.b0 + ib) * a.q.token_stride + (cc.h * a.s.group + rb % a.s.group) * a.q.head_stride) * 2;
+      if constexpr (!kQuant) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          qf[s][0] = va ? *reinterpret_cast<const uint32_t*>(pa + (16 * s + 2 * q) * 2) : 0u;
+          qf[s][1] = vb ? *reinterpret_cast<const uint32_t*>(pb + (16 * s + 2 * q) * 2) : 0u;
+          qf[s][2] = va ? *reinterpret_cast<const uint32_t*>(pa + (16 * s + 2 * q + 8) * 2) : 0u;
+          qf[s][3] = vb ? *reinterpret_cast<const uint32_t*>(pb + (16 * s + 2 * q + 8) * 2) : 0u;
+        }
+        sc0 = sc1 = a.scale_log2;
+      } else {
+        // step 4 h + w, slots 2 q, 2 q + 1 and 2 q + 8, 2 q + 9 hold channels 16 (q + 4 h) + 4 w + 0 .. 3
+        float xa = 0.f, xb = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < kSteps / 4; ++hh) {
+#pragma unroll
+          for (int w = 0; w < 4; w += 2) {
+            const int d = 16 * (q + 4 * hh) + 4 * w;
+            const uint4 ua = va ? *reinterpret_cast<const uint4*>(pa + d * 2) : make_uint4(0, 0, 0, 0);
+            const uint4 ub = vb ? *reinterpret_cast<const uint4*>(pb + d * 2) : make_uint4(0, 0, 0, 0);
+            qf[4 * hh + w][0] = ua.x, qf[4 * hh + w][2] = ua.y, qf[4 * hh + w + 1][0] = ua.z, qf[4 * hh + w + 1][2] = ua.w;
+            qf[4 * hh + w][1] = ub.x, qf[4 * hh + w][3] = ub.y, qf[4 * hh + w + 1][1] = ub.z, qf[4 * hh + w + 1][3] = ub.w;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<QBF>(qf[s][e]);
+            float& x = (e & 1) ? xb : xa;
+            x = fmaxf(x, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+#pragma unroll
+        for (int of = 1; of <= 2; of <<= 1) {
+          xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, of));
+          xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, of));
+        }
+        // 2^-e with the row's largest magnitude in [2^e, 2^(e + 1)); 1 for zero and nonfinite rows
+        auto shift = [](float x) {
+          const uint32_t ex = __float_as_uint(x) >> 23;
+          return ex == 0 || ex >= 254 ? 1.f : __uint_as_float((254u - ex) << 23);
+        };
+        const float fa = shift(xa), fb = shift(xb);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<QBF>(qf[s][e]);
+            const float m = (e & 1) ? fb : fa;
+            qf[s][e] = pack2<false>(f.x * m, f.y * m);
+          }
+        sc0 = a.scale_log2 / fa;
+        sc1 = a.scale_log2 / fb;
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = vref = 0.f;
+    }
+
+    cp_wait<S - 2>();
+    __syncthreads();  // tile j has landed; tile j - 1's buffer and the offsets of tile j + S - 1 are free / written
+    if (j + S - 1 < n_tiles) issue(j + S - 1);
+    cp_commit();
+    look_up();  // tile j + S
+
+    const uint32_t ks = ring + (j % S) * G::kStage, vs = ks + G::kSide;
+    const float* ksc = reinterpret_cast<const float*>(sm + (j % S) * G::kStage + 2 * G::kSide);
+    const float* vsc = ksc + kBN;
+    const int kw = kg * WK;  // first key of this warp in the tile
+    const int key0 = (cc.u.t0 + cc.i) * kBN;
+
+    // ---- scores
+    float z[WK / 8][4];
+#pragma unroll
+    for (int t = 0; t < WK / 8; ++t) z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
+    if constexpr (!kQuant) {
+#pragma unroll
+      for (int t = 0; t < WK / 8; t += 2) {
+        const int row = kw + 8 * t + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t b[4];
+          ldsm4(b, ks + row * G::kRowBytes + (((2 * s + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+          mma16<kBF>(z[t], qf[s], b[0], b[1]);
+          mma16<kBF>(z[t + 1], qf[s], b[2], b[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < WK / 8; ++t) {
+        const int row = kw + 8 * t + g;
+#pragma unroll
+        for (int hh = 0; hh < kSteps / 4; ++hh) {
+          const int ch = q + 4 * hh;
+          const uint4 w = lds16(ks + row * G::kRowBytes + ((D == 128 ? ch ^ ((row & 1) << 2) : ch) << 4));
+          mma16<false>(z[t], qf[4 * hh + 0], codes2<FMT, 0>(w.x), codes2<FMT, 1>(w.x));
+          mma16<false>(z[t], qf[4 * hh + 1], codes2<FMT, 0>(w.y), codes2<FMT, 1>(w.y));
+          mma16<false>(z[t], qf[4 * hh + 2], codes2<FMT, 0>(w.z), codes2<FMT, 1>(w.z));
+          mma16<false>(z[t], qf[4 * hh + 3], codes2<FMT, 0>(w.w), codes2<FMT, 1>(w.w));
+        }
+      }
+    }
+    // ---- scale, mask, running maximum
+    const int* bad = badp + 2 * (j % (S + 1));
+    const bool any_bad = (bad[0] | bad[1]) != 0;
+    const bool masked = key0 < lo_max || key0 + kBN > hi_min || any_bad;
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < WK / 8; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float s0 = z[t][e] * sc0, s1 = z[t][2 + e] * sc1;
+        const int kk = kw + 8 * t + 2 * q + e;
+        if constexpr (kQuant) {
+          const float f = ksc[kk];
+          s0 *= f;
+          s1 *= f;
+        }
+        if (masked) {
+          const int key = key0 + kk;
+          bool v0 = key >= lo0 && key < hi0, v1 = key >= lo1 && key < hi1;
+          if (a.s.causal == 2 && key >= base) {
+            v0 = v0 && ((w0 >> (key - base)) & 1ull);
+            v1 = v1 && ((w1 >> (key - base)) & 1ull);
+          }
+          if (any_bad && offs[(j % (S + 1)) * kBN + kk] < 0) v0 = v1 = false;
+          s0 = v0 ? s0 : -INFINITY;
+          s1 = v1 ? s1 : -INFINITY;
+        }
+        z[t][e] = s0;
+        z[t][2 + e] = s1;
+        x0 = fmaxf(x0, s0);
+        x1 = fmaxf(x1, s1);
+      }
+    }
+#pragma unroll
+    for (int of = 1; of <= 2; of <<= 1) {
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, of));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, of));
+    }
+    const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+    // a row that has seen nothing keeps weights of zero: 2^(-inf - 0)
+    const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+    float f0 = ex2(m0 - r0), f1 = ex2(m1 - r1);
+    m0 = n0;
+    m1 = n1;
+    l0 *= f0;
+    l1 *= f1;
+    if constexpr (kQuant) {
+      // the largest finite value scale of this warp's keys
+      float v = 0.f;
+#pragma unroll
+      for (int i = lane; i < WK; i += 32) v = vsc[kw + i] < INFINITY ? fmaxf(v, vsc[kw + i]) : v;
+      if (WK < 32 && lane >= WK) v = 0.f;
+      v = warp_max(v);
+      if (v > vref) {
+        v = fmaxf(v, 1.17549435e-38f);
+        const float f = vref / v;
+        vref = v;
+        vinv = 1.f / v;
+        f0 *= f;
+        f1 *= f;
+      }
+    }
+    if (f0 != 1.f || f1 != 1.f) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[t][0] *= f0;
+        o[t][1] *= f0;
+        o[t][2] *= f1;
+        o[t][3] *= f1;
+      }
+    }
+    // ---- weights and the values' product
+#pragma unroll
+    for (int t = 0; t < WK / 8; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float p0 = ex2(z[t][e] - r0), p1 = ex2(z[t][2 + e] - r1);
+        l0 += p0;
+        l1 += p1;
+        if constexpr (kQuant) {
+          const float f = vsc[kw + 8 * t + 2 * q + e] * vinv;
+          p0 = p0 == 0.f ? 0.f : p0 * f;  // (a masked position's scale may be anything)
+          p1 = p1 == 0.f ? 0.f : p1 * f;
+        }
+        z[t][e] = p0;
+        z[t][2 + e] = p1;
+      }
+    }
+    // 16-bit values may be infinities or NaN at positions that only some rows see: there the
+    // product takes zeros in their place, and each is added to the rows whose weight for it is not zero
+    bool poison = false;
+    if constexpr (!kQuant) {
+      if (masked && mixed_rows) {
+        bool bad_v = false;
+        constexpr uint32_t ex = kBF ? 0x7F80u : 0x7C00u;
+        for (int i = lane; i < WK * G::kChunks; i += 32) {
+          const uint4 w = lds16(vs + kw * G::kRowBytes + i * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) bad_v |= (ww[u] & ex) == ex || ((ww[u] >> 16) & ex) == ex;
+        }
+        poison = __any_sync(0xffffffffu, bad_v);
+      }
+    }
+    if (poison) {
+      if constexpr (!kQuant) {
+#pragma unroll
+        for (int t = 0; t < WK / 8; ++t) {
+          for (int qq = 0; qq < 4; ++qq) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int src = (lane & ~3) | qq, row = kw + 8 * t + 2 * qq + e;
+              const float p0 = __shfl_sync(0xffffffffu, z[t][e], src), p1 = __shfl_sync(0xffffffffu, z[t][2 + e], src);
+#pragma unroll
+              for (int d = 0; d < NT; ++d) {
+                uint32_t w;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vs + row * G::kRowBytes + ((d ^ (row & 7)) << 4) + 4 * q) : "memory");
+                const float2 v = unpack2<kBF>(w);
+                if (!isfinite(v.x)) {
+                  if (p0 != 0.f) o[d][0] += v.x;
+                  if (p1 != 0.f) o[d][2] += v.x;
+                }
+                if (!isfinite(v.y)) {
+                  if (p0 != 0.f) o[d][1] += v.y;
+                  if (p1 != 0.f) o[d][3] += v.y;
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+    {
+#pragma unroll
+      for (int kk = 0; kk < WK / 16; ++kk) {
+        const uint32_t pf[4] = {pack2<kBF>(z[2 * kk][0], z[2 * kk][1]), pack2<kBF>(z[2 * kk][2], z[2 * kk][3]),
+                                pack2<kBF>(z[2 * kk + 1][0], z[2 * kk + 1][1]),
+                                pack2<kBF>(z[2 * kk + 1][2], z[2 * kk + 1][3])};
+        if constexpr (!kQuant) {
+          const int row = kw + 16 * kk + (lane & 15);
+#pragma unroll
+          for (int t = 0; t < NT; t += 2) {
+            uint32_t b[4];
+            ldsm4_t(b, vs + row * G::kRowBytes + (((t + (lane >> 4)) ^ (row & 7)) << 4));
+            if (poison) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) b[i] = finite2<kBF>(b[i]);
+            }
+            mma16<kBF>(o[t], pf, b[0], b[1]);
+            mma16<kBF>(o[t + 1], pf, b[2], b[3]);
+          }
+        } else {
+          const int row = kw + 16 * kk + 2 * q;
+          uint32_t r[4][NT / 4];  // codes of channels (D / 8) g .. of keys row, row + 1, row + 8, row + 9
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = row + (i & 1) + ((i >> 1) << 3);
+            if constexpr (D == 128) {
+              const uint4 w = lds16(vs + rr * G::kRowBytes + ((g ^ (rr & 6)) << 4));
+              r[i][0] = w.x, r[i][1] = w.y, r[i][2] = w.z, r[i][3] = w.w;
+            } else {
+              const uint2 w = lds8(vs + rr * G::kRowBytes + (((g >> 1) ^ ((rr >> 1) & 3)) << 4) + (g & 1) * 8);
+              r[i][0] = w.x, r[i][1] = w.y;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < NT / 4; ++w) {
+            const uint32_t ab = __byte_perm(r[0][w], r[1][w], 0x5140), ab2 = __byte_perm(r[0][w], r[1][w], 0x7362);
+            const uint32_t cd = __byte_perm(r[2][w], r[3][w], 0x5140), cd2 = __byte_perm(r[2][w], r[3][w], 0x7362);
+            mma16<false>(o[4 * w + 0], pf, codes2<FMT, 0>(ab), codes2<FMT, 0>(cd));
+            mma16<false>(o[4 * w + 1], pf, codes2<FMT, 1>(ab), codes2<FMT, 1>(cd));
+            mma16<false>(o[4 * w + 2], pf, codes2<FMT, 0>(ab2), codes2<FMT, 0>(cd2));
+            mma16<false>(o[4 * w + 3], pf, codes2<FMT, 1>(ab2), codes2<FMT, 1>(cd2));
+          }
+        }
+      }
+    }
+
+    put(j + S);
+    soff_next = my_soff;
+    sval_next = my_off >= 0;
+
+    // ---- end of the unit or of the run: join the key groups, write
+    const bool last = j == n_tiles - 1;
+    if (cc.unit_ends() || last) {
+      if constexpr (kQuant) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] *= vref;
+      }
+#pragma unroll
+      for (int of = 1; of <= 2; of <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, of);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, of);
+      }
+      if constexpr (KG > 1) {
+        stat[wid * 32 + lane] = make_float4(m0, m1, l0, l1);
+        __syncthreads();
+        float y0 = m0, y1 = m1;
+#pragma unroll
+        for (int i = 0; i < KG; ++i) {
+          const float4 st = stat[(i * MT + rg) * 32 + lane];
+          y0 = fmaxf(y0, st.x);
+          y1 = fmaxf(y1, st.y);
+        }
+        const float b0 = y0 == -INFINITY ? 0.f : y0, b1 = y1 == -INFINITY ? 0.f : y1;
+        const float e0 = ex2(m0 - b0), e1 = ex2(m1 - b1);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          o[t][0] *= e0;
+          o[t][1] *= e0;
+          o[t][2] *= e1;
+          o[t][3] *= e1;
+        }
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < KG; ++i) {
+          const float4 st = stat[(i * MT + rg) * 32 + lane];
+          l0 += st.z * ex2(st.x - b0);
+          l1 += st.w * ex2(st.y - b1);
+        }
+        m0 = y0;
+        m1 = y1;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          constexpr int MC = G::kMergeCols;
+          if (part) __syncthreads();
+          if (kg > 0) {
+#pragma unroll
+            for (int t = 0; t < MC; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) merge[((((kg - 1) * MT + rg) * MC + t) * 4 + e) * 32 + lane] = o[part * MC + t][e];
+          }
+          __syncthreads();
+          if (kg == 0) {
+#pragma unroll
+            for (int i = 0; i < KG - 1; ++i)
+#pragma unroll
+              for (int t = 0; t < MC; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[part * MC + t][e] += merge[(((i * MT + rg) * MC + t) * 4 + e) * 32 + lane];
+          }
+        }
+        // the buffers are next written after the next tile's barrier
+      }
+      if (kg == 0) {
+        const int rows = cc.n * a.s.group;
+        const bool whole = cc.unit_t >= t_begin && cc.unit_ends();
+        const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
+        if (!whole && tid == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
+          const long long tl = cc.unit_t + cc.u.nt;
+          long long cb = (tl * C - 1) / T;  // the CTA of the unit's last tile
+          int* dd = a.desc + 4 * c;
+          dd[1] = cc.h;
+          dd[2] = cc.qt;
+          dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
+          dd[0] = cc.r;
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int lr = rg * 16 + g + 8 * hf, row = cc.qt * G::kRows + lr;
+          if (row >= rows) continue;
+          const float l = hf ? l1 : l0, m = hf ? m1 : m0;
+          if (whole) {
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (a NaN sum stays NaN)
+            const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
+            char* po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
+            if constexpr (!kQuant) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                *reinterpret_cast<uint32_t*>(po + (8 * t + 2 * q) * 2) =
+                    pack2<QBF>(o[t][2 * hf] * inv, o[t][2 * hf + 1] * inv);
+            } else {
+              // this thread's columns: (D / 8) (2 q + e) + t
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int t = 0; t < NT; t += 8)
+                  *reinterpret_cast<uint4*>(po + (NT * (2 * q + e) + t) * 2) = make_uint4(
+                      pack2<QBF>(o[t][2 * hf + e] * inv, o[t + 1][2 * hf + e] * inv),
+                      pack2<QBF>(o[t + 2][2 * hf + e] * inv, o[t + 3][2 * hf + e] * inv),
+                      pack2<QBF>(o[t + 4][2 * hf + e] * inv, o[t + 5][2 * hf + e] * inv),
+                      pack2<QBF>(o[t + 6][2 * hf + e] * inv, o[t + 7][2 * hf + e] * inv));
+            }
+            if (a.lse && q == 0)
+              a.lse[static_cast<long long>(cc.b0 + i) * (a.c.n_kv * a.s.group) + head] =
+                  l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+          } else {
+            float* pp = a.part + slot * (G::kRows * (D + 2)) + lr * D;
+            if constexpr (!kQuant) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                *reinterpret_cast<float2*>(pp + 8 * t + 2 * q) = make_float2(o[t][2 * hf], o[t][2 * hf + 1]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int t = 0; t < NT; t += 4)
+                  *reinterpret_cast<float4*>(pp + NT * (2 * q + e) + t) =
+                      make_float4(o[t][2 * hf + e], o[t + 1][2 * hf + e], o[t + 2][2 * hf + e], o[t + 3][2 * hf + e]);
+            }
+            if (q == 0)
+              *reinterpret_cast<float2*>(a.part + slot * (G::kRows * (D + 2)) + G::kRows * D + 2 * lr) = make_float2(m, l);
+          }
+        }
+      }
+      fresh = true;
+    }
+    cc.next(a);
+  }
+}
+
+// Joins the partials of the units cut between CTAs: one warp per row, the partials added
+// in CTA order.
+template <int D, bool QBF>
+__global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+  const int* dd = a.desc + 4 * blockIdx.x;
+  const int r = dd[0];
+  if (r < 0) return;
+  const int h = dd[1], qt = dd[2], c1 = dd[3] >> 1, c0 = blockIdx.x;
+  const long long first = 2ll * c0 + (dd[3] & 1);
+  const int b0 = a.rq.begin[r], n = a.rq.begin[r + 1] - b0;
+  const int R = a.s.rows, lane = threadIdx.x & 31;
+  const long long stride = static_cast<long long>(R) * (D + 2);
+  constexpr int V = D / 32;  // channels per lane
+  for (int lr = blockIdx.y * 4 + (threadIdx.x >> 5); lr < R; lr += 4 * gridDim.y) {
+    const int row = qt * R + lr;
+    if (row >= n * a.s.group) return;
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const long long s = c == c0 ? first : 2ll * c;
+      m = fmaxf(m, a.part[s * stride + R * D + 2 * lr]);
+    }
+    m = warp_max(m);
+    const float ms = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float* p = a.part + (c == c0 ? first : 2ll * c) * stride;
+      const float2 st = *reinterpret_cast<const float2*>(p + R * D + 2 * lr);
+      const float f = ex2(st.x - ms);
+      l += st.y * f;
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + lr * D + 4 * lane);
+        o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p + lr * D + 2 * lane);
+        o[0] += x.x * f, o[1] += x.y * f;
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int i = row / a.s.group, head = h * a.s.group + row % a.s.group;
+    char* po = a.out.p + ((b0 + i) * a.out.token_stride + head * a.out.head_stride + V * lane) * 2;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(po) = make_uint2(pack2<QBF>(o[0] * inv, o[1] * inv), pack2<QBF>(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(po) = pack2<QBF>(o[0] * inv, o[1] * inv);
+    if (a.lse && lane == 0)
+      a.lse[static_cast<long long>(b0 + i) * (a.c.n_kv * a.s.group) + head] =
+          l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+  }
+}
+
+template <int D, int FMT, int MT, bool QBF>
+cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
+  using G = Geo<D, FMT, MT>;
+  static std::atomic<unsigned long long> done{0};
+  const int smem = G::kFixed + (a.rq.n_req + 1 + 8) * 8;
+  cudaError_t e = set_smem_once(paged_attn_kernel<D, FMT, MT, QBF>, G::kFixed + (1024 + 16) * 8, done);
+  if (e != cudaSuccess) return e;
+  const int per_sm = kPagedMaxCtasPerSm;
+  // no more CTAs than tiles there can be
+  const long long rt = (static_cast<long long>(a.rq.max_new) * a.s.group + G::kRows - 1) / G::kRows;
+  const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + kBN - 1) / kBN + 1);
+  a.ctas = static_cast<int>(most < static_cast<long long>(num_sms) * per_sm ? most : num_sms * per_sm);
+  paged_attn_kernel<D, FMT, MT, QBF><<<a.ctas, kThreads, smem, st>>>(a);
+  paged_combine_kernel<D, QBF><<<dim3(a.ctas, MT), 128, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, int FMT, bool QBF>
+cudaError_t launch_fmt(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
+  a.s.rows = paged_rows(a.rq.max_new, a.s.group);
+  a.s.bn = kBN;
+  if (a.s.rows == 16) return launch_rows<D, FMT, 1, QBF>(a, num_sms, st);
+  if (a.s.rows == 32) return launch_rows<D, FMT, 2, QBF>(a, num_sms, st);
+  return launch_rows<D, FMT, 4, QBF>(a, num_sms, st);
+}
+
+template <int D>
+cudaError_t launch_dim(PagedAttnArgs& a, int fmt, int qtype, int num_sms, cudaStream_t st) {
+  const bool bf = qtype == kTBf16;
+  switch (fmt) {
+    case kKvBf16: return launch_fmt<D, kKvBf16, true>(a, num_sms, st);
+    case kKvF16: return launch_fmt<D, kKvF16, false>(a, num_sms, st);
+    case kKvInt8: return bf ? launch_fmt<D, kKvInt8, true>(a, num_sms, st) : launch_fmt<D, kKvInt8, false>(a, num_sms, st);
+    default: return bf ? launch_fmt<D, kKvE4m3, true>(a, num_sms, st) : launch_fmt<D, kKvE4m3, false>(a, num_sms, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
+  return head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
+}
+
+}  // namespace df2

@@ -473,6 +473,163 @@ dflash2_status dflash2_head_topk_noalloc(const void* lm_head, int32_t vocab, int
 dflash2_status dflash2_debug_set_pipeline_error(dflash2_handle* h, void* stream);
 dflash2_status dflash2_debug_noalloc_inject_error(int32_t on);
 
+/* ------------------------------------------------------------------------------------
+ * The target's side of a step: a paged K/V cache (quantised as it is written), attention
+ * of new tokens over it, and truncated sampling.  These calls need no drafter handle.
+ *
+ * A paged handle fixes the geometry of one target layer and owns the attention's scratch;
+ * the pools, page tables and lengths are the caller's and are passed to each call (one
+ * handle serves every layer of that geometry, one stream at a time).
+ *
+ * Requests: the new tokens of a call are packed request after request; request r has
+ * rows token_begin[r] .. token_begin[r + 1] - 1 (int32 [n_req + 1], device), n of them.
+ * kv_len[r] (int32 [n_req], device) is the length of its cache with the new tokens in
+ * it: new token i is at position kv_len[r] - n + i.  Position p of request r is row
+ * p % page_size of page page_table[r][p / page_size].
+ *
+ * Errors found on the device go to status [n_req] (int32, or NULL), which the calls only
+ * ever set to DFLASH2_E_INVAL and never clear: a token range outside the call's rows, a
+ * length outside the page table's row (or max_len), more new tokens than max_new, a page
+ * id outside 0 .. n_pages - 1.  No address outside the pools is formed for them.  A
+ * request with a bad range or length is skipped (its output rows keep what they held); a
+ * bad page's rows are not written, read back as zeros, and are masked in the attention.
+ * ------------------------------------------------------------------------------------ */
+
+/* Cache formats.  INT8 and E4M3 hold codes and one fp32 scale per (position, KV head) and
+ * side: scale = max(amax|x| / Q, 2^-126), Q = 127 or 448; code = x / scale rounded to
+ * nearest (ties to even), saturated; the value is code * scale.  A row with an infinity or a NaN
+ * gets a nonfinite scale and zero codes, and reads back as NaN. */
+enum { DFLASH2_KV_BF16 = 0, DFLASH2_KV_F16 = 1, DFLASH2_KV_INT8 = 2, DFLASH2_KV_E4M3 = 3 };
+/* Element types of rows outside the cache. */
+enum { DFLASH2_T_BF16 = 0, DFLASH2_T_F16 = 1, DFLASH2_T_F32 = 2 };
+
+#define DFLASH2_PAGED_MAX_REQUESTS 1024
+/* new tokens of a request with a tree mask: one bit of a 64-bit word each */
+#define DFLASH2_PAGED_MAX_TREE 64
+
+typedef struct dflash2_paged_handle dflash2_paged_handle;
+
+typedef struct dflash2_paged_config {
+  int32_t n_q_heads;     /* a multiple of n_kv_heads, at most 64 times it               */
+  int32_t n_kv_heads;
+  int32_t head_dim;      /* 64 or 128                                                   */
+  int32_t page_size;     /* positions per page: any from 1                              */
+  int32_t kv_format;     /* DFLASH2_KV_*                                                */
+  int32_t max_requests;  /* most requests of a call: 1 .. DFLASH2_PAGED_MAX_REQUESTS    */
+} dflash2_paged_config;
+
+/* One layer's pools.  Element (page, row, head, channel) of k and of v is at
+ * page * page_stride + row * token_stride + head * head_stride + channel (elements; any
+ * order of pages, rows and heads).  k, v 16-byte aligned, strides whole 16 bytes.
+ * k_scale, v_scale: fp32, the same with scale_* strides and no channel (NULL with 16-bit
+ * formats).  page_table int32 [n_req][table_stride], its first max_pages columns used. */
+typedef struct dflash2_paged_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+  int64_t table_stride;
+  int32_t n_pages;
+  int32_t max_pages;
+} dflash2_paged_cache;
+
+/* Rows [tokens][heads][head_dim] outside the cache: channels contiguous, p 16-byte
+ * aligned, strides (elements) whole 16 bytes. */
+typedef struct dflash2_rows {
+  void* p;
+  int64_t token_stride, head_stride;
+  int32_t type; /* DFLASH2_T_* */
+  int32_t reserved;
+} dflash2_rows;
+
+/* Creates and destroys a handle (destroy waits for the device's work). */
+dflash2_status dflash2_paged_create(const dflash2_paged_config* cfg, dflash2_paged_handle** out);
+dflash2_status dflash2_paged_destroy(dflash2_paged_handle* h);
+
+/* Writes the new tokens' keys and values (rows of any DFLASH2_T_* type, n_kv_heads heads)
+ * into their positions of the cache, quantising as they are written.  n_tokens: rows of k
+ * and v (host). */
+dflash2_status dflash2_paged_write(dflash2_paged_handle* h, const dflash2_paged_cache* cache, int32_t n_req,
+                                   int32_t n_tokens, const int32_t* token_begin, const int32_t* kv_len,
+                                   const dflash2_rows* k, const dflash2_rows* v, int32_t* status, void* stream);
+
+/* Reads the same positions back: the values code * scale (or the 16-bit values), rounded
+ * to the rows' type. */
+dflash2_status dflash2_paged_read(dflash2_paged_handle* h, const dflash2_paged_cache* cache, int32_t n_req,
+                                  int32_t n_tokens, const int32_t* token_begin, const int32_t* kv_len,
+                                  const dflash2_rows* k, const dflash2_rows* v, int32_t* status, void* stream);
+
+/* Attention of the new tokens (already written) over their requests' caches:
+ *   out[i][h] = sum_j softmax_j(scale * <q[i][h], k_j>) v_j, KV head h / (n_q_heads / n_kv_heads),
+ * over the visible positions j of token i at position p = kv_len - n + i:
+ *   j < kv_len;  causal != 0: j <= p;  window > 0: p - j < window;
+ *   tree_mask != NULL (causal ignored): among the new tokens, bit (j - (kv_len - n)) of
+ *   tree_mask[row of i] (uint64; n <= DFLASH2_PAGED_MAX_TREE); older positions are visible.
+ * A token that sees nothing gets zeros (and lse = -infinity).  Masked positions carry no
+ * weight whatever they hold (NaN and infinities included).  q, out: bf16 or fp16, the
+ * same type, which with a 16-bit cache is the cache's.  Scores, sums and products are
+ * accumulated in fp32. */
+typedef struct dflash2_paged_attention_args {
+  int32_t n_req;
+  int32_t n_tokens;    /* rows of q, out, tree_mask, lse                                  */
+  int32_t max_new;     /* at least every request's number of new tokens (host bound)      */
+  int32_t max_len;     /* at least every request's kv_len (host bound)                    */
+  int32_t causal;
+  int32_t window;      /* 0: none                                                         */
+  float scale;         /* finite                                                          */
+  int32_t reserved;
+  const int32_t* token_begin;
+  const int32_t* kv_len;
+  dflash2_rows q, out; /* n_q_heads heads                                                 */
+  const uint64_t* tree_mask; /* [n_tokens] or NULL                                        */
+  float* lse;          /* fp32 [n_tokens][n_q_heads] or NULL: natural log of the sum of exp(score) */
+  int32_t* status;
+} dflash2_paged_attention_args;
+dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_paged_cache* cache,
+                                       const dflash2_paged_attention_args* args, void* stream);
+
+/* Truncated sampling of n_rows rows of logits [vocab] (type DFLASH2_T_*, row_stride
+ * elements apart) with the caller's uniforms.  Per row: weights w_i = exp((x_i - max x) / T);
+ *   top_k > 0: the top_k largest logits stay (equal logits: smaller ids first);
+ *   top_p < 1: in that order, id i stays while the weight before it is less than top_p
+ *     of the weight that top_k left (the first always stays);
+ *   min_p > 0: w_i >= min_p stays;
+ * and the token is the first id, in id order, whose running weight exceeds u times the
+ * weight left (weights and sums carry about 30 bits and are summed exactly, so the result
+ * does not depend on the order of the device's work).  T = 0: the largest logit (smallest
+ * id); -infinity logits are never taken.
+ *   temperature, top_p, min_p, uniform: fp32 [n_rows]; top_k int32 [n_rows]; each of
+ *     top_k, top_p, min_p may be NULL (off).
+ *   token int32 [n_rows]; prob fp32 [n_rows] or NULL: the token's share of the weight left.
+ *   kept fp32 [n_rows][vocab] (kept_stride elements apart) or NULL: the logits that stay,
+ *     -1e30 elsewhere: with the row's temperature these are the target rows
+ *     of dflash2_verify for the truncated distribution.  May be the logits' own memory.
+ *   status int32 [n_rows] or NULL, written: DFLASH2_OK; DFLASH2_E_NONFINITE (a NaN or
+ *     +infinity, or no logit above -infinity); DFLASH2_E_INVAL (T < 0 or not finite, top_p not above 0,
+ *     min_p outside [0, 1], u outside [0, 1)).  Such a row gets token -1, prob 0, kept -1e30. */
+typedef struct dflash2_sample_args {
+  int32_t n_rows;
+  int32_t vocab;
+  int32_t logits_type;
+  int32_t reserved;
+  const void* logits;
+  int64_t row_stride;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* uniform;
+  int32_t* token;
+  float* prob;
+  float* kept;
+  int64_t kept_stride;
+  int32_t* status;
+} dflash2_sample_args;
+dflash2_status dflash2_sample(const dflash2_sample_args* args, void* stream);
+
 /* Human-readable text of a status code (static string). */
 const char* dflash2_status_string(dflash2_status s);
 
