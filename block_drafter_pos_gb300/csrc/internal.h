@@ -129,19 +129,24 @@ cudaError_t launch_wide(GemvArgs& a, int fmt, int num_sms, bool pdl, cudaStream_
 // pdl: launch with programmatic stream serialisation.
 cudaError_t launch_gemv(GemvArgs& a, int fmt, int max_tiles, int num_sms, bool pdl, cudaStream_t st);
 
-// Raises a kernel's dynamic shared-memory limit on the current device, once per
+// Sets a kernel's attribute (set_smem_once: its dynamic shared-memory limit) on the current device, once per
 // (call site, device): the attribute belongs to a device, so a process driving
 // several GPUs sets it on each.  `done` is the call site's set of devices (bit d).
 template <typename Kern>
-cudaError_t set_smem_once(Kern kern, int smem, std::atomic<unsigned long long>& done) {
+cudaError_t set_attr_once(Kern kern, cudaFuncAttribute attr, int value, std::atomic<unsigned long long>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
   if (bit != 0ull && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(kern, attr, value);
   if (e == cudaSuccess && bit != 0ull) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+
+template <typename Kern>
+cudaError_t set_smem_once(Kern kern, int smem, std::atomic<unsigned long long>& done) {
+  return set_attr_once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, done);
 }
 
 // Launch helper: cudaLaunchKernelEx with the programmatic stream serialisation

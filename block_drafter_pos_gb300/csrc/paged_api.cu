@@ -220,6 +220,14 @@ dflash2_status dflash2_sample(const dflash2_sample_args* args, void* stream) {
   a.kept = x.kept;
   a.kept_stride = x.kept_stride;
   a.status = x.status;
+  const char *l0 = static_cast<const char*>(x.logits), *k0 = reinterpret_cast<const char*>(x.kept);
+  const int64_t lb = ((x.n_rows - 1) * x.row_stride + x.vocab) * t_size(x.logits_type);
+  const int64_t kb = ((x.n_rows - 1) * x.kept_stride + x.vocab) * 4;
+  a.kept_in_place = k0 != nullptr && k0 < l0 + lb && l0 < k0 + kb;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&a.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DFLASH2_E_CUDA;
   return launch_sample(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DFLASH2_OK : DFLASH2_E_CUDA;
 }
 

@@ -1,16 +1,22 @@
 // Truncated sampling: temperature, top-k, top-p and min-p from the caller's uniforms.
 //
-// One thread-block cluster per row; its CTAs keep the row's logits in shared memory, so
-// HBM is read once.  Every weight is a whole number, w = round(2^44 2^((x - max) log2(e) / T)),
-// and sums of them are exact in 64 bits: no decision depends on the order in which the
-// device adds, and equal logits get equal weights.
-//
-// What stays is a threshold in the order (logit descending, id ascending).  It is found by
-// radix selection on the logits' order-preserving 32-bit keys, 11 + 11 + 10 bits: counts for
-// top-k, then weights for top-p (a digit's histogram lies in shared memory, one per CTA,
-// and is added up through distributed shared memory).  Only elements that share the digits
-// found so far enter the next histogram.  Of the elements that equal the threshold the
-// ones with the smallest ids stay, as many as the count or the weight asks for.
+// One thread-block cluster per row, each CTA a slice of it.  Every weight is a whole
+// number, w = round(2^44 2^((x - max) log2(e) / T)), and sums of them are exact in 64 bits:
+// no decision depends on the order in which the device adds, and equal logits get equal
+// weights.  What stays is a prefix of the order (logit descending, id ascending), whose
+// elements are the distinct 64-bit numbers (order-preserving key of the logit, ~id).  Two
+// ways find its last element:
+//  * The short one reads the row once.  Any CTA's k-th largest thread maximum is a lower
+//    bound of the row's k-th largest logit, and min_p bounds the logits outright; elements
+//    above the bound known so far go to a list as the slice streams by (the bound is drawn
+//    tighter after 1, 2, 4, ... chunks), and the `kept` row is filled with its cut value in
+//    the same pass.  The first CTA sorts the few hundred candidates that pass the final
+//    bound, reads top-k, top-p and min-p off the running weights, draws, and puts the logits that
+//    stay into `kept`.  (top-p without top-k needs the weight of all: one more pass.)
+//  * The long one, for rows whose nucleus is wide, or whose bound lets too many pass: a
+//    histogram of counts (top-k) or weights (top-p) over the weight's exponent in steps of
+//    1/32, whose bins spread the shared-memory atomics; the bin with the border is sorted as
+//    above or, where equal logits flood it, searched by the digits of the 64-bit number.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -21,10 +27,17 @@ namespace cg = cooperative_groups;
 namespace df2 {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCtas = 8;
+constexpr int kMaxCtas = 16;
+constexpr int kSlice = 1 << 16;  // most elements of a CTA (its histogram adds 16-bit pieces in 32 bits)
+constexpr int kGroups = 4;       // groups of 4 consecutive elements a thread holds of a chunk
+constexpr int kChunk = kThreads * 4 * kGroups;
+constexpr int kList = 2048;      // candidates of a CTA
+constexpr int kSort = 2048;      // candidates of a row
+constexpr int kShortK = 384;     // largest top_k of the short way
+constexpr int kProbe = 64;       // thread maxima above the bound, per CTA, for top-p alone
 constexpr float kCut = -1e30f;
 
 // round(2^31 2^(j / 32))
@@ -38,11 +51,32 @@ struct Scale {
   float xmax, ch, cl;  // log2(e) / T as ch + cl
 };
 
-DF2_DEV float to_f32(const void* p, long long i, int type) {
-  if (type == 2) return static_cast<const float*>(p)[i];
-  const uint16_t b = static_cast<const uint16_t*>(p)[i];
-  if (type == 0) return bf16_to_f32(b);
+template <int T>  // 0: bf16, 1: fp16, 2: fp32
+DF2_DEV float load1(const char* p, int i) {
+  if constexpr (T == 2) return reinterpret_cast<const float*>(p)[i];
+  const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
+  if constexpr (T == 0) return bf16_to_f32(b);
   return __half2float(__ushort_as_half(b));
+}
+
+// Elements i .. i + 3 of a row; vec: the row is aligned for one wide load.
+template <int T>
+DF2_DEV void load4(const char* p, int i, bool vec, float (&x)[4]) {
+  if (!vec) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = load1<T>(p, i + e);
+  } else if constexpr (T == 2) {
+    const float4 v = *reinterpret_cast<const float4*>(p + 4ll * i);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p + 2ll * i);
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint16_t b = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+      x[e] = T == 0 ? bf16_to_f32(b) : __half2float(__ushort_as_half(b));
+    }
+  }
 }
 
 // 2^44 2^((x - xmax) (ch + cl)), rounded.  The exponent is carried as a sum of two floats (the
@@ -76,16 +110,30 @@ DF2_DEV unsigned long long warp_sum_u64(unsigned long long v) {
   return v;
 }
 
+// The bin of the weight's exponent: -rint(32 log2 w), by the rounded difference's product alone, so it
+// never falls where the logit falls; at most kBins - 1.
+DF2_DEV uint32_t weight_step(float x, const Scale& s) {
+  const float th = (x - s.xmax) * s.ch;
+  return th > -46.f ? static_cast<uint32_t>(static_cast<int>(rintf(th * -32.f))) : kBins - 1;
+}
+
+
 struct Shared {
-  unsigned long long hist[kBins];
+  union {
+    unsigned long long hist[kBins];   // the digits' histogram
+    uint32_t piece[3][kBins];         // the steps' histogram: 16-bit pieces of counts or weights
+    unsigned long long sort[kSort];
+  };
+  unsigned long long w[kSort];           // weights of the sorted candidates
+  unsigned long long list[kList];        // this CTA's candidates
   unsigned long long warp_sum[kWarps];   // of this CTA's warps
-  unsigned long long scan[kWarps + 1];
-  unsigned long long best;               // (key << 32 | ~id) of this CTA
+  unsigned long long scan[kWarps];
+  unsigned long long best;               // this CTA's largest element
   unsigned long long total;
   unsigned long long before;             // weight or count above the digit found
-  uint32_t digit, bad;
+  unsigned long long result;             // the last element that stays; 0: not found
+  uint32_t tau, count, digit, bad, n_sort, run_max;
   uint32_t pw[32];
-  int found;
 };
 
 struct Ctx {
@@ -95,132 +143,293 @@ struct Ctx {
   int wlo, whi;                   // this warp's part of them
 };
 
-// Sum over the cluster of each CTA's `total`.
-DF2_DEV unsigned long long cluster_total(Ctx& c, unsigned long long mine) {
+// Exclusive sum over the block's threads, in thread order; the block's sum in `all`.
+DF2_DEV unsigned long long block_scan(Shared* sh, unsigned long long v, unsigned long long& all) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  mine = warp_sum_u64(mine);
-  if (lane == 0) c.sh->warp_sum[wid] = mine;
-  __syncthreads();
-  if (wid == 0) {
-    const unsigned long long t = warp_sum_u64(c.sh->warp_sum[lane]);
-    if (lane == 0) c.sh->total = t;
-  }
-  c.cl.sync();
-  unsigned long long t = 0;
-  for (int r = 0; r < c.ctas; ++r) t += c.cl.map_shared_rank(c.sh, r)->total;
-  c.cl.sync();
-  return t;
-}
-
-// Adds the cluster's histograms and finds the digit, from the highest down, at which the
-// running sum passes `target` (the first digit with sum above > = target - own); sets digit
-// and the sum above it.  The digit found is never empty.
-template <typename F>
-DF2_DEV void find_digit(Ctx& c, F reached, uint32_t& digit, unsigned long long& above) {
-  Shared* sh = c.sh;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  c.cl.sync();
-  // thread t holds bins kBins - 1 - 2 t and kBins - 2 - 2 t (from the highest down)
-  const int b0 = kBins - 1 - 2 * static_cast<int>(threadIdx.x), b1 = b0 - 1;
-  unsigned long long h0 = 0, h1 = 0;
-  for (int r = 0; r < c.ctas; ++r) {
-    const Shared* o = c.cl.map_shared_rank(sh, r);
-    h0 += o->hist[b0];
-    h1 += o->hist[b1];
-  }
-  unsigned long long x = h0 + h1;
+  unsigned long long x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) sh->scan[wid] = x;
-  if (threadIdx.x == 0) sh->found = 0;
   __syncthreads();
   unsigned long long base = 0;
-  for (int i = 0; i < wid; ++i) base += sh->scan[i];
-  const unsigned long long s0 = base + x - h0 - h1;  // above b0
-  // the digit: the sum above it has not reached the target, the sum with it has
-  if (h0 != 0 && !reached(s0) && reached(s0 + h0)) {
-    sh->digit = b0;
-    sh->before = s0;
-    sh->found = 1;
-  }
-  if (h1 != 0 && !reached(s0 + h0) && reached(s0 + h0 + h1)) {
-    sh->digit = b1;
-    sh->before = s0 + h0;
-    sh->found = 1;
+  all = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const unsigned long long t = sh->scan[i];
+    if (i < wid) base += t;
+    all += t;
   }
   __syncthreads();
-  digit = sh->digit;
+  return base + x - v;
+}
+
+// This CTA's sum into `total` (each warp's in warp_sum); the caller synchronises the cluster.
+DF2_DEV unsigned long long put_total(Ctx& c, unsigned long long mine) {
+  mine = warp_sum_u64(mine);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  if (lane == 0) c.sh->warp_sum[wid] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned long long t = 0;
+    for (int i = 0; i < kWarps; ++i) t += c.sh->warp_sum[i];
+    c.sh->total = t;
+  }
+  return mine;
+}
+
+// Adds the cluster's histograms and finds the bin, from kBins - 1 down, at which the running sum
+// first reaches the target; also the sum above it.  The bin found is never empty.
+template <bool PIECES, typename F>
+DF2_DEV void find_bin(Ctx& c, F reached, uint32_t& bin, unsigned long long& above) {
+  constexpr int kPer = kBins / kThreads;
+  Shared* sh = c.sh;
+  c.cl.sync();
+  const int b0 = kBins - 1 - kPer * static_cast<int>(threadIdx.x);
+  unsigned long long h[kPer], sum = 0, all;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) h[i] = 0;
+  for (int r = 0; r < c.ctas; ++r) {
+    const Shared* o = c.cl.map_shared_rank(sh, r);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      h[i] += PIECES ? o->piece[0][b0 - i] + (static_cast<unsigned long long>(o->piece[1][b0 - i]) << 16) +
+                           (static_cast<unsigned long long>(o->piece[2][b0 - i]) << 32)
+                     : o->hist[b0 - i];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sum += h[i];
+  unsigned long long s = block_scan(sh, sum, all);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (h[i] != 0 && !reached(s) && reached(s + h[i])) {
+      sh->digit = b0 - i;
+      sh->before = s;
+    }
+    s += h[i];
+  }
+  __syncthreads();
+  bin = sh->digit;
   above = sh->before;
   c.cl.sync();
 }
 
-template <bool HELD>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs a) {
-  __shared__ Shared shm;
-  extern __shared__ float held[];
+// Sorts the first n2 (a power of two) elements, largest first.
+DF2_DEV void sort_desc(unsigned long long* v, int n2) {
+  for (int size = 2; size <= n2; size <<= 1)
+    for (int st = size >> 1; st > 0; st >>= 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n2 / 2; i += kThreads) {
+        const int a = 2 * i - (i & (st - 1)), b = a + st;
+        const unsigned long long x = v[a], y = v[b];
+        if ((x < y) == ((a & size) == 0)) {
+          v[a] = y;
+          v[b] = x;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+
+// Appends the warp's elements that are `in` to this CTA's list.
+DF2_DEV void append(Shared* sh, bool in, unsigned long long v) {
+  const uint32_t m = __ballot_sync(0xffffffffu, in);
+  if (m == 0) return;
+  const int lane = threadIdx.x & 31, lead = __ffs(m) - 1;
+  uint32_t at = 0;
+  if (lane == lead) at = atomicAdd(&sh->count, __popc(m));
+  at = __shfl_sync(0xffffffffu, at, lead) + __popc(m & ((1u << lane) - 1u));
+  if (in && at < kList) sh->list[at] = v;
+}
+
+// The first CTA gathers the cluster's lists (elements >= least) into its sort buffer, sorted; returns the number,
+// or more than kSort if they do not fit.  Called by every thread of that CTA after a cluster barrier.
+DF2_DEV int gather_sorted(Ctx& c, unsigned long long least) {
+  Shared* sh = c.sh;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  if (threadIdx.x == 0) sh->n_sort = 0;
+  __syncthreads();
+  bool over = false;
+  for (int r = 0; r < c.ctas; ++r) {
+    const Shared* o = c.cl.map_shared_rank(sh, r);
+    const int cr = static_cast<int>(o->count);
+    over |= cr > kList;
+    if (over) break;
+    for (int i0 = wid * 32; i0 < cr; i0 += kThreads) {
+      const unsigned long long v = i0 + lane < cr ? o->list[i0 + lane] : 0ull;
+      const bool in = i0 + lane < cr && v >= least;
+      const uint32_t m = __ballot_sync(0xffffffffu, in);
+      if (m == 0) continue;
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&sh->n_sort, __popc(m));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+      if (in && at < kSort) sh->sort[at] = v;
+    }
+  }
+  __syncthreads();
+  const int n = over ? kSort + 1 : static_cast<int>(sh->n_sort);
+  if (n > kSort) return n;
+  int n2 = 64;
+  while (n2 < n) n2 <<= 1;
+  for (int i = n + threadIdx.x; i < n2; i += kThreads) sh->sort[i] = 0;
+  sort_desc(sh->sort, n2);
+  return n;
+}
+
+template <int T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Shared& shm = *reinterpret_cast<Shared*>(smem_raw);
   Ctx c{cg::this_cluster(), &shm};
   c.rank = c.cl.block_rank();
   c.ctas = c.cl.num_blocks();
   const int row = blockIdx.x / c.ctas;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int per = (a.vocab + c.ctas - 1) / c.ctas;
+  const int per = ((a.vocab + c.ctas - 1) / c.ctas + 7) & ~7;
   c.lo = min(a.vocab, c.rank * per);
   c.n = min(a.vocab, c.lo + per) - c.lo;
-  const int wper = (c.n + kWarps - 1) / kWarps;
+  const int wper = ((c.n + kWarps - 1) / kWarps + 31) & ~31;
   c.wlo = min(c.n, wid * wper);
   c.whi = min(c.n, c.wlo + wper);
-  const char* src = static_cast<const char*>(a.logits) + row * a.row_stride * (a.type == 2 ? 4 : 2);
-  auto get = [&](int i) { return HELD ? held[i] : to_f32(src, c.lo + i, a.type); };
+  const char* src = static_cast<const char*>(a.logits) + (row * a.row_stride + c.lo) * (T == 2 ? 4 : 2);
+  const bool vec = (reinterpret_cast<uintptr_t>(src) & (T == 2 ? 15 : 7)) == 0;
+  float* const kept = a.kept ? a.kept + row * a.kept_stride + c.lo : nullptr;
+  const bool kvec = (reinterpret_cast<uintptr_t>(kept) & 15) == 0;
+  const bool fill = kept && !a.kept_in_place;  // (in place the logits may be read again)
+  auto element = [&](float x, int i) { return topk_key(x, c.lo + i); };
   if (threadIdx.x < 32) shm.pw[threadIdx.x] = kPow[threadIdx.x];
-  if (threadIdx.x == 0) shm.bad = 0;
+  if (threadIdx.x == 0) shm.bad = shm.count = shm.run_max = 0;
+  const float temp = a.temperature[row], u = a.uniform[row];
+  const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
+  const int top_k_raw = a.top_k ? a.top_k[row] : 0;
+  const int top_k = top_k_raw > 0 && top_k_raw < a.vocab ? top_k_raw : 0;
+  const bool whole = a.vocab <= kList;  // every element is a candidate
+  // thread maxima that the bound has to leave above it (0: no such bound)
+  const int want = temp == 0.f || whole ? 0 : (top_k ? (top_k <= kShortK ? top_k : 0) : (top_p < 1.f ? kProbe : 0));
+  // min_p bounds the logits, x - max >= T ln(min_p), with room for every rounding here; but top-p
+  // after top-k is a share of all that top-k left
+  const bool by_min = !whole && temp > 0.f && min_p > 0.f && min_p <= 1.f && !(top_k && top_p < 1.f);
+  const float reach = by_min ? temp * logf(min_p) * 1.0001f - 1e-4f * temp : 0.f;
+  auto min_bound = [&](float x) { return float_order(x + (reach - 1e-6f * fabsf(x))); };
+  const bool listing = temp > 0.f && (want != 0 || by_min || whole);
   __syncthreads();
 
-  // ---- the largest logit, and nonfinite ones
+  // ---- the slice streams by: each thread's largest, nonfinite ones, candidates
   unsigned long long best = 0;
   bool bad = false;
-  for (int i = c.wlo + lane; i < c.whi; i += 32) {
-    const float x = to_f32(src, c.lo + i, a.type);
-    if (HELD) held[i] = x;
-    bad |= !(x < INFINITY);  // NaN or +infinity
-    const unsigned long long k = topk_key(x, c.lo + i);
-    best = k > best ? k : best;
+  uint32_t tau = 0;
+  auto tighten = [&]() {  // to the want-th largest thread maximum so far, to 14 bits
+    const uint32_t mine = static_cast<uint32_t>(best >> 32);
+    uint32_t t0 = 0;
+#pragma unroll 1
+    for (int b = 31; b >= 18; --b) {
+      const uint32_t t = t0 | (1u << b);
+      if (__syncthreads_count(mine >= t) >= want) t0 = t;
+    }
+    tau = max(tau, t0);
+  };
+  const int chunks = (c.n + kChunk - 1) / kChunk;
+  for (int ck = 0; ck < chunks; ++ck) {
+    float x[kGroups][4];
+    const int base = ck * kChunk + threadIdx.x * 4;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int i = base + g * kThreads * 4;
+      if (i + 3 < c.n) {
+        load4<T>(src, i, vec, x[g]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[g][e] = i + e < c.n ? load1<T>(src, i + e) : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int i = base + g * kThreads * 4;
+      float m = -INFINITY;
+      bool nan = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        nan |= !(x[g][e] < INFINITY);  // NaN or +infinity
+        m = fmaxf(m, x[g][e]);
+      }
+      bad |= nan;
+      if (i < c.n && (best == 0 || float_order(m) > static_cast<uint32_t>(best >> 32))) {
+#pragma unroll
+        for (int e = 3; e >= 0; --e)  // (the smallest id of equal ones)
+          if (i + e < c.n && x[g][e] == m) best = element(m, i + e);
+      }
+      if (fill) {
+        if (kvec && i + 3 < c.n) {
+          *reinterpret_cast<float4*>(kept + i) = make_float4(kCut, kCut, kCut, kCut);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < c.n) kept[i + e] = kCut;
+        }
+      }
+    }
+    if (listing) {
+      if (by_min) {  // the bound of the largest logit so far
+        const uint32_t wm = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
+        if (lane == 0) atomicMax(&shm.run_max, wm);
+        __syncthreads();
+        const float top = order_to_float(shm.run_max);
+        if (top > -INFINITY && top < INFINITY) tau = max(tau, min_bound(top));
+      }
+      if (want && (ck & (ck + 1)) == 0) tighten();  // after 1, 2, 4, ... chunks
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int i = base + g * kThreads * 4;
+        uint32_t any = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= (i + e < c.n && float_order(x[g][e]) >= tau) ? 1u << e : 0u;
+        if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) append(&shm, (any >> e) & 1u, element(x[g][e], i + e));
+        }
+      }
+    }
   }
+  if (want && chunks > 0) tighten();
   best = warp_max_u64(best);
   if (lane == 0) shm.warp_sum[wid] = best;
   if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&shm.bad, 1u);
   __syncthreads();
-  if (wid == 0) {
-    const unsigned long long b = warp_max_u64(shm.warp_sum[lane]);
-    if (lane == 0) shm.best = b;
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kWarps; ++i) best = shm.warp_sum[i] > best ? shm.warp_sum[i] : best;
+    shm.best = best;
+    shm.tau = tau;
   }
   c.cl.sync();
   uint32_t any_bad = 0;
   best = 0;
-  for (int r = 0; r < c.ctas; ++r) {
-    const Shared* o = c.cl.map_shared_rank(&shm, r);
-    any_bad |= o->bad;
-    best = o->best > best ? o->best : best;
+  if (lane < c.ctas) {
+    const Shared* o = c.cl.map_shared_rank(&shm, lane);
+    any_bad = o->bad;
+    best = o->best;
+    tau = o->tau;
   }
-  const float temp = a.temperature[row], u = a.uniform[row];
-  const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
-  const int top_k = a.top_k ? a.top_k[row] : 0;
+  any_bad = __any_sync(0xffffffffu, any_bad != 0);
+  best = warp_max_u64(best);
+  tau = __reduce_max_sync(0xffffffffu, tau);
   Scale s;
   s.xmax = key_value(best);
   int status = 0;
   if (any_bad || !(s.xmax > -INFINITY)) status = 2;  // DFLASH2_E_NONFINITE
   if (!(temp >= 0.f) || !(temp < INFINITY) || !(top_p > 0.f) || !(min_p >= 0.f) || !(min_p <= 1.f) || !(u >= 0.f) || !(u < 1.f))
     status = 1;  // DFLASH2_E_INVAL
-  float* const kept = a.kept ? a.kept + row * a.kept_stride : nullptr;
   if (status != 0 || temp == 0.f) {
-    const int id = static_cast<int>(key_index(best));
+    const int id = static_cast<int>(key_index(best)) - c.lo;
     if (kept)
-      for (int i = c.wlo + lane; i < c.whi; i += 32)
-        kept[c.lo + i] = status == 0 && c.lo + i == id ? s.xmax : kCut;
+      for (int i = threadIdx.x; i < c.n; i += kThreads) {
+        const bool stays = status == 0 && i == id;
+        if (!fill || stays) kept[i] = stays ? s.xmax : kCut;
+      }
     if (c.rank == 0 && threadIdx.x == 0) {
-      a.token[row] = status ? -1 : id;
+      a.token[row] = status ? -1 : id + c.lo;
       if (a.prob) a.prob[row] = status ? 0.f : 1.f;
       if (a.status) a.status[row] = status;
     }
@@ -233,145 +442,254 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     s.cl = static_cast<float>(cc - static_cast<double>(s.ch));
     if (!(s.ch < INFINITY)) s.ch = 3.4028235e38f, s.cl = 0.f;
   }
-
-  // ---- the threshold: elements with a larger key stay, and `ties` of those that equal it
-  uint32_t key_min = 0;                     // every key >= it is a candidate
-  unsigned long long ties = ~0ull;          // of the elements with key == key_min, in id order
-  bool cut = false;
-  for (int stage = 0; stage < 2; ++stage) {  // 0: top-k (counts), 1: top-p (weights)
-    const bool by_weight = stage == 1;
-    if (!by_weight && !(top_k > 0 && top_k < a.vocab)) continue;
-    if (by_weight && !(top_p < 1.f)) continue;
-    // candidates of this stage: keys above key_min0, and the first ties0 that equal it.  Their weights
-    // are equal, so which of the equal ones they are does not matter to the sums below.
-    const uint32_t key0 = key_min;
-    const unsigned long long ties0 = ties;
-    double target = 0.0;
-    if (by_weight) {
-      unsigned long long z = 0;
-      for (int i = c.wlo + lane; i < c.whi; i += 32) {
-        const float x = get(i);
-        const uint32_t k = float_order(x);
-        if (k > key0 || (k == key0 && ties0 == ~0ull)) z += weight(x, s, shm.pw);
-      }
-      z = cluster_total(c, z);
-      if (ties0 != ~0ull) z += ties0 * weight(order_to_float(key0), s, shm.pw);
-      target = static_cast<double>(top_p) * static_cast<double>(z);
-    }
-    unsigned long long above = 0;
-    uint32_t prefix = 0;
-    int shift = 21, bits = 11;
-    for (int round = 0; round < 3; ++round) {
-      for (int i = threadIdx.x; i < kBins; i += kThreads) shm.hist[i] = 0;
-      __syncthreads();
-      for (int i = c.wlo + lane; i < c.whi; i += 32) {
-        const float x = get(i);
-        const uint32_t k = float_order(x);
-        if (k < key0 || (round > 0 && (k >> (shift + bits)) != prefix)) continue;
-        if (by_weight && k == key0 && ties0 != ~0ull) continue;  // added once below
-        atomicAdd(&shm.hist[(k >> shift) & (kBins - 1)], by_weight ? weight(x, s, shm.pw) : 1ull);
-      }
-      __syncthreads();
-      if (by_weight && ties0 != ~0ull && c.rank == 0 && threadIdx.x == 0 &&
-          (round == 0 || (key0 >> (shift + bits)) == prefix))
-        shm.hist[(key0 >> shift) & (kBins - 1)] += ties0 * weight(order_to_float(key0), s, shm.pw);
-      uint32_t digit;
-      unsigned long long up;
-      const unsigned long long already = above;
-      if (by_weight) {
-        find_digit(c, [&](unsigned long long v) { return static_cast<double>(already + v) >= target; }, digit, up);
-      } else {
-        const unsigned long long want = static_cast<unsigned long long>(top_k);
-        find_digit(c, [&](unsigned long long v) { return already + v >= want; }, digit, up);
-      }
-      above += up;
-      prefix = round == 0 ? digit : (prefix << bits) | digit;
-      if (round == 0) shift = 10;
-      else if (round == 1) shift = 0, bits = 10;
-    }
-    key_min = prefix;
-    cut = true;
-    if (by_weight) {
-      const unsigned long long w = weight(order_to_float(key_min), s, shm.pw);
-      // the j-th equal element stays while above + j w < target
-      unsigned long long r = 1;
-      if (w != 0) {
-        const double left = (target - static_cast<double>(above)) / static_cast<double>(w);
-        r = static_cast<unsigned long long>(left);
-        while (r > 0 && static_cast<double>(above + (r - 1) * w) >= target) --r;
-        while (static_cast<double>(above + r * w) < target) ++r;
-        if (r == 0) r = 1;
-      }
-      ties = (key_min == key0 && ties0 < r) ? ties0 : r;
-    } else {
-      ties = static_cast<unsigned long long>(top_k) - above;
+  const double floor_w = static_cast<double>(min_p) * 17592186044416.0;  // 2^44
+  bool bounded = whole || (top_k != 0 && want != 0);  // every element that may stay is a candidate
+  if (by_min) {
+    const uint32_t t = min_bound(s.xmax);
+    if (t >= tau) {
+      tau = t;
+      bounded = true;
     }
   }
 
-  // ---- of the equal elements the first `ties` stay: the id of the last one
-  int last_id = a.vocab;
-  if (cut) {
-    unsigned long long eq = 0;
-    for (int i = c.wlo + lane; i < c.whi; i += 32) eq += float_order(get(i)) == key_min ? 1 : 0;
-    eq = warp_sum_u64(eq);
-    if (lane == 0) shm.warp_sum[wid] = eq;
+  // Adds the weight (or 1) of every element >= least to the steps' histogram; returns the thread's sum.
+  auto steps = [&](bool by_weight, unsigned long long least) {
+    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&shm.piece[0][0])[i] = 0;
     __syncthreads();
-    if (wid == 0) {
-      const unsigned long long t = warp_sum_u64(shm.warp_sum[lane]);
-      if (lane == 0) shm.total = t;
-    }
-    if (threadIdx.x == 0) shm.found = -1;
-    c.cl.sync();
-    unsigned long long before = 0;
-    for (int r = 0; r < c.rank; ++r) before += c.cl.map_shared_rank(&shm, r)->total;
-    for (int i = 0; i < wid; ++i) before += shm.warp_sum[i];
-    if (before < ties && before + eq >= ties) {  // this warp holds the last one that stays
-      for (int i0 = c.wlo; i0 < c.whi; i0 += 32) {
-        const int i = i0 + lane;
-        const bool hit = i < c.whi && float_order(get(i)) == key_min;
-        const uint32_t m = __ballot_sync(0xffffffffu, hit);
-        const int cnt = __popc(m);
-        if (before + cnt >= ties) {
-          const int need = static_cast<int>(ties - before);  // 1-based
-          if (hit && __popc(m & ((2u << lane) - 1u)) == need) shm.found = c.lo + i;
-          break;
+    unsigned long long z = 0;
+    for (int i0 = threadIdx.x; i0 < c.n; i0 += 4 * kThreads) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = i0 + e * kThreads < c.n ? load1<T>(src, i0 + e * kThreads) : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * kThreads;
+        if (i >= c.n || element(x[e], i) < least) continue;
+        const unsigned long long w = by_weight ? weight(x[e], s, shm.pw) : 1ull;
+        if (w == 0) continue;
+        z += w;
+        const int b = kBins - 1 - weight_step(x[e], s);
+        atomicAdd(&shm.piece[0][b], static_cast<uint32_t>(w) & 0xFFFFu);
+        if (w >> 16) {
+          atomicAdd(&shm.piece[1][b], static_cast<uint32_t>(w >> 16) & 0xFFFFu);
+          if (w >> 32) atomicAdd(&shm.piece[2][b], static_cast<uint32_t>(w >> 32));
         }
-        before += cnt;
+      }
+    }
+    return z;
+  };
+
+  // ---- the short way
+  double target = 0.0;   // top-p's share of the weight that top-k left
+  bool have_steps = false;
+  if (listing) {
+    if (top_p < 1.f && top_k == 0) {
+      put_total(c, steps(true, 0ull));
+      have_steps = true;
+      c.cl.sync();
+      unsigned long long zt = 0;
+      if (lane < c.ctas) zt = c.cl.map_shared_rank(&shm, lane)->total;
+      target = static_cast<double>(top_p) * static_cast<double>(warp_sum_u64(zt));
+    }
+    // (the first CTA's sort buffer shares the histogram's memory, which waits in registers meanwhile)
+    unsigned long long* const pieces = reinterpret_cast<unsigned long long*>(&shm.piece[0][0]);
+    unsigned long long save[3 * kBins / 2 / kThreads];
+    if (c.rank == 0) {
+      if (have_steps) {
+#pragma unroll
+        for (int i = 0; i < 3 * kBins / 2 / kThreads; ++i) save[i] = pieces[threadIdx.x + i * kThreads];
+        __syncthreads();
+      }
+      const int n = gather_sorted(c, static_cast<unsigned long long>(tau) << 32);
+      unsigned long long result = 0;
+      if (n <= kSort) {
+        constexpr int kPer = kSort / kThreads;
+        const int lim = top_k ? min(top_k, n) : n;
+        unsigned long long w[kPer], sum_w = 0, all;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int j = threadIdx.x * kPer + i;
+          w[i] = j < lim ? weight(key_value(shm.sort[j]), s, shm.pw) : 0ull;
+          sum_w += w[i];
+          shm.w[j] = w[i];
+        }
+        unsigned long long run = block_scan(&shm, sum_w, all);
+        const double goal_w = top_k ? static_cast<double>(top_p) * static_cast<double>(all) : target;
+        int stay = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int j = threadIdx.x * kPer + i;
+          if (j < lim && (j == 0 || top_p >= 1.f || static_cast<double>(run) < goal_w) && static_cast<double>(w[i]) >= floor_w &&
+              (shm.sort[j] >> 32) > 0x007FFFFFu)  // (above -infinity)
+            ++stay;
+          run += w[i];
+        }
+        unsigned long long total, kk;
+        block_scan(&shm, static_cast<unsigned long long>(stay), kk);
+        const int K = static_cast<int>(kk);  // a prefix stays
+        if (bounded || K < n || n == a.vocab) {
+          result = shm.sort[K - 1];
+          sum_w = 0;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) sum_w += static_cast<int>(threadIdx.x) * kPer + i < K ? w[i] : 0ull;
+          block_scan(&shm, sum_w, total);
+          const double goal = static_cast<double>(u) * static_cast<double>(total);
+          // the draw in id order: the weight of the smaller ids among those that stay
+          for (int j = threadIdx.x; j < K; j += kThreads) {
+            const unsigned long long v = shm.sort[j];
+            const uint32_t me = static_cast<uint32_t>(v);  // ~id: larger for smaller ids
+            unsigned long long before = 0;
+#pragma unroll 4
+            for (int i = 0; i < K; ++i) before += static_cast<uint32_t>(shm.sort[i]) > me ? shm.w[i] : 0ull;
+            const unsigned long long wj = shm.w[j];
+            const int id = static_cast<int>(0xFFFFFFFFu - me);
+            if (static_cast<double>(before) <= goal && static_cast<double>(before + wj) > goal) {
+              a.token[row] = id;
+              if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(wj) / static_cast<double>(total));
+              if (a.status) a.status[row] = 0;
+            }
+            if (fill) kept[id] = key_value(v);  // (every CTA's filling came before the barrier; rank 0's row starts at id 0)
+          }
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) shm.result = result;
+      if (have_steps && result == 0) {
+#pragma unroll
+        for (int i = 0; i < 3 * kBins / 2 / kThreads; ++i) pieces[threadIdx.x + i * kThreads] = save[i];
       }
     }
     c.cl.sync();
-    for (int r = 0; r < c.ctas; ++r) {
-      const int f = c.cl.map_shared_rank(&shm, r)->found;
-      if (f >= 0) last_id = f;
+    const unsigned long long last = c.cl.map_shared_rank(&shm, 0)->result;
+    c.cl.sync();
+    if (last != 0) {
+      if (kept && !fill)
+        for (int i = threadIdx.x; i < c.n; i += kThreads) {
+          const float x = load1<T>(src, i);
+          kept[i] = element(x, i) >= last ? x : kCut;
+        }
+      return;
+    }
+  }
+
+  // ---- the long way
+  unsigned long long least = 0;  // elements >= it stay
+  for (int stage = 0; stage < 2; ++stage) {  // 0: top-k (counts), 1: top-p (weights)
+    const bool by_weight = stage == 1;
+    if (!by_weight && top_k == 0) continue;
+    if (by_weight && !(top_p < 1.f)) continue;
+    if (!(by_weight && have_steps)) {
+      put_total(c, steps(by_weight, least));
+      c.cl.sync();
+      if (by_weight) {
+        unsigned long long zt = 0;
+        if (lane < c.ctas) zt = c.cl.map_shared_rank(&shm, lane)->total;
+        target = static_cast<double>(top_p) * static_cast<double>(warp_sum_u64(zt));
+      }
+    }
+    const unsigned long long want_k = static_cast<unsigned long long>(top_k);
+    unsigned long long above = 0;
+    auto reached = [&](unsigned long long v) {
+      return by_weight ? static_cast<double>(above + v) >= target : above + v >= want_k;
+    };
+    auto value = [&](float x) { return by_weight ? weight(x, s, shm.pw) : 1ull; };
+    uint32_t bin;
+    unsigned long long up;
+    if (threadIdx.x == 0) shm.count = 0;
+    find_bin<true>(c, reached, bin, up);
+    above = up;
+    const uint32_t step = kBins - 1 - bin;
+    // the bin's elements to the lists
+    for (int i0 = 0; i0 < c.n; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      const float x = i < c.n ? load1<T>(src, i) : 0.f;
+      const unsigned long long v = element(x, i);
+      append(&shm, i < c.n && v >= least && weight_step(x, s) == step, v);
     }
     c.cl.sync();
+    if (c.rank == 0) {
+      const int n = gather_sorted(c, 0ull);
+      if (threadIdx.x == 0) shm.result = 0;
+      __syncthreads();
+      if (n <= kSort) {
+        constexpr int kPer = kSort / kThreads;
+        unsigned long long w[kPer], sum = 0, all;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int j = threadIdx.x * kPer + i;
+          w[i] = j < n ? value(key_value(shm.sort[j])) : 0ull;
+          sum += w[i];
+        }
+        unsigned long long run = block_scan(&shm, sum, all);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (w[i] != 0 && !reached(run) && reached(run + w[i])) shm.result = shm.sort[threadIdx.x * kPer + i];
+          run += w[i];
+        }
+      }
+    }
+    c.cl.sync();
+    unsigned long long last = c.cl.map_shared_rank(&shm, 0)->result;
+    c.cl.sync();
+    if (last == 0) {
+      // equal logits flood the bin: its elements by the digits of (key, ~id): 11 + 11 + 10 and 11 + 8 bits
+      // (ids are below 2^19)
+      unsigned long long prefix = 0;
+      int shift = 51;
+      for (int round = 0; round < 5; ++round) {
+        const int bits = round == 2 ? 10 : (round == 4 ? 8 : 11);
+        shift -= bits;
+        for (int i = threadIdx.x; i < kBins; i += kThreads) shm.hist[i] = 0;
+        __syncthreads();
+        for (int i0 = c.wlo; i0 < c.whi; i0 += 32) {
+          const int i = i0 + lane;
+          const float x = i < c.whi ? load1<T>(src, i) : 0.f;
+          const unsigned long long v = element(x, i), e = ((v >> 32) << 19) | (v & 0x7FFFFu);
+          const bool in = i < c.whi && v >= least && weight_step(x, s) == step && (round == 0 || (e >> (shift + bits)) == prefix);
+          const uint32_t m = __ballot_sync(0xffffffffu, in);
+          if (m == 0) continue;
+          const uint32_t d = static_cast<uint32_t>(e >> shift) & ((1u << bits) - 1u);
+          const unsigned long long w = in ? value(x) : 0ull;
+          const uint32_t lead = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
+          if (__all_sync(0xffffffffu, !in || d == lead)) {
+            const unsigned long long t = warp_sum_u64(w);  // one digit for the warp
+            if (lane == __ffs(m) - 1) atomicAdd(&shm.hist[d], t);
+          } else if (in) {
+            atomicAdd(&shm.hist[d], w);
+          }
+        }
+        uint32_t digit;
+        find_bin<false>(c, reached, digit, up);
+        above += up;
+        prefix = (prefix << bits) | digit;
+      }
+      last = ((prefix >> 19) << 32) | (0xFFF80000u | (prefix & 0x7FFFFu));
+    }
+    least = last;
+    have_steps = false;
   }
 
   // ---- the weight left, and the draw
-  const double floor_w = static_cast<double>(min_p) * 17592186044416.0;  // 2^44
-  // weight of id i, and whether it stays (a weight of zero may: it is then never drawn)
   auto left = [&](int i, float x, bool& stays) -> unsigned long long {
-    const uint32_t k = float_order(x);
-    stays = x > -INFINITY && (!cut || k > key_min || (k == key_min && c.lo + i <= last_id));
+    stays = x > -INFINITY && element(x, i) >= least;
     if (!stays) return 0ull;
     const unsigned long long w = weight(x, s, shm.pw);
-    stays = static_cast<double>(w) >= floor_w;
+    stays = static_cast<double>(w) >= floor_w;  // (a weight of zero may stay: it is then never drawn)
     return stays ? w : 0ull;
   };
   unsigned long long mine = 0;
-  for (int i = c.wlo + lane; i < c.whi; i += 32) {
-    const float x = get(i);
-    bool stays;
-    mine += left(i, x, stays);
-    if (kept) kept[c.lo + i] = stays ? x : kCut;
+  for (int i0 = c.wlo + lane; i0 < c.whi; i0 += 128) {
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = i0 + 32 * e < c.whi ? load1<T>(src, i0 + 32 * e) : -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bool stays;
+      mine += left(i0 + 32 * e, x[e], stays);
+      if (kept && i0 + 32 * e < c.whi) kept[i0 + 32 * e] = stays ? x[e] : kCut;
+    }
   }
-  mine = warp_sum_u64(mine);
-  if (lane == 0) shm.warp_sum[wid] = mine;
-  __syncthreads();
-  if (wid == 0) {
-    const unsigned long long t = warp_sum_u64(shm.warp_sum[lane]);
-    if (lane == 0) shm.total = t;
-  }
+  mine = put_total(c, mine);
   c.cl.sync();
   unsigned long long total = 0, before = 0;
   for (int r = 0; r < c.ctas; ++r) {
@@ -386,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     for (int i0 = c.wlo; i0 < c.whi; i0 += 32) {
       const int i = i0 + lane;
       bool stays;
-      const unsigned long long w = i < c.whi ? left(i, get(i), stays) : 0ull;
+      const unsigned long long w = i < c.whi ? left(i, load1<T>(src, i), stays) : 0ull;
       unsigned long long x = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -408,16 +726,17 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   c.cl.sync();
 }
 
-}  // namespace
-
-cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
-  const int ctas = a.vocab > 8192 ? kMaxCtas : 1;
-  const int per = (a.vocab + ctas - 1) / ctas;
-  const bool held = per * 4 <= 200 * 1024;
+template <int T>
+cudaError_t launch(const SampleArgs& a, int ctas, cudaStream_t st) {
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = set_smem_once(sample_kernel<T>, sizeof(Shared), done[0]);
+  if (e != cudaSuccess) return e;
+  e = set_attr_once(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done[1]);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_rows * ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = held ? per * 4 : 0;
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -426,13 +745,19 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (held) {
-    static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = set_smem_once(sample_kernel<true>, 200 * 1024, done);
-    if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<true>, a);
-  }
-  return cudaLaunchKernelEx(&cfg, sample_kernel<false>, a);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
+  // CTAs per row: slices of at most kSlice elements; more while the rows leave half of the two CTAs
+  // of each SM idle and a slice is more than one chunk
+  int ctas = 1;
+  while ((a.vocab + ctas - 1) / ctas > kSlice - 8) ctas *= 2;
+  while (ctas < kMaxCtas && a.n_rows * ctas <= a.num_sms && a.vocab / ctas > kChunk) ctas *= 2;
+  if (a.type == 0) return launch<0>(a, ctas, st);
+  return a.type == 1 ? launch<1>(a, ctas, st) : launch<2>(a, ctas, st);
 }
 
 }  // namespace df2

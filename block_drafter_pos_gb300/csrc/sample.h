@@ -25,6 +25,8 @@ struct SampleArgs {
   float* kept;
   long long kept_stride;
   int32_t* status;
+  int kept_in_place;  // kept overlaps the logits
+  int num_sms;
 };
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st);
 
