@@ -20,7 +20,8 @@ LIB = os.path.join(OUT_DIR, "libdflash2.so")
 ROOT = os.path.dirname(HERE)
 
 SOURCES = ["api.cu", "gemv.cu", "wide.cu", "glue.cu", "attention.cu", "lmhead.cu", "select.cu", "verify.cu", "noalloc.cu",
-           "paged_api.cu", "paged_cache.cu", "paged_attention.cu", "sample.cu"]
+           "paged_api.cu", "paged_cache.cu", "paged_attention.cu",
+           "paged_chunk.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

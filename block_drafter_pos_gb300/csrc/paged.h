@@ -127,10 +127,16 @@ inline int paged_rows(int max_new, int group) {
 }
 constexpr int kPagedBn = 64;
 constexpr int kPagedMaxCtasPerSm = 2;
-// Scratch of the partials: two slots of 64 rows for each CTA.
+// The kernel for many rows: one CTA per SM, units of 256 rows against tiles of 128 keys.
+constexpr int kChunkBn = 128;
+constexpr int kChunkRows = 256;
+// Most rows of a request for the kernel for few rows.
+constexpr int kChunkMinRows = 64;
+// Scratch of the partials: two slots for each CTA, of 64 rows (two CTAs per SM) or 256.
 inline size_t paged_part_floats(int num_sms, int head_dim) {
-  return static_cast<size_t>(num_sms) * kPagedMaxCtasPerSm * 2 * 64 * (head_dim + 2);
+  return static_cast<size_t>(num_sms) * 2 * kChunkRows * (head_dim + 2);
 }
+cudaError_t launch_paged_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 
 }  // namespace df2

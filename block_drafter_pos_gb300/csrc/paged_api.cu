@@ -125,6 +125,7 @@ dflash2_status dflash2_paged_create(const dflash2_paged_config* cfg, dflash2_pag
   }
   // two partial slots per CTA of the attention, and the cut units' descriptions
   const size_t ctas = static_cast<size_t>(h->num_sms) * kPagedMaxCtasPerSm;
+  static_assert(kChunkRows >= 64 * kPagedMaxCtasPerSm, "the larger scratch serves both kernels");
   const size_t part = paged_part_floats(h->num_sms, c.head_dim) * 4;
   char* p = nullptr;
   if (cudaMalloc(&p, part + ctas * 16) != cudaSuccess) {
@@ -181,7 +182,7 @@ dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_pa
                   std::min(x.max_len, cap)};
   a.s.group = h->cfg.n_q_heads / h->cfg.n_kv_heads;
   a.s.causal = x.tree_mask ? 2 : (x.causal ? 1 : 0);
-  a.s.window = x.window;
+  a.s.window = std::min(x.window, 1 << 30);  // (differences of positions stay within 32 bits)
   a.q = rows_of(x.q);
   a.out = rows_of(x.out);
   a.tree = reinterpret_cast<const unsigned long long*>(x.tree_mask);

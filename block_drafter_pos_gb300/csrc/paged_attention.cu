@@ -21,9 +21,8 @@
 //    after an exact power-of-two shift of their row.  A lane loads the codes as 16-byte
 //    pieces and the contraction order (keys) and the output columns (values) are permuted
 //    to match, so no code passes through shared memory twice.
-#include <cuda_fp8.h>
-
 #include "common.cuh"
+#include "paged_mma.cuh"
 #include "paged_sched.cuh"
 
 namespace df2 {
@@ -32,18 +31,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kBN = kPagedBn;
 
-DF2_DEV uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-DF2_DEV void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-DF2_DEV void cp_async4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-DF2_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-DF2_DEV void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 DF2_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -69,53 +56,11 @@ DF2_DEV uint2 lds8(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
   return r;
 }
-DF2_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <bool BF>
 DF2_DEV void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (BF) mma_bf16(d, a[0], a[1], a[2], a[3], b0, b1);
   else mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
 }
-template <bool BF>
-DF2_DEV uint32_t pack2(float lo, float hi) {
-  if constexpr (BF) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-template <bool BF>
-DF2_DEV float2 unpack2(uint32_t w) {
-  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-// Two 16-bit values with zeros in the place of infinities and NaN.
-template <bool BF>
-DF2_DEV uint32_t finite2(uint32_t w) {
-  constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
-  if ((w & ex) == ex) w &= 0xFFFF0000u;
-  if (((w >> 16) & ex) == ex) w &= 0x0000FFFFu;
-  return w;
-}
-
-// Two codes (bytes 0, 1 or 2, 3 of w) as exact fp16 values.
-template <int FMT, int HI>
-DF2_DEV uint32_t codes2(uint32_t w) {
-  if constexpr (FMT == kKvInt8) {
-    return codes_to_half2(w ^ 0x80808080u, HI ? 0x4342u : 0x4140u);
-  } else {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-  }
-}
-
 // FMT: cache format; QBF: queries and output in bf16 (else fp16); MT: 16-row tiles per unit.
 template <int D, int FMT, int MT>
 struct Geo {
@@ -311,12 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, of));
           xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, of));
         }
-        // 2^-e with the row's largest magnitude in [2^e, 2^(e + 1)); 1 for zero and nonfinite rows
-        auto shift = [](float x) {
-          const uint32_t ex = __float_as_uint(x) >> 23;
-          return ex == 0 || ex >= 254 ? 1.f : __uint_as_float((254u - ex) << 23);
-        };
-        const float fa = shift(xa), fb = shift(xb);
+        const float fa = pow2_shift(xa), fb = pow2_shift(xb);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -756,7 +696,6 @@ cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + kBN - 1) / kBN + 1);
   a.ctas = static_cast<int>(most < static_cast<long long>(num_sms) * per_sm ? most : num_sms * per_sm);
   paged_attn_kernel<D, FMT, MT, QBF><<<a.ctas, kThreads, smem, st>>>(a);
-  paged_combine_kernel<D, QBF><<<dim3(a.ctas, MT), 128, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -783,7 +722,20 @@ cudaError_t launch_dim(PagedAttnArgs& a, int fmt, int qtype, int num_sms, cudaSt
 }  // namespace
 
 cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
-  return head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
+  const long long rows = static_cast<long long>(a.rq.max_new) * a.s.group;
+  cudaError_t e;
+  if (rows > kChunkMinRows) e = launch_paged_chunk(a, head_dim, fmt, qtype, num_sms, st);
+  else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(a.ctas, a.s.rows / 16);
+  if (head_dim == 64) {
+    if (qtype == kTBf16) paged_combine_kernel<64, true><<<grid, 128, 0, st>>>(a);
+    else paged_combine_kernel<64, false><<<grid, 128, 0, st>>>(a);
+  } else {
+    if (qtype == kTBf16) paged_combine_kernel<128, true><<<grid, 128, 0, st>>>(a);
+    else paged_combine_kernel<128, false><<<grid, 128, 0, st>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace df2

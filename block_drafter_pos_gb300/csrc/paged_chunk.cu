@@ -1,0 +1,823 @@
+// Attention of new tokens over a paged cache: the kernel for many query rows per KV head
+// (prompt chunks, large trees), on the fifth-generation tensor cores.
+//
+// A unit is 256 rows of one KV head (two tiles of 128: the MMA's M) against its visible keys in
+// tiles of 128; units and runs are dealt as in the kernel for few rows (paged.h), so a chunk's
+// causal triangle, ragged prompts and few heads all load the machine evenly.
+//
+//  * S = Q K^T and O += P V are tcgen05.mma with fp32 accumulators in tensor memory: S of the
+//    two row tiles in columns 0 .. 255, O in 256 .. 511.  P (16 bit) overwrites the first half of
+//    its S and is read by the MMA from there; Q, K, V lie in shared memory under the
+//    128-byte swizzle, V as the MN-major operand, so it needs no transposition.
+//  * Warps 0 - 3 and 4 - 7 own a row tile each, one row per thread: running maximum and sum in
+//    registers, no shuffles.  O is rescaled only when a row's maximum has grown by more than
+//    2^8 (weights then stay below 2^8, within range of either 16-bit type, and the fp32 sums lose
+//    nothing), which after a unit's first tiles is rare; the tile's own warps do it.
+//  * While one tile's weights are being computed the tensor core works on the other's
+//    products: one thread of warp 8 issues O0, S0', O1, S1', ...
+//  * Warps 9 - 11 bring the keys and values: cp.async of 16-byte pieces through the page table
+//    (any page size; its rows are looked up one tile ahead), or, for 8-bit caches, cp.async of the
+//    codes into a staging area from which the same thread writes them as exact fp16 values.  The
+//    keys' scale multiplies the score and the values' scale the weight, relative to a
+//    reference the loaders raise when a scale exceeds 16 of it.
+//  * Every wait is bounded; one that gives up sets the requests' status and ends the CTA
+//    once its own copies and products are done.
+#include "common.cuh"
+#include "paged_mma.cuh"
+#include "paged_sched.cuh"
+#include "pipeline.cuh"
+
+namespace df2 {
+namespace {
+
+using pipe::lds128;
+using pipe::mbar_arrive;
+using pipe::mbar_init_count;
+using pipe::mbar_wait;
+using pipe::smem_u32;
+
+constexpr int kThreads = 384;
+constexpr int kLoaders = 96;
+constexpr int kBN = kChunkBn;      // keys per tile
+constexpr int kM = 128;            // rows per tile
+constexpr float kGrow = 8.f;       // log2 of the largest weight
+
+template <int D, int FMT>
+struct ChunkGeo {
+  static constexpr bool kQuant = FMT == kKvInt8 || FMT == kKvE4m3;
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kHalves * 128 * 128;        // a 16-bit operand tile
+  static constexpr int kSlots = kQuant ? 3 : 4;
+  static constexpr int kOffRing = 2 * kTile;
+  static constexpr int kOffStage = kOffRing + kSlots * kTile;
+  static constexpr int kStage = kQuant ? 128 * D : 0;      // codes of a tile
+  static constexpr int kOffInfo = kOffStage + 2 * kStage;
+  // tile information, a ring of 4: key scales, value factors, bad-page bits, value reference
+  static constexpr int kInfo = 128 * 4 * 2 + 16 + 16;
+  static constexpr int kOffOffs = kOffInfo + 4 * kInfo;    // element offsets of a tile's keys, two tiles
+  static constexpr int kOffPre = kOffOffs + 2 * 128 * 8;   // tiles before each request
+  static constexpr int kFixed = kOffPre + 1024;            // + alignment
+};
+
+DF2_DEV uint64_t desc_k(uint32_t saddr) {  // K-major, 128-byte rows
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// MN-major: rows of 64 channels under the swizzle, 8 keys per atom; the next 64 channels a half tile on
+// (leading offset), the next 8 keys 1024 bytes on.
+DF2_DEV uint64_t desc_mn(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+DF2_DEV uint32_t instr(bool bf, int n, bool b_mn) {
+  const uint32_t ab = bf ? 1u : 0u;
+  return (1u << 4) | (ab << 7) | (ab << 10) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(kM >> 4) << 24);
+}
+DF2_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+DF2_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+DF2_DEV void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+DF2_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+DF2_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+DF2_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+DF2_DEV void tm_ld32(uint32_t t, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]),
+        "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]),
+        "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]),
+        "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(t));
+}
+template <typename V>
+DF2_DEV void tm_st32(uint32_t t, const V* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+DF2_DEV void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+DF2_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+DF2_DEV void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+DF2_DEV void loaders_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+
+// Two fp32 values at a time (the packed fp32 instructions of this architecture).
+DF2_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+DF2_DEV float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+DF2_DEV float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+// What a unit's rows see, as ranges: keys in [lo_max, hi_min) are visible to every row.
+struct UnitMask {
+  int base, hi_min, lo_max;
+  bool mixed;  // rows differ (or a tree decides key by key)
+  DF2_DEV void set(const PagedShape& s, const PagedCursor& c) {
+    base = c.len - c.n;
+    const int rows = c.n * s.group, i0 = c.qt * s.rows / s.group;
+    const int i1 = (min((c.qt + 1) * s.rows, rows) - 1) / s.group;
+    hi_min = s.causal == 1 ? min(c.len, base + i0 + 1) : (s.causal == 2 ? min(c.len, base) : c.len);
+    lo_max = s.window > 0 ? base + i1 - s.window + 1 : 0;
+    mixed = i1 > i0 || s.causal == 2;
+  }
+  DF2_DEV bool masked(int key0) const { return key0 < lo_max || key0 + kBN > hi_min; }
+};
+
+template <int D, int FMT, bool QBF>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ PagedAttnArgs a) {
+  using G = ChunkGeo<D, FMT>;
+  constexpr bool kQuant = G::kQuant;
+  constexpr bool kBF = kQuant ? false : QBF;
+  constexpr int NS = G::kSlots;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[NS * 2 + 4 + 8];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int poison_sh[4];
+  __shared__ long long tmp[kThreads / 32 + 1];
+  __shared__ float vmax_sh[2][4];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  unsigned char* const sgen = smem_raw + (sbase - smem_u32(smem_raw));
+  const uint32_t full = smem_u32(bars), empty = full + 8 * NS, info = empty + 8 * NS, s_full = info + 8 * 4,
+                 p_full = s_full + 16, q_full = p_full + 16, o_done = q_full + 16;
+  long long* const pre = reinterpret_cast<long long*>(sgen + G::kOffPre);
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init_count(full + 8 * i, kLoaders);
+      mbar_init_count(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init_count(info + 8 * i, kLoaders);
+      poison_sh[i] = 0;
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init_count(s_full + 8 * t, 1);
+      mbar_init_count(p_full + 8 * t, 4);
+      mbar_init_count(q_full + 8 * t, 4);
+      mbar_init_count(o_done + 8 * t, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  const long long T = paged_scan<kThreads>(a, pre, tmp);
+  const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
+  if (tid == 0) a.desc[4 * c] = -1;
+  if (c >= C) return;
+  const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
+  if (wid == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_sh)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_sh;
+  bool ok = true;
+
+  if (wid < 8) {
+    // ---------------------------------------------------------------- weights of row tile t
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int t = wid >> 2, lrow = tid & 127;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((wid & 3) * 32) << 16);
+    const uint32_t s_col = lane_base + 128 * t, o_col = lane_base + 256 + 128 * t;
+    PagedCursor cc;
+    cc.start(a, pre, t_begin, t_end);
+    int n = 0, units = 0, gtile = 0, gunit = 0;  // this tile's key tiles and units so far; the run's
+    float m = 0.f, l = 0.f, sc = 0.f, vref = 0.f;
+    int lo = 0, hi = 0;
+    unsigned long long word = 0;
+    UnitMask um;
+    bool fresh = true;
+    while (cc.valid() && ok) {
+      const int rows = cc.n * a.s.group - cc.qt * a.s.rows;      // of the unit (may exceed it)
+      const bool active = t == 0 || rows > kM;
+      if (fresh) {
+        fresh = false;
+        um.set(a.s, cc);
+        if (active) {
+          // ---- this row's query
+          const int row = cc.qt * a.s.rows + t * kM + lrow;
+          const bool valid = t * kM + lrow < rows;
+          const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
+          hi = valid ? (a.s.causal == 1 ? min(cc.len, um.base + i + 1) : cc.len) : 0;
+          lo = a.s.window > 0 ? max(um.base + i - a.s.window + 1, 0) : 0;
+          if (a.s.causal == 2) word = valid ? __ldg(a.tree + cc.b0 + i) : 0ull;
+          const uint4* p = reinterpret_cast<const uint4*>(a.q.p + ((cc.b0 + i) * a.q.token_stride + head * a.q.head_stride) * 2);
+          uint4 w[D / 8];
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) w[x] = valid ? __ldg(p + x) : make_uint4(0, 0, 0, 0);
+          const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;    // (the score's factor stays positive)
+          sc = fabsf(a.scale_log2);
+          if constexpr (kQuant) {
+            float x = 0.f;
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y) {
+              const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack2<QBF>(ww[e]);
+                x = fmaxf(x, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+            }
+            const float f = pow2_shift(x);
+            sc /= f;
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y) {
+              uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 v = unpack2<QBF>(ww[e]);
+                ww[e] = pack2<false>(v.x * (f * sign), v.y * (f * sign));
+              }
+              w[y] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+            }
+          } else if (sign < 0.f) {
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y)
+              w[y] = make_uint4(w[y].x ^ 0x80008000u, w[y].y ^ 0x80008000u, w[y].z ^ 0x80008000u, w[y].w ^ 0x80008000u);
+          }
+          // (the previous unit's scores are complete, so its queries have been read)
+          const uint32_t q = sbase + t * G::kTile + lrow * 128;
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) sts128(q + (x >> 3) * 16384 + (((x & 7) ^ (lrow & 7)) << 4), w[x]);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full + 8 * t);
+          m = -INFINITY;
+          l = 0.f;
+          vref = 0.f;
+        }
+      }
+      if (active) {
+        // ---- scores of one key tile
+        const int key0 = (cc.u.t0 + cc.i) * kBN;
+        const int ring = gtile & 3;
+        const float* ks = reinterpret_cast<const float*>(sgen + G::kOffInfo + ring * G::kInfo);
+        const float* vf = ks + 128;
+        const uint32_t* badw = reinterpret_cast<const uint32_t*>(vf + 128);
+        const float* vr = reinterpret_cast<const float*>(badw + 4);
+        // (the scores' products follow the tile's information, whose barrier is then in this use's phase)
+        ok = mbar_wait(s_full + 8 * t, static_cast<uint32_t>(n & 1)) &&
+             mbar_wait(info + 8 * ring, static_cast<uint32_t>((gtile >> 2) & 1));
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        float s[128];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tm_ld32(s_col + 32 * x, s + 32 * x);
+        tm_wait_ld();
+        if constexpr (kQuant) {
+#pragma unroll
+          for (int x = 0; x < 128; x += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(ks + x);
+            const float2 y0 = mul2(make_float2(s[x], s[x + 1]), make_float2(f.x, f.y));
+            const float2 y1 = mul2(make_float2(s[x + 2], s[x + 3]), make_float2(f.z, f.w));
+            s[x] = y0.x, s[x + 1] = y0.y, s[x + 2] = y1.x, s[x + 3] = y1.y;
+          }
+        }
+        const bool any_bad = (badw[0] | badw[1] | badw[2] | badw[3]) != 0;
+        const bool masked = um.masked(key0) || any_bad;
+        if (masked) {
+          const int kl = lo - key0, kh = hi - key0;
+#pragma unroll
+          for (int x = 0; x < 128; ++x) {
+            bool v = x >= kl && x < kh;
+            if (a.s.causal == 2 && key0 + x >= um.base) v = v && ((word >> (key0 + x - um.base)) & 1ull);
+            if (any_bad) v = v && !((badw[x >> 5] >> (x & 31)) & 1u);
+            s[x] = v ? s[x] : -INFINITY;
+          }
+        }
+        float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+#pragma unroll
+        for (int x = 4; x < 128; x += 4) {
+          x0 = fmaxf(x0, s[x]);
+          x1 = fmaxf(x1, s[x + 1]);
+          x2 = fmaxf(x2, s[x + 2]);
+          x3 = fmaxf(x3, s[x + 3]);
+        }
+        // (a factor of zero would make 0 * infinity of a masked score: those stay -infinity)
+        float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+        mx = mx == -INFINITY ? mx : mx * sc;
+        float fm = 1.f;  // of the sum; O's also carries a new value reference
+        const bool first = cc.i == 0 || cc.t == t_begin;
+        if (first) {
+          m = mx;
+        } else if (mx > m + kGrow || (m == -INFINITY && mx > m)) {
+          fm = ex2(m - mx);
+          m = mx;
+        }
+        l *= fm;
+        float f = fm;
+        if constexpr (kQuant) {
+          const float v = *vr;
+          if (!first && v != vref) f *= vref / v;
+          vref = v;
+        }
+        if (__any_sync(0xffffffffu, f != 1.f)) {
+          ok = mbar_wait(o_done + 8 * t, static_cast<uint32_t>((n - 1) & 1));
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            float o[32];
+            tm_ld32(o_col + 32 * x, o);
+            tm_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] *= f;
+            tm_st32(o_col + 32 * x, o);
+          }
+          tm_wait_st();
+        }
+        // ---- weights
+        const float mr = m == -INFINITY ? 0.f : -m;
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+        const float2 sc2 = make_float2(sc, sc), mr2 = make_float2(mr, mr);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t p[32];
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            const int e = 64 * x + 2 * y;
+            float2 a0 = make_float2(s[e], s[e + 1]), a1 = make_float2(s[e + 2], s[e + 3]);
+            if (masked) {
+              a0.x = a0.x == -INFINITY ? -INFINITY : fmaf(a0.x, sc, mr);
+              a0.y = a0.y == -INFINITY ? -INFINITY : fmaf(a0.y, sc, mr);
+              a1.x = a1.x == -INFINITY ? -INFINITY : fmaf(a1.x, sc, mr);
+              a1.y = a1.y == -INFINITY ? -INFINITY : fmaf(a1.y, sc, mr);
+            } else {
+              a0 = fma2(a0, sc2, mr2);
+              a1 = fma2(a1, sc2, mr2);
+            }
+            a0 = make_float2(ex2(a0.x), ex2(a0.y));
+            a1 = make_float2(ex2(a1.x), ex2(a1.y));
+            acc0 = add2(acc0, a0);
+            acc1 = add2(acc1, a1);
+            if constexpr (kQuant) {
+              const float4 w = *reinterpret_cast<const float4*>(vf + e);
+              if (masked) {  // (a masked position's scale may be anything)
+                a0 = make_float2(a0.x == 0.f ? 0.f : a0.x * w.x, a0.y == 0.f ? 0.f : a0.y * w.y);
+                a1 = make_float2(a1.x == 0.f ? 0.f : a1.x * w.z, a1.y == 0.f ? 0.f : a1.y * w.w);
+              } else {
+                a0 = mul2(a0, make_float2(w.x, w.y));
+                a1 = mul2(a1, make_float2(w.z, w.w));
+              }
+            }
+            p[y] = pack2<kBF>(a0.x, a0.y);
+            p[y + 1] = pack2<kBF>(a1.x, a1.y);
+          }
+          tm_st32(s_col + 32 * x, p);
+        }
+        tm_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * t);
+        acc0 = add2(acc0, acc1);
+        l += acc0.x + acc0.y;
+        ++n;
+      }
+      // ---- the unit's (or the run's) end
+      const bool ends = cc.unit_ends() || cc.t == t_end - 1;
+      if (ends) {
+        if (active) {
+          const bool whole = cc.unit_t >= t_begin && cc.unit_ends();
+          const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
+          if (!whole && t == 0 && lrow == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
+            const long long cb = ((cc.unit_t + cc.u.nt) * C - 1) / T;
+            int* dd = a.desc + 4 * c;
+            dd[1] = cc.h;
+            dd[2] = cc.qt;
+            dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
+            dd[0] = cc.r;
+          }
+          ok = mbar_wait(o_done + 8 * t, static_cast<uint32_t>((n - 1) & 1));
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const int lr = t * kM + lrow, row = cc.qt * a.s.rows + lr;
+          const bool valid = lr < rows;
+          const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
+          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (a NaN sum stays NaN)
+          const float out_f = kQuant ? (whole ? inv * vref : vref) : (whole ? inv : 1.f);
+          char* const po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
+          float* const pp = a.part + slot * (a.s.rows * (D + 2)) + lr * D;
+          const bool poison = !kQuant && poison_sh[gunit & 3] != 0;
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            float o[32];
+            __syncwarp();
+            tm_ld32(o_col + 32 * x, o);
+            tm_wait_ld();
+            if constexpr (!kQuant) {
+              if (poison && valid) {
+                // values that are not finite where only some rows see them: the product had zeros there
+                const int first_i = cc.unit_t >= t_begin ? 0 : static_cast<int>(t_begin - cc.unit_t);
+                for (int ti = first_i; ti <= cc.i; ++ti) {
+                  const int k0 = (cc.u.t0 + ti) * kBN;
+                  if (!um.masked(k0)) continue;
+                  for (int key = max(k0, lo); key < min(k0 + kBN, hi); ++key) {
+                    if (a.s.causal == 2 && key >= um.base && !((word >> (key - um.base)) & 1ull)) continue;
+                    const int page = __ldg(a.c.table + cc.r * a.c.table_stride + key / a.c.page_size);
+                    long long off, so;
+                    if (!paged_row(a.c, page, key % a.c.page_size, cc.h, &off, &so)) continue;
+                    const uint32_t* v = reinterpret_cast<const uint32_t*>(a.c.v + (off + 32 * x) * 2);
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                      const float2 vv = unpack2<kBF>(__ldg(v + y));
+                      if (!isfinite(vv.x)) o[2 * y] += vv.x;
+                      if (!isfinite(vv.y)) o[2 * y + 1] += vv.y;
+                    }
+                  }
+                }
+              }
+            }
+            if (valid) {
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] *= out_f;
+              if (whole) {
+#pragma unroll
+                for (int y = 0; y < 32; y += 8)
+                  *reinterpret_cast<uint4*>(po + (32 * x + y) * 2) =
+                      make_uint4(pack2<QBF>(o[y], o[y + 1]), pack2<QBF>(o[y + 2], o[y + 3]), pack2<QBF>(o[y + 4], o[y + 5]),
+                                 pack2<QBF>(o[y + 6], o[y + 7]));
+              } else {
+#pragma unroll
+                for (int y = 0; y < 32; y += 4)
+                  *reinterpret_cast<float4*>(pp + 32 * x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+              }
+            }
+          }
+          if (valid) {
+            if (whole) {
+              if (a.lse)
+                a.lse[static_cast<long long>(cc.b0 + i) * (a.c.n_kv * a.s.group) + head] =
+                    l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+            } else {
+              *reinterpret_cast<float2*>(a.part + slot * (a.s.rows * (D + 2)) + a.s.rows * D + 2 * lr) = make_float2(m, l);
+            }
+          }
+          __syncwarp();
+          fence_before();  // O has been read before this tile's next weights are announced
+          ++units;
+        }
+        fresh = true;
+        ++gunit;
+      }
+      ++gtile;
+      cc.next(a);
+    }
+    if (!ok && lane == 0 && a.rq.status) a.rq.status[cc.r] = 3;  // DFLASH2_E_CUDA
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (wid == 8) {
+      // -------------------------------------------------------------- products (one thread)
+      if (lane == 0) {
+        const uint32_t id_s = instr(kBF, kBN, false), id_o = instr(kBF, D, true);
+        PagedCursor cs;  // the tile whose scores come next
+        cs.start(a, pre, t_begin, t_end);
+        const int total = static_cast<int>(t_end - t_begin);
+        int sn = 0, s_units[2] = {0, 0}, pn[2] = {0, 0};
+        bool s_first = true;
+        bool two_cur = false, first_cur = true;  // of the tile whose weights come next
+        bool two_next = false, first_next = true;
+        // scores of row tile t of key tile sn (cs)
+        auto scores = [&](int t, bool two) {
+          const int idx = 2 * sn;
+          if (t == 0 && !mbar_wait(full + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1))) return false;
+          if (s_first) {
+            if (!mbar_wait(q_full + 8 * t, static_cast<uint32_t>(s_units[t] & 1))) return false;
+            ++s_units[t];
+          }
+          fence_after();
+          const uint32_t q = sbase + t * G::kTile, k = sbase + G::kOffRing + (idx % NS) * G::kTile;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            mma_ss(tmem + 128 * t, desc_k(q + (x >> 2) * 16384) + 2 * (x & 3), desc_k(k + (x >> 2) * 16384) + 2 * (x & 3), id_s,
+                   x == 0 ? 0u : 1u);
+          mma_commit(s_full + 8 * t);
+          if (t == 1 || !two) mma_commit(empty + 8 * (idx % NS));
+          return true;
+        };
+        // outputs of row tile t of key tile n
+        auto outputs = [&](int t, int n, bool two, bool first) {
+          const int idx = 2 * n + 1;
+          if (t == 0 && !mbar_wait(full + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1))) return false;
+          if (!mbar_wait(p_full + 8 * t, static_cast<uint32_t>(pn[t] & 1))) return false;
+          ++pn[t];
+          fence_after();
+          const uint32_t v = sbase + G::kOffRing + (idx % NS) * G::kTile;
+#pragma unroll
+          for (int x = 0; x < kBN / 16; ++x)
+            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, desc_mn(v) + 128 * x, id_o, first && x == 0 ? 0u : 1u);
+          mma_commit(o_done + 8 * t);
+          if (t == 1 || !two) mma_commit(empty + 8 * (idx % NS));
+          return true;
+        };
+        auto see = [&](bool& two, bool& first) {  // of tile sn
+          two = cs.n * a.s.group - cs.qt * a.s.rows > kM;
+          first = s_first;
+        };
+        see(two_cur, first_cur);
+        ok = scores(0, two_cur) && (!two_cur || scores(1, two_cur));
+        for (int n = 0; n < total && ok; ++n) {
+          const bool more = n + 1 < total;
+          if (more) {
+            s_first = cs.unit_ends();
+            cs.next(a);
+            ++sn;
+            see(two_next, first_next);
+          }
+          ok = outputs(0, n, two_cur, first_cur);
+          if (ok && more) ok = scores(0, two_next);
+          if (ok && two_cur) ok = outputs(1, n, two_cur, first_cur);
+          if (ok && more && two_next) ok = scores(1, two_next);
+          two_cur = two_next;
+          first_cur = first_next;
+        }
+        if (!ok && a.rq.status) a.rq.status[cs.r] = 3;
+      }
+    } else {
+      // -------------------------------------------------------------- keys and values
+      const int lt = tid - 9 * 32;
+      long long* const offs = reinterpret_cast<long long*>(sgen + G::kOffOffs);
+      PagedCursor lc;
+      lc.start(a, pre, t_begin, t_end);
+      const int total = static_cast<int>(t_end - t_begin);
+      UnitMask um;
+      long long off[2];
+      float ksv[2], vsv[2];
+      bool badv[2];
+      int key0 = 0, unit = 0;
+      bool piece_first = true, mixed = false, l_first = true;
+      // offsets and scales of the cursor's tile for this thread's keys lt and lt + 96
+      auto look_up = [&]() {
+        um.set(a.s, lc);
+        key0 = (lc.u.t0 + lc.i) * kBN;
+        mixed = um.mixed && um.masked(key0);
+        piece_first = l_first;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          off[x] = -1;
+          ksv[x] = vsv[x] = 0.f;
+          badv[x] = false;
+          const int kk = lt + 96 * x, key = key0 + kk;
+          if (kk < kBN && key >= lc.u.lo && key < lc.u.hi) {
+            const int page = __ldg(a.c.table + lc.r * a.c.table_stride + key / a.c.page_size);
+            long long so;
+            if (paged_row(a.c, page, key % a.c.page_size, lc.h, &off[x], &so)) {
+              if (kQuant) {
+                ksv[x] = __ldg(a.c.k_scale + so);
+                vsv[x] = __ldg(a.c.v_scale + so);
+              }
+            } else {
+              badv[x] = true;
+              if (a.rq.status) a.rq.status[lc.r] = 1;  // DFLASH2_E_INVAL
+            }
+          }
+        }
+        l_first = lc.unit_ends();
+        lc.next(a);
+      };
+      float vref = 0.f, vinv = 0.f;
+      look_up();
+      // arrival for operand idx once its copies (all but the last `pending` groups) have landed
+      auto landed = [&](int idx) {
+        fence_async();
+        mbar_arrive(full + 8 * (idx % NS));
+      };
+      // 8-bit: codes of operand idx from the staging area to its slot
+      auto convert = [&](int idx) {
+        const int use = idx / NS;
+        if (use > 0 && !mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((use + 1) & 1))) return false;
+        if constexpr (kQuant) {
+          const uint32_t st = sbase + G::kOffStage + (idx & 1) * G::kStage, dst = sbase + G::kOffRing + (idx % NS) * G::kTile;
+          constexpr int kCh = D / 16;  // 16-byte pieces of a key's codes
+#pragma unroll 2
+          for (int x = lt; x < 128 * kCh; x += kLoaders) {
+            const int row = x / kCh, ch = x % kCh;
+            const uint4 w = lds128(st + x * 16);
+            const uint4 h0 = make_uint4(codes2<FMT, 0>(w.x), codes2<FMT, 1>(w.x), codes2<FMT, 0>(w.y), codes2<FMT, 1>(w.y));
+            const uint4 h1 = make_uint4(codes2<FMT, 0>(w.z), codes2<FMT, 1>(w.z), codes2<FMT, 0>(w.w), codes2<FMT, 1>(w.w));
+            const uint32_t base = dst + (ch >> 2) * 16384 + row * 128;
+            const int c0 = (2 * ch) & 7;
+            sts128(base + ((c0 ^ (row & 7)) << 4), h0);
+            sts128(base + (((c0 + 1) ^ (row & 7)) << 4), h1);
+          }
+        }
+        landed(idx);
+        return true;
+      };
+      // (after a failed wait a loader goes through the motions, so that the loaders' barrier stays whole)
+      for (int j = 0; j < total; ++j) {
+        // ---- the tile's information
+        const int ring = j & 3;
+        float* ks = reinterpret_cast<float*>(sgen + G::kOffInfo + ring * G::kInfo);
+        uint32_t* badw = reinterpret_cast<uint32_t*>(ks + 256);
+        long long* o = offs + (j & 1) * 128;
+        if (piece_first) {
+          if (j > 0) ++unit;
+          vref = 0.f;
+          if (lt == 0) poison_sh[unit & 3] = 0;
+        }
+        // (the ring's previous tile was four tiles ago, whose weights are done: its slot's products are)
+        if (j >= 2) {
+          const int idx = 2 * (j - 2);
+          ok = ok && mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1));
+        }
+        if constexpr (kQuant) {
+          float v = 0.f;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (vsv[x] < INFINITY) v = fmaxf(v, vsv[x]);
+          v = warp_max(v);
+          if (lane == 0) vmax_sh[j & 1][wid - 9] = v;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int kk = lt + 96 * x;
+          if (kk < kBN) o[kk] = off[x];
+          const uint32_t b = __ballot_sync(0xffffffffu, badv[x]);
+          if (lane == 0 && kk < kBN) badw[kk >> 5] = b;
+        }
+        loaders_sync();
+        if constexpr (kQuant) {
+          const float v = fmaxf(fmaxf(vmax_sh[j & 1][0], vmax_sh[j & 1][1]), vmax_sh[j & 1][2]);
+          if (vref == 0.f || v > 16.f * vref) {
+            vref = fmaxf(v, 1.17549435e-38f);
+            vinv = 1.f / vref;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int kk = lt + 96 * x;
+            if (kk < kBN) {
+              ks[kk] = ksv[x];
+              ks[128 + kk] = vsv[x] * vinv;
+            }
+          }
+          if (lt == 0) ks[256 + 4] = vref;
+        }
+        mbar_arrive(info + 8 * ring);
+        const bool mixed_now = mixed;
+        const int unit_now = unit;
+        if (j + 1 < total) look_up();
+        // ---- keys (side 0) and values (side 1)
+#pragma unroll 1
+        for (int side = 0; side < 2 && ok; ++side) {
+          const int idx = 2 * j + side;
+          const char* pool = side ? a.c.v : a.c.k;
+          if constexpr (kQuant) {
+            const uint32_t st = sbase + G::kOffStage + (idx & 1) * G::kStage;
+            constexpr int kCh = D / 16;
+            for (int x = lt; x < 128 * kCh; x += kLoaders) {
+              const long long of = o[x / kCh];
+              cp_async16(st + x * 16, pool + (of >= 0 ? of : 0) + (x % kCh) * 16, of >= 0 ? 16 : 0);
+            }
+            cp_commit();
+            if (idx > 0) {
+              cp_wait<1>();
+              ok = convert(idx - 1);
+            }
+          } else {
+            const int use = idx / NS;
+            ok = use == 0 || mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((use + 1) & 1));
+            if (!ok) break;
+            const uint32_t dst = sbase + G::kOffRing + (idx % NS) * G::kTile;
+            constexpr int kCh = D / 8;
+            if (side == 1 && mixed_now) {
+              // values that only some rows see: infinities and NaN become zeros (the rows that see them add them at the end)
+              bool found = false;
+#pragma unroll 4
+              for (int x = lt; x < 128 * kCh; x += kLoaders) {
+                const int row = x / kCh, ch = x % kCh;
+                const long long of = o[row];
+                uint4 w = of >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + of * 2 + ch * 16)) : make_uint4(0, 0, 0, 0);
+                const uint4 z = make_uint4(finite2<kBF>(w.x), finite2<kBF>(w.y), finite2<kBF>(w.z), finite2<kBF>(w.w));
+                found |= z.x != w.x || z.y != w.y || z.z != w.z || z.w != w.w;
+                sts128(dst + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), z);
+              }
+              if (found) poison_sh[unit_now & 3] = 1;
+            } else {
+              for (int x = lt; x < 128 * kCh; x += kLoaders) {
+                const int row = x / kCh, ch = x % kCh;
+                const long long of = o[row];
+                cp_async16(dst + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                           pool + (of >= 0 ? of * 2 : 0) + ch * 16, of >= 0 ? 16 : 0);
+              }
+            }
+            cp_commit();
+            if (idx > 0) {
+              cp_wait<1>();
+              landed(idx - 1);
+            }
+          }
+        }
+      }
+      cp_wait<0>();
+      if (ok) {
+        const int idx = 2 * total - 1;
+        if constexpr (kQuant) ok = convert(idx);
+        else landed(idx);
+      }
+      if (!ok && lt == 0 && a.rq.status) a.rq.status[lc.r] = 3;
+    }
+  }
+  // every product has completed: its commits were waited for by the rows' last outputs, or (after an error) here
+  __syncthreads();
+  if (wid == 8) {
+    if (lane == 0) {
+      // an extra commit covers whatever was issued; its barrier is one that nobody uses any more
+      mbar_init_count(info, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      mma_commit(info);
+      mbar_wait(info, 0);
+    }
+    __syncwarp();
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+template <int D, int FMT, bool QBF>
+cudaError_t launch_one(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
+  using G = ChunkGeo<D, FMT>;
+  static std::atomic<unsigned long long> done{0};
+  const int smem = G::kFixed + (a.rq.n_req + 1) * 8;
+  static_assert(G::kFixed + 1025 * 8 + 512 <= 227 * 1024, "shared memory");
+  cudaError_t e = set_smem_once(paged_chunk_kernel<D, FMT, QBF>, G::kFixed + 1025 * 8, done);
+  if (e != cudaSuccess) return e;
+  // the register split of the warps (2 x 128 x 216 + 128 x 72) needs the launch's 384 x 168
+  static const int regs = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, paged_chunk_kernel<D, FMT, QBF>) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs != 168) return cudaErrorInvalidConfiguration;
+  const long long rt = (static_cast<long long>(a.rq.max_new) * a.s.group + kChunkRows - 1) / kChunkRows;
+  const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + kBN - 1) / kBN + 1);
+  a.ctas = static_cast<int>(most < num_sms ? most : num_sms);
+  paged_chunk_kernel<D, FMT, QBF><<<a.ctas, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_dim(PagedAttnArgs& a, int fmt, int qtype, int num_sms, cudaStream_t st) {
+  const bool bf = qtype == kTBf16;
+  switch (fmt) {
+    case kKvBf16: return launch_one<D, kKvBf16, true>(a, num_sms, st);
+    case kKvF16: return launch_one<D, kKvF16, false>(a, num_sms, st);
+    case kKvInt8: return bf ? launch_one<D, kKvInt8, true>(a, num_sms, st) : launch_one<D, kKvInt8, false>(a, num_sms, st);
+    default: return bf ? launch_one<D, kKvE4m3, true>(a, num_sms, st) : launch_one<D, kKvE4m3, false>(a, num_sms, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
+  a.s.rows = kChunkRows;
+  a.s.bn = kBN;
+  return head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
+}
+
+}  // namespace df2

@@ -1,0 +1,72 @@
+// Pieces that the paged attention's kernels share.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace df2 {
+
+DF2_DEV uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+DF2_DEV void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DF2_DEV void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+DF2_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DF2_DEV void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+DF2_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF>
+DF2_DEV uint32_t pack2(float lo, float hi) {
+  if constexpr (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <bool BF>
+DF2_DEV float2 unpack2(uint32_t w) {
+  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Two 16-bit values with zeros in the place of infinities and NaN.
+template <bool BF>
+DF2_DEV uint32_t finite2(uint32_t w) {
+  constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
+  if ((w & ex) == ex) w &= 0xFFFF0000u;
+  if (((w >> 16) & ex) == ex) w &= 0x0000FFFFu;
+  return w;
+}
+
+// Two codes (bytes 0, 1 or 2, 3 of w) as exact fp16 values.
+template <int FMT, int HI>
+DF2_DEV uint32_t codes2(uint32_t w) {
+  if constexpr (FMT == kKvInt8) {
+    return codes_to_half2(w ^ 0x80808080u, HI ? 0x4342u : 0x4140u);
+  } else {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+  }
+}
+
+// 2^-e with x in [2^e, 2^(e + 1)); 1 for zero, tiny and nonfinite x.  Rows of queries are brought to
+// fp16's range with it, exactly.
+DF2_DEV float pow2_shift(float x) {
+  const uint32_t ex = __float_as_uint(x) >> 23;
+  return ex == 0 || ex >= 254 ? 1.f : __uint_as_float((254u - ex) << 23);
+}
+
+}  // namespace df2
