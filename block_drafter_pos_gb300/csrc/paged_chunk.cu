@@ -36,8 +36,9 @@ using pipe::mbar_init_count;
 using pipe::mbar_wait;
 using pipe::smem_u32;
 
-constexpr int kThreads = 384;
-constexpr int kLoaders = 96;
+constexpr int kThreads = 512;
+constexpr int kLoaders = 128;
+constexpr int kSoftRegs = 200, kOtherRegs = 56;  // 256 threads each: the 512 x 128 of the launch
 constexpr int kBN = kChunkBn;      // keys per tile
 constexpr int kM = 128;            // rows per tile
 constexpr float kGrow = 8.f;       // log2 of the largest weight
@@ -59,31 +60,31 @@ struct ChunkGeo {
   static constexpr int kFixed = kOffPre + 1024;            // + alignment
 };
 
-DF2_DEV uint64_t desc_k(uint32_t saddr) {  // K-major, 128-byte rows
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-// MN-major: rows of 64 channels under the swizzle, 8 keys per atom; the next 64 channels a half tile on
-// (leading offset), the next 8 keys 1024 bytes on.
-DF2_DEV uint64_t desc_mn(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory matrix descriptors under the 128-byte swizzle: the low words hold the address and the
+// leading offset, the high word is the same for all (8-row groups 1024 bytes apart, this architecture's
+// version, the swizzle).  K-major tiles (queries, keys): rows of 64 channels; the leading offset is not used.
+// MN-major (values): rows of 64 channels, 8 keys per atom; the next 64 channels are the leading offset on.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+DF2_DEV uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+DF2_DEV uint32_t desc_mn(uint32_t saddr) { return (saddr >> 4) | ((16384u >> 4) << 16); }
 DF2_DEV uint32_t instr(bool bf, int n, bool b_mn) {
   const uint32_t ab = bf ? 1u : 0u;
   return (1u << 4) | (ab << 7) | (ab << 10) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kM >> 4) << 24);
 }
-DF2_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+template <bool ACC>
+DF2_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "n"(ACC ? 1 : 0), "r"(kDescHi)
       : "memory");
 }
-DF2_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+DF2_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
       : "memory");
 }
 DF2_DEV void mma_commit(uint32_t bar) {
@@ -103,6 +104,20 @@ DF2_DEV void tm_ld32(uint32_t t, float* r) {
         "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(t));
 }
+DF2_DEV void tm_ld16(uint32_t t, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]),
+        "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(t));
+}
+DF2_DEV void tm_st16(uint32_t t, const float* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]),
+      "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+      : "memory");
+}
 template <typename V>
 DF2_DEV void tm_st32(uint32_t t, const V* v) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
@@ -120,7 +135,7 @@ DF2_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "m
 DF2_DEV void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-DF2_DEV void loaders_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+DF2_DEV void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // Two fp32 values at a time (the packed fp32 instructions of this architecture).
 DF2_DEV float2 fma2(float2 a, float2 b, float2 c) {
@@ -173,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   __shared__ int poison_sh[4];
   __shared__ long long tmp[kThreads / 32 + 1];
   __shared__ float vmax_sh[2][4];
+  static_assert(256 * (kSoftRegs + kOtherRegs) == kThreads * 128, "the register split");
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* const sgen = smem_raw + (sbase - smem_u32(smem_raw));
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   if (tid == 0) a.desc[4 * c] = -1;
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
-  if (wid == 8) {
+  if (wid == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_sh)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -213,78 +229,74 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 
   if (wid < 8) {
     // ---------------------------------------------------------------- weights of row tile t
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int t = wid >> 2, lrow = tid & 127;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((wid & 3) * 32) << 16);
     const uint32_t s_col = lane_base + 128 * t, o_col = lane_base + 256 + 128 * t;
     PagedCursor cc;
     cc.start(a, pre, t_begin, t_end);
-    int n = 0, units = 0, gtile = 0, gunit = 0;  // this tile's key tiles and units so far; the run's
-    float m = 0.f, l = 0.f, sc = 0.f, vref = 0.f;
+    int n = 0, gtile = 0, gunit = 0;  // this row tile's key tiles so far; the run's key tiles and units
+    float m = -INFINITY, l = 0.f, sc = 0.f, vref = 0.f;
     int lo = 0, hi = 0;
     unsigned long long word = 0;
     UnitMask um;
-    bool fresh = true;
-    while (cc.valid() && ok) {
-      const int rows = cc.n * a.s.group - cc.qt * a.s.rows;      // of the unit (may exceed it)
-      const bool active = t == 0 || rows > kM;
-      if (fresh) {
-        fresh = false;
-        um.set(a.s, cc);
-        if (active) {
-          // ---- this row's query
-          const int row = cc.qt * a.s.rows + t * kM + lrow;
-          const bool valid = t * kM + lrow < rows;
-          const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
-          hi = valid ? (a.s.causal == 1 ? min(cc.len, um.base + i + 1) : cc.len) : 0;
-          lo = a.s.window > 0 ? max(um.base + i - a.s.window + 1, 0) : 0;
-          if (a.s.causal == 2) word = valid ? __ldg(a.tree + cc.b0 + i) : 0ull;
-          const uint4* p = reinterpret_cast<const uint4*>(a.q.p + ((cc.b0 + i) * a.q.token_stride + head * a.q.head_stride) * 2);
-          uint4 w[D / 8];
+    bool active = false;
+    // This row's query of the cursor's unit into shared memory (the row tile's scores so far are complete, so
+    // its former queries have been read), and what the row sees.
+    auto enter = [&](const PagedCursor& u) {
+      const int rows = u.n * a.s.group - u.qt * a.s.rows;  // of the unit (may exceed it)
+      active = t == 0 || rows > kM;
+      um.set(a.s, u);
+      if (!active) return;
+      const int row = u.qt * a.s.rows + t * kM + lrow;
+      const bool valid = t * kM + lrow < rows;
+      const int i = row / a.s.group, head = u.h * a.s.group + row % a.s.group;
+      hi = valid ? (a.s.causal == 1 ? min(u.len, um.base + i + 1) : u.len) : 0;
+      lo = a.s.window > 0 ? max(um.base + i - a.s.window + 1, 0) : 0;
+      if (a.s.causal == 2) word = valid ? __ldg(a.tree + u.b0 + i) : 0ull;
+      const uint4* p = reinterpret_cast<const uint4*>(a.q.p + ((u.b0 + i) * a.q.token_stride + head * a.q.head_stride) * 2);
+      uint4 w[D / 8];
 #pragma unroll
-          for (int x = 0; x < D / 8; ++x) w[x] = valid ? __ldg(p + x) : make_uint4(0, 0, 0, 0);
-          const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;    // (the score's factor stays positive)
-          sc = fabsf(a.scale_log2);
-          if constexpr (kQuant) {
-            float x = 0.f;
+      for (int x = 0; x < D / 8; ++x) w[x] = valid ? __ldg(p + x) : make_uint4(0, 0, 0, 0);
+      const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;    // (the score's factor stays positive)
+      sc = fabsf(a.scale_log2);
+      if constexpr (kQuant) {
+        float x = 0.f;
 #pragma unroll
-            for (int y = 0; y < D / 8; ++y) {
-              const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+        for (int y = 0; y < D / 8; ++y) {
+          const uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack2<QBF>(ww[e]);
-                x = fmaxf(x, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-            }
-            const float f = pow2_shift(x);
-            sc /= f;
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y) {
-              uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 v = unpack2<QBF>(ww[e]);
-                ww[e] = pack2<false>(v.x * (f * sign), v.y * (f * sign));
-              }
-              w[y] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
-            }
-          } else if (sign < 0.f) {
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y)
-              w[y] = make_uint4(w[y].x ^ 0x80008000u, w[y].y ^ 0x80008000u, w[y].z ^ 0x80008000u, w[y].w ^ 0x80008000u);
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<QBF>(ww[e]);
+            x = fmaxf(x, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
-          // (the previous unit's scores are complete, so its queries have been read)
-          const uint32_t q = sbase + t * G::kTile + lrow * 128;
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x) sts128(q + (x >> 3) * 16384 + (((x & 7) ^ (lrow & 7)) << 4), w[x]);
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full + 8 * t);
-          m = -INFINITY;
-          l = 0.f;
-          vref = 0.f;
         }
+        const float f = pow2_shift(x);
+        sc /= f;
+#pragma unroll
+        for (int y = 0; y < D / 8; ++y) {
+          uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = unpack2<QBF>(ww[e]);
+            ww[e] = pack2<false>(v.x * (f * sign), v.y * (f * sign));
+          }
+          w[y] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+        }
+      } else if (sign < 0.f) {
+#pragma unroll
+        for (int y = 0; y < D / 8; ++y)
+          w[y] = make_uint4(w[y].x ^ 0x80008000u, w[y].y ^ 0x80008000u, w[y].z ^ 0x80008000u, w[y].w ^ 0x80008000u);
       }
+      const uint32_t q = sbase + t * G::kTile + lrow * 128;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) sts128(q + (x >> 3) * 16384 + (((x & 7) ^ (lrow & 7)) << 4), w[x]);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full + 8 * t);
+    };
+    enter(cc);
+    while (cc.valid() && ok) {
       if (active) {
         // ---- scores of one key tile
         const int key0 = (cc.u.t0 + cc.i) * kBN;
@@ -360,13 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
           fence_after();
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            float o[32];
-            tm_ld32(o_col + 32 * x, o);
+          for (int x = 0; x < D / 16; ++x) {
+            float o[16];
+            tm_ld16(o_col + 16 * x, o);
             tm_wait_ld();
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] *= f;
-            tm_st32(o_col + 32 * x, o);
+            for (int y = 0; y < 16; ++y) o[y] *= f;
+            tm_st16(o_col + 16 * x, o);
           }
           tm_wait_st();
         }
@@ -417,10 +429,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         l += acc0.x + acc0.y;
         ++n;
       }
-      // ---- the unit's (or the run's) end
+      // ---- the unit's (or the run's) end: the next unit's queries first, then this one's outputs
       const bool ends = cc.unit_ends() || cc.t == t_end - 1;
+      PagedCursor nc = cc;
+      nc.next(a);
+      ++gtile;
       if (ends) {
-        if (active) {
+        const int old_lo = lo, old_hi = hi;
+        const unsigned long long old_word = word;
+        const UnitMask old_um = um;
+        const bool was_active = active;
+        if (nc.valid()) enter(nc);
+        if (was_active) {
+          const int rows = cc.n * a.s.group - cc.qt * a.s.rows;
           const bool whole = cc.unit_t >= t_begin && cc.unit_ends();
           const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
           if (!whole && t == 0 && lrow == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
@@ -457,9 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 const int first_i = cc.unit_t >= t_begin ? 0 : static_cast<int>(t_begin - cc.unit_t);
                 for (int ti = first_i; ti <= cc.i; ++ti) {
                   const int k0 = (cc.u.t0 + ti) * kBN;
-                  if (!um.masked(k0)) continue;
-                  for (int key = max(k0, lo); key < min(k0 + kBN, hi); ++key) {
-                    if (a.s.causal == 2 && key >= um.base && !((word >> (key - um.base)) & 1ull)) continue;
+                  if (!old_um.masked(k0)) continue;
+                  for (int key = max(k0, old_lo); key < min(k0 + kBN, old_hi); ++key) {
+                    if (a.s.causal == 2 && key >= old_um.base && !((old_word >> (key - old_um.base)) & 1ull)) continue;
                     const int page = __ldg(a.c.table + cc.r * a.c.table_stride + key / a.c.page_size);
                     long long off, so;
                     if (!paged_row(a.c, page, key % a.c.page_size, cc.h, &off, &so)) continue;
@@ -501,18 +522,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
           __syncwarp();
           fence_before();  // O has been read before this tile's next weights are announced
-          ++units;
         }
-        fresh = true;
+        m = -INFINITY;
+        l = vref = 0.f;
         ++gunit;
       }
-      ++gtile;
-      cc.next(a);
+      cc = nc;
     }
     if (!ok && lane == 0 && a.rq.status) a.rq.status[cc.r] = 3;  // DFLASH2_E_CUDA
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (wid == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (wid == 12) {
       // -------------------------------------------------------------- products (one thread)
       if (lane == 0) {
         const uint32_t id_s = instr(kBF, kBN, false), id_o = instr(kBF, D, true);
@@ -532,11 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             ++s_units[t];
           }
           fence_after();
-          const uint32_t q = sbase + t * G::kTile, k = sbase + G::kOffRing + (idx % NS) * G::kTile;
+          const uint32_t q = desc_k(sbase + t * G::kTile), kd = desc_k(sbase + G::kOffRing + (idx % NS) * G::kTile);
+          mma_ss<false>(tmem + 128 * t, q, kd, id_s);
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x)
-            mma_ss(tmem + 128 * t, desc_k(q + (x >> 2) * 16384) + 2 * (x & 3), desc_k(k + (x >> 2) * 16384) + 2 * (x & 3), id_s,
-                   x == 0 ? 0u : 1u);
+          for (int x = 1; x < D / 16; ++x)
+            mma_ss<true>(tmem + 128 * t, q + (x >> 2) * 1024 + 2 * (x & 3), kd + (x >> 2) * 1024 + 2 * (x & 3), id_s);
           mma_commit(s_full + 8 * t);
           if (t == 1 || !two) mma_commit(empty + 8 * (idx % NS));
           return true;
@@ -548,10 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           if (!mbar_wait(p_full + 8 * t, static_cast<uint32_t>(pn[t] & 1))) return false;
           ++pn[t];
           fence_after();
-          const uint32_t v = sbase + G::kOffRing + (idx % NS) * G::kTile;
+          const uint32_t v = desc_mn(sbase + G::kOffRing + (idx % NS) * G::kTile);
+          mma_ts(tmem + 256 + 128 * t, tmem + 128 * t, v, id_o, first ? 0u : 1u);
 #pragma unroll
-          for (int x = 0; x < kBN / 16; ++x)
-            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, desc_mn(v) + 128 * x, id_o, first && x == 0 ? 0u : 1u);
+          for (int x = 1; x < kBN / 16; ++x) mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, v + 128 * x, id_o, 1u);
           mma_commit(o_done + 8 * t);
           if (t == 1 || !two) mma_commit(empty + 8 * (idx % NS));
           return true;
@@ -579,43 +599,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         if (!ok && a.rq.status) a.rq.status[cs.r] = 3;
       }
-    } else {
+    } else if (wid < 12) {
       // -------------------------------------------------------------- keys and values
-      const int lt = tid - 9 * 32;
+      const int lt = tid - 256;
       long long* const offs = reinterpret_cast<long long*>(sgen + G::kOffOffs);
       PagedCursor lc;
       lc.start(a, pre, t_begin, t_end);
       const int total = static_cast<int>(t_end - t_begin);
       UnitMask um;
-      long long off[2];
-      float ksv[2], vsv[2];
-      bool badv[2];
-      int key0 = 0, unit = 0;
-      bool piece_first = true, mixed = false, l_first = true;
-      // offsets and scales of the cursor's tile for this thread's keys lt and lt + 96
+      um.set(a.s, lc);
+      long long off = -1;
+      float ksv = 0.f, vsv = 0.f;
+      bool badv = false, piece_first = true, mixed = false, l_first = true;
+      int unit = 0;
+      // offset and scales of the cursor's tile for this thread's key
       auto look_up = [&]() {
-        um.set(a.s, lc);
-        key0 = (lc.u.t0 + lc.i) * kBN;
+        if (l_first) um.set(a.s, lc);
+        const int key0 = (lc.u.t0 + lc.i) * kBN, key = key0 + lt;
         mixed = um.mixed && um.masked(key0);
         piece_first = l_first;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          off[x] = -1;
-          ksv[x] = vsv[x] = 0.f;
-          badv[x] = false;
-          const int kk = lt + 96 * x, key = key0 + kk;
-          if (kk < kBN && key >= lc.u.lo && key < lc.u.hi) {
-            const int page = __ldg(a.c.table + lc.r * a.c.table_stride + key / a.c.page_size);
-            long long so;
-            if (paged_row(a.c, page, key % a.c.page_size, lc.h, &off[x], &so)) {
-              if (kQuant) {
-                ksv[x] = __ldg(a.c.k_scale + so);
-                vsv[x] = __ldg(a.c.v_scale + so);
-              }
-            } else {
-              badv[x] = true;
-              if (a.rq.status) a.rq.status[lc.r] = 1;  // DFLASH2_E_INVAL
+        off = -1;
+        ksv = vsv = 0.f;
+        badv = false;
+        if (key >= lc.u.lo && key < lc.u.hi) {
+          const int pi = key / a.c.page_size;
+          const int page = __ldg(a.c.table + lc.r * a.c.table_stride + pi);
+          long long so;
+          if (paged_row(a.c, page, key - pi * a.c.page_size, lc.h, &off, &so)) {
+            if (kQuant) {
+              ksv = __ldg(a.c.k_scale + so);
+              vsv = __ldg(a.c.v_scale + so);
             }
+          } else {
+            badv = true;
+            if (a.rq.status) a.rq.status[lc.r] = 1;  // DFLASH2_E_INVAL
           }
         }
         l_first = lc.unit_ends();
@@ -623,28 +640,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       };
       float vref = 0.f, vinv = 0.f;
       look_up();
-      // arrival for operand idx once its copies (all but the last `pending` groups) have landed
-      auto landed = [&](int idx) {
+      // A thread copies piece ch of rows r0, r0 + kStep, ...: the swizzle's row bits are its own constant.
+      constexpr int kPieces = D * (kQuant ? 1 : 2) / 16, kStep = kLoaders / kPieces, kCount = 128 / kStep;
+      constexpr int kBatch = kCount < 8 ? kCount : 8;
+      const int ch = lt % kPieces, r0 = lt / kPieces;
+      // where piece ch of row r0 goes (16-bit: itself; codes: the first of its two pieces of fp16)
+      const int piece = kQuant ? 2 * ch : ch;
+      const uint32_t put0 = (piece >> 3) * 16384 + r0 * 128 + (((piece & 7) ^ (r0 & 7)) << 4);
+      const uint32_t put1 = (piece >> 3) * 16384 + r0 * 128 + ((((piece & 7) + 1) ^ (r0 & 7)) << 4);
+      static_assert(kStep % 8 == 0, "a thread's rows share their place in the swizzle");
+      auto landed = [&](int idx) {  // this thread's part of operand idx is in place
         fence_async();
         mbar_arrive(full + 8 * (idx % NS));
       };
-      // 8-bit: codes of operand idx from the staging area to its slot
-      auto convert = [&](int idx) {
+      auto freed = [&](int idx) {  // the operand that had idx's slot has been read
         const int use = idx / NS;
-        if (use > 0 && !mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((use + 1) & 1))) return false;
+        return use == 0 || mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((use + 1) & 1));
+      };
+      // 8-bit: this thread's codes of operand idx from the staging area to its slot
+      auto convert = [&](int idx) {
+        if (!freed(idx)) return false;
         if constexpr (kQuant) {
-          const uint32_t st = sbase + G::kOffStage + (idx & 1) * G::kStage, dst = sbase + G::kOffRing + (idx % NS) * G::kTile;
-          constexpr int kCh = D / 16;  // 16-byte pieces of a key's codes
-#pragma unroll 2
-          for (int x = lt; x < 128 * kCh; x += kLoaders) {
-            const int row = x / kCh, ch = x % kCh;
-            const uint4 w = lds128(st + x * 16);
-            const uint4 h0 = make_uint4(codes2<FMT, 0>(w.x), codes2<FMT, 1>(w.x), codes2<FMT, 0>(w.y), codes2<FMT, 1>(w.y));
-            const uint4 h1 = make_uint4(codes2<FMT, 0>(w.z), codes2<FMT, 1>(w.z), codes2<FMT, 0>(w.w), codes2<FMT, 1>(w.w));
-            const uint32_t base = dst + (ch >> 2) * 16384 + row * 128;
-            const int c0 = (2 * ch) & 7;
-            sts128(base + ((c0 ^ (row & 7)) << 4), h0);
-            sts128(base + (((c0 + 1) ^ (row & 7)) << 4), h1);
+          const uint32_t st = sbase + G::kOffStage + (idx & 1) * G::kStage + lt * 16;
+          const uint32_t dst = sbase + G::kOffRing + (idx % NS) * G::kTile;
+#pragma unroll
+          for (int x0 = 0; x0 < kCount; x0 += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = lds128(st + (x0 + x) * (kLoaders * 16));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t d = dst + (x0 + x) * (kStep * 128);
+              sts128(d + put0, make_uint4(codes2<FMT, 0>(w[x].x), codes2<FMT, 1>(w[x].x), codes2<FMT, 0>(w[x].y), codes2<FMT, 1>(w[x].y)));
+              sts128(d + put1, make_uint4(codes2<FMT, 0>(w[x].z), codes2<FMT, 1>(w[x].z), codes2<FMT, 0>(w[x].w), codes2<FMT, 1>(w[x].w)));
+            }
           }
         }
         landed(idx);
@@ -662,41 +691,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           vref = 0.f;
           if (lt == 0) poison_sh[unit & 3] = 0;
         }
-        // (the ring's previous tile was four tiles ago, whose weights are done: its slot's products are)
+        // (the ring's previous tile was four tiles ago; the scores of the tile two ago being done, its weights are)
         if (j >= 2) {
           const int idx = 2 * (j - 2);
           ok = ok && mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1));
         }
         if constexpr (kQuant) {
-          float v = 0.f;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (vsv[x] < INFINITY) v = fmaxf(v, vsv[x]);
-          v = warp_max(v);
-          if (lane == 0) vmax_sh[j & 1][wid - 9] = v;
+          const float v = warp_max(vsv < INFINITY ? vsv : 0.f);
+          if (lane == 0) vmax_sh[j & 1][wid - 8] = v;
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int kk = lt + 96 * x;
-          if (kk < kBN) o[kk] = off[x];
-          const uint32_t b = __ballot_sync(0xffffffffu, badv[x]);
-          if (lane == 0 && kk < kBN) badw[kk >> 5] = b;
-        }
+        o[lt] = off;
+        const uint32_t b = __ballot_sync(0xffffffffu, badv);
+        if (lane == 0) badw[wid - 8] = b;
         loaders_sync();
         if constexpr (kQuant) {
-          const float v = fmaxf(fmaxf(vmax_sh[j & 1][0], vmax_sh[j & 1][1]), vmax_sh[j & 1][2]);
+          const float* vm = vmax_sh[j & 1];
+          const float v = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
           if (vref == 0.f || v > 16.f * vref) {
             vref = fmaxf(v, 1.17549435e-38f);
             vinv = 1.f / vref;
           }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int kk = lt + 96 * x;
-            if (kk < kBN) {
-              ks[kk] = ksv[x];
-              ks[128 + kk] = vsv[x] * vinv;
-            }
-          }
+          ks[lt] = ksv;
+          ks[128 + lt] = vsv * vinv;
           if (lt == 0) ks[256 + 4] = vref;
         }
         mbar_arrive(info + 8 * ring);
@@ -707,51 +723,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll 1
         for (int side = 0; side < 2 && ok; ++side) {
           const int idx = 2 * j + side;
-          const char* pool = side ? a.c.v : a.c.k;
+          const char* pool = (side ? a.c.v : a.c.k) + ch * 16;
+          uint32_t dst;
           if constexpr (kQuant) {
-            const uint32_t st = sbase + G::kOffStage + (idx & 1) * G::kStage;
-            constexpr int kCh = D / 16;
-            for (int x = lt; x < 128 * kCh; x += kLoaders) {
-              const long long of = o[x / kCh];
-              cp_async16(st + x * 16, pool + (of >= 0 ? of : 0) + (x % kCh) * 16, of >= 0 ? 16 : 0);
-            }
-            cp_commit();
-            if (idx > 0) {
-              cp_wait<1>();
-              ok = convert(idx - 1);
-            }
+            dst = sbase + G::kOffStage + (idx & 1) * G::kStage + lt * 16;
           } else {
-            const int use = idx / NS;
-            ok = use == 0 || mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((use + 1) & 1));
+            ok = freed(idx);
             if (!ok) break;
-            const uint32_t dst = sbase + G::kOffRing + (idx % NS) * G::kTile;
-            constexpr int kCh = D / 8;
-            if (side == 1 && mixed_now) {
-              // values that only some rows see: infinities and NaN become zeros (the rows that see them add them at the end)
-              bool found = false;
+            dst = sbase + G::kOffRing + (idx % NS) * G::kTile + put0;
+          }
+          constexpr int kNext = kQuant ? kLoaders * 16 : kStep * 128;
+          if (!kQuant && side == 1 && mixed_now) {
+            // values that only some rows see: infinities and NaN become zeros (the rows that see them add them at the end)
+            bool found = false;
 #pragma unroll 4
-              for (int x = lt; x < 128 * kCh; x += kLoaders) {
-                const int row = x / kCh, ch = x % kCh;
-                const long long of = o[row];
-                uint4 w = of >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + of * 2 + ch * 16)) : make_uint4(0, 0, 0, 0);
-                const uint4 z = make_uint4(finite2<kBF>(w.x), finite2<kBF>(w.y), finite2<kBF>(w.z), finite2<kBF>(w.w));
-                found |= z.x != w.x || z.y != w.y || z.z != w.z || z.w != w.w;
-                sts128(dst + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), z);
-              }
-              if (found) poison_sh[unit_now & 3] = 1;
-            } else {
-              for (int x = lt; x < 128 * kCh; x += kLoaders) {
-                const int row = x / kCh, ch = x % kCh;
-                const long long of = o[row];
-                cp_async16(dst + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                           pool + (of >= 0 ? of * 2 : 0) + ch * 16, of >= 0 ? 16 : 0);
-              }
+            for (int x = 0; x < kCount; ++x) {
+              const long long of = o[r0 + x * kStep];
+              const uint4 w = of >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + of * 2)) : make_uint4(0, 0, 0, 0);
+              const uint4 z = make_uint4(finite2<kBF>(w.x), finite2<kBF>(w.y), finite2<kBF>(w.z), finite2<kBF>(w.w));
+              found |= z.x != w.x || z.y != w.y || z.z != w.z || z.w != w.w;
+              sts128(dst + x * kNext, z);
             }
-            cp_commit();
-            if (idx > 0) {
-              cp_wait<1>();
-              landed(idx - 1);
+            if (found) poison_sh[unit_now & 3] = 1;
+          } else {
+#pragma unroll
+            for (int x0 = 0; x0 < kCount; x0 += kBatch) {
+              long long of[kBatch];
+#pragma unroll
+              for (int x = 0; x < kBatch; ++x) of[x] = o[r0 + (x0 + x) * kStep];
+#pragma unroll
+              for (int x = 0; x < kBatch; ++x)
+                cp_async16(dst + (x0 + x) * kNext, pool + (of[x] >= 0 ? of[x] * (kQuant ? 1 : 2) : 0), of[x] >= 0 ? 16 : 0);
             }
+          }
+          cp_commit();
+          if (idx > 0) {
+            cp_wait<1>();
+            if constexpr (kQuant) ok = convert(idx - 1);
+            else landed(idx - 1);
           }
         }
       }
@@ -766,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   }
   // every product has completed: its commits were waited for by the rows' last outputs, or (after an error) here
   __syncthreads();
-  if (wid == 8) {
+  if (wid == 12) {
     if (lane == 0) {
       // an extra commit covers whatever was issued; its barrier is one that nobody uses any more
       mbar_init_count(info, 1);
@@ -788,12 +797,12 @@ cudaError_t launch_one(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   static_assert(G::kFixed + 1025 * 8 + 512 <= 227 * 1024, "shared memory");
   cudaError_t e = set_smem_once(paged_chunk_kernel<D, FMT, QBF>, G::kFixed + 1025 * 8, done);
   if (e != cudaSuccess) return e;
-  // the register split of the warps (2 x 128 x 216 + 128 x 72) needs the launch's 384 x 168
+  // the warps' register split needs the launch's 512 x 128
   static const int regs = [] {
     cudaFuncAttributes f;
     return cudaFuncGetAttributes(&f, paged_chunk_kernel<D, FMT, QBF>) == cudaSuccess ? f.numRegs : 0;
   }();
-  if (regs != 168) return cudaErrorInvalidConfiguration;
+  if (regs != 128) return cudaErrorInvalidConfiguration;
   const long long rt = (static_cast<long long>(a.rq.max_new) * a.s.group + kChunkRows - 1) / kChunkRows;
   const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + kBN - 1) / kBN + 1);
   a.ctas = static_cast<int>(most < num_sms ? most : num_sms);
