@@ -176,6 +176,12 @@ struct UnitMask {
   DF2_DEV bool masked(int key0) const { return key0 < lo_max || key0 + kBN > hi_min; }
 };
 
+// 64 columns as bits: those below n, and a word whose bit 0 is column n.
+DF2_DEV unsigned long long columns_below(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull); }
+DF2_DEV unsigned long long columns_shifted(unsigned long long w, int n) {
+  return n >= 64 || n <= -64 ? 0ull : (n >= 0 ? w << n : w >> -n);
+}
+
 template <int D, int FMT, bool QBF>
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ PagedAttnArgs a) {
   using G = ChunkGeo<D, FMT>;
@@ -183,17 +189,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   constexpr bool kBF = kQuant ? false : QBF;
   constexpr int NS = G::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[NS * 2 + 4 + 8];
+  __shared__ __align__(8) uint64_t bars[NS * 2 + 4 + 10];
   __shared__ uint32_t tmem_sh;
   __shared__ int poison_sh[4];
   __shared__ long long tmp[kThreads / 32 + 1];
   __shared__ float vmax_sh[2][4];
+  __shared__ int flag_sh[2][4];
   static_assert(256 * (kSoftRegs + kOtherRegs) == kThreads * 128, "the register split");
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* const sgen = smem_raw + (sbase - smem_u32(smem_raw));
   const uint32_t full = smem_u32(bars), empty = full + 8 * NS, info = empty + 8 * NS, s_full = info + 8 * 4,
-                 p_full = s_full + 16, q_full = p_full + 16, o_done = q_full + 16;
+                 p_full = s_full + 16, q_full = p_full + 32, o_done = q_full + 16;
   long long* const pre = reinterpret_cast<long long*>(sgen + G::kOffPre);
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -206,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init_count(s_full + 8 * t, 1);
-      mbar_init_count(p_full + 8 * t, 4);
+      mbar_init_count(p_full + 16 * t, 4);
+      mbar_init_count(p_full + 16 * t + 8, 4);
       mbar_init_count(q_full + 8 * t, 4);
       mbar_init_count(o_done + 8 * t, 1);
     }
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) w[x] = valid ? __ldg(p + x) : make_uint4(0, 0, 0, 0);
       const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;    // (the score's factor stays positive)
-      sc = fabsf(a.scale_log2);
+      sc = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);      // (so that a masked score stays -infinity at a scale of 0)
       if constexpr (kQuant) {
         float x = 0.f;
 #pragma unroll
@@ -297,17 +305,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     };
     enter(cc);
     while (cc.valid() && ok) {
-      if (active) {
+      const int piece = cc.piece();
+      for (int j = 0; active && j < piece; ++j) {
         // ---- scores of one key tile
-        const int key0 = (cc.u.t0 + cc.i) * kBN;
-        const int ring = gtile & 3;
+        const int key0 = (cc.u.t0 + cc.i + j) * kBN;
+        const int ring = (gtile + j) & 3;
         const float* ks = reinterpret_cast<const float*>(sgen + G::kOffInfo + ring * G::kInfo);
         const float* vf = ks + 128;
         const uint32_t* badw = reinterpret_cast<const uint32_t*>(vf + 128);
-        const float* vr = reinterpret_cast<const float*>(badw + 4);
         // (the scores' products follow the tile's information, whose barrier is then in this use's phase)
         ok = mbar_wait(s_full + 8 * t, static_cast<uint32_t>(n & 1)) &&
-             mbar_wait(info + 8 * ring, static_cast<uint32_t>((gtile >> 2) & 1));
+             mbar_wait(info + 8 * ring, static_cast<uint32_t>(((gtile + j) >> 2) & 1));
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -316,6 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         float s[128];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tm_ld32(s_col + 32 * x, s + 32 * x);
+        // the tile's information: flags (bit 0: some page is bad, bit 1: some value factor is not finite), reference
+        const int2 fl = *reinterpret_cast<const int2*>(badw + 4);
         tm_wait_ld();
         if constexpr (kQuant) {
 #pragma unroll
@@ -326,42 +336,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             s[x] = y0.x, s[x + 1] = y0.y, s[x + 2] = y1.x, s[x + 3] = y1.y;
           }
         }
-        const bool any_bad = (badw[0] | badw[1] | badw[2] | badw[3]) != 0;
-        const bool masked = um.masked(key0) || any_bad;
+        const bool masked = um.masked(key0) || (fl.x & 1);
         if (masked) {
-          const int kl = lo - key0, kh = hi - key0;
-#pragma unroll
-          for (int x = 0; x < 128; ++x) {
-            bool v = x >= kl && x < kh;
-            if (a.s.causal == 2 && key0 + x >= um.base) v = v && ((word >> (key0 + x - um.base)) & 1ull);
-            if (any_bad) v = v && !((badw[x >> 5] >> (x & 31)) & 1u);
-            s[x] = v ? s[x] : -INFINITY;
+          // the columns that the row sees, one bit each
+          unsigned long long v0 = columns_below(hi - key0) & ~columns_below(lo - key0);
+          unsigned long long v1 = columns_below(hi - key0 - 64) & ~columns_below(lo - key0 - 64);
+          if (a.s.causal == 2) {
+            const int d = um.base - key0;  // the column of the tree's first token
+            v0 &= columns_below(d) | columns_shifted(word, d);
+            v1 &= columns_below(d - 64) | columns_shifted(word, d - 64);
           }
+          if (fl.x & 1) {
+            v0 &= ~(static_cast<unsigned long long>(badw[1]) << 32 | badw[0]);
+            v1 &= ~(static_cast<unsigned long long>(badw[3]) << 32 | badw[2]);
+          }
+          const uint32_t vw[4] = {static_cast<uint32_t>(v0), static_cast<uint32_t>(v0 >> 32), static_cast<uint32_t>(v1),
+                                  static_cast<uint32_t>(v1 >> 32)};
+#pragma unroll
+          for (int x = 0; x < 128; ++x) s[x] = (vw[x >> 5] >> (x & 31)) & 1u ? s[x] : -INFINITY;
         }
         float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
-        for (int x = 4; x < 128; x += 4) {
-          x0 = fmaxf(x0, s[x]);
-          x1 = fmaxf(x1, s[x + 1]);
-          x2 = fmaxf(x2, s[x + 2]);
-          x3 = fmaxf(x3, s[x + 3]);
+        for (int x = 4; x < 124; x += 8) {
+          x0 = fmaxf(fmaxf(x0, s[x]), s[x + 4]);
+          x1 = fmaxf(fmaxf(x1, s[x + 1]), s[x + 5]);
+          x2 = fmaxf(fmaxf(x2, s[x + 2]), s[x + 6]);
+          x3 = fmaxf(fmaxf(x3, s[x + 3]), s[x + 7]);
         }
-        // (a factor of zero would make 0 * infinity of a masked score: those stay -infinity)
-        float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
-        mx = mx == -INFINITY ? mx : mx * sc;
-        float fm = 1.f;  // of the sum; O's also carries a new value reference
-        const bool first = cc.i == 0 || cc.t == t_begin;
-        if (first) {
+        x0 = fmaxf(fmaxf(x0, s[124]), x2);
+        x1 = fmaxf(fmaxf(x1, s[125]), x3);
+        const float mx = fmaxf(fmaxf(fmaxf(x0, s[126]), s[127]), x1) * sc;
+        float f = 1.f;  // O's factor
+        if (j == 0) {
           m = mx;
-        } else if (mx > m + kGrow || (m == -INFINITY && mx > m)) {
-          fm = ex2(m - mx);
+        } else if (mx > m + kGrow) {
+          f = ex2(m - mx);
           m = mx;
+          l *= f;
         }
-        l *= fm;
-        float f = fm;
         if constexpr (kQuant) {
-          const float v = *vr;
-          if (!first && v != vref) f *= vref / v;
+          const float v = __int_as_float(fl.y);
+          if (j != 0 && v != vref) f *= vref / v;
           vref = v;
         }
         if (__any_sync(0xffffffffu, f != 1.f)) {
@@ -380,61 +395,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             for (int y = 0; y < 16; ++y) o[y] *= f;
             tm_st16(o_col + 16 * x, o);
           }
-          tm_wait_st();
         }
-        // ---- weights
+        // ---- weights (a row that has seen nothing: 2^(-infinity)), announced by halves
         const float mr = m == -INFINITY ? 0.f : -m;
         float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
         const float2 sc2 = make_float2(sc, sc), mr2 = make_float2(mr, mr);
+        const bool careful = kQuant && masked && (fl.x & 2);  // a masked position's factor may be anything
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t p[32];
 #pragma unroll
           for (int y = 0; y < 32; y += 2) {
             const int e = 64 * x + 2 * y;
-            float2 a0 = make_float2(s[e], s[e + 1]), a1 = make_float2(s[e + 2], s[e + 3]);
-            if (masked) {
-              a0.x = a0.x == -INFINITY ? -INFINITY : fmaf(a0.x, sc, mr);
-              a0.y = a0.y == -INFINITY ? -INFINITY : fmaf(a0.y, sc, mr);
-              a1.x = a1.x == -INFINITY ? -INFINITY : fmaf(a1.x, sc, mr);
-              a1.y = a1.y == -INFINITY ? -INFINITY : fmaf(a1.y, sc, mr);
-            } else {
-              a0 = fma2(a0, sc2, mr2);
-              a1 = fma2(a1, sc2, mr2);
-            }
+            float2 a0 = fma2(make_float2(s[e], s[e + 1]), sc2, mr2), a1 = fma2(make_float2(s[e + 2], s[e + 3]), sc2, mr2);
             a0 = make_float2(ex2(a0.x), ex2(a0.y));
             a1 = make_float2(ex2(a1.x), ex2(a1.y));
             acc0 = add2(acc0, a0);
             acc1 = add2(acc1, a1);
             if constexpr (kQuant) {
               const float4 w = *reinterpret_cast<const float4*>(vf + e);
-              if (masked) {  // (a masked position's scale may be anything)
-                a0 = make_float2(a0.x == 0.f ? 0.f : a0.x * w.x, a0.y == 0.f ? 0.f : a0.y * w.y);
-                a1 = make_float2(a1.x == 0.f ? 0.f : a1.x * w.z, a1.y == 0.f ? 0.f : a1.y * w.w);
-              } else {
-                a0 = mul2(a0, make_float2(w.x, w.y));
-                a1 = mul2(a1, make_float2(w.z, w.w));
+              const float2 b0 = mul2(a0, make_float2(w.x, w.y)), b1 = mul2(a1, make_float2(w.z, w.w));
+              p[y] = pack2<kBF>(b0.x, b0.y);
+              p[y + 1] = pack2<kBF>(b1.x, b1.y);
+              if (careful) {
+                if (a0.x == 0.f) p[y] &= 0xFFFF0000u;
+                if (a0.y == 0.f) p[y] &= 0x0000FFFFu;
+                if (a1.x == 0.f) p[y + 1] &= 0xFFFF0000u;
+                if (a1.y == 0.f) p[y + 1] &= 0x0000FFFFu;
               }
+            } else {
+              p[y] = pack2<kBF>(a0.x, a0.y);
+              p[y + 1] = pack2<kBF>(a1.x, a1.y);
             }
-            p[y] = pack2<kBF>(a0.x, a0.y);
-            p[y + 1] = pack2<kBF>(a1.x, a1.y);
           }
           tm_st32(s_col + 32 * x, p);
+          tm_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 8 * (2 * t + x));
         }
-        tm_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * t);
         acc0 = add2(acc0, acc1);
         l += acc0.x + acc0.y;
         ++n;
       }
-      // ---- the unit's (or the run's) end: the next unit's queries first, then this one's outputs
-      const bool ends = cc.unit_ends() || cc.t == t_end - 1;
+      if (!ok) break;
+      // ---- the end of the unit (or of the run): the next unit's queries first, then this one's outputs
       PagedCursor nc = cc;
-      nc.next(a);
-      ++gtile;
-      if (ends) {
+      nc.skip(a, piece);
+      {
         const int old_lo = lo, old_hi = hi;
         const unsigned long long old_word = word;
         const UnitMask old_um = um;
@@ -442,7 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (nc.valid()) enter(nc);
         if (was_active) {
           const int rows = cc.n * a.s.group - cc.qt * a.s.rows;
-          const bool whole = cc.unit_t >= t_begin && cc.unit_ends();
+          const int i_last = cc.i + piece - 1;
+          const bool whole = cc.unit_t >= t_begin && i_last == cc.u.nt - 1;
           const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
           if (!whole && t == 0 && lrow == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
             const long long cb = ((cc.unit_t + cc.u.nt) * C - 1) / T;
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
               if (poison && valid) {
                 // values that are not finite where only some rows see them: the product had zeros there
                 const int first_i = cc.unit_t >= t_begin ? 0 : static_cast<int>(t_begin - cc.unit_t);
-                for (int ti = first_i; ti <= cc.i; ++ti) {
+                for (int ti = first_i; ti <= i_last; ++ti) {
                   const int k0 = (cc.u.t0 + ti) * kBN;
                   if (!old_um.masked(k0)) continue;
                   for (int key = max(k0, old_lo); key < min(k0 + kBN, old_hi); ++key) {
@@ -525,8 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         m = -INFINITY;
         l = vref = 0.f;
-        ++gunit;
       }
+      ++gunit;
+      gtile += piece;
       cc = nc;
     }
     if (!ok && lane == 0 && a.rq.status) a.rq.status[cc.r] = 3;  // DFLASH2_E_CUDA
@@ -536,13 +546,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // -------------------------------------------------------------- products (one thread)
       if (lane == 0) {
         const uint32_t id_s = instr(kBF, kBN, false), id_o = instr(kBF, D, true);
-        PagedCursor cs;  // the tile whose scores come next
+        PagedCursor cs;  // the unit whose scores come next
         cs.start(a, pre, t_begin, t_end);
         const int total = static_cast<int>(t_end - t_begin);
         int sn = 0, s_units[2] = {0, 0}, pn[2] = {0, 0};
+        int left = cs.piece(), piece = left;  // tiles of that unit still to come
         bool s_first = true;
-        bool two_cur = false, first_cur = true;  // of the tile whose weights come next
-        bool two_next = false, first_next = true;
+        bool two_cur = cs.n * a.s.group - cs.qt * a.s.rows > kM, first_cur = true;  // of the tile whose weights come next
+        bool two_next = two_cur;
         // scores of row tile t of key tile sn (cs)
         auto scores = [&](int t, bool two) {
           const int idx = 2 * sn;
@@ -565,37 +576,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         auto outputs = [&](int t, int n, bool two, bool first) {
           const int idx = 2 * n + 1;
           if (t == 0 && !mbar_wait(full + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1))) return false;
-          if (!mbar_wait(p_full + 8 * t, static_cast<uint32_t>(pn[t] & 1))) return false;
-          ++pn[t];
+          if (!mbar_wait(p_full + 16 * t, static_cast<uint32_t>(pn[t] & 1))) return false;
           fence_after();
           const uint32_t v = desc_mn(sbase + G::kOffRing + (idx % NS) * G::kTile);
           mma_ts(tmem + 256 + 128 * t, tmem + 128 * t, v, id_o, first ? 0u : 1u);
 #pragma unroll
-          for (int x = 1; x < kBN / 16; ++x) mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, v + 128 * x, id_o, 1u);
+          for (int x = 1; x < kBN / 32; ++x) mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, v + 128 * x, id_o, 1u);
+          if (!mbar_wait(p_full + 16 * t + 8, static_cast<uint32_t>(pn[t] & 1))) return false;
+          ++pn[t];
+          fence_after();
+#pragma unroll
+          for (int x = kBN / 32; x < kBN / 16; ++x) mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, v + 128 * x, id_o, 1u);
           mma_commit(o_done + 8 * t);
           if (t == 1 || !two) mma_commit(empty + 8 * (idx % NS));
           return true;
         };
-        auto see = [&](bool& two, bool& first) {  // of tile sn
-          two = cs.n * a.s.group - cs.qt * a.s.rows > kM;
-          first = s_first;
-        };
-        see(two_cur, first_cur);
         ok = scores(0, two_cur) && (!two_cur || scores(1, two_cur));
         for (int n = 0; n < total && ok; ++n) {
           const bool more = n + 1 < total;
           if (more) {
-            s_first = cs.unit_ends();
-            cs.next(a);
+            s_first = --left == 0;
+            if (s_first) {
+              cs.skip(a, piece);
+              left = piece = cs.piece();
+              two_next = cs.n * a.s.group - cs.qt * a.s.rows > kM;
+            }
             ++sn;
-            see(two_next, first_next);
           }
           ok = outputs(0, n, two_cur, first_cur);
           if (ok && more) ok = scores(0, two_next);
           if (ok && two_cur) ok = outputs(1, n, two_cur, first_cur);
           if (ok && more && two_next) ok = scores(1, two_next);
           two_cur = two_next;
-          first_cur = first_next;
+          first_cur = s_first;
         }
         if (!ok && a.rq.status) a.rq.status[cs.r] = 3;
       }
@@ -702,8 +715,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         o[lt] = off;
         const uint32_t b = __ballot_sync(0xffffffffu, badv);
-        if (lane == 0) badw[wid - 8] = b;
+        // (NaN and infinity; a factor of 0 times either is not finite)
+        const uint32_t odd = __ballot_sync(0xffffffffu, kQuant && !(fabsf(vsv) < INFINITY));
+        if (lane == 0) {
+          badw[wid - 8] = b;
+          flag_sh[j & 1][wid - 8] = (b ? 1 : 0) | (odd ? 2 : 0);
+        }
         loaders_sync();
+        if (lt == 0) badw[4] = flag_sh[j & 1][0] | flag_sh[j & 1][1] | flag_sh[j & 1][2] | flag_sh[j & 1][3];
         if constexpr (kQuant) {
           const float* vm = vmax_sh[j & 1];
           const float v = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
@@ -713,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
           ks[lt] = ksv;
           ks[128 + lt] = vsv * vinv;
-          if (lt == 0) ks[256 + 4] = vref;
+          if (lt == 0) ks[256 + 5] = vref;
         }
         mbar_arrive(info + 8 * ring);
         const bool mixed_now = mixed;

@@ -95,7 +95,16 @@ struct PagedCursor {
     unit_t = t - i;
   }
 
-  DF2_DEV bool unit_begins() const { return i == 0; }
+  // Tiles of the unit that are in this run, from the present one; skip() passes over them.
+  DF2_DEV int piece() const {
+    const long long left = t1 - t;
+    return left < u.nt - i ? static_cast<int>(left) : u.nt - i;
+  }
+  DF2_DEV void skip(const PagedAttnArgs& a, int tiles) {
+    t += tiles - 1;
+    i += tiles - 1;
+    next(a);
+  }
   DF2_DEV bool unit_ends() const { return i == u.nt - 1; }
 
   DF2_DEV void next(const PagedAttnArgs& a) {
