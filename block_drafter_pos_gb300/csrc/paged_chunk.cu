@@ -67,28 +67,45 @@ struct ChunkGeo {
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 DF2_DEV uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 DF2_DEV uint32_t desc_mn(uint32_t saddr) { return (saddr >> 4) | ((16384u >> 4) << 16); }
-DF2_DEV uint32_t instr(bool bf, int n, bool b_mn) {
+__host__ __device__ constexpr uint32_t instr(bool bf, int n, bool b_mn) {
   const uint32_t ab = bf ? 1u : 0u;
   return (1u << 4) | (ab << 7) | (ab << 10) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kM >> 4) << 24);
 }
-template <bool ACC>
-DF2_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+// The products are issued by one lane (`go`) of a warp that stays converged, so that the descriptors live in
+// uniform registers.
+DF2_DEV void mma_ss(uint32_t go, uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "n"(ACC ? 1 : 0), "r"(kDescHi)
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 x, {%1, %5};\n"
+      " mov.b64 y, {%2, %5};\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi), "r"(go)
       : "memory");
 }
-DF2_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+DF2_DEV void mma_ts(uint32_t go, uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 y, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi), "r"(go)
       : "memory");
 }
-DF2_DEV void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+DF2_DEV void mma_commit(uint32_t go, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(go)
+      : "memory");
+}
+// mbar_wait of a whole warp, its loop out of the compiler's sight (1 if the phase completed within the limit).
+DF2_DEV uint32_t mbar_wait_warp(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .u32 i;\n mov.u32 i, 0;\n mov.u32 %0, 1;\n"
+      "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n add.u32 i, i, 1;\n"
+      " setp.lt.u32 p, i, %3;\n @p bra AGAIN;\n mov.u32 %0, 0;\nDONE:\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "n"(static_cast<int>(pipe::kSpinLimit))
+      : "memory");
+  return done;
 }
 DF2_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 DF2_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -196,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   __shared__ float vmax_sh[2][4];
   __shared__ int flag_sh[2][4];
   static_assert(256 * (kSoftRegs + kOtherRegs) == kThreads * 128, "the register split");
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* const sgen = smem_raw + (sbase - smem_u32(smem_raw));
   const uint32_t full = smem_u32(bars), empty = full + 8 * NS, info = empty + 8 * NS, s_full = info + 8 * 4,
@@ -543,75 +560,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (wid == 12) {
-      // -------------------------------------------------------------- products (one thread)
-      if (lane == 0) {
-        const uint32_t id_s = instr(kBF, kBN, false), id_o = instr(kBF, D, true);
-        PagedCursor cs;  // the unit whose scores come next
-        cs.start(a, pre, t_begin, t_end);
-        const int total = static_cast<int>(t_end - t_begin);
-        int sn = 0, s_units[2] = {0, 0}, pn[2] = {0, 0};
-        int left = cs.piece(), piece = left;  // tiles of that unit still to come
-        bool s_first = true;
-        bool two_cur = cs.n * a.s.group - cs.qt * a.s.rows > kM, first_cur = true;  // of the tile whose weights come next
-        bool two_next = two_cur;
-        // scores of row tile t of key tile sn (cs)
-        auto scores = [&](int t, bool two) {
-          const int idx = 2 * sn;
-          if (t == 0 && !mbar_wait(full + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1))) return false;
+      // -------------------------------------------------------------- products
+      const uint32_t go = lane == 0 ? 1u : 0u;
+      constexpr uint32_t id_s = instr(kBF, kBN, false), id_o = instr(kBF, D, true);
+      PagedCursor cs;  // the unit whose scores come next
+      cs.start(a, pre, t_begin, t_end);
+      const int total = static_cast<int>(t_end - t_begin);
+      int sn = 0, units = 0, left = cs.piece(), piece = left;  // tiles of that unit still to come
+      uint32_t units1 = 0, pn0 = 0, pn1 = 0;
+      uint32_t fine = 1;
+      bool s_first = true;
+      bool two_cur = cs.n * a.s.group - cs.qt * a.s.rows > kM, first_cur = true;  // of the tile whose weights come next
+      bool two_next = two_cur;
+      // scores of row tile t of key tile sn (cs's unit)
+      auto scores = [&](uint32_t t, bool two) {
+        const uint32_t idx = 2 * sn, slot = idx % NS;
+        if (t == 0) fine &= mbar_wait_warp(full + 8 * slot, (idx / NS) & 1);
+        if (s_first) fine &= mbar_wait_warp(q_full + 8 * t, (t ? units1 : units) & 1);
+        fence_after();
+        const uint32_t q = desc_k(sbase + t * G::kTile), kd = desc_k(sbase + G::kOffRing + slot * G::kTile);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          mma_ss(go, tmem + 128 * t, q + (x >> 2) * 1024 + 2 * (x & 3), kd + (x >> 2) * 1024 + 2 * (x & 3), id_s, x != 0);
+        mma_commit(go, s_full + 8 * t);
+        if (t == 1 || !two) mma_commit(go, empty + 8 * slot);
+      };
+      // outputs of row tile t of key tile n
+      auto outputs = [&](uint32_t t, int n, bool two, bool first) {
+        const uint32_t idx = 2 * n + 1, slot = idx % NS, ph = (t ? pn1 : pn0) & 1;
+        if (t == 0) fine &= mbar_wait_warp(full + 8 * slot, (idx / NS) & 1);
+        fine &= mbar_wait_warp(p_full + 16 * t, ph);
+        fence_after();
+        const uint32_t v = desc_mn(sbase + G::kOffRing + slot * G::kTile), p = tmem + 128 * t, o = tmem + 256 + 128 * t;
+#pragma unroll
+        for (int x = 0; x < kBN / 32; ++x) mma_ts(go, o, p + 8 * x, v + 128 * x, id_o, x == 0 ? !first : 1);
+        fine &= mbar_wait_warp(p_full + 16 * t + 8, ph);
+        fence_after();
+#pragma unroll
+        for (int x = kBN / 32; x < kBN / 16; ++x) mma_ts(go, o, p + 8 * x, v + 128 * x, id_o, 1);
+        mma_commit(go, o_done + 8 * t);
+        if (t == 1 || !two) mma_commit(go, empty + 8 * slot);
+        if (t) ++pn1;
+        else ++pn0;
+      };
+      // (a failed wait ends the loop at the tile's end: the others' waits run out in turn)
+      for (int n = -1; n < total; ++n) {
+        const bool more = n + 1 < total;
+        if (n >= 0 && more) {
+          s_first = --left == 0;
           if (s_first) {
-            if (!mbar_wait(q_full + 8 * t, static_cast<uint32_t>(s_units[t] & 1))) return false;
-            ++s_units[t];
+            ++units;
+            if (two_next) ++units1;
+            cs.skip(a, piece);
+            left = piece = cs.piece();
+            two_next = __any_sync(0xffffffffu, cs.n * a.s.group - cs.qt * a.s.rows > kM);
           }
-          fence_after();
-          const uint32_t q = desc_k(sbase + t * G::kTile), kd = desc_k(sbase + G::kOffRing + (idx % NS) * G::kTile);
-          mma_ss<false>(tmem + 128 * t, q, kd, id_s);
-#pragma unroll
-          for (int x = 1; x < D / 16; ++x)
-            mma_ss<true>(tmem + 128 * t, q + (x >> 2) * 1024 + 2 * (x & 3), kd + (x >> 2) * 1024 + 2 * (x & 3), id_s);
-          mma_commit(s_full + 8 * t);
-          if (t == 1 || !two) mma_commit(empty + 8 * (idx % NS));
-          return true;
-        };
-        // outputs of row tile t of key tile n
-        auto outputs = [&](int t, int n, bool two, bool first) {
-          const int idx = 2 * n + 1;
-          if (t == 0 && !mbar_wait(full + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1))) return false;
-          if (!mbar_wait(p_full + 16 * t, static_cast<uint32_t>(pn[t] & 1))) return false;
-          fence_after();
-          const uint32_t v = desc_mn(sbase + G::kOffRing + (idx % NS) * G::kTile);
-          mma_ts(tmem + 256 + 128 * t, tmem + 128 * t, v, id_o, first ? 0u : 1u);
-#pragma unroll
-          for (int x = 1; x < kBN / 32; ++x) mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, v + 128 * x, id_o, 1u);
-          if (!mbar_wait(p_full + 16 * t + 8, static_cast<uint32_t>(pn[t] & 1))) return false;
-          ++pn[t];
-          fence_after();
-#pragma unroll
-          for (int x = kBN / 32; x < kBN / 16; ++x) mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * x, v + 128 * x, id_o, 1u);
-          mma_commit(o_done + 8 * t);
-          if (t == 1 || !two) mma_commit(empty + 8 * (idx % NS));
-          return true;
-        };
-        ok = scores(0, two_cur) && (!two_cur || scores(1, two_cur));
-        for (int n = 0; n < total && ok; ++n) {
-          const bool more = n + 1 < total;
-          if (more) {
-            s_first = --left == 0;
-            if (s_first) {
-              cs.skip(a, piece);
-              left = piece = cs.piece();
-              two_next = cs.n * a.s.group - cs.qt * a.s.rows > kM;
-            }
-            ++sn;
-          }
-          ok = outputs(0, n, two_cur, first_cur);
-          if (ok && more) ok = scores(0, two_next);
-          if (ok && two_cur) ok = outputs(1, n, two_cur, first_cur);
-          if (ok && more && two_next) ok = scores(1, two_next);
-          two_cur = two_next;
-          first_cur = s_first;
+          ++sn;
         }
-        if (!ok && a.rq.status) a.rq.status[cs.r] = 3;
+#pragma unroll 1
+        for (uint32_t t = 0; t < 2; ++t) {
+          if (n >= 0 && (t == 0 || two_cur)) outputs(t, n, two_cur, first_cur);
+          if (more && (t == 0 || two_next)) scores(t, two_next);
+        }
+        two_cur = two_next;
+        first_cur = s_first;
+        if (!__all_sync(0xffffffffu, fine != 0)) {
+          ok = false;
+          break;
+        }
       }
+      if (!ok && lane == 0 && a.rq.status) a.rq.status[cs.r] = 3;
     } else if (wid < 12) {
       // -------------------------------------------------------------- keys and values
       const int lt = tid - 256;
@@ -799,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // an extra commit covers whatever was issued; its barrier is one that nobody uses any more
       mbar_init_count(info, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      mma_commit(info);
+      mma_commit(1, info);
       mbar_wait(info, 0);
     }
     __syncwarp();
