@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Dict, Optional
 
 from .builder import LIB
@@ -328,43 +329,60 @@ def dflash2_lmhead_bytes(h, n_req) -> int:
 KV_BF16, KV_F16, KV_INT8, KV_E4M3 = 0, 1, 2, 3
 T_BF16, T_F16, T_F32 = 0, 1, 2
 _KV_NAMES = {"bf16": KV_BF16, "fp16": KV_F16, "int8": KV_INT8, "e4m3": KV_E4M3}
-_dtype_ids = None
-_paged_cfg: Dict[int, PagedConfig] = {}      # geometry of each live handle, for the checks below
+_paged_cfg: Dict[int, tuple] = {}      # geometry of each live handle, for the checks below
+# The structures' bytes (checked against the header by the layout test): a packed bytes object is a
+# fraction of a ctypes structure's cost, and a call's host side is all that a single token's pass waits for.
+_PACK_CACHE = struct.Struct("@5P7q2i")
+_PACK_ROWS = struct.Struct("@P2q2i")
+_PACK_ATTN = struct.Struct("@6ifi2P" + "P2q2i" * 2 + "3P")
+_PACK_SAMPLE = struct.Struct("@4iPq8PqP")
+_fast = None
 
 
-def _dtypes():
-    global _dtype_ids
-    if _dtype_ids is None:
+def _calls():
+    """(torch's types, the entry points with plain pointer arguments, the current stream's handle)."""
+    global _fast
+    if _fast is None:
         import torch
-        _dtype_ids = ({torch.bfloat16: T_BF16, torch.float16: T_F16, torch.float32: T_F32},
-                      {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.int8: KV_INT8,
-                       torch.float8_e4m3fn: KV_E4M3}, torch.int32, torch.float32, torch.int64)
-    return _dtype_ids
+        L = lib()
+        c, vp, i32 = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int32
+        fn = lambda name, *args: ctypes.CFUNCTYPE(i32, *args)((name, L))  # noqa: E731
+        move = (vp, c, i32, i32, vp, vp, c, c, vp, vp)
+        _fast = (torch, {torch.bfloat16: T_BF16, torch.float16: T_F16, torch.float32: T_F32},
+                 {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3},
+                 fn("dflash2_paged_write", *move), fn("dflash2_paged_read", *move),
+                 fn("dflash2_paged_attention", vp, c, c, vp), fn("dflash2_sample", c, vp))
+    return _fast
+
+
+def _raw_stream(torch, stream) -> Optional[int]:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _inval(what: str, why: str):
     return Dflash2Error(E_INVAL, f"{what}: {why}")
 
 
-def _vector(what, name, t, dtype, n, none_ok=True):
-    """A contiguous 1-D device tensor of n elements (or more than one row: n counts elements)."""
+def _vector(what, name, t, dtype, n):
+    """Address of a contiguous CUDA tensor of n elements, or 0 for None."""
     if t is None:
-        if none_ok:
-            return None
-        raise _inval(what, f"{name} is missing")
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        return 0
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
         raise _inval(what, f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
     return t.data_ptr()
 
 
-def _rows(what, name, t, heads, dim) -> Rows:
-    sh, st = t.shape, t.stride()
-    ty = _dtypes()[0].get(t.dtype)
-    if ty is None or len(sh) != 3 or sh[1] != heads or sh[2] != dim or not t.is_cuda:
+def _rows(what, name, t, types, heads, dim):
+    """The fields of dflash2_rows."""
+    ty = types.get(t.dtype)
+    if ty is None or t.dim() != 3 or not t.is_cuda:
         raise _inval(what, f"{name} must be a bf16, fp16 or fp32 CUDA tensor [tokens, {heads}, {dim}]")
-    if st[2] != 1:
-        raise _inval(what, f"{name}: the last dimension must be contiguous")
-    return Rows(t.data_ptr(), st[0], st[1], ty, 0)
+    sh, st = t.shape, t.stride()
+    if sh[1] != heads or sh[2] != dim or st[2] != 1:
+        raise _inval(what, f"{name} must be [tokens, {heads}, {dim}] with contiguous channels")
+    return t.data_ptr(), st[0], st[1], ty, 0
 
 
 def make_paged_config(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, kv_format: str,
@@ -373,33 +391,40 @@ def make_paged_config(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size:
     return PagedConfig(n_q_heads, n_kv_heads, head_dim, page_size, _KV_NAMES[kv_format], max_requests)
 
 
-def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedCache:
+class PagedPool:
+    """The cache structure of one layer (paged_cache makes it); it keeps the tensors alive."""
+    __slots__ = ("raw", "geometry", "n_req", "_keep")
+
+
+def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedPool:
     """The cache structure of pools k, v [pages, page_size, n_kv_heads, head_dim] (any order of
     the first three dimensions, the same for both), scales [pages, page_size, n_kv_heads]
-    (8-bit pools) and page_table int32 [requests, pages of a request].  It keeps the
-    tensors alive."""
+    (8-bit pools) and page_table int32 [requests, pages of a request]."""
     what = "paged_cache"
-    fmt = _dtypes()[1].get(k.dtype)
-    if fmt is None or k.dim() != 4 or k.dtype != v.dtype or k.shape != v.shape or k.stride() != v.stride():
-        raise _inval(what, "k and v must be pools of one type, shape and layout")
-    if k.stride(3) != 1 or not k.is_cuda or not v.is_cuda:
-        raise _inval(what, "the pools must be CUDA tensors with contiguous channels")
-    if page_table.dtype != _dtypes()[2] or page_table.dim() != 2 or not page_table.is_cuda or page_table.stride(1) != 1:
+    torch, _, formats = _calls()[:3]
+    fmt = formats.get(k.dtype)
+    if fmt is None or k.dim() != 4 or k.dtype is not v.dtype:
+        raise _inval(what, "k and v must be pools of one type [pages, page_size, heads, head_dim]")
+    sh, st = k.shape, k.stride()
+    if sh != v.shape or st != v.stride() or st[3] != 1 or not k.is_cuda or not v.is_cuda:
+        raise _inval(what, "k and v must be CUDA tensors of one shape and layout with contiguous channels")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or page_table.stride(1) != 1:
         raise _inval(what, "page_table must be an int32 CUDA tensor [requests, pages] with contiguous rows")
-    c = PagedCache()
-    c.k, c.v, c.page_table = k.data_ptr(), v.data_ptr(), page_table.data_ptr()
-    c.page_stride, c.token_stride, c.head_stride = k.stride()[:3]
-    if fmt in (KV_INT8, KV_E4M3):
-        f32 = _dtypes()[3]
-        if k_scale is None or v_scale is None or k_scale.dtype != f32 or v_scale.dtype != f32 or \
-                k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3] or k_scale.stride() != v_scale.stride() or \
-                not k_scale.is_cuda or not v_scale.is_cuda:
-            raise _inval(what, "8-bit pools need float32 scales [pages, page_size, heads] of one layout")
-        c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-        c.scale_page_stride, c.scale_token_stride, c.scale_head_stride = k_scale.stride()
-    c.n_pages = k.shape[0]
-    c.max_pages, c.table_stride = page_table.shape[1], max(page_table.stride(0), page_table.shape[1])
-    c.n_req, c.fmt, c.shape = page_table.shape[0], fmt, tuple(k.shape[1:])
+    c = PagedPool()
+    c.n_req, max_pages = page_table.shape
+    ks = vs = 0
+    ss = (0, 0, 0)
+    if fmt >= KV_INT8:
+        if k_scale is None or v_scale is None or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or \
+                k_scale.shape != sh[:3] or v_scale.shape != sh[:3] or not k_scale.is_cuda or not v_scale.is_cuda:
+            raise _inval(what, "8-bit pools need float32 scales [pages, page_size, heads]")
+        ss = k_scale.stride()
+        if ss != v_scale.stride():
+            raise _inval(what, "the scales must have one layout")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    c.raw = _PACK_CACHE.pack(k.data_ptr(), v.data_ptr(), ks, vs, page_table.data_ptr(), st[0], st[1], st[2], *ss,
+                             page_table.stride(0) if c.n_req > 1 else max_pages, sh[0], max_pages)
+    c.geometry = (fmt, sh[1], sh[2], sh[3])
     c._keep = (k, v, page_table, k_scale, v_scale)
     return c
 
@@ -407,7 +432,7 @@ def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedCache:
 def dflash2_paged_create(cfg: PagedConfig) -> int:
     h = ctypes.c_void_p()
     _check(lib().dflash2_paged_create(ctypes.byref(cfg), ctypes.byref(h)), "dflash2_paged_create")
-    _paged_cfg[h.value] = cfg
+    _paged_cfg[h.value] = ((cfg.kv_format, cfg.page_size, cfg.n_kv_heads, cfg.head_dim), cfg.n_q_heads)
     return h.value
 
 
@@ -416,37 +441,41 @@ def dflash2_paged_destroy(h: int):
     _paged_cfg.pop(h, None)
 
 
-def _paged_check(what, h, cache, token_begin, kv_len, status):
-    """The handle's geometry against the cache's; returns (geometry, number of requests)."""
+def _paged_check(what, torch, h, cache, token_begin, kv_len, status):
+    """The handle's geometry against the cache's; returns (geometry, query heads, requests, three addresses)."""
     g = _paged_cfg.get(h)
     if g is None:
         raise _inval(what, "not a paged handle")
-    if cache.fmt != g.kv_format or cache.shape != (g.page_size, g.n_kv_heads, g.head_dim):
+    if cache.geometry != g[0]:
         raise _inval(what, "the pools are not of the handle's format, page size or heads")
     n = kv_len.numel()
     if n > cache.n_req:
         raise _inval(what, "the page table has fewer rows than there are requests")
-    i32 = _dtypes()[2]
-    return g, n, _vector(what, "token_begin", token_begin, i32, n + 1, False), \
-        _vector(what, "kv_len", kv_len, i32, n, False), _vector(what, "status", status, i32, n)
+    i32 = torch.int32
+    return g[0], g[1], n, _vector(what, "token_begin", token_begin, i32, n + 1), \
+        _vector(what, "kv_len", kv_len, i32, n), _vector(what, "status", status, i32, n)
 
 
-def _paged_move(what, call, h, cache, k, v, token_begin, kv_len, status, stream):
-    g, n, begin, length, st = _paged_check(what, h, cache, token_begin, kv_len, status)
-    if k.shape != v.shape or k.dtype != v.dtype:
+def _paged_move(what, which, h, cache, k, v, token_begin, kv_len, status, stream):
+    f = _calls()
+    g, _, n, begin, length, st = _paged_check(what, f[0], h, cache, token_begin, kv_len, status)
+    if k.shape != v.shape or k.dtype is not v.dtype:
         raise _inval(what, "k and v must have one shape and type")
-    rk, rv = _rows(what, "k", k, g.n_kv_heads, g.head_dim), _rows(what, "v", v, g.n_kv_heads, g.head_dim)
-    _check(call(h, cache, n, k.shape[0], begin, length, rk, rv, st, _stream(stream)), what)
+    rk, rv = _rows(what, "k", k, f[1], g[2], g[3]), _rows(what, "v", v, f[1], g[2], g[3])
+    s = f[which](h, cache.raw, n, k.shape[0], begin, length, _PACK_ROWS.pack(*rk), _PACK_ROWS.pack(*rv), st,
+                 _raw_stream(f[0], stream))
+    if s:
+        _check(s, what)
 
 
 def dflash2_paged_write(h, cache, k, v, token_begin, kv_len, status=None, stream=None):
     """Writes the new tokens' keys and values [tokens, n_kv_heads, head_dim] into their positions."""
-    _paged_move("dflash2_paged_write", lib().dflash2_paged_write, h, cache, k, v, token_begin, kv_len, status, stream)
+    _paged_move("dflash2_paged_write", 3, h, cache, k, v, token_begin, kv_len, status, stream)
 
 
 def dflash2_paged_read(h, cache, k, v, token_begin, kv_len, status=None, stream=None):
     """Reads the same positions back into k and v."""
-    _paged_move("dflash2_paged_read", lib().dflash2_paged_read, h, cache, k, v, token_begin, kv_len, status, stream)
+    _paged_move("dflash2_paged_read", 4, h, cache, k, v, token_begin, kv_len, status, stream)
 
 
 def dflash2_paged_attention(h, cache, q, out, token_begin, kv_len, max_new, max_len, scale, causal=True, window=0,
@@ -454,35 +483,43 @@ def dflash2_paged_attention(h, cache, q, out, token_begin, kv_len, max_new, max_
     """Attention of the new tokens q [tokens, n_q_heads, head_dim] over their requests' caches, into out.
     tree_mask: int64 [tokens] (the bits of a uint64)."""
     what = "dflash2_paged_attention"
-    g, n, begin, length, st = _paged_check(what, h, cache, token_begin, kv_len, status)
-    rq, ro = _rows(what, "q", q, g.n_q_heads, g.head_dim), _rows(what, "out", out, g.n_q_heads, g.head_dim)
+    f = _calls()
+    torch = f[0]
+    g, hq, n, begin, length, st = _paged_check(what, torch, h, cache, token_begin, kv_len, status)
+    rq, ro = _rows(what, "q", q, f[1], hq, g[3]), _rows(what, "out", out, f[1], hq, g[3])
     tokens = q.shape[0]
     if out.shape[0] != tokens:
         raise _inval(what, "q and out must have the same rows")
-    a = PagedAttentionArgs(n, tokens, max_new, max_len, 1 if causal else 0, window, scale, 0, begin, length, rq, ro,
-                           _vector(what, "tree_mask", tree_mask, _dtypes()[4], tokens),
-                           _vector(what, "lse", lse, _dtypes()[3], tokens * g.n_q_heads), st)
-    _check(lib().dflash2_paged_attention(h, cache, a, _stream(stream)), what)
+    a = _PACK_ATTN.pack(n, tokens, max_new, max_len, 1 if causal else 0, window, scale, 0, begin, length, *rq, *ro,
+                        _vector(what, "tree_mask", tree_mask, torch.int64, tokens),
+                        _vector(what, "lse", lse, torch.float32, tokens * hq), st)
+    s = f[5](h, cache.raw, a, _raw_stream(torch, stream))
+    if s:
+        _check(s, what)
 
 
 def dflash2_sample(logits, temperature, top_k, top_p, min_p, uniform, token, prob=None, kept=None, status=None,
                    stream=None):
     """Truncated sampling of the rows of logits [rows, vocab]; top_k, top_p and min_p may be None."""
     what = "dflash2_sample"
-    ty = _dtypes()[0].get(logits.dtype)
+    f = _calls()
+    torch = f[0]
+    ty = f[1].get(logits.dtype)
     if ty is None or logits.dim() != 2 or logits.stride(1) != 1 or not logits.is_cuda:
         raise _inval(what, "logits must be a bf16, fp16 or fp32 CUDA tensor [rows, vocab] with contiguous rows")
     n, v = logits.shape
-    i32, f32 = _dtypes()[2:4]
-    if kept is not None and (kept.dtype != f32 or kept.shape != logits.shape or kept.stride(1) != 1 or not kept.is_cuda):
+    i32, f32 = torch.int32, torch.float32
+    if kept is not None and (kept.dtype is not f32 or kept.shape != logits.shape or kept.stride(1) != 1 or not kept.is_cuda):
         raise _inval(what, "kept must be a float32 CUDA tensor of the logits' shape with contiguous rows")
-    a = SampleArgs(n, v, ty, 0, logits.data_ptr(), logits.stride(0),
-                   _vector(what, "temperature", temperature, f32, n, False), _vector(what, "top_k", top_k, i32, n),
-                   _vector(what, "top_p", top_p, f32, n), _vector(what, "min_p", min_p, f32, n),
-                   _vector(what, "uniform", uniform, f32, n, False), _vector(what, "token", token, i32, n, False),
-                   _vector(what, "prob", prob, f32, n), _p(kept), kept.stride(0) if kept is not None else 0,
-                   _vector(what, "status", status, i32, n))
-    _check(lib().dflash2_sample(a, _stream(stream)), what)
+    a = _PACK_SAMPLE.pack(n, v, ty, 0, logits.data_ptr(), logits.stride(0),
+                          _vector(what, "temperature", temperature, f32, n), _vector(what, "top_k", top_k, i32, n),
+                          _vector(what, "top_p", top_p, f32, n), _vector(what, "min_p", min_p, f32, n),
+                          _vector(what, "uniform", uniform, f32, n), _vector(what, "token", token, i32, n),
+                          _vector(what, "prob", prob, f32, n), 0 if kept is None else kept.data_ptr(),
+                          0 if kept is None else kept.stride(0), _vector(what, "status", status, i32, n))
+    s = f[6](a, _raw_stream(torch, stream))
+    if s:
+        _check(s, what)
 
 
 # ----------------------------------------------------------------------------- convenience

@@ -167,6 +167,9 @@ def test_structures_match_the_header(tmp_path):
     cls = {"dflash2_paged_config": b.PagedConfig, "dflash2_paged_cache": b.PagedCache, "dflash2_rows": b.Rows,
            "dflash2_paged_attention_args": b.PagedAttentionArgs, "dflash2_sample_args": b.SampleArgs}
     assert len(lines) == 21
+    for packed, name in [(b._PACK_CACHE, "dflash2_paged_cache"), (b._PACK_ROWS, "dflash2_rows"),
+                         (b._PACK_ATTN, "dflash2_paged_attention_args"), (b._PACK_SAMPLE, "dflash2_sample_args")]:
+        assert packed.size == ctypes.sizeof(cls[name])
     for line in lines:
         name, value = line.split()
         t, _, field = name.partition(".")
