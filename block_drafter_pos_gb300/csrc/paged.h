@@ -125,7 +125,6 @@ inline int paged_rows(int max_new, int group) {
   const long long r = static_cast<long long>(max_new) * group;
   return r <= 16 ? 16 : (r <= 32 ? 32 : 64);
 }
-constexpr int kPagedBn = 64;
 constexpr int kPagedMaxCtasPerSm = 2;
 // The kernel for many rows: one CTA per SM, units of 256 rows against tiles of 128 keys.
 constexpr int kChunkBn = 128;

@@ -9,7 +9,7 @@
 //  * The launch's key tiles are dealt to the CTAs in contiguous equal runs (paged.h), so
 //    ragged batches and single long requests fill the machine alike; a unit cut between
 //    CTAs leaves fp32 partials, joined by the combine kernel in CTA order (no atomics).
-//  * Tiles of 64 keys come by 16-byte cp.async, zero-filled past the visible range; the
+//  * Tiles of 64 keys (128 of 8 bits) come by 16-byte cp.async, zero-filled past the visible range; the
 //    page table is read one tile ahead of the copies, so its latency is off the path, and
 //    a tile may cross any number of pages.
 //  * Four warps: rows / 16 row groups x key groups of the tile, each with its own running
@@ -29,7 +29,7 @@ namespace df2 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBN = kPagedBn;
+constexpr float kGrow = 8.f;  // a row's reference follows its maximum when that has grown by more than 2^8
 
 DF2_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -65,6 +65,7 @@ DF2_DEV void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t 
 template <int D, int FMT, int MT>
 struct Geo {
   static constexpr bool kQuant = FMT == kKvInt8 || FMT == kKvE4m3;
+  static constexpr int kBN = kQuant ? 128 : 64;        // keys of a tile (32 KB of keys and values at D = 128)
   static constexpr int kRowBytes = D * (kQuant ? 1 : 2);
   static constexpr int kChunks = kRowBytes / 16;       // 16-byte pieces of a key
   static constexpr int kSide = kBN * kRowBytes;        // keys (or values) of a tile
@@ -74,11 +75,12 @@ struct Geo {
   static constexpr int kRows = 16 * MT;
   static constexpr int kKG = 4 / MT;                   // key groups
   static constexpr int kWK = kBN / kKG;                // keys of a warp
+  static constexpr int kKS = kWK < 64 ? kWK : 64;      // keys of one update of the running state
   static constexpr int kNT = D / 8;                    // output column tiles
   static constexpr int kMergeCols = kNT / 4;           // column tiles joined at a time
   static constexpr int kMerge = (kKG - 1) * MT * kMergeCols * 4 * 32 * 4;
   static constexpr int kStat = 4 * 32 * 16;
-  static constexpr int kOff = (kStages + 1) * kBN * 8 + (kStages + 1) * 8 + 64;
+  static constexpr int kOff = (kStages + 1) * kBN * 8 + (kStages + 1) * 16 + 64;
   static constexpr int kFixed = kStages * kStage + kMerge + kStat + kOff;
 };
 
@@ -87,15 +89,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   using G = Geo<D, FMT, MT>;
   constexpr bool kQuant = G::kQuant;
   constexpr bool kBF = kQuant ? false : QBF;  // operand type of both products
-  constexpr int S = G::kStages, KG = G::kKG, WK = G::kWK, NT = G::kNT;
+  constexpr int S = G::kStages, KG = G::kKG, WK = G::kWK, NT = G::kNT, KS = G::kKS, kBN = G::kBN;
   constexpr int kSteps = D / 16;
   extern __shared__ __align__(128) char sm[];
   const uint32_t ring = smem_addr(sm);
   float* const merge = reinterpret_cast<float*>(sm + S * G::kStage);
   float4* const stat = reinterpret_cast<float4*>(sm + S * G::kStage + G::kMerge);
   long long* const offs = reinterpret_cast<long long*>(sm + S * G::kStage + G::kMerge + G::kStat);  // [S + 1][kBN]
-  int* const badp = reinterpret_cast<int*>(offs + (S + 1) * kBN);                                    // [S + 1][2]
-  long long* const tmp = reinterpret_cast<long long*>(badp + (S + 1) * 2);
+  int* const badp = reinterpret_cast<int*>(offs + (S + 1) * kBN);                                    // [S + 1][4]
+  long long* const tmp = reinterpret_cast<long long*>(badp + (S + 1) * 4);
   long long* const pre = tmp + 8;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, q = lane & 3;
   const int rg = wid % MT, kg = wid / MT;
@@ -107,59 +109,66 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
 
-  // ---- the page rows of a tile: threads 0 .. 63, one key each
+  // ---- the page rows of a tile: one key for each of the first kBN threads.  The page table is read (fetch)
+  // one tile before its entries become offsets (resolve), so that its latency lies under a tile's work.
   PagedCursor oc;
   oc.start(a, pre, t_begin, t_end);
   long long my_off = -1, my_soff = 0;
   int my_bad = 0;
-  auto look_up = [&]() {  // offsets of tile oc into registers; advances oc
-    my_off = -1;
-    my_bad = 0;
+  int pg = 0, pg_row = 0, pg_h = 0, pg_r = 0;
+  bool pg_in = false;
+  auto fetch = [&]() {  // tile oc; advances oc
+    pg_in = false;
     if (!oc.valid()) return;
     if (tid < kBN) {
       const int key = (oc.u.t0 + oc.i) * kBN + tid;
-      if (key >= oc.u.lo && key < oc.u.hi) {
-        const int pi = key / a.c.page_size, row = key - pi * a.c.page_size;
-        const int page = __ldg(a.c.table + oc.r * a.c.table_stride + pi);
-        if (!paged_row(a.c, page, row, oc.h, &my_off, &my_soff)) {
-          my_bad = 1;
-          if (a.rq.status) a.rq.status[oc.r] = 1;
-        }
+      pg_in = key >= oc.u.lo && key < oc.u.hi;
+      if (pg_in) {
+        const int pi = key / a.c.page_size;
+        pg_row = key - pi * a.c.page_size;
+        pg_h = oc.h;
+        pg_r = oc.r;
+        pg = __ldg(a.c.table + oc.r * a.c.table_stride + pi);
       }
     }
     oc.next(a);
   };
-  // quantised: the scales' copies are issued with the look-up, one group ahead of the codes
-  auto put = [&](int j) {  // into slot j of the offsets' ring
-    const int s = j % (S + 1);
+  auto resolve = [&]() {
+    my_off = -1;
+    my_bad = 0;
+    if (pg_in && !paged_row(a.c, pg, pg_row, pg_h, &my_off, &my_soff)) {
+      my_bad = 1;
+      if (a.rq.status) a.rq.status[pg_r] = 1;  // DFLASH2_E_INVAL
+    }
+  };
+  auto put = [&](int slot) {  // into a slot of the offsets' ring
     if (tid < kBN) {
-      offs[s * kBN + tid] = my_off;
+      offs[slot * kBN + tid] = my_off;
       const int any = __any_sync(0xffffffffu, my_bad);
-      if (lane == 0) badp[2 * s + wid] = any;
+      if (lane == 0) badp[4 * slot + wid] = any;
     }
   };
   long long soff_next = 0;
   bool sval_next = false;
-  auto issue = [&](int j) {  // the copies of tile j of the run
-    const uint32_t dst = ring + (j % S) * G::kStage;
-    const long long* o = offs + (j % (S + 1)) * kBN;
-    constexpr int kRowsPer = kThreads / G::kChunks;
-    const int ch = tid % G::kChunks;
+  // A thread copies piece ch of keys r0, r0 + kStep, ...: the swizzles' key bits are its own constants.
+  constexpr int kStep = kThreads / G::kChunks, kCount = kBN / kStep;
+  static_assert(kStep % 8 == 0, "a thread's keys share their place in the swizzle");
+  const int ch = tid % G::kChunks, r0 = tid / G::kChunks;
+  const uint32_t put_k = r0 * G::kRowBytes + 16 * (kQuant ? (D == 128 ? ch ^ ((r0 & 1) << 2) : ch) : ch ^ (r0 & 7));
+  const uint32_t put_v = G::kSide + r0 * G::kRowBytes +
+                         16 * (kQuant ? (D == 128 ? ch ^ (r0 & 6) : ch ^ ((r0 >> 1) & 3)) : ch ^ (r0 & 7));
+  auto issue = [&](int stage, int slot) {  // the copies of a tile whose offsets are in `slot`
+    const uint32_t dst = ring + stage * G::kStage;
+    const long long* o = offs + slot * kBN + r0;
+    long long off[kCount];
 #pragma unroll
-    for (int i = 0; i < kBN / kRowsPer; ++i) {
-      const int row = tid / G::kChunks + i * kRowsPer;
-      const long long off = o[row];
-      const int bytes = off >= 0 ? 16 : 0;
-      const long long byte = (off >= 0 ? off * (kQuant ? 1 : 2) : 0) + ch * 16;
-      int ck, cv;
-      if constexpr (kQuant) {
-        ck = D == 128 ? ch ^ ((row & 1) << 2) : ch;
-        cv = D == 128 ? ch ^ (row & 6) : ch ^ ((row >> 1) & 3);
-      } else {
-        ck = cv = ch ^ (row & 7);
-      }
-      cp_async16(dst + row * G::kRowBytes + ck * 16, a.c.k + byte, bytes);
-      cp_async16(dst + G::kSide + row * G::kRowBytes + cv * 16, a.c.v + byte, bytes);
+    for (int i = 0; i < kCount; ++i) off[i] = o[i * kStep];
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const int bytes = off[i] >= 0 ? 16 : 0;
+      const long long byte = (off[i] >= 0 ? off[i] * (kQuant ? 1 : 2) : 0) + ch * 16;
+      cp_async16(dst + put_k + i * (kStep * G::kRowBytes), a.c.k + byte, bytes);
+      cp_async16(dst + put_v + i * (kStep * G::kRowBytes), a.c.v + byte, bytes);
     }
     if constexpr (kQuant) {
       if (tid < kBN) {
@@ -173,18 +182,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   // prologue: tiles 0 .. S - 2 in flight, the offsets of tile S - 1 looked up
 #pragma unroll
   for (int j = 0; j < S - 1; ++j) {
-    look_up();
+    fetch();
+    resolve();
     put(j);
     soff_next = my_soff;
     sval_next = my_off >= 0;
     __syncthreads();
-    if (j < n_tiles) issue(j);
+    if (j < n_tiles) issue(j, j);
     cp_commit();
   }
-  look_up();
+  fetch();
+  resolve();
   put(S - 1);
   soff_next = my_soff;
   sval_next = my_off >= 0;
+  fetch();  // tile S
 
   PagedCursor cc;
   cc.start(a, pre, t_begin, t_end);
@@ -196,6 +208,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   bool mixed_rows = false;
   unsigned long long w0 = 0, w1 = 0;
   bool fresh = true;
+  int st_now = 0, st_next = S - 1;       // stages of tiles j and j + S - 1
+  int sl_now = 0, sl_next = S - 1;       // offset slots of the same (ring of S + 1); tile j + S takes the one after
 
   for (int j = 0; j < n_tiles; ++j) {
     if (fresh) {
@@ -276,23 +290,28 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 
     cp_wait<S - 2>();
     __syncthreads();  // tile j has landed; tile j - 1's buffer and the offsets of tile j + S - 1 are free / written
-    if (j + S - 1 < n_tiles) issue(j + S - 1);
+    if (j + S - 1 < n_tiles) issue(st_next, sl_next);
     cp_commit();
-    look_up();  // tile j + S
+    resolve();  // tile j + S
+    fetch();    // tile j + S + 1
 
-    const uint32_t ks = ring + (j % S) * G::kStage, vs = ks + G::kSide;
-    const float* ksc = reinterpret_cast<const float*>(sm + (j % S) * G::kStage + 2 * G::kSide);
+    const uint32_t ks = ring + st_now * G::kStage, vs = ks + G::kSide;
+    const float* ksc = reinterpret_cast<const float*>(sm + st_now * G::kStage + 2 * G::kSide);
     const float* vsc = ksc + kBN;
-    const int kw = kg * WK;  // first key of this warp in the tile
     const int key0 = (cc.u.t0 + cc.i) * kBN;
+    const int* bad = badp + 4 * sl_now;
+    const bool any_bad = (bad[0] | bad[1] | (kBN > 64 ? bad[2] | bad[3] : 0)) != 0;
+    const bool masked = key0 < lo_max || key0 + kBN > hi_min || any_bad;
+#pragma unroll 1
+    for (int kw = kg * WK; kw < (kg + 1) * WK; kw += KS) {  // keys kw .. kw + KS - 1 of the tile
 
     // ---- scores
-    float z[WK / 8][4];
+    float z[KS / 8][4];
 #pragma unroll
-    for (int t = 0; t < WK / 8; ++t) z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
+    for (int t = 0; t < KS / 8; ++t) z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
     if constexpr (!kQuant) {
 #pragma unroll
-      for (int t = 0; t < WK / 8; t += 2) {
+      for (int t = 0; t < KS / 8; t += 2) {
         const int row = kw + 8 * t + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -304,12 +323,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < WK / 8; ++t) {
-        const int row = kw + 8 * t + g;
+      for (int t = 0; t < KS / 8; ++t) {
+        const uint32_t row = ks + (kw + 8 * t + g) * G::kRowBytes;
 #pragma unroll
         for (int hh = 0; hh < kSteps / 4; ++hh) {
-          const int ch = q + 4 * hh;
-          const uint4 w = lds16(ks + row * G::kRowBytes + ((D == 128 ? ch ^ ((row & 1) << 2) : ch) << 4));
+          const int c16 = q + 4 * hh;
+          const uint4 w = lds16(row + ((D == 128 ? c16 ^ ((g & 1) << 2) : c16) << 4));
           mma16<false>(z[t], qf[4 * hh + 0], codes2<FMT, 0>(w.x), codes2<FMT, 1>(w.x));
           mma16<false>(z[t], qf[4 * hh + 1], codes2<FMT, 0>(w.y), codes2<FMT, 1>(w.y));
           mma16<false>(z[t], qf[4 * hh + 2], codes2<FMT, 0>(w.z), codes2<FMT, 1>(w.z));
@@ -317,61 +336,65 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
     }
-    // ---- scale, mask, running maximum
-    const int* bad = badp + 2 * (j % (S + 1));
-    const bool any_bad = (bad[0] | bad[1]) != 0;
-    const bool masked = key0 < lo_max || key0 + kBN > hi_min || any_bad;
-    float x0 = -INFINITY, x1 = -INFINITY;
+    // ---- scale, mask, running reference
 #pragma unroll
-    for (int t = 0; t < WK / 8; ++t) {
+    for (int t = 0; t < KS / 8; ++t) {
+      float2 f = make_float2(1.f, 1.f);
+      if constexpr (kQuant) f = *reinterpret_cast<const float2*>(ksc + kw + 8 * t + 2 * q);
+      z[t][0] *= sc0 * f.x, z[t][1] *= sc0 * f.y;
+      z[t][2] *= sc1 * f.x, z[t][3] *= sc1 * f.y;
+    }
+    if (masked) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float s0 = z[t][e] * sc0, s1 = z[t][2 + e] * sc1;
-        const int kk = kw + 8 * t + 2 * q + e;
-        if constexpr (kQuant) {
-          const float f = ksc[kk];
-          s0 *= f;
-          s1 *= f;
-        }
-        if (masked) {
-          const int key = key0 + kk;
+      for (int t = 0; t < KS / 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int kk = kw + 8 * t + 2 * q + e, key = key0 + kk;
           bool v0 = key >= lo0 && key < hi0, v1 = key >= lo1 && key < hi1;
           if (a.s.causal == 2 && key >= base) {
-            v0 = v0 && ((w0 >> (key - base)) & 1ull);
-            v1 = v1 && ((w1 >> (key - base)) & 1ull);
+            v0 = v0 && ((w0 >> ((key - base) & 63)) & 1ull);
+            v1 = v1 && ((w1 >> ((key - base) & 63)) & 1ull);
           }
-          if (any_bad && offs[(j % (S + 1)) * kBN + kk] < 0) v0 = v1 = false;
-          s0 = v0 ? s0 : -INFINITY;
-          s1 = v1 ? s1 : -INFINITY;
+          if (any_bad && offs[sl_now * kBN + kk] < 0) v0 = v1 = false;
+          z[t][e] = v0 ? z[t][e] : -INFINITY;
+          z[t][2 + e] = v1 ? z[t][2 + e] : -INFINITY;
         }
-        z[t][e] = s0;
-        z[t][2 + e] = s1;
-        x0 = fmaxf(x0, s0);
-        x1 = fmaxf(x1, s1);
-      }
+    }
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < KS / 8; ++t) {
+      x0 = fmaxf(x0, fmaxf(z[t][0], z[t][1]));
+      x1 = fmaxf(x1, fmaxf(z[t][2], z[t][3]));
     }
 #pragma unroll
     for (int of = 1; of <= 2; of <<= 1) {
       x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, of));
       x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, of));
     }
-    const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-    // a row that has seen nothing keeps weights of zero: 2^(-inf - 0)
-    const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
-    float f0 = ex2(m0 - r0), f1 = ex2(m1 - r1);
-    m0 = n0;
-    m1 = n1;
+    // O and the sum are rescaled only when a maximum has grown by more than 2^8 (weights stay below 2^8)
+    float f0 = 1.f, f1 = 1.f;
+    if (x0 > m0 + kGrow) {
+      f0 = ex2(m0 - x0);
+      m0 = x0;
+    }
+    if (x1 > m1 + kGrow) {
+      f1 = ex2(m1 - x1);
+      m1 = x1;
+    }
     l0 *= f0;
     l1 *= f1;
+    // a row that has seen nothing keeps weights of zero: 2^(-inf - 0)
+    const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
     if constexpr (kQuant) {
-      // the largest finite value scale of this warp's keys
+      // the values' reference: the largest finite scale of this warp's keys, raised when one exceeds 16 of it
       float v = 0.f;
 #pragma unroll
-      for (int i = lane; i < WK; i += 32) v = vsc[kw + i] < INFINITY ? fmaxf(v, vsc[kw + i]) : v;
-      if (WK < 32 && lane >= WK) v = 0.f;
-      v = warp_max(v);
-      if (v > vref) {
-        v = fmaxf(v, 1.17549435e-38f);
+      for (int i = 0; i < KS; i += 32) {
+        const float y = vsc[kw + i + lane];
+        v = y < INFINITY ? fmaxf(v, y) : v;
+      }
+      if (__any_sync(0xffffffffu, v > 16.f * vref || (vref == 0.f && v > 0.f))) {
+        v = fmaxf(warp_max(v), 1.17549435e-38f);
         const float f = vref / v;
         vref = v;
         vinv = 1.f / v;
@@ -379,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         f1 *= f;
       }
     }
-    if (f0 != 1.f || f1 != 1.f) {
+    if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         o[t][0] *= f0;
@@ -390,19 +413,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     // ---- weights and the values' product
 #pragma unroll
-    for (int t = 0; t < WK / 8; ++t) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float p0 = ex2(z[t][e] - r0), p1 = ex2(z[t][2 + e] - r1);
-        l0 += p0;
-        l1 += p1;
-        if constexpr (kQuant) {
-          const float f = vsc[kw + 8 * t + 2 * q + e] * vinv;
-          p0 = p0 == 0.f ? 0.f : p0 * f;  // (a masked position's scale may be anything)
-          p1 = p1 == 0.f ? 0.f : p1 * f;
+    for (int t = 0; t < KS / 8; ++t) {
+      const float p0 = ex2(z[t][0] - ref0), p1 = ex2(z[t][1] - ref0), p2 = ex2(z[t][2] - ref1), p3 = ex2(z[t][3] - ref1);
+      l0 += p0 + p1;
+      l1 += p2 + p3;
+      z[t][0] = p0, z[t][1] = p1, z[t][2] = p2, z[t][3] = p3;
+      if constexpr (kQuant) {
+        float2 f = *reinterpret_cast<const float2*>(vsc + kw + 8 * t + 2 * q);
+        f.x *= vinv;
+        f.y *= vinv;
+        z[t][0] *= f.x, z[t][1] *= f.y;
+        z[t][2] *= f.x, z[t][3] *= f.y;
+        if (masked) {  // (a masked position's scale may be anything)
+          if (p0 == 0.f) z[t][0] = 0.f;
+          if (p1 == 0.f) z[t][1] = 0.f;
+          if (p2 == 0.f) z[t][2] = 0.f;
+          if (p3 == 0.f) z[t][3] = 0.f;
         }
-        z[t][e] = p0;
-        z[t][2 + e] = p1;
       }
     }
     // 16-bit values may be infinities or NaN at positions that only some rows see: there the
@@ -412,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       if (masked && mixed_rows) {
         bool bad_v = false;
         constexpr uint32_t ex = kBF ? 0x7F80u : 0x7C00u;
-        for (int i = lane; i < WK * G::kChunks; i += 32) {
+        for (int i = lane; i < KS * G::kChunks; i += 32) {
           const uint4 w = lds16(vs + kw * G::kRowBytes + i * 16);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -424,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     if (poison) {
       if constexpr (!kQuant) {
 #pragma unroll
-        for (int t = 0; t < WK / 8; ++t) {
+        for (int t = 0; t < KS / 8; ++t) {
           for (int qq = 0; qq < 4; ++qq) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -451,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     {
 #pragma unroll
-      for (int kk = 0; kk < WK / 16; ++kk) {
+      for (int kk = 0; kk < KS / 16; ++kk) {
         const uint32_t pf[4] = {pack2<kBF>(z[2 * kk][0], z[2 * kk][1]), pack2<kBF>(z[2 * kk][2], z[2 * kk][3]),
                                 pack2<kBF>(z[2 * kk + 1][0], z[2 * kk + 1][1]),
                                 pack2<kBF>(z[2 * kk + 1][2], z[2 * kk + 1][3])};
@@ -494,10 +521,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
     }
+    }  // keys of the warp
 
-    put(j + S);
+    sl_next = sl_next == S ? 0 : sl_next + 1;
+    put(sl_next);
     soff_next = my_soff;
     sval_next = my_off >= 0;
+    sl_now = sl_now == S ? 0 : sl_now + 1;
+    st_now = st_now == S - 1 ? 0 : st_now + 1;
+    st_next = st_next == S - 1 ? 0 : st_next + 1;
 
     // ---- end of the unit or of the run: join the key groups, write
     const bool last = j == n_tiles - 1;
@@ -686,6 +718,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
 template <int D, int FMT, int MT, bool QBF>
 cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   using G = Geo<D, FMT, MT>;
+  a.s.bn = G::kBN;
   static std::atomic<unsigned long long> done{0};
   const int smem = G::kFixed + (a.rq.n_req + 1 + 8) * 8;
   cudaError_t e = set_smem_once(paged_attn_kernel<D, FMT, MT, QBF>, G::kFixed + (1024 + 16) * 8, done);
@@ -693,7 +726,7 @@ cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   const int per_sm = kPagedMaxCtasPerSm;
   // no more CTAs than tiles there can be
   const long long rt = (static_cast<long long>(a.rq.max_new) * a.s.group + G::kRows - 1) / G::kRows;
-  const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + kBN - 1) / kBN + 1);
+  const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + G::kBN - 1) / G::kBN + 1);
   a.ctas = static_cast<int>(most < static_cast<long long>(num_sms) * per_sm ? most : num_sms * per_sm);
   paged_attn_kernel<D, FMT, MT, QBF><<<a.ctas, kThreads, smem, st>>>(a);
   return cudaGetLastError();
@@ -702,7 +735,6 @@ cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
 template <int D, int FMT, bool QBF>
 cudaError_t launch_fmt(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   a.s.rows = paged_rows(a.rq.max_new, a.s.group);
-  a.s.bn = kBN;
   if (a.s.rows == 16) return launch_rows<D, FMT, 1, QBF>(a, num_sms, st);
   if (a.s.rows == 32) return launch_rows<D, FMT, 2, QBF>(a, num_sms, st);
   return launch_rows<D, FMT, 4, QBF>(a, num_sms, st);

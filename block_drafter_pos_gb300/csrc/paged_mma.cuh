@@ -57,8 +57,10 @@ DF2_DEV uint32_t codes2(uint32_t w) {
   if constexpr (FMT == kKvInt8) {
     return codes_to_half2(w ^ 0x80808080u, HI ? 0x4342u : 0x4140u);
   } else {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+    uint32_t h;
+    if constexpr (HI) asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %1;\n cvt.rn.f16x2.e4m3x2 %0, y;\n}\n" : "=r"(h) : "r"(w));
+    else asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %1;\n cvt.rn.f16x2.e4m3x2 %0, x;\n}\n" : "=r"(h) : "r"(w));
+    return h;
   }
 }
 
