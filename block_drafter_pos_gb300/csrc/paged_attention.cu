@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, q = lane & 3;
   const int rg = wid % MT, kg = wid / MT;
 
+  pdl_trigger();
   const long long T = paged_scan<kThreads>(a, pre, tmp);
   // (no empty runs: a cut unit's CTAs are then consecutive)
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
@@ -666,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 // in CTA order.
 template <int D, bool QBF>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+  pdl_wait();  // (launched while the attention still runs)
   const int* dd = a.desc + 4 * blockIdx.x;
   const int r = dd[0];
   if (r < 0) return;
@@ -760,14 +762,11 @@ cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int 
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.ctas, a.s.rows / 16);
-  if (head_dim == 64) {
-    if (qtype == kTBf16) paged_combine_kernel<64, true><<<grid, 128, 0, st>>>(a);
-    else paged_combine_kernel<64, false><<<grid, 128, 0, st>>>(a);
-  } else {
-    if (qtype == kTBf16) paged_combine_kernel<128, true><<<grid, 128, 0, st>>>(a);
-    else paged_combine_kernel<128, false><<<grid, 128, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  if (head_dim == 64)
+    return qtype == kTBf16 ? launch_ex(paged_combine_kernel<64, true>, grid, dim3(128), 0, st, true, a)
+                           : launch_ex(paged_combine_kernel<64, false>, grid, dim3(128), 0, st, true, a);
+  return qtype == kTBf16 ? launch_ex(paged_combine_kernel<128, true>, grid, dim3(128), 0, st, true, a)
+                         : launch_ex(paged_combine_kernel<128, false>, grid, dim3(128), 0, st, true, a);
 }
 
 }  // namespace df2

@@ -4,13 +4,12 @@
 // x / s rounded to nearest even and saturated, value = code * s.  Both divisions are IEEE
 // (so a code never depends on how a reciprocal rounds), and |x / s| <= Q up to one rounding.
 //
-// Both directions are streams over rows of one (token, KV head): 8 channels per lane, the
-// keys' and the values' loads issued together, amax by shuffles within the row's lanes, so
-// each source element is read once and each code written once.
-#include <cuda_fp8.h>
-
+// Both directions are streams: a warp per token, 8 channels per lane and load, the keys' and
+// the values' loads issued together, amax by shuffles within the row's lanes, so each source
+// element is read once and each code written once.
 #include "common.cuh"
 #include "paged.h"
+#include "paged_mma.cuh"
 
 namespace df2 {
 namespace {
@@ -87,131 +86,194 @@ DF2_DEV void store8(char* p, long long off, const float (&x)[8]) {
   }
 }
 
-// Codes of 8 channels; `ok` is false where the row holds an infinity or a NaN (zero codes).
-template <int FMT>
-DF2_DEV uint2 codes8(const float (&x)[8], float scale, bool ok) {
-  uint32_t w[2] = {0u, 0u};
+// |x| of 8 values as bits, the largest: ordered as the values are, infinity above every number and NaN above
+// infinity, so a nonfinite element always wins.
+template <int T>
+DF2_DEV uint32_t largest8(const float (&x)[8]) {
+  if constexpr (T == kTBf16) {  // two to a word, as they came
+    uint32_t m2 = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = ok ? __fdiv_rn(x[i], scale) : 0.f;
-    uint32_t b;
-    if constexpr (FMT == kKvInt8) {
-      int c = __float2int_rn(y);
-      c = c > 127 ? 127 : (c < -127 ? -127 : c);
-      b = static_cast<uint32_t>(c) & 0xFFu;
-    } else {
-      b = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632) & 0x7FFF7FFFu;
+      asm("max.u16x2 %0, %0, %1;" : "+r"(m2) : "r"(w));
     }
-    w[i >> 2] |= b << (8 * (i & 3));
+    return max(m2 << 16, m2 & 0xFFFF0000u);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// Codes of 8 channels: x / s, IEEE-rounded, then rounded to nearest even and saturated.  x (1 / s) (1 +- 2^-21) bound that
+// quotient from both sides, and rounding to a code is monotonic: where both give one code it is the quotient's, and
+// only where they differ (a few in 100,000) is the division done.  (16 divisions a thread made the kernel issue-bound.)
+template <int FMT>
+DF2_DEV uint2 codes8(const float (&x)[8], float s) {
+  float inv;  // within 2^-23; s is at least 2^-126
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float up = inv * 1.000000476837158f, down = inv * 0.999999523162842f;
+  uint32_t w[2] = {0u, 0u}, differ = 0u;
+  if constexpr (FMT == kKvInt8) {
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded integer
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = __float_as_uint(fmaf(x[i], up, kMagic));
+      differ |= c[i] ^ __float_as_uint(fmaf(x[i], down, kMagic));
+    }
+    if (differ) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(__fdiv_rn(x[i], s) + kMagic);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+  } else {
+    auto pair = [](float lo, float hi) {
+      uint16_t c;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+      return static_cast<uint32_t>(c);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = pair(x[2 * i] * up, x[2 * i + 1] * up);
+      differ |= c ^ pair(x[2 * i] * down, x[2 * i + 1] * down);
+      w[i >> 1] |= c << (16 * (i & 1));
+    }
+    if (differ) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[i] = pair(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s)) | (pair(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s)) << 16);
+    }
   }
   return make_uint2(w[0], w[1]);
 }
 
-// One row (token, KV head) per D / 8 lanes.
+// A warp moves one token: its position is found once, and lane l takes pieces l, l + 32, ... of 8 channels of its
+// heads' rows (a row's D / 8 lanes are neighbours), two at a time so that four loads are in flight.
 template <int D, int FMT, int T>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ PagedMoveArgs a) {
-  constexpr int kLanes = D / 8;
-  const long long item = static_cast<long long>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int ch = (threadIdx.x % kLanes) * 8;
-  const bool in = item < static_cast<long long>(a.rq.n_tokens) * a.c.n_kv;
-  const int t = in ? static_cast<int>(item / a.c.n_kv) : 0, h = in ? static_cast<int>(item % a.c.n_kv) : 0;
-  float kx[8], vx[8];
-  if (in) {
-    load8<T>(a.k.p, t * a.k.token_stride + h * a.k.head_stride + ch, kx);
-    load8<T>(a.v.p, t * a.v.token_stride + h * a.v.head_stride + ch, vx);
-  }
+  constexpr int kLanes = D / 8;  // of a row
+  const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= a.rq.n_tokens) return;
+  const char* const pk = a.k.p + t * a.k.token_stride * (T == kTF32 ? 4 : 2);
+  const char* const pv = a.v.p + t * a.v.token_stride * (T == kTF32 ? 4 : 2);
+  const int pieces = a.c.n_kv * kLanes;
   int r, pos;
-  long long off = 0, soff = 0;
-  const bool go = in && find_position(a.rq, t, r, pos) && find_row(a.c, a.rq, r, pos, h, off, soff);
-  // a row's lanes decide alike, so the shuffles of the rows that stay need only their own lanes;
-  // idle rows take part with zeros to keep the warp together
-  if (!go) {
+  long long off, soff;
+  const bool go = find_position(a.rq, t, r, pos) && find_row(a.c, a.rq, r, pos, 0, off, soff);
+  if (!go) return;  // (the whole warp)
+  for (int p0 = 0; p0 < pieces; p0 += 64) {
+    float x[2][2][8];
+    int h[2];
+    const int ch = (lane % kLanes) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) kx[i] = vx[i] = 0.f;
-  }
-  if constexpr (FMT == kKvBf16 || FMT == kKvF16) {
-    if (!go) return;
-    store8<FMT == kKvBf16 ? kTBf16 : kTF16>(a.c.k, off + ch, kx);
-    store8<FMT == kKvBf16 ? kTBf16 : kTF16>(a.c.v, off + ch, vx);
-  } else {
-    uint32_t mk = 0, mv = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // |x| as bits: ordered as the values are, infinity above every number and NaN above
-      // infinity, so a nonfinite element always wins
-      mk = max(mk, __float_as_uint(kx[i]) & 0x7FFFFFFFu);
-      mv = max(mv, __float_as_uint(vx[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 2; ++i) {
+      const int p = p0 + 32 * i + lane;
+      h[i] = p < pieces ? p / kLanes : 0;  // (idle lanes redo head 0 and store nothing)
+      load8<T>(pk, h[i] * a.k.head_stride + ch, x[i][0]);
+      load8<T>(pv, h[i] * a.v.head_stride + ch, x[i][1]);
     }
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-      mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-      mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-    }
-    if (!go) return;
-    const bool okk = mk < 0x7F800000u, okv = mv < 0x7F800000u;
-    constexpr float kQ = FMT == kKvInt8 ? 127.f : 448.f;
-    float sk = __fdiv_rn(__uint_as_float(mk), kQ), sv = __fdiv_rn(__uint_as_float(mv), kQ);
-    if (okk) sk = fmaxf(sk, 1.17549435e-38f);  // 2^-126
-    if (okv) sv = fmaxf(sv, 1.17549435e-38f);
-    *reinterpret_cast<uint2*>(a.c.k + off + ch) = codes8<FMT>(kx, sk, okk);
-    *reinterpret_cast<uint2*>(a.c.v + off + ch) = codes8<FMT>(vx, sv, okv);
-    if (ch == 0) {
-      a.c.k_scale[soff] = sk;
-      a.c.v_scale[soff] = sv;
+    for (int i = 0; i < 2; ++i) {
+      const bool in = p0 + 32 * i + lane < pieces;
+      const long long o = off + h[i] * a.c.head_stride + ch, so = soff + h[i] * a.c.s_head_stride;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        char* const pool = side ? a.c.v : a.c.k;
+        if constexpr (FMT == kKvBf16 || FMT == kKvF16) {
+          if (in) store8<FMT == kKvBf16 ? kTBf16 : kTF16>(pool, o, x[i][side]);
+        } else {
+          uint32_t m = largest8<T>(x[i][side]);
+#pragma unroll
+          for (int of = kLanes / 2; of > 0; of >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, of));
+          const bool fine = m < 0x7F800000u;
+          float s = __fdiv_rn(__uint_as_float(m), FMT == kKvInt8 ? 127.f : 448.f);
+          if (fine) s = fmaxf(s, 1.17549435e-38f);  // 2^-126
+          uint2 w = codes8<FMT>(x[i][side], s);
+          if (!fine) w = make_uint2(0u, 0u);
+          if (in) {
+            *reinterpret_cast<uint2*>(pool + o) = w;
+            if (ch == 0) (side ? a.c.v_scale : a.c.k_scale)[so] = s;
+          }
+        }
+      }
     }
   }
 }
 
 template <int FMT>
-DF2_DEV void read8(const char* pool, const float* scales, long long off, long long soff, int ch, float (&x)[8]) {
-  if constexpr (FMT == kKvBf16 || FMT == kKvF16) {
-    load8<FMT == kKvBf16 ? kTBf16 : kTF16>(pool, off + ch, x);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(pool + off + ch);
-    const float s = scales[soff];
-    const uint32_t ww[2] = {w.x, w.y};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = (ww[i >> 2] >> (8 * (i & 3))) & 0xFFu;
-      float c;
-      if constexpr (FMT == kKvInt8) {
-        c = static_cast<float>(static_cast<int8_t>(b));
-      } else {
-        const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3);
-        c = __half2float(*reinterpret_cast<const __half*>(&hr));
-      }
-      x[i] = c * s;
+struct Raw8 {  // 8 channels as the pool holds them
+  uint4 w;
+  float s;
+  DF2_DEV void load(const char* pool, const float* scales, long long off, long long soff) {
+    if constexpr (FMT == kKvBf16 || FMT == kKvF16) {
+      w = *reinterpret_cast<const uint4*>(pool + off * 2);
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(pool + off);
+      w.x = v.x, w.y = v.y;
+      s = scales[soff];
     }
   }
-}
+  DF2_DEV void values(float (&x)[8]) const {
+    if constexpr (FMT == kKvBf16 || FMT == kKvF16) {
+      const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 c = unpack2<FMT == kKvBf16>(p[i]);
+        x[2 * i] = c.x, x[2 * i + 1] = c.y;
+      }
+    } else {
+      const uint32_t p[4] = {codes2<FMT, 0>(w.x), codes2<FMT, 1>(w.x), codes2<FMT, 0>(w.y), codes2<FMT, 1>(w.y)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 c = unpack2<false>(p[i]);  // (exact)
+        x[2 * i] = c.x * s, x[2 * i + 1] = c.y * s;
+      }
+    }
+  }
+};
 
 template <int D, int FMT, int T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ PagedMoveArgs a) {
   constexpr int kLanes = D / 8;
-  const long long item = static_cast<long long>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int ch = (threadIdx.x % kLanes) * 8;
-  if (item >= static_cast<long long>(a.rq.n_tokens) * a.c.n_kv) return;
-  const int t = static_cast<int>(item / a.c.n_kv), h = static_cast<int>(item % a.c.n_kv);
+  const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= a.rq.n_tokens) return;
   int r, pos;
   if (!find_position(a.rq, t, r, pos)) return;
-  long long off, soff;
-  float kx[8], vx[8];
-  if (find_row(a.c, a.rq, r, pos, h, off, soff)) {
-    read8<FMT>(a.c.k, a.c.k_scale, off, soff, ch, kx);
-    read8<FMT>(a.c.v, a.c.v_scale, off, soff, ch, vx);
-  } else {
+  long long off = 0, soff = 0;
+  const bool good = find_row(a.c, a.rq, r, pos, 0, off, soff);
+  char* const pk = a.k.p + t * a.k.token_stride * (T == kTF32 ? 4 : 2);
+  char* const pv = a.v.p + t * a.v.token_stride * (T == kTF32 ? 4 : 2);
+  const int pieces = a.c.n_kv * kLanes, ch = (lane % kLanes) * 8;
+  for (int p0 = lane; p0 < pieces; p0 += 128) {
+    Raw8<FMT> k[4], v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) kx[i] = vx[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int h = (p0 + 32 * i) / kLanes;
+      if (good && p0 + 32 * i < pieces) {
+        k[i].load(a.c.k, a.c.k_scale, off + h * a.c.head_stride + ch, soff + h * a.c.s_head_stride);
+        v[i].load(a.c.v, a.c.v_scale, off + h * a.c.head_stride + ch, soff + h * a.c.s_head_stride);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = (p0 + 32 * i) / kLanes;
+      if (p0 + 32 * i >= pieces) break;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (good) k[i].values(x);
+      store8<T>(pk, h * a.k.head_stride + ch, x);
+      if (good) v[i].values(x);
+      store8<T>(pv, h * a.v.head_stride + ch, x);
+    }
   }
-  store8<T>(a.k.p, t * a.k.token_stride + h * a.k.head_stride + ch, kx);
-  store8<T>(a.v.p, t * a.v.token_stride + h * a.v.head_stride + ch, vx);
 }
 
 template <int D, int FMT>
 cudaError_t launch_move(const PagedMoveArgs& a, bool write, cudaStream_t st) {
-  const long long items = static_cast<long long>(a.rq.n_tokens) * a.c.n_kv;
-  const int per = kThreads / (D / 8);
-  const dim3 grid(static_cast<unsigned>((items + per - 1) / per));
+  constexpr int kTokens = kThreads / 32;  // of a block
+  const dim3 grid((a.rq.n_tokens + kTokens - 1) / kTokens);
   switch (a.k.type * 2 + (write ? 1 : 0)) {
     case kTBf16 * 2 + 1: write_kernel<D, FMT, kTBf16><<<grid, kThreads, 0, st>>>(a); break;
     case kTF16 * 2 + 1: write_kernel<D, FMT, kTF16><<<grid, kThreads, 0, st>>>(a); break;

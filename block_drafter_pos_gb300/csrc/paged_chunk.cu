@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  pdl_trigger();
   const long long T = paged_scan<kThreads>(a, pre, tmp);
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
   if (tid == 0) a.desc[4 * c] = -1;
