@@ -342,16 +342,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         float s[128];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tm_ld32(s_col + 32 * x, s + 32 * x);
-        // the tile's information: flags (bit 0: some page is bad, bit 1: some value factor is not finite), reference
+        // the tile's information: whether some page is bad, the values' reference
         const int2 fl = *reinterpret_cast<const int2*>(badw + 4);
         tm_wait_ld();
         if constexpr (kQuant) {
+          float4 w[4], v[4];  // 16 keys' scales, and the next 16
 #pragma unroll
-          for (int x = 0; x < 128; x += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(ks + x);
-            const float2 y0 = mul2(make_float2(s[x], s[x + 1]), make_float2(f.x, f.y));
-            const float2 y1 = mul2(make_float2(s[x + 2], s[x + 3]), make_float2(f.z, f.w));
-            s[x] = y0.x, s[x + 1] = y0.y, s[x + 2] = y1.x, s[x + 3] = y1.y;
+          for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const float4*>(ks + 4 * y);
+#pragma unroll
+          for (int x = 0; x < 128; x += 16) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (x + 16 < 128) v[y] = *reinterpret_cast<const float4*>(ks + x + 16 + 4 * y);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int e = x + 4 * y;
+              const float2 y0 = mul2(make_float2(s[e], s[e + 1]), make_float2(w[y].x, w[y].y));
+              const float2 y1 = mul2(make_float2(s[e + 2], s[e + 3]), make_float2(w[y].z, w[y].w));
+              s[e] = y0.x, s[e + 1] = y0.y, s[e + 2] = y1.x, s[e + 3] = y1.y;
+              w[y] = v[y];
+            }
           }
         }
         const bool masked = um.masked(key0) || (fl.x & 1);
@@ -418,32 +428,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         const float mr = m == -INFINITY ? 0.f : -m;
         float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
         const float2 sc2 = make_float2(sc, sc), mr2 = make_float2(mr, mr);
-        const bool careful = kQuant && masked && (fl.x & 2);  // a masked position's factor may be anything
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t p[32];
+          float4 w[4], v[4];  // 16 keys' value factors, and the next 16
+          if constexpr (kQuant) {
 #pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            const int e = 64 * x + 2 * y;
-            float2 a0 = fma2(make_float2(s[e], s[e + 1]), sc2, mr2), a1 = fma2(make_float2(s[e + 2], s[e + 3]), sc2, mr2);
-            a0 = make_float2(ex2(a0.x), ex2(a0.y));
-            a1 = make_float2(ex2(a1.x), ex2(a1.y));
-            acc0 = add2(acc0, a0);
-            acc1 = add2(acc1, a1);
+            for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const float4*>(vf + 64 * x + 4 * y);
+          }
+#pragma unroll
+          for (int y0 = 0; y0 < 32; y0 += 8) {
             if constexpr (kQuant) {
-              const float4 w = *reinterpret_cast<const float4*>(vf + e);
-              const float2 b0 = mul2(a0, make_float2(w.x, w.y)), b1 = mul2(a1, make_float2(w.z, w.w));
-              p[y] = pack2<kBF>(b0.x, b0.y);
-              p[y + 1] = pack2<kBF>(b1.x, b1.y);
-              if (careful) {
-                if (a0.x == 0.f) p[y] &= 0xFFFF0000u;
-                if (a0.y == 0.f) p[y] &= 0x0000FFFFu;
-                if (a1.x == 0.f) p[y + 1] &= 0xFFFF0000u;
-                if (a1.y == 0.f) p[y + 1] &= 0x0000FFFFu;
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                if (y0 + 8 < 32) v[y] = *reinterpret_cast<const float4*>(vf + 64 * x + 2 * y0 + 16 + 4 * y);
+            }
+#pragma unroll
+            for (int y = y0; y < y0 + 8; y += 2) {
+              const int e = 64 * x + 2 * y;
+              float2 a0 = fma2(make_float2(s[e], s[e + 1]), sc2, mr2), a1 = fma2(make_float2(s[e + 2], s[e + 3]), sc2, mr2);
+              a0 = make_float2(ex2(a0.x), ex2(a0.y));
+              a1 = make_float2(ex2(a1.x), ex2(a1.y));
+              acc0 = add2(acc0, a0);
+              acc1 = add2(acc1, a1);
+              if constexpr (kQuant) {
+                const float4 f4 = w[(y - y0) / 2];
+                const float2 b0 = mul2(a0, make_float2(f4.x, f4.y)), b1 = mul2(a1, make_float2(f4.z, f4.w));
+                p[y] = pack2<kBF>(b0.x, b0.y);
+                p[y + 1] = pack2<kBF>(b1.x, b1.y);
+                w[(y - y0) / 2] = v[(y - y0) / 2];
+              } else {
+                p[y] = pack2<kBF>(a0.x, a0.y);
+                p[y + 1] = pack2<kBF>(a1.x, a1.y);
               }
-            } else {
-              p[y] = pack2<kBF>(a0.x, a0.y);
-              p[y + 1] = pack2<kBF>(a1.x, a1.y);
             }
           }
           tm_st32(s_col + 32 * x, p);
@@ -492,25 +509,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           const float out_f = kQuant ? (whole ? inv * vref : vref) : (whole ? inv : 1.f);
           char* const po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
           float* const pp = a.part + slot * (a.s.rows * (D + 2)) + lr * D;
-          const bool poison = !kQuant && poison_sh[gunit & 3] != 0;
+          const bool poison = poison_sh[gunit & 3] != 0;
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
             float o[32];
             __syncwarp();
             tm_ld32(o_col + 32 * x, o);
             tm_wait_ld();
-            if constexpr (!kQuant) {
-              if (poison && valid) {
-                // values that are not finite where only some rows see them: the product had zeros there
-                const int first_i = cc.unit_t >= t_begin ? 0 : static_cast<int>(t_begin - cc.unit_t);
-                for (int ti = first_i; ti <= i_last; ++ti) {
-                  const int k0 = (cc.u.t0 + ti) * kBN;
-                  if (!old_um.masked(k0)) continue;
-                  for (int key = max(k0, old_lo); key < min(k0 + kBN, old_hi); ++key) {
-                    if (a.s.causal == 2 && key >= old_um.base && !((old_word >> (key - old_um.base)) & 1ull)) continue;
-                    const int page = __ldg(a.c.table + cc.r * a.c.table_stride + key / a.c.page_size);
-                    long long off, so;
-                    if (!paged_row(a.c, page, key % a.c.page_size, cc.h, &off, &so)) continue;
+            if (poison && valid) {
+              // values that are not finite: the product had zeros there (16 bits: in tiles where rows differ;
+              // 8 bits: where the scale is not finite)
+              const int first_i = cc.unit_t >= t_begin ? 0 : static_cast<int>(t_begin - cc.unit_t);
+              for (int ti = first_i; ti <= i_last; ++ti) {
+                const int k0 = (cc.u.t0 + ti) * kBN;
+                if (!kQuant && !old_um.masked(k0)) continue;
+                for (int key = max(k0, old_lo); key < min(k0 + kBN, old_hi); ++key) {
+                  if (a.s.causal == 2 && key >= old_um.base && !((old_word >> (key - old_um.base)) & 1ull)) continue;
+                  const int page = __ldg(a.c.table + cc.r * a.c.table_stride + key / a.c.page_size);
+                  long long off, so;
+                  if (!paged_row(a.c, page, key % a.c.page_size, cc.h, &off, &so)) continue;
+                  if constexpr (kQuant) {
+                    const float vs = __ldg(a.c.v_scale + so);
+                    if (fabsf(vs) < INFINITY) continue;
+                    const uint32_t* v = reinterpret_cast<const uint32_t*>(a.c.v + off + 32 * x);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                      const uint32_t w = __ldg(v + y);
+                      const float2 v0 = unpack2<false>(codes2<FMT, 0>(w)), v1 = unpack2<false>(codes2<FMT, 1>(w));
+                      o[4 * y] += v0.x * vs, o[4 * y + 1] += v0.y * vs, o[4 * y + 2] += v1.x * vs, o[4 * y + 3] += v1.y * vs;
+                    }
+                  } else {
                     const uint32_t* v = reinterpret_cast<const uint32_t*>(a.c.v + (off + 32 * x) * 2);
 #pragma unroll
                     for (int y = 0; y < 16; ++y) {
@@ -734,11 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         o[lt] = off;
         const uint32_t b = __ballot_sync(0xffffffffu, badv);
-        // (NaN and infinity; a factor of 0 times either is not finite)
-        const uint32_t odd = __ballot_sync(0xffffffffu, kQuant && !(fabsf(vsv) < INFINITY));
         if (lane == 0) {
           badw[wid - 8] = b;
-          flag_sh[j & 1][wid - 8] = (b ? 1 : 0) | (odd ? 2 : 0);
+          flag_sh[j & 1][wid - 8] = b ? 1 : 0;
         }
         loaders_sync();
         if (lt == 0) badw[4] = flag_sh[j & 1][0] | flag_sh[j & 1][1] | flag_sh[j & 1][2] | flag_sh[j & 1][3];
@@ -750,7 +776,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             vinv = 1.f / vref;
           }
           ks[lt] = ksv;
-          ks[128 + lt] = vsv * vinv;
+          // (a scale that is not finite counts as 0 here; the rows that see it add the products at the end)
+          const bool finite = fabsf(vsv) < INFINITY;
+          ks[128 + lt] = finite ? vsv * vinv : 0.f;
+          if (!finite) poison_sh[unit & 3] = 1;
           if (lt == 0) ks[256 + 5] = vref;
         }
         mbar_arrive(info + 8 * ring);
