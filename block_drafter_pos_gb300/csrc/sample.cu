@@ -7,7 +7,8 @@
 // elements are the distinct 64-bit numbers (order-preserving key of the logit, ~id).  Two
 // ways find its last element:
 //  * The short one reads the row once.  Any CTA's k-th largest thread maximum is a lower
-//    bound of the row's k-th largest logit, and min_p bounds the logits outright; elements
+//    bound of the row's k-th largest logit (as is the least, over n CTAs, of their
+//    k/n-th largest), and min_p bounds the logits outright; elements
 //    above the bound known so far go to a list as the slice streams by (the bound is drawn
 //    tighter after 1, 2, 4, ... chunks), and the `kept` row is filled with its cut value in
 //    the same pass.  The first CTA sorts the few hundred candidates that pass the final
@@ -31,13 +32,14 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCtas = 16;
-constexpr int kSlice = 1 << 16;  // most elements of a CTA (its histogram adds 16-bit pieces in 32 bits)
-constexpr int kGroups = 4;       // groups of 4 consecutive elements a thread holds of a chunk
+constexpr int kSlice = (1 << 17) - 8;  // most elements of a CTA (its histogram adds 15-bit pieces in 32 bits)
+constexpr int kGroups = 2;       // groups of 4 consecutive elements a thread holds of a chunk
 constexpr int kChunk = kThreads * 4 * kGroups;
 constexpr int kList = 2048;      // candidates of a CTA
 constexpr int kSort = 2048;      // candidates of a row
 constexpr int kShortK = 384;     // largest top_k of the short way
 constexpr int kProbe = 64;       // thread maxima above the bound, per CTA, for top-p alone
+constexpr int kWaveCtas = 4;     // CTAs started for each SM (two at a time)
 constexpr float kCut = -1e30f;
 
 // round(2^31 2^(j / 32))
@@ -121,7 +123,7 @@ DF2_DEV uint32_t weight_step(float x, const Scale& s) {
 struct Shared {
   union {
     unsigned long long hist[kBins];   // the digits' histogram
-    uint32_t piece[3][kBins];         // the steps' histogram: 16-bit pieces of counts or weights
+    uint32_t piece[3][kBins];         // the steps' histogram: 15-bit pieces of counts or weights
     unsigned long long sort[kSort];
   };
   unsigned long long w[kSort];           // weights of the sorted candidates
@@ -132,7 +134,7 @@ struct Shared {
   unsigned long long total;
   unsigned long long before;             // weight or count above the digit found
   unsigned long long result;             // the last element that stays; 0: not found
-  uint32_t tau, count, digit, bad, n_sort, run_max;
+  uint32_t tau, share, count, digit, bad, n_sort, run_max;
   uint32_t pw[32];
 };
 
@@ -191,12 +193,13 @@ DF2_DEV void find_bin(Ctx& c, F reached, uint32_t& bin, unsigned long long& abov
   unsigned long long h[kPer], sum = 0, all;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) h[i] = 0;
+#pragma unroll 4
   for (int r = 0; r < c.ctas; ++r) {
     const Shared* o = c.cl.map_shared_rank(sh, r);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      h[i] += PIECES ? o->piece[0][b0 - i] + (static_cast<unsigned long long>(o->piece[1][b0 - i]) << 16) +
-                           (static_cast<unsigned long long>(o->piece[2][b0 - i]) << 32)
+      h[i] += PIECES ? o->piece[0][b0 - i] + (static_cast<unsigned long long>(o->piece[1][b0 - i]) << 15) +
+                           (static_cast<unsigned long long>(o->piece[2][b0 - i]) << 30)
                      : o->hist[b0 - i];
   }
 #pragma unroll
@@ -249,16 +252,18 @@ DF2_DEV void append(Shared* sh, bool in, unsigned long long v) {
 // or more than kSort if they do not fit.  Called by every thread of that CTA after a cluster barrier.
 DF2_DEV int gather_sorted(Ctx& c, unsigned long long least) {
   Shared* sh = c.sh;
+  static_assert(kMaxCtas <= kWarps, "a warp for each CTA's list");
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   if (threadIdx.x == 0) sh->n_sort = 0;
+  const uint32_t count = lane < c.ctas ? c.cl.map_shared_rank(sh, lane)->count : 0u;
+  const bool over = __any_sync(0xffffffffu, count > kList);
   __syncthreads();
-  bool over = false;
-  for (int r = 0; r < c.ctas; ++r) {
+  // warp w copies from CTAs w mod ctas: with fewer CTAs than warps, several share a list
+  const int shares = c.ctas < kWarps ? kWarps / c.ctas : 1;
+  if (!over && wid < c.ctas * shares) {
+    const int r = wid % c.ctas, cr = static_cast<int>(__shfl_sync(0xffffffffu, count, r));
     const Shared* o = c.cl.map_shared_rank(sh, r);
-    const int cr = static_cast<int>(o->count);
-    over |= cr > kList;
-    if (over) break;
-    for (int i0 = wid * 32; i0 < cr; i0 += kThreads) {
+    for (int i0 = (wid / c.ctas) * 32; i0 < cr; i0 += shares * 32) {
       const unsigned long long v = i0 + lane < cr ? o->list[i0 + lane] : 0ull;
       const bool in = i0 + lane < cr && v >= least;
       const uint32_t m = __ballot_sync(0xffffffffu, in);
@@ -321,30 +326,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   unsigned long long best = 0;
   bool bad = false;
   uint32_t tau = 0;
-  auto tighten = [&]() {  // to the want-th largest thread maximum so far, to 14 bits
+  auto nth = [&](int nth_largest) {  // a bound from below, to 14 bits, of the thread maxima's n-th largest so far
     const uint32_t mine = static_cast<uint32_t>(best >> 32);
     uint32_t t0 = 0;
 #pragma unroll 1
     for (int b = 31; b >= 18; --b) {
       const uint32_t t = t0 | (1u << b);
-      if (__syncthreads_count(mine >= t) >= want) t0 = t;
+      if (__syncthreads_count(mine >= t) >= nth_largest) t0 = t;
     }
-    tau = max(tau, t0);
+    return t0;
   };
+  auto tighten = [&]() { tau = max(tau, nth(want)); };
   const int chunks = (c.n + kChunk - 1) / kChunk;
+  float next[kGroups][4];
+  auto fetch = [&](int ck) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int i = ck * kChunk + threadIdx.x * 4 + g * kThreads * 4;
+      if (i + 3 < c.n) {
+        load4<T>(src, i, vec, next[g]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) next[g][e] = i + e < c.n ? load1<T>(src, i + e) : -INFINITY;
+      }
+    }
+  };
+  fetch(0);
   for (int ck = 0; ck < chunks; ++ck) {
     float x[kGroups][4];
     const int base = ck * kChunk + threadIdx.x * 4;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int i = base + g * kThreads * 4;
-      if (i + 3 < c.n) {
-        load4<T>(src, i, vec, x[g]);
-      } else {
+    for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[g][e] = i + e < c.n ? load1<T>(src, i + e) : -INFINITY;
-      }
-    }
+      for (int e = 0; e < 4; ++e) x[g][e] = next[g][e];
+    fetch(ck + 1);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int i = base + g * kThreads * 4;
@@ -393,7 +408,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   }
-  if (want && chunks > 0) tighten();
+  // at the end also the bound that all CTAs share: each has its part of top_k above its own bound, so the row has
+  // top_k above the least of them
+  uint32_t share = 0;
+  if (want && chunks > 0) {
+    tighten();
+    if (top_k && c.ctas > 1) share = nth((top_k + c.ctas - 1) / c.ctas);
+  }
   best = warp_max_u64(best);
   if (lane == 0) shm.warp_sum[wid] = best;
   if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&shm.bad, 1u);
@@ -402,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int i = 1; i < kWarps; ++i) best = shm.warp_sum[i] > best ? shm.warp_sum[i] : best;
     shm.best = best;
     shm.tau = tau;
+    shm.share = share;
   }
   c.cl.sync();
   uint32_t any_bad = 0;
@@ -411,10 +433,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     any_bad = o->bad;
     best = o->best;
     tau = o->tau;
+    share = o->share;
+  } else {
+    share = 0xFFFFFFFFu;
   }
   any_bad = __any_sync(0xffffffffu, any_bad != 0);
   best = warp_max_u64(best);
-  tau = __reduce_max_sync(0xffffffffu, tau);
+  tau = max(__reduce_max_sync(0xffffffffu, tau), __reduce_min_sync(0xffffffffu, share));
   Scale s;
   s.xmax = key_value(best);
   int status = 0;
@@ -457,22 +482,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&shm.piece[0][0])[i] = 0;
     __syncthreads();
     unsigned long long z = 0;
-    for (int i0 = threadIdx.x; i0 < c.n; i0 += 4 * kThreads) {
-      float x[4];
+    for (int i0 = threadIdx.x; i0 < c.n; i0 += 8 * kThreads) {
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = i0 + e * kThreads < c.n ? load1<T>(src, i0 + e * kThreads) : -INFINITY;
+      for (int e = 0; e < 8; ++e) x[e] = i0 + e * kThreads < c.n ? load1<T>(src, i0 + e * kThreads) : -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 8; ++e) {
         const int i = i0 + e * kThreads;
         if (i >= c.n || element(x[e], i) < least) continue;
         const unsigned long long w = by_weight ? weight(x[e], s, shm.pw) : 1ull;
         if (w == 0) continue;
         z += w;
         const int b = kBins - 1 - weight_step(x[e], s);
-        atomicAdd(&shm.piece[0][b], static_cast<uint32_t>(w) & 0xFFFFu);
-        if (w >> 16) {
-          atomicAdd(&shm.piece[1][b], static_cast<uint32_t>(w >> 16) & 0xFFFFu);
-          if (w >> 32) atomicAdd(&shm.piece[2][b], static_cast<uint32_t>(w >> 32));
+        atomicAdd(&shm.piece[0][b], static_cast<uint32_t>(w) & 0x7FFFu);
+        if (w >> 15) {
+          atomicAdd(&shm.piece[1][b], static_cast<uint32_t>(w >> 15) & 0x7FFFu);
+          if (w >> 30) atomicAdd(&shm.piece[2][b], static_cast<uint32_t>(w >> 30));
         }
       }
     }
@@ -600,11 +625,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     above = up;
     const uint32_t step = kBins - 1 - bin;
     // the bin's elements to the lists
-    for (int i0 = 0; i0 < c.n; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      const float x = i < c.n ? load1<T>(src, i) : 0.f;
-      const unsigned long long v = element(x, i);
-      append(&shm, i < c.n && v >= least && weight_step(x, s) == step, v);
+    for (int i0 = 0; i0 < c.n; i0 += 8 * kThreads) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + e * kThreads + threadIdx.x;
+        x[e] = i < c.n ? load1<T>(src, i) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + e * kThreads + threadIdx.x;
+        const unsigned long long v = element(x[e], i);
+        append(&shm, i < c.n && v >= least && weight_step(x[e], s) == step, v);
+      }
     }
     c.cl.sync();
     if (c.rank == 0) {
@@ -678,12 +711,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return stays ? w : 0ull;
   };
   unsigned long long mine = 0;
-  for (int i0 = c.wlo + lane; i0 < c.whi; i0 += 128) {
-    float x[4];
+  for (int i0 = c.wlo + lane; i0 < c.whi; i0 += 256) {
+    float x[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = i0 + 32 * e < c.whi ? load1<T>(src, i0 + 32 * e) : -INFINITY;
+    for (int e = 0; e < 8; ++e) x[e] = i0 + 32 * e < c.whi ? load1<T>(src, i0 + 32 * e) : -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       bool stays;
       mine += left(i0 + 32 * e, x[e], stays);
       if (kept && i0 + 32 * e < c.whi) kept[i0 + 32 * e] = stays ? x[e] : kCut;
@@ -697,30 +730,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (r < c.rank) before += t;
     total += t;
   }
-  for (int i = 0; i < wid; ++i) before += shm.warp_sum[i];
   const double goal = static_cast<double>(u) * static_cast<double>(total);
-  // the first id whose running weight exceeds the goal; u < 1, so there is one
-  if (static_cast<double>(before) <= goal && static_cast<double>(before + mine) > goal) {
-    for (int i0 = c.wlo; i0 < c.whi; i0 += 32) {
-      const int i = i0 + lane;
+  // the first id whose running weight exceeds the goal; u < 1, so there is one: the CTA that holds it, its warp's part of
+  // the slice, then that part again, spread over the CTA's threads
+  auto holds = [&](unsigned long long from, unsigned long long w) {
+    return static_cast<double>(from) <= goal && static_cast<double>(from + w) > goal;
+  };
+  if (holds(before, shm.total)) {
+    unsigned long long from = before;
+    for (int i = 0; i < wid; ++i) from += shm.warp_sum[i];
+    if (lane == 0 && holds(from, mine)) {
+      shm.digit = static_cast<uint32_t>(wid);
+      shm.before = from;
+    }
+    __syncthreads();
+    const int lo = min(c.n, static_cast<int>(shm.digit) * wper), hi = min(c.n, lo + wper);
+    const int each = (wper + kThreads - 1) / kThreads, i0 = lo + threadIdx.x * each;
+    unsigned long long part = 0, all;
+    for (int e = 0; e < each; ++e) {
       bool stays;
-      const unsigned long long w = i < c.whi ? left(i, load1<T>(src, i), stays) : 0ull;
-      unsigned long long x = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, static_cast<double>(before + x) > goal);
-      if (m) {
-        if (lane == __ffs(m) - 1) {
-          a.token[row] = c.lo + i;
+      if (i0 + e < hi) part += left(i0 + e, load1<T>(src, i0 + e), stays);
+    }
+    from = shm.before + block_scan(&shm, part, all);
+    if (holds(from, part)) {
+      for (int e = 0; e < each && i0 + e < hi; ++e) {
+        bool stays;
+        const unsigned long long w = left(i0 + e, load1<T>(src, i0 + e), stays);
+        if (holds(from, w)) {
+          a.token[row] = c.lo + i0 + e;
           if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
           if (a.status) a.status[row] = 0;
+          break;
         }
-        break;
+        from += w;
       }
-      before += __shfl_sync(0xffffffffu, x, 31);
     }
   }
   c.cl.sync();
@@ -751,11 +794,11 @@ cudaError_t launch(const SampleArgs& a, int ctas, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
-  // CTAs per row: slices of at most kSlice elements; more while the rows leave half of the two CTAs
-  // of each SM idle and a slice is more than one chunk
+  // CTAs per row: slices of at most kSlice elements; more while all the rows' CTAs (two to an SM) run at once and a
+  // slice is more than 8192 elements
   int ctas = 1;
   while ((a.vocab + ctas - 1) / ctas > kSlice - 8) ctas *= 2;
-  while (ctas < kMaxCtas && a.n_rows * ctas <= a.num_sms && a.vocab / ctas > kChunk) ctas *= 2;
+  while (ctas < kMaxCtas && a.n_rows * ctas * 2 <= kWaveCtas * a.num_sms && a.vocab / ctas > 8192) ctas *= 2;
   if (a.type == 0) return launch<0>(a, ctas, st);
   return a.type == 1 ? launch<1>(a, ctas, st) : launch<2>(a, ctas, st);
 }
