@@ -333,17 +333,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   unsigned long long best = 0;
   bool bad = false;
   uint32_t tau = 0;
-  auto nth = [&](int nth_largest) {  // a bound from below, to 14 bits, of the thread maxima's n-th largest so far
+  float best_x = -INFINITY;
+  auto nth = [&](int nth_largest, int low) {  // a bound from below, down to bit `low`, of the thread maxima's n-th largest so far
     const uint32_t mine = static_cast<uint32_t>(best >> 32);
     uint32_t t0 = 0;
 #pragma unroll 1
-    for (int b = 31; b >= 18; --b) {
+    for (int b = 31; b >= low; --b) {
       const uint32_t t = t0 | (1u << b);
       if (__syncthreads_count(mine >= t) >= nth_largest) t0 = t;
     }
     return t0;
   };
-  auto tighten = [&]() { tau = max(tau, nth(want)); };
+  auto tighten = [&](int low) { tau = max(tau, nth(want, low)); };
   const int chunks = (c.n + kChunk - 1) / kChunk;
   float next[kGroups][4];
   auto fetch = [&](int ck) {
@@ -370,15 +371,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int i = base + g * kThreads * 4;
-      float m = -INFINITY;
-      bool nan = false;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        nan |= !(x[g][e] < INFINITY);  // NaN or +infinity
-        m = fmaxf(m, x[g][e]);
-      }
-      bad |= nan;
-      if (i < c.n && (best == 0 || float_order(m) > static_cast<uint32_t>(best >> 32))) {
+      bad |= !(x[g][0] < INFINITY && x[g][1] < INFINITY && x[g][2] < INFINITY && x[g][3] < INFINITY);  // NaN or +infinity
+      const float m = fmaxf(fmaxf(x[g][0], x[g][1]), fmaxf(x[g][2], x[g][3]));
+      if (i < c.n && (best == 0 || m > best_x)) {
+        best_x = m;
 #pragma unroll
         for (int e = 3; e >= 0; --e)  // (the smallest id of equal ones)
           if (i + e < c.n && x[g][e] == m) best = element(m, i + e);
@@ -401,16 +397,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const float top = order_to_float(shm.run_max);
         if (top > -INFINITY && top < INFINITY) tau = max(tau, min_bound(top));
       }
-      if (want && (ck & (ck + 1)) == 0) tighten();  // after 1, 2, 4, ... chunks
+      if (want && (ck & (ck + 1)) == 0) tighten(20);  // after 1, 2, 4, ... chunks
+      const float tau_x = tau > 0x007FFFFFu ? order_to_float(tau) : -INFINITY;  // (every element from -infinity on)
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const int i = base + g * kThreads * 4;
-        uint32_t any = 0;
+        const float m = fmaxf(fmaxf(x[g][0], x[g][1]), fmaxf(x[g][2], x[g][3]));
+        if (m >= tau_x) {  // (a few in a hundred: no need to gather the warp's)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) any |= (i + e < c.n && float_order(x[g][e]) >= tau) ? 1u << e : 0u;
-        if (__any_sync(0xffffffffu, any != 0)) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) append(&shm, (any >> e) & 1u, element(x[g][e], i + e));
+          for (int e = 0; e < 4; ++e)
+            if (i + e < c.n && x[g][e] >= tau_x) {
+              const uint32_t at = atomicAdd(&shm.count, 1u);
+              if (at < kList) shm.list[at] = element(x[g][e], i + e);
+            }
         }
       }
     }
@@ -419,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // top_k above the least of them
   uint32_t share = 0;
   if (want && chunks > 0) {
-    tighten();
-    if (top_k && c.ctas > 1) share = nth((top_k + c.ctas - 1) / c.ctas);
+    tighten(18);
+    if (top_k && c.ctas > 1) share = nth((top_k + c.ctas - 1) / c.ctas, 18);
   }
   best = warp_max_u64(best);
   if (lane == 0) shm.warp_sum[wid] = best;
