@@ -4,16 +4,19 @@
 // out = softmax(scale q K^T) V in one pass over the keys: per row a running maximum m and
 // sum l in base 2, o <- o 2^(m - m') + sum 2^(z - m') v.
 //
-//  * A KV head's query rows (new tokens x group) share every key read: rows = 16, 32 or 64
-//    of the MMA's M per unit.
+//  * A KV head's query rows (new tokens x group) share every key read: one or two row
+//    tiles of 16 (the MMA's M) per unit.
 //  * The launch's key tiles are dealt to the CTAs in contiguous equal runs (paged.h), so
 //    ragged batches and single long requests fill the machine alike; a unit cut between
 //    CTAs leaves fp32 partials, joined by the combine kernel in CTA order (no atomics).
 //  * Tiles of 64 keys (128 of 8 bits) come by 16-byte cp.async, zero-filled past the visible range; the
 //    page table is read one tile ahead of the copies, so its latency is off the path, and
 //    a tile may cross any number of pages.
-//  * Four warps: rows / 16 row groups x key groups of the tile, each with its own running
-//    state, joined through shared memory when the unit (or the run) ends.
+//  * Four warps: one row tile x four key groups of the tile, or two x two, each with its own
+//    running state, joined through shared memory when the unit (or the run) ends.  (Both row
+//    tiles in one warp, so that a key's codes are converted once, was slower: 32 rows of 16
+//    requests over 8192 int8 positions 142 us against 109, the second tile's registers
+//    costing the third buffer.)
 //  * 16-bit caches feed mma.sync through ldmatrix.  8-bit codes are exact in fp16, so both
 //    products run on fp16 codes: the keys' scale multiplies the score, and the values'
 //    scale the weight, relative to the largest scale seen (so the fp16 weight cannot
@@ -73,9 +76,8 @@ struct Geo {
   static constexpr int kStage = 2 * kSide + kScales;
   static constexpr int kStages = 3;
   static constexpr int kRows = 16 * MT;
-  static constexpr int kKG = 4 / MT;                   // key groups
+  static constexpr int kKG = 4 / MT;                   // key groups (a warp: one row tile, one group)
   static constexpr int kWK = kBN / kKG;                // keys of a warp
-  static constexpr int kKS = kWK < 64 ? kWK : 64;      // keys of one update of the running state
   static constexpr int kNT = D / 8;                    // output column tiles
   static constexpr int kMergeCols = kNT / 4;           // column tiles joined at a time
   static constexpr int kMerge = (kKG - 1) * MT * kMergeCols * 4 * 32 * 4;
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   using G = Geo<D, FMT, MT>;
   constexpr bool kQuant = G::kQuant;
   constexpr bool kBF = kQuant ? false : QBF;  // operand type of both products
-  constexpr int S = G::kStages, KG = G::kKG, WK = G::kWK, NT = G::kNT, KS = G::kKS, kBN = G::kBN;
+  constexpr int S = G::kStages, KG = G::kKG, WK = G::kWK, NT = G::kNT, kBN = G::kBN;
   constexpr int kSteps = D / 16;
   extern __shared__ __align__(128) char sm[];
   const uint32_t ring = smem_addr(sm);
@@ -303,16 +305,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     const int* bad = badp + 4 * sl_now;
     const bool any_bad = (bad[0] | bad[1] | (kBN > 64 ? bad[2] | bad[3] : 0)) != 0;
     const bool masked = key0 < lo_max || key0 + kBN > hi_min || any_bad;
-#pragma unroll 1
-    for (int kw = kg * WK; kw < (kg + 1) * WK; kw += KS) {  // keys kw .. kw + KS - 1 of the tile
+    const int kw = kg * WK;  // keys kw .. kw + WK - 1 of the tile
 
     // ---- scores
-    float z[KS / 8][4];
+    float z[WK / 8][4];
 #pragma unroll
-    for (int t = 0; t < KS / 8; ++t) z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
+    for (int t = 0; t < WK / 8; ++t) z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
     if constexpr (!kQuant) {
 #pragma unroll
-      for (int t = 0; t < KS / 8; t += 2) {
+      for (int t = 0; t < WK / 8; t += 2) {
         const int row = kw + 8 * t + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < KS / 8; ++t) {
+      for (int t = 0; t < WK / 8; ++t) {
         const uint32_t row = ks + (kw + 8 * t + g) * G::kRowBytes;
 #pragma unroll
         for (int hh = 0; hh < kSteps / 4; ++hh) {
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     // ---- scale, mask, running reference
 #pragma unroll
-    for (int t = 0; t < KS / 8; ++t) {
+    for (int t = 0; t < WK / 8; ++t) {
       float2 f = make_float2(1.f, 1.f);
       if constexpr (kQuant) f = *reinterpret_cast<const float2*>(ksc + kw + 8 * t + 2 * q);
       z[t][0] *= sc0 * f.x, z[t][1] *= sc0 * f.y;
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     if (masked) {
 #pragma unroll
-      for (int t = 0; t < KS / 8; ++t)
+      for (int t = 0; t < WK / 8; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int kk = kw + 8 * t + 2 * q + e, key = key0 + kk;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < KS / 8; ++t) {
+    for (int t = 0; t < WK / 8; ++t) {
       x0 = fmaxf(x0, fmaxf(z[t][0], z[t][1]));
       x1 = fmaxf(x1, fmaxf(z[t][2], z[t][3]));
     }
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       // the values' reference: the largest finite scale of this warp's keys, raised when one exceeds 16 of it
       float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < KS; i += 32) {
+      for (int i = 0; i < WK; i += 32) {
         const float y = vsc[kw + i + lane];
         v = y < INFINITY ? fmaxf(v, y) : v;
       }
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     // ---- weights and the values' product
 #pragma unroll
-    for (int t = 0; t < KS / 8; ++t) {
+    for (int t = 0; t < WK / 8; ++t) {
       const float p0 = ex2(z[t][0] - ref0), p1 = ex2(z[t][1] - ref0), p2 = ex2(z[t][2] - ref1), p3 = ex2(z[t][3] - ref1);
       l0 += p0 + p1;
       l1 += p2 + p3;
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       if (masked && mixed_rows) {
         bool bad_v = false;
         constexpr uint32_t ex = kBF ? 0x7F80u : 0x7C00u;
-        for (int i = lane; i < KS * G::kChunks; i += 32) {
+        for (int i = lane; i < WK * G::kChunks; i += 32) {
           const uint4 w = lds16(vs + kw * G::kRowBytes + i * 16);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     if (poison) {
       if constexpr (!kQuant) {
 #pragma unroll
-        for (int t = 0; t < KS / 8; ++t) {
+        for (int t = 0; t < WK / 8; ++t) {
           for (int qq = 0; qq < 4; ++qq) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     {
 #pragma unroll
-      for (int kk = 0; kk < KS / 16; ++kk) {
+      for (int kk = 0; kk < WK / 16; ++kk) {
         const uint32_t pf[4] = {pack2<kBF>(z[2 * kk][0], z[2 * kk][1]), pack2<kBF>(z[2 * kk][2], z[2 * kk][3]),
                                 pack2<kBF>(z[2 * kk + 1][0], z[2 * kk + 1][1]),
                                 pack2<kBF>(z[2 * kk + 1][2], z[2 * kk + 1][3])};
@@ -522,7 +523,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
     }
-    }  // keys of the warp
 
     sl_next = sl_next == S ? 0 : sl_next + 1;
     put(sl_next);
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         l0 += __shfl_xor_sync(0xffffffffu, l0, of);
         l1 += __shfl_xor_sync(0xffffffffu, l1, of);
       }
-      if constexpr (KG > 1) {
+      {
         stat[wid * 32 + lane] = make_float4(m0, m1, l0, l1);
         __syncthreads();
         float y0 = m0, y1 = m1;
@@ -737,9 +737,7 @@ cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
 template <int D, int FMT, bool QBF>
 cudaError_t launch_fmt(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   a.s.rows = paged_rows(a.rq.max_new, a.s.group);
-  if (a.s.rows == 16) return launch_rows<D, FMT, 1, QBF>(a, num_sms, st);
-  if (a.s.rows == 32) return launch_rows<D, FMT, 2, QBF>(a, num_sms, st);
-  return launch_rows<D, FMT, 4, QBF>(a, num_sms, st);
+  return a.s.rows == 16 ? launch_rows<D, FMT, 1, QBF>(a, num_sms, st) : launch_rows<D, FMT, 2, QBF>(a, num_sms, st);
 }
 
 template <int D>
