@@ -10,7 +10,7 @@ Pin status: every function here is pinned by a `-m "not gpu"` test against
 closed forms, brute force, textbook special cases or the cuRAND library (see
 tests/test_oracle_*.py); no function is "parity unpinned".
 """
-from . import philox  # noqa: F401
+from . import philox, target  # noqa: F401
 from .dflash2 import (  # noqa: F401
     STATUS_OK, STATUS_INVAL, STATUS_NONFINITE, bf16_to_f64, round_to_bf16, matrix_f64,
     rmsnorm, rope_neox, rope_inv_freq, dyn_conv, block_attention, visible_context_range,

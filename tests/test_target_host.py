@@ -190,6 +190,15 @@ def test_schedule_and_bounds_against_brute_force(tmp_path):
     assert out.stdout.startswith("ok ") and int(out.stdout.split()[1]) > 10000
 
 
+def test_packed_bytes_are_the_structures():
+    r = b.Rows(1, 2, 3, 1, 0)
+    assert bytes(b.PagedCache(*range(1, 15))) == b._PACK_CACHE.pack(*range(1, 15))
+    assert bytes(r) == b._PACK_ROWS.pack(1, 2, 3, 1, 0)
+    assert bytes(b.PagedAttentionArgs(1, 2, 3, 4, 5, 6, 0.5, 0, 7, 8, r, r, 9, 10, 11)) == \
+        b._PACK_ATTN.pack(1, 2, 3, 4, 5, 6, 0.5, 0, 7, 8, 1, 2, 3, 1, 0, 1, 2, 3, 1, 0, 9, 10, 11)
+    assert bytes(b.SampleArgs(1, 2, 0, 0, *range(4, 16))) == b._PACK_SAMPLE.pack(1, 2, 0, 0, *range(4, 16))
+
+
 # ----------------------------------------------------------------------------- the oracle's pins
 
 def test_oracle_e4m3_rounding_against_the_type():
