@@ -52,10 +52,15 @@ struct ChunkGeo {
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffStage = kOffRing + kSlots * kTile;
   static constexpr int kStage = kQuant ? 128 * D : 0;      // codes of a tile
-  static constexpr int kOffInfo = kOffStage + 2 * kStage;
-  // tile information, a ring of 4: key scales, value factors, bad-page bits, value reference
+  static constexpr int kBufs = kQuant ? (D == 64 ? 4 : 2) : 0;
+  // operands copied ahead of the one that is announced (16 bits: two ahead was slower, 1.79 ms against 1.66 for a
+  // 4096-token chunk over 32768 keys: a full ring then holds back what has landed)
+  static constexpr int kLag = kQuant ? kBufs - 1 : 1;
+  static constexpr int kOffInfo = kOffStage + kBufs * kStage;
+  // tile information, a ring of 8: key scales, value factors, bad-page bits, value reference
+  static constexpr int kRing = 8;
   static constexpr int kInfo = 128 * 4 * 2 + 16 + 16;
-  static constexpr int kOffOffs = kOffInfo + 4 * kInfo;    // element offsets of a tile's keys, two tiles
+  static constexpr int kOffOffs = kOffInfo + kRing * kInfo;    // element offsets of a tile's keys, two tiles
   static constexpr int kOffPre = kOffOffs + 2 * 128 * 8;   // tiles before each request
   static constexpr int kFixed = kOffPre + 1024;            // + alignment
 };
@@ -206,9 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   constexpr bool kBF = kQuant ? false : QBF;
   constexpr int NS = G::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[NS * 2 + 4 + 10];
+  __shared__ __align__(8) uint64_t bars[NS * 2 + G::kRing + 10];
   __shared__ uint32_t tmem_sh;
-  __shared__ int poison_sh[4];
+  __shared__ int poison_sh[G::kRing];  // by unit
   __shared__ long long tmp[kThreads / 32 + 1];
   __shared__ float vmax_sh[2][4];
   __shared__ int flag_sh[2][4];
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* const sgen = smem_raw + (sbase - smem_u32(smem_raw));
-  const uint32_t full = smem_u32(bars), empty = full + 8 * NS, info = empty + 8 * NS, s_full = info + 8 * 4,
+  const uint32_t full = smem_u32(bars), empty = full + 8 * NS, info = empty + 8 * NS, s_full = info + 8 * G::kRing,
                  p_full = s_full + 16, q_full = p_full + 32, o_done = q_full + 16;
   long long* const pre = reinterpret_cast<long long*>(sgen + G::kOffPre);
   if (tid == 0) {
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       mbar_init_count(full + 8 * i, kLoaders);
       mbar_init_count(empty + 8 * i, 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < G::kRing; ++i) {
       mbar_init_count(info + 8 * i, kLoaders);
       poison_sh[i] = 0;
     }
@@ -327,13 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       for (int j = 0; active && j < piece; ++j) {
         // ---- scores of one key tile
         const int key0 = (cc.u.t0 + cc.i + j) * kBN;
-        const int ring = (gtile + j) & 3;
+        const int ring = (gtile + j) % G::kRing;
         const float* ks = reinterpret_cast<const float*>(sgen + G::kOffInfo + ring * G::kInfo);
         const float* vf = ks + 128;
         const uint32_t* badw = reinterpret_cast<const uint32_t*>(vf + 128);
         // (the scores' products follow the tile's information, whose barrier is then in this use's phase)
         ok = mbar_wait(s_full + 8 * t, static_cast<uint32_t>(n & 1)) &&
-             mbar_wait(info + 8 * ring, static_cast<uint32_t>(((gtile + j) >> 2) & 1));
+             mbar_wait(info + 8 * ring, static_cast<uint32_t>(((gtile + j) / G::kRing) & 1));
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           const float out_f = kQuant ? (whole ? inv * vref : vref) : (whole ? inv : 1.f);
           char* const po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
           float* const pp = a.part + slot * (a.s.rows * (D + 2)) + lr * D;
-          const bool poison = poison_sh[gunit & 3] != 0;
+          const bool poison = poison_sh[gunit % G::kRing] != 0;
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
             float o[32];
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       look_up();
       // A thread copies piece ch of rows r0, r0 + kStep, ...: the swizzle's row bits are its own constant.
       constexpr int kPieces = D * (kQuant ? 1 : 2) / 16, kStep = kLoaders / kPieces, kCount = 128 / kStep;
-      constexpr int kBatch = kCount < 8 ? kCount : 8;
+      constexpr int kBatch = kCount < 8 ? kCount : 8, BUFS = G::kBufs > 0 ? G::kBufs : 1;
       const int ch = lt % kPieces, r0 = lt / kPieces;
       // where piece ch of row r0 goes (16-bit: itself; codes: the first of its two pieces of fp16)
       const int piece = kQuant ? 2 * ch : ch;
@@ -721,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       auto convert = [&](int idx) {
         if (!freed(idx)) return false;
         if constexpr (kQuant) {
-          const uint32_t st = sbase + G::kOffStage + (idx & 1) * G::kStage + lt * 16;
+          const uint32_t st = sbase + G::kOffStage + (idx % BUFS) * G::kStage + lt * 16;
           const uint32_t dst = sbase + G::kOffRing + (idx % NS) * G::kTile;
 #pragma unroll
           for (int x0 = 0; x0 < kCount; x0 += 4) {
@@ -739,23 +744,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         landed(idx);
         return true;
       };
+      int said = 0;  // operands announced
       // (after a failed wait a loader goes through the motions, so that the loaders' barrier stays whole)
       for (int j = 0; j < total; ++j) {
         // ---- the tile's information
-        const int ring = j & 3;
+        const int ring = j % G::kRing;
         float* ks = reinterpret_cast<float*>(sgen + G::kOffInfo + ring * G::kInfo);
         uint32_t* badw = reinterpret_cast<uint32_t*>(ks + 256);
         long long* o = offs + (j & 1) * 128;
         if (piece_first) {
           if (j > 0) ++unit;
           vref = 0.f;
-          if (lt == 0) poison_sh[unit & 3] = 0;
+          if (lt == 0) poison_sh[unit % G::kRing] = 0;
         }
-        // (the ring's previous tile was four tiles ago; the scores of the tile two ago being done, its weights are)
-        if (j >= 2) {
-          const int idx = 2 * (j - 2);
-          ok = ok && mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((idx / NS) & 1));
-        }
+        // (The slot's previous tile was eight tiles ago: operands up to that of tile j - 5 have been read, or this
+        // thread could not be here, so the weights of tile j - 5 and everything of earlier units are done.)
         if constexpr (kQuant) {
           const float v = warp_max(vsv < INFINITY ? vsv : 0.f);
           if (lane == 0) vmax_sh[j & 1][wid - 8] = v;
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           // (a scale that is not finite counts as 0 here; the rows that see it add the products at the end)
           const bool finite = fabsf(vsv) < INFINITY;
           ks[128 + lt] = finite ? vsv * vinv : 0.f;
-          if (!finite) poison_sh[unit & 3] = 1;
+          if (!finite) poison_sh[unit % G::kRing] = 1;
           if (lt == 0) ks[256 + 5] = vref;
         }
         mbar_arrive(info + 8 * ring);
@@ -793,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           const char* pool = (side ? a.c.v : a.c.k) + ch * 16;
           uint32_t dst;
           if constexpr (kQuant) {
-            dst = sbase + G::kOffStage + (idx & 1) * G::kStage + lt * 16;
+            dst = sbase + G::kOffStage + (idx % BUFS) * G::kStage + lt * 16;
           } else {
             ok = freed(idx);
             if (!ok) break;
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
               found |= z.x != w.x || z.y != w.y || z.z != w.z || z.w != w.w;
               sts128(dst + x * kNext, z);
             }
-            if (found) poison_sh[unit_now & 3] = 1;
+            if (found) poison_sh[unit_now % G::kRing] = 1;
           } else {
 #pragma unroll
             for (int x0 = 0; x0 < kCount; x0 += kBatch) {
@@ -824,18 +827,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             }
           }
           cp_commit();
-          if (idx > 0) {
-            cp_wait<1>();
-            if constexpr (kQuant) ok = convert(idx - 1);
-            else landed(idx - 1);
+          if (said <= idx - G::kLag) {
+            cp_wait<G::kLag>();
+            if constexpr (kQuant) ok = convert(said++);
+            else landed(said++);
           }
         }
       }
       cp_wait<0>();
-      if (ok) {
-        const int idx = 2 * total - 1;
-        if constexpr (kQuant) ok = convert(idx);
-        else landed(idx);
+      while (ok && said < 2 * total) {
+        if constexpr (kQuant) ok = convert(said++);
+        else landed(said++);
       }
       if (!ok && lt == 0 && a.rq.status) a.rq.status[lc.r] = 3;
     }
