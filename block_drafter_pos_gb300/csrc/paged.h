@@ -116,7 +116,10 @@ struct PagedAttnArgs {
   float* lse;
   float scale_log2;  // score scale * log2(e)
   float* part;       // partial results: slots of rows * head_dim outputs, then rows * (max, sum)
-  int* desc;         // [CTAs][4]: the cut unit that begins in CTA c's run (request, KV head, row tile, last CTA), or -1
+  // [CTAs][8]: the cut unit that begins in CTA c's run (request, KV head, row tile, last CTA and first slot, first
+  // row of the request, its new tokens), or -1
+  int* desc;
+  unsigned* count;   // [CTAs] partials of that unit that have come (zero between calls)
   int ctas;
 };
 

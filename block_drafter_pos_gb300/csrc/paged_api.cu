@@ -12,9 +12,9 @@
 
 using namespace df2;
 
-static_assert(DFLASH2_KV_BF16 == kKvBf16 && DFLASH2_KV_F16 == kKvF16 && DFLASH2_KV_INT8 == kKvInt8 &&
-                  DFLASH2_KV_E4M3 == kKvE4m3 && DFLASH2_T_BF16 == kTBf16 && DFLASH2_T_F16 == kTF16 &&
-                  DFLASH2_T_F32 == kTF32,
+static_assert(int(DFLASH2_KV_BF16) == int(kKvBf16) && int(DFLASH2_KV_F16) == int(kKvF16) &&
+                  int(DFLASH2_KV_INT8) == int(kKvInt8) && int(DFLASH2_KV_E4M3) == int(kKvE4m3) &&
+                  int(DFLASH2_T_BF16) == int(kTBf16) && int(DFLASH2_T_F16) == int(kTF16) && int(DFLASH2_T_F32) == int(kTF32),
               "the header's enumerations");
 
 struct dflash2_paged_handle {
@@ -22,6 +22,7 @@ struct dflash2_paged_handle {
   int num_sms;
   float* part;
   int* desc;
+  unsigned* count;
 };
 
 namespace {
@@ -128,13 +129,20 @@ dflash2_status dflash2_paged_create(const dflash2_paged_config* cfg, dflash2_pag
   static_assert(kChunkRows >= 64 * kPagedMaxCtasPerSm, "the larger scratch serves both kernels");
   const size_t part = paged_part_floats(h->num_sms, c.head_dim) * 4;
   char* p = nullptr;
-  if (cudaMalloc(&p, part + ctas * 16) != cudaSuccess) {
+  if (cudaMalloc(&p, part + ctas * 36) != cudaSuccess) {
     cudaGetLastError();
+    delete h;
+    return DFLASH2_E_CUDA;
+  }
+  // (finished before the handle is used on any stream)
+  if (cudaMemset(p + part, 0, ctas * 36) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
+    cudaFree(p);
     delete h;
     return DFLASH2_E_CUDA;
   }
   h->part = reinterpret_cast<float*>(p);
   h->desc = reinterpret_cast<int*>(p + part);
+  h->count = reinterpret_cast<unsigned*>(p + part + ctas * 32);
   *out = h;
   return DFLASH2_OK;
 }
@@ -190,6 +198,7 @@ dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_pa
   a.scale_log2 = x.scale * 1.44269504f;
   a.part = h->part;
   a.desc = h->desc;
+  a.count = h->count;
   const cudaError_t e = launch_paged_attention(a, h->cfg.head_dim, h->cfg.kv_format, x.q.type, h->num_sms,
                                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DFLASH2_OK : DFLASH2_E_CUDA;

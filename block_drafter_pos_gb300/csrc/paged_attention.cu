@@ -8,7 +8,7 @@
 //    tiles of 16 (the MMA's M) per unit.
 //  * The launch's key tiles are dealt to the CTAs in contiguous equal runs (paged.h), so
 //    ragged batches and single long requests fill the machine alike; a unit cut between
-//    CTAs leaves fp32 partials, joined by the combine kernel in CTA order (no atomics).
+//    CTAs leaves fp32 partials, joined in CTA order (whoever joins them, the same bits).
 //  * Tiles of 64 keys (128 of 8 bits) come by 16-byte cp.async, zero-filled past the visible range; the
 //    page table is read one tile ahead of the copies, so its latency is off the path, and
 //    a tile may cross any number of pages.
@@ -86,6 +86,67 @@ struct Geo {
   static constexpr int kFixed = kStages * kStage + kMerge + kStat + kOff;
 };
 
+// One warp joins row lr of a cut unit (KV head h, row tile qt of the request with rows b0 .. b0 + n - 1 new tokens): the
+// partials of CTAs c0 .. c1 (c0's in its slot `first`) are added in CTA order, eight at a time (their loads
+// together: what this costs is latency).
+template <int D, bool QBF>
+DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int slot0, int b0, int n, int lr) {
+  const int R = a.s.rows, lane = threadIdx.x & 31, row = qt * R + lr;
+  if (row >= n * a.s.group) return;
+  const long long first = 2ll * c0 + slot0, stride = static_cast<long long>(R) * (D + 2);
+  constexpr int V = D / 32;  // channels per lane
+      float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = 0.f;
+      for (int c = c0; c <= c1; c += 8) {
+        float2 st[8];
+        float x[8][V];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          st[i] = make_float2(-INFINITY, 0.f);
+          if (c + i <= c1) {
+            const float* p = a.part + (c + i == c0 ? first : 2ll * (c + i)) * stride;
+            st[i] = __ldcg(reinterpret_cast<const float2*>(p + R * D + 2 * lr));
+            if constexpr (V == 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p + lr * D + 4 * lane));
+              x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+            } else {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(p + lr * D + 2 * lane));
+              x[i][0] = v.x, x[i][1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[i][e] = 0.f;
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, st[i].x);
+        const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(m - ref);
+        m = top;
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] *= f0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = ex2(st[i].x - ref);
+          l += st[i].y * f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] += x[i][e] * f;
+        }
+      }
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      const int i = row / a.s.group, head = h * a.s.group + row % a.s.group;
+      char* po = a.out.p + ((b0 + i) * a.out.token_stride + head * a.out.head_stride + V * lane) * 2;
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(po) = make_uint2(pack2<QBF>(o[0] * inv, o[1] * inv), pack2<QBF>(o[2] * inv, o[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(po) = pack2<QBF>(o[0] * inv, o[1] * inv);
+      if (a.lse && lane == 0)
+        a.lse[static_cast<long long>(b0 + i) * (a.c.n_kv * a.s.group) + head] =
+        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+}
+
 template <int D, int FMT, int MT, bool QBF>
 __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
   using G = Geo<D, FMT, MT>;
@@ -100,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   long long* const offs = reinterpret_cast<long long*>(sm + S * G::kStage + G::kMerge + G::kStat);  // [S + 1][kBN]
   int* const badp = reinterpret_cast<int*>(offs + (S + 1) * kBN);                                    // [S + 1][4]
   long long* const tmp = reinterpret_cast<long long*>(badp + (S + 1) * 4);
+  unsigned* const last_sh = reinterpret_cast<unsigned*>(tmp + 7);
   long long* const pre = tmp + 8;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, q = lane & 3;
   const int rg = wid % MT, kg = wid / MT;
@@ -108,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   const long long T = paged_scan<kThreads>(a, pre, tmp);
   // (no empty runs: a cut unit's CTAs are then consecutive)
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
-  if (tid == 0) a.desc[4 * c] = -1;
+  if (MT > 1 && tid == 0) a.desc[8 * c] = -1;
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
 
@@ -600,13 +662,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         const int rows = cc.n * a.s.group;
         const bool whole = cc.unit_t >= t_begin && cc.unit_ends();
         const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
-        if (!whole && tid == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
+        if (MT > 1 && !whole && tid == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
           const long long tl = cc.unit_t + cc.u.nt;
           long long cb = (tl * C - 1) / T;  // the CTA of the unit's last tile
-          int* dd = a.desc + 4 * c;
+          int* dd = a.desc + 8 * c;
           dd[1] = cc.h;
           dd[2] = cc.qt;
           dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
+          dd[4] = cc.b0;
+          dd[5] = cc.n;
           dd[0] = cc.r;
         }
 #pragma unroll
@@ -657,64 +721,39 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           }
         }
       }
+      if constexpr (MT == 1) {
+        // one row tile: the CTA that brings a cut unit's last partial joins them (up to four rows a warp), which saves a
+        // launch; the counter wraps to zero by itself
+        if (cc.unit_t < t_begin || !cc.unit_ends()) {
+          const int c0 = cc.unit_t >= t_begin ? static_cast<int>(c) : static_cast<int>(((cc.unit_t + 1) * C - 1) / T);
+          const int c1 = static_cast<int>(((cc.unit_t + cc.u.nt) * C - 1) / T);
+          __threadfence();  // this thread's partials before the count
+          __syncthreads();
+          if (tid == 0) *last_sh = atomicInc(a.count + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
+          __syncthreads();
+          if (*last_sh) {
+            __threadfence();
+            const int slot0 = paged_run_begin(c0, C, T) == cc.unit_t ? 0 : 1;
+            for (int lr = wid; lr < G::kRows; lr += kThreads / 32)
+              join_row<D, QBF>(a, cc.h, cc.qt, c0, c1, slot0, cc.b0, cc.n, lr);
+          }
+        }
+      }
       fresh = true;
     }
     cc.next(a);
   }
 }
 
-// Joins the partials of the units cut between CTAs: one warp per row, the partials added
-// in CTA order.
+// Joins the partials of the units cut between CTAs, where the attention leaves that to a launch of its own.
 template <int D, bool QBF>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();  // (launched while the attention still runs)
-  const int* dd = a.desc + 4 * blockIdx.x;
-  const int r = dd[0];
-  if (r < 0) return;
-  const int h = dd[1], qt = dd[2], c1 = dd[3] >> 1, c0 = blockIdx.x;
-  const long long first = 2ll * c0 + (dd[3] & 1);
-  const int b0 = a.rq.begin[r], n = a.rq.begin[r + 1] - b0;
-  const int R = a.s.rows, lane = threadIdx.x & 31;
-  const long long stride = static_cast<long long>(R) * (D + 2);
-  constexpr int V = D / 32;  // channels per lane
-  for (int lr = blockIdx.y * 4 + (threadIdx.x >> 5); lr < R; lr += 4 * gridDim.y) {
-    const int row = qt * R + lr;
-    if (row >= n * a.s.group) return;
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const long long s = c == c0 ? first : 2ll * c;
-      m = fmaxf(m, a.part[s * stride + R * D + 2 * lr]);
-    }
-    m = warp_max(m);
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = a.part + (c == c0 ? first : 2ll * c) * stride;
-      const float2 st = *reinterpret_cast<const float2*>(p + R * D + 2 * lr);
-      const float f = ex2(st.x - ms);
-      l += st.y * f;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p + lr * D + 4 * lane);
-        o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(p + lr * D + 2 * lane);
-        o[0] += x.x * f, o[1] += x.y * f;
-      }
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int i = row / a.s.group, head = h * a.s.group + row % a.s.group;
-    char* po = a.out.p + ((b0 + i) * a.out.token_stride + head * a.out.head_stride + V * lane) * 2;
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(po) = make_uint2(pack2<QBF>(o[0] * inv, o[1] * inv), pack2<QBF>(o[2] * inv, o[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(po) = pack2<QBF>(o[0] * inv, o[1] * inv);
-    if (a.lse && lane == 0)
-      a.lse[static_cast<long long>(b0 + i) * (a.c.n_kv * a.s.group) + head] =
-          l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
-  }
+  const int4 d0 = *reinterpret_cast<const int4*>(a.desc + 8 * blockIdx.x);
+  const int2 d1 = *reinterpret_cast<const int2*>(a.desc + 8 * blockIdx.x + 4);
+  if (d0.x < 0) return;
+  for (int lr = blockIdx.y * 4 + (threadIdx.x >> 5); lr < a.s.rows; lr += 4 * gridDim.y)
+    join_row<D, QBF>(a, d0.y, d0.z, blockIdx.x, d0.w >> 1, d0.w & 1, d1.x, d1.y, lr);
 }
 
 template <int D, int FMT, int MT, bool QBF>
@@ -758,7 +797,7 @@ cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int 
   cudaError_t e;
   if (rows > kChunkMinRows) e = launch_paged_chunk(a, head_dim, fmt, qtype, num_sms, st);
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
   const dim3 grid(a.ctas, a.s.rows / 16);
   if (head_dim == 64)
     return qtype == kTBf16 ? launch_ex(paged_combine_kernel<64, true>, grid, dim3(128), 0, st, true, a)

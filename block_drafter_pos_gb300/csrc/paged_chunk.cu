@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   pdl_trigger();
   const long long T = paged_scan<kThreads>(a, pre, tmp);
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
-  if (tid == 0) a.desc[4 * c] = -1;
+  if (tid == 0) a.desc[8 * c] = -1;
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
   if (wid == 12) {
@@ -495,10 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
           if (!whole && t == 0 && lrow == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
             const long long cb = ((cc.unit_t + cc.u.nt) * C - 1) / T;
-            int* dd = a.desc + 4 * c;
+            int* dd = a.desc + 8 * c;
             dd[1] = cc.h;
             dd[2] = cc.qt;
             dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
+            dd[4] = cc.b0;
+            dd[5] = cc.n;
             dd[0] = cc.r;
           }
           ok = mbar_wait(o_done + 8 * t, static_cast<uint32_t>((n - 1) & 1));
