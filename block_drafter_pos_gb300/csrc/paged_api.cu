@@ -234,6 +234,9 @@ dflash2_status dflash2_sample(const dflash2_sample_args* args, void* stream) {
   const int64_t lb = ((x.n_rows - 1) * x.row_stride + x.vocab) * t_size(x.logits_type);
   const int64_t kb = ((x.n_rows - 1) * x.kept_stride + x.vocab) * 4;
   a.kept_in_place = k0 != nullptr && k0 < l0 + lb && l0 < k0 + kb;
+  // in place: the same rows, or one row's kept logits would overwrite another's before they are read
+  if (a.kept_in_place && (k0 != l0 || x.logits_type != DFLASH2_T_F32 || (x.n_rows > 1 && x.kept_stride != x.row_stride)))
+    return DFLASH2_E_INVAL;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&a.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

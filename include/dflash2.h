@@ -568,7 +568,8 @@ dflash2_status dflash2_paged_read(dflash2_paged_handle* h, const dflash2_paged_c
  *   j < kv_len;  causal != 0: j <= p;  window > 0: p - j < window;
  *   tree_mask != NULL (causal ignored): among the new tokens, bit (j - (kv_len - n)) of
  *   tree_mask[row of i] (uint64; n <= DFLASH2_PAGED_MAX_TREE); older positions are visible.
- * A token that sees nothing gets zeros (and lse = -infinity).  Masked positions carry no
+ * A token that sees nothing gets zeros (and lse = -infinity); rows that no request holds keep
+ * what they held.  Masked positions carry no
  * weight whatever they hold (NaN and infinities included).  q, out: bf16 or fp16, the
  * same type, which with a 16-bit cache is the cache's.  Scores, sums and products are
  * accumulated in fp32. */
@@ -606,7 +607,8 @@ dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_pa
  *   token int32 [n_rows]; prob fp32 [n_rows] or NULL: the token's share of the weight left.
  *   kept fp32 [n_rows][vocab] (kept_stride elements apart) or NULL: the logits that stay,
  *     -1e30 elsewhere: with the row's temperature these are the target rows
- *     of dflash2_verify for the truncated distribution.  May be the logits' own memory.
+ *     of dflash2_verify for the truncated distribution.  May be the logits themselves (fp32, the same
+ *     strides); any other overlap is refused.
  *   status int32 [n_rows] or NULL, written: DFLASH2_OK; DFLASH2_E_NONFINITE (a NaN or
  *     +infinity, or no logit above -infinity); DFLASH2_E_INVAL (T < 0 or not finite, top_p not above 0,
  *     min_p outside [0, 1], u outside [0, 1)).  Such a row gets token -1, prob 0, kept -1e30. */

@@ -226,6 +226,7 @@ FORMATS = [("bf16", "bf16"), ("fp16", "fp16"), ("int8", "bf16"), ("int8", "fp16"
     ([5, 0, 16, 1], [70, 10, 400, 333], 8, 1, 48),         # a request without new tokens
     ([40], [131], 6, 2, 64),                               # more rows than one unit holds
     ([70, 33], [70, 200], 4, 2, 16),                       # prompts
+    ([1, 3], [140, 9], 64, 1, 16),                         # the widest group
 ])
 def test_attention_causal(fmt, qt, dim, new, length, hq, hk, page):
     s = Setup(new, length, hq=hq, hk=hk, dim=dim, page=page, fmt=fmt, seed=len(new) + page)
@@ -431,6 +432,19 @@ def test_attention_long_and_mixed(fmt, qt, dim):
     check_attention(s, q, out, lse)
     out, lse = s.attend(q, window=700, max_len=20000)
     check_attention(s, q, out, lse, window=700)
+    s.close()
+
+
+@pytest.mark.parametrize("n,group", [(1, 4), (5, 8)])
+def test_attention_of_many_requests(n, group):
+    """More requests than a block has threads, most of them short."""
+    g = np.random.default_rng(n)
+    length = (n + g.integers(0, 40, 530)).tolist()
+    s = Setup([n] * 530, length, hq=group, hk=1, dim=64, fmt="bf16", seed=5)
+    q = s.queries("bf16")
+    out, lse = s.attend(q)
+    check_attention(s, q, out, lse, skip=[r for r in range(530) if r % 7 and r < 520])
+    assert torch.isfinite(out.float()).all()
     s.close()
 
 

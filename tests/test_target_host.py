@@ -130,7 +130,7 @@ def test_sample_refuses_bad_arguments():
     f = bd.lib().dflash2_sample
 
     def args(**kw):
-        a = b.SampleArgs(2, 100, b.T_F32, 0, P, 100, P, P, P, P, P, P, P, P, 100, P)
+        a = b.SampleArgs(2, 100, b.T_F32, 0, P, 100, P, P, P, P, P, P, P, 4 * P, 100, P)
         for k, v in kw.items():
             setattr(a, k, v)
         return a
@@ -139,6 +139,9 @@ def test_sample_refuses_bad_arguments():
     for kw in [dict(n_rows=-1), dict(vocab=0), dict(logits_type=3), dict(logits=None), dict(temperature=None),
                dict(uniform=None), dict(token=None), dict(row_stride=99), dict(kept_stride=99)]:
         assert f(args(**kw), None) == b.E_INVAL, kw
+    # kept over the logits: the same rows only
+    for kw in [dict(kept=P + 4), dict(kept=P - 400), dict(kept_stride=200), dict(logits_type=b.T_F16)]:
+        assert f(args(**{"kept": P, **kw}), None) == b.E_INVAL, kw
     assert f(args(vocab=(1 << 19) + 1, row_stride=1 << 20, kept_stride=1 << 20), None) == b.E_UNSUPPORTED
     assert f(args(n_rows=0), None) == b.OK
 
