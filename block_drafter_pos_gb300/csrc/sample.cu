@@ -28,7 +28,7 @@ namespace cg = cooperative_groups;
 namespace df2 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;   // (256, four CTAs to an SM: rows of one kind gain, long rows among short ones cost more)
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCtas = 16;
@@ -37,9 +37,9 @@ constexpr int kGroups = 2;       // groups of 4 consecutive elements a thread ho
 constexpr int kChunk = kThreads * 4 * kGroups;
 constexpr int kList = 2048;      // candidates of a CTA
 constexpr int kSort = 2048;      // candidates of a row
-constexpr int kShortK = 384;     // largest top_k of the short way
+constexpr int kShortK = 384;     // largest top_k of the short way (of a CTA's 512 thread maxima)
 constexpr int kProbe = 384;      // thread maxima above the CTAs' bounds, in all, for top-p alone
-constexpr int kWaveCtas = 4;     // CTAs started for each SM (two at a time)
+constexpr int kWaveCtas = 4;     // CTAs started for each SM, two at a time
 constexpr float kCut = -1e30f;
 
 // round(2^31 2^(j / 32))
@@ -55,10 +55,11 @@ struct Scale {
 
 template <int T>  // 0: bf16, 1: fp16, 2: fp32
 DF2_DEV float load1(const char* p, int i) {
-  if constexpr (T == 2) return reinterpret_cast<const float*>(p)[i];
+  // (+ 0 makes one zero of the two, which the order would otherwise tell apart)
+  if constexpr (T == 2) return reinterpret_cast<const float*>(p)[i] + 0.f;
   const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
-  if constexpr (T == 0) return bf16_to_f32(b);
-  return __half2float(__ushort_as_half(b));
+  if constexpr (T == 0) return bf16_to_f32(b) + 0.f;
+  return __half2float(__ushort_as_half(b)) + 0.f;
 }
 
 // Elements i .. i + 3 of a row; vec: the row is aligned for one wide load.
@@ -83,27 +84,31 @@ DF2_DEV void load4(const char* p, int i, bool vec, float (&x)[4]) {
 
 // 2^44 2^((x - xmax) (ch + cl)), rounded.  The exponent is carried as a sum of two floats (the
 // difference's own rounding included); 2^(j / 32) comes from a 32-bit table and the rest, within
-// 2^-6, from four terms of its series: about 30 bits, with errors of either sign.
+// 2^-6, from four terms of its series, applied as a 28-bit fraction: about 29 bits, with errors of either sign.
+// Roundings to integers are sums with 1.5 * 2^23, and the table has a copy for each lane: conversions and bank
+// conflicts bounded the passes over whole rows (`pw` is this lane's copy, entries 32 apart).
 DF2_DEV unsigned long long weight(float x, const Scale& s, const uint32_t* pw) {
+  constexpr float kMagic = 12582912.f;
   const float d = x - s.xmax;
   const float th = d * s.ch;
   if (!(th > -46.f)) return 0ull;
   const float bb = d - x;
   const float e = (x - (d - bb)) + (-s.xmax - bb);
   const float tl = fmaf(d, s.ch, -th) + fmaf(d, s.cl, e * s.ch);
-  const float nj = rintf(th * 32.f);
+  const float t = fmaf(th, 32.f, kMagic), nj = t - kMagic;
+  const int n = __float_as_int(t) - __float_as_int(kMagic);
   const float r = fmaf(nj, -0.03125f, th) + tl;
   // 2^r - 1 = r ln 2 + (r ln 2)^2 / 2 + ...
   float q = fmaf(r, 0.0096181291f, 0.0555041087f);
   q = fmaf(q, r, 0.2402265070f);
   q = fmaf(q, r, 0.6931471806f);
   q *= r;
-  const int n = static_cast<int>(nj);
-  const uint32_t p = pw[n & 31];
-  const uint32_t m = p + static_cast<uint32_t>(__float2int_rn(static_cast<float>(p) * q));
-  const int sh = -(n >> 5);
-  const unsigned long long w = static_cast<unsigned long long>(m) << 13;
-  return sh <= 0 ? w << -sh : (sh > 45 ? 0ull : (w + (1ull << (sh - 1))) >> sh);
+  const int qi = __float_as_int(fmaf(q, 268435456.f, kMagic)) - __float_as_int(kMagic);  // 2^28 q, within +- 2^22
+  const uint32_t p = pw[(n & 31) * 32];
+  const uint32_t m = p + static_cast<uint32_t>(__mulhi(static_cast<int>(p >> 1), qi << 5));
+  const int up = 13 + (n >> 5);  // 2^31 of m is 2^44
+  if (up >= 0) return static_cast<unsigned long long>(m) * (1u << up);
+  return up < -31 ? 0ull : ((m >> (-up - 1)) + 1u) >> 1;
 }
 
 DF2_DEV unsigned long long warp_sum_u64(unsigned long long v) {
@@ -116,7 +121,7 @@ DF2_DEV unsigned long long warp_sum_u64(unsigned long long v) {
 // never falls where the logit falls; at most kBins - 1.
 DF2_DEV uint32_t weight_step(float x, const Scale& s) {
   const float th = (x - s.xmax) * s.ch;
-  return th > -46.f ? static_cast<uint32_t>(static_cast<int>(rintf(th * -32.f))) : kBins - 1;
+  return th > -46.f ? static_cast<uint32_t>(__float_as_int(fmaf(th, -32.f, 12582912.f)) - __float_as_int(12582912.f)) : kBins - 1;
 }
 
 
@@ -126,8 +131,10 @@ struct Shared {
     uint32_t piece[3][kBins];         // the steps' histogram: 15-bit pieces of counts or weights
     unsigned long long sort[kSort];
   };
-  unsigned long long w[kSort];           // weights of the sorted candidates
-  unsigned long long list[kList];        // this CTA's candidates
+  union {
+    unsigned long long list[kList];      // this CTA's candidates, until they are gathered
+    unsigned long long w[kSort];         // weights of the sorted candidates; a histogram's sums
+  };
   unsigned long long warp_sum[kWarps];   // of this CTA's warps
   unsigned long long scan[kWarps];
   unsigned long long best;               // this CTA's largest element
@@ -135,7 +142,7 @@ struct Shared {
   unsigned long long before;             // weight or count above the digit found
   unsigned long long result;             // the last element that stays; 0: not found
   uint32_t tau, share, count, digit, bad, n_sort, run_max;
-  uint32_t pw[32];
+  uint32_t pw[32][32];  // the table, a copy for each lane
 };
 
 struct Ctx {
@@ -244,6 +251,9 @@ DF2_DEV void sort_desc(unsigned long long* v, int n2) {
 }
 
 
+// Whether (x, id) comes no later than (lx, lid) in the order.
+DF2_DEV bool reaches(float x, int id, float lx, int lid) { return x > lx || (x == lx && id <= lid); }
+
 // Appends the warp's elements that are `in` to this CTA's list.
 DF2_DEV void append(Shared* sh, bool in, unsigned long long v) {
   const uint32_t m = __ballot_sync(0xffffffffu, in);
@@ -259,18 +269,17 @@ DF2_DEV void append(Shared* sh, bool in, unsigned long long v) {
 // or more than kSort if they do not fit.  Called by every thread of that CTA after a cluster barrier.
 DF2_DEV int gather_sorted(Ctx& c, unsigned long long least) {
   Shared* sh = c.sh;
-  static_assert(kMaxCtas <= kWarps, "a warp for each CTA's list");
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   if (threadIdx.x == 0) sh->n_sort = 0;
   const uint32_t count = lane < c.ctas ? c.cl.map_shared_rank(sh, lane)->count : 0u;
   const bool over = __any_sync(0xffffffffu, count > kList);
   __syncthreads();
-  // warp w copies from CTAs w mod ctas: with fewer CTAs than warps, several share a list
+  // a warp for each list, or several where there are fewer lists than warps
   const int shares = c.ctas < kWarps ? kWarps / c.ctas : 1;
-  if (!over && wid < c.ctas * shares) {
-    const int r = wid % c.ctas, cr = static_cast<int>(__shfl_sync(0xffffffffu, count, r));
+  for (int r = wid % c.ctas; !over && r < c.ctas; r += kWarps) {
+    const int cr = static_cast<int>(__shfl_sync(0xffffffffu, count, r));
     const Shared* o = c.cl.map_shared_rank(sh, r);
-    for (int i0 = (wid / c.ctas) * 32; i0 < cr; i0 += shares * 32) {
+    for (int i0 = (shares > 1 ? wid / c.ctas : 0) * 32; i0 < cr; i0 += shares * 32) {
       const unsigned long long v = i0 + lane < cr ? o->list[i0 + lane] : 0ull;
       const bool in = i0 + lane < cr && v >= least;
       const uint32_t m = __ballot_sync(0xffffffffu, in);
@@ -312,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const bool kvec = (reinterpret_cast<uintptr_t>(kept) & 15) == 0;
   const bool fill = kept && !a.kept_in_place;  // (in place the logits may be read again)
   auto element = [&](float x, int i) { return topk_key(x, c.lo + i); };
-  if (threadIdx.x < 32) shm.pw[threadIdx.x] = kPow[threadIdx.x];
+  for (int i = threadIdx.x; i < 32 * 32; i += kThreads) shm.pw[i >> 5][i & 31] = kPow[i >> 5];
+  const uint32_t* const pw = &shm.pw[0][lane];
   if (threadIdx.x == 0) shm.bad = shm.count = shm.run_max = 0;
   const float temp = a.temperature[row], u = a.uniform[row];
   const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[g][e] = next[g][e];
+      for (int e = 0; e < 4; ++e) x[g][e] = next[g][e] + 0.f;  // (one zero, see load1; here, or the fetch would wait)
     fetch(ck + 1);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
@@ -473,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     s.cl = static_cast<float>(cc - static_cast<double>(s.ch));
     if (!(s.ch < INFINITY)) s.ch = 3.4028235e38f, s.cl = 0.f;
   }
-  const double floor_w = static_cast<double>(min_p) * 17592186044416.0;  // 2^44
+  // (compared as whole numbers: conversions to 64-bit floats, two a clock, bounded the passes over whole rows)
+  const unsigned long long floor_w = static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * 17592186044416.0));  // 2^44
   bool bounded = whole || (top_k != 0 && want != 0);  // every element that may stay is a candidate
   if (by_min) {
     const uint32_t t = min_bound(s.xmax);
@@ -485,6 +496,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // Adds the weight (or 1) of every element >= least to the steps' histogram; returns the thread's sum.
   auto steps = [&](bool by_weight, unsigned long long least) {
+    const float least_x = least ? key_value(least) : -INFINITY;
+    const int least_id = least ? static_cast<int>(key_index(least)) : a.vocab;
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&shm.piece[0][0])[i] = 0;
     __syncthreads();
     unsigned long long z = 0;
@@ -495,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = i0 + e * kThreads;
-        if (i >= c.n || element(x[e], i) < least) continue;
-        const unsigned long long w = by_weight ? weight(x[e], s, shm.pw) : 1ull;
+        if (i >= c.n || !reaches(x[e], c.lo + i, least_x, least_id)) continue;
+        const unsigned long long w = by_weight ? weight(x[e], s, pw) : 1ull;
         if (w == 0) continue;
         z += w;
         const int b = kBins - 1 - weight_step(x[e], s);
@@ -540,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int j = threadIdx.x * kPer + i;
-          w[i] = j < lim ? weight(key_value(shm.sort[j]), s, shm.pw) : 0ull;
+          w[i] = j < lim ? weight(key_value(shm.sort[j]), s, pw) : 0ull;
           sum_w += w[i];
           shm.w[j] = w[i];
         }
@@ -550,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int j = threadIdx.x * kPer + i;
-          if (j < lim && (j == 0 || top_p >= 1.f || static_cast<double>(run) < goal_w) && static_cast<double>(w[i]) >= floor_w &&
+          if (j < lim && (j == 0 || top_p >= 1.f || static_cast<double>(run) < goal_w) && w[i] >= floor_w &&
               (shm.sort[j] >> 32) > 0x007FFFFFu)  // (above -infinity)
             ++stay;
           run += w[i];
@@ -623,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     auto reached = [&](unsigned long long v) {
       return by_weight ? static_cast<double>(above + v) >= target : above + v >= want_k;
     };
-    auto value = [&](float x) { return by_weight ? weight(x, s, shm.pw) : 1ull; };
+    auto value = [&](float x) { return by_weight ? weight(x, s, pw) : 1ull; };
     uint32_t bin;
     unsigned long long up;
     if (threadIdx.x == 0) shm.count = 0;
@@ -709,11 +722,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 
   // ---- the weight left, and the draw
+  const float least_x = least ? key_value(least) : -INFINITY;
+  const int least_id = least ? static_cast<int>(key_index(least)) : a.vocab;
   auto left = [&](int i, float x, bool& stays) -> unsigned long long {
-    stays = x > -INFINITY && element(x, i) >= least;
+    stays = x > -INFINITY && reaches(x, c.lo + i, least_x, least_id);
     if (!stays) return 0ull;
-    const unsigned long long w = weight(x, s, shm.pw);
-    stays = static_cast<double>(w) >= floor_w;  // (a weight of zero may stay: it is then never drawn)
+    const unsigned long long w = weight(x, s, pw);
+    stays = w >= floor_w;  // (a weight of zero may stay: it is then never drawn)
     return stays ? w : 0ull;
   };
   unsigned long long mine = 0;
@@ -800,8 +815,8 @@ cudaError_t launch(const SampleArgs& a, int ctas, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
-  // CTAs per row: slices of at most kSlice elements; more while all the rows' CTAs (two to an SM) run at once and a
-  // slice is more than 8192 elements
+  // CTAs per row: slices of at most kSlice elements; more while the rows' CTAs are at most four to an SM and a slice
+  // is more than 8192 elements
   int ctas = 1;
   while ((a.vocab + ctas - 1) / ctas > kSlice - 8) ctas *= 2;
   while (ctas < kMaxCtas && a.n_rows * ctas * 2 <= kWaveCtas * a.num_sms && a.vocab / ctas > 8192) ctas *= 2;

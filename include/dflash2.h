@@ -599,7 +599,7 @@ dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_pa
  *     of the weight that top_k left (the first always stays);
  *   min_p > 0: w_i >= min_p stays;
  * and the token is the first id, in id order, whose running weight exceeds u times the
- * weight left (weights and sums carry about 30 bits and are summed exactly, so the result
+ * weight left (weights carry about 29 bits and are summed exactly, so the result
  * does not depend on the order of the device's work).  T = 0: the largest logit (smallest
  * id); -infinity logits are never taken.
  *   temperature, top_p, min_p, uniform: fp32 [n_rows]; top_k int32 [n_rows]; each of
