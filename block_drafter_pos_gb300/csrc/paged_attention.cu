@@ -27,8 +27,8 @@
 //
 // Measured: 64 single tokens of 32 query heads over 8 KV heads' e4m3 caches, ragged to 16384 positions (1.34 GB): 257 us,
 // 5.2 TB/s, 77% of a copy's rate; DRAM moves 15% more than that, the scales' 32-byte sectors being read once per head.
-// 16 blocks of 8 over int8 caches ragged to 8192 (0.21 GB): 88 us, bound by the latency of 8 warps an SM
-// making fp16 of the codes (0.44 instructions a scheduler and clock).  16 requests of 4 tokens over 8192 bf16 positions
+// 16 blocks of 8 over int8 caches ragged to 8192 (0.21 GB): 84 us, bound by the latency of 8 warps an SM
+// (3 us per tile of 128 keys; 0.44 instructions a scheduler and clock).  16 requests of 4 tokens over 8192 bf16 positions
 // (0.54 GB): 105 us, 5.1 TB/s.
 #include "common.cuh"
 #include "paged_mma.cuh"
@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   // one tile before its entries become offsets (resolve), so that its latency lies under a tile's work.
   PagedCursor oc;
   oc.start(a, pre, t_begin, t_end);
+  PagedCursor cc = oc;  // the tile that is worked on
   long long my_off = -1, my_soff = 0;
   int my_bad = 0;
   int pg = 0, pg_row = 0, pg_h = 0, pg_r = 0;
@@ -269,8 +270,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   sval_next = my_off >= 0;
   fetch();  // tile S
 
-  PagedCursor cc;
-  cc.start(a, pre, t_begin, t_end);
   uint32_t qf[kSteps][4];
   float o[NT][4];
   float m0 = 0, m1 = 0, l0 = 0, l1 = 0, sc0 = 0, sc1 = 0, vref = 0, vinv = 0;
@@ -804,7 +803,8 @@ cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int 
   if (rows > kChunkMinRows) e = launch_paged_chunk(a, head_dim, fmt, qtype, num_sms, st);
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
-  const dim3 grid(a.ctas, a.s.rows / 16);
+  // a row per warp for units of 32 rows (four in turn took 2 to 3 us more), four for those of 256
+  const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / 16);
   if (head_dim == 64)
     return qtype == kTBf16 ? launch_ex(paged_combine_kernel<64, true>, grid, dim3(128), 0, st, true, a)
                            : launch_ex(paged_combine_kernel<64, false>, grid, dim3(128), 0, st, true, a);

@@ -464,7 +464,7 @@ def run_sample(x, t, k, p, m, u, kept=True):
     return token.cpu().numpy(), prob.cpu().numpy(), None if ko is None else ko.cpu().numpy(), status.cpu().numpy()
 
 
-# weights carry 30 bits with errors of either sign, and sums of them are exact: a decision further than this from
+# weights carry 29 bits with errors of either sign, and sums of them are exact: a decision further than this from
 # its border is certain (probabilities: 2^-29 for the token's weight, and as much for the sum, and the fp32 result)
 MARGIN = 2.0 ** -27
 
