@@ -19,10 +19,12 @@
 //    1/32, whose bins spread the shared-memory atomics; the bin with the border is sorted as
 //    above or, where equal logits flood it, searched by the digits of the 64-bit number.
 //
-// Measured with 248320 fp32 logits a row: 128 rows, top-k 50, the kept rows written (254 MB), 103 us; with mixed settings
-// 172 us, of which the last are a few rows with a wide nucleus (three passes over the row, about 120 us each); one row
+// Measured with 248320 fp32 logits a row: 128 rows, top-k 50, the kept rows written (254 MB), 74 us; with mixed settings
+// 127 to 189 us, by the rows with a wide nucleus among them (three passes over the row); one row
 // 24 to 39 us, bound by latency (a 16-CTA cluster: 9 us of streaming, the rest barriers, the sort and the draw).
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "sample.h"
@@ -43,7 +45,9 @@ constexpr int kList = 2048;      // candidates of a CTA
 constexpr int kSort = 2048;      // candidates of a row
 constexpr int kShortK = 384;     // largest top_k of the short way (of a CTA's 512 thread maxima)
 constexpr int kProbe = 384;      // thread maxima above the CTAs' bounds, in all, for top-p alone
-constexpr int kWaveCtas = 4;     // CTAs started for each SM, two at a time
+constexpr int kWaveCtas = 2;     // CTAs an SM holds
+// The rows of a launch: all; those of the long way, where they are few; the others and, where they are many, those too.
+enum Part { kAll, kFew, kRest };
 constexpr float kCut = -1e30f;
 
 // round(2^31 2^(j / 32))
@@ -305,14 +309,45 @@ DF2_DEV int gather_sorted(Ctx& c, unsigned long long least) {
 }
 
 template <int T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
+DF2_DEV void sample_row(const SampleArgs& a, int part, int few) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Shared& shm = *reinterpret_cast<Shared*>(smem_raw);
   Ctx c{cg::this_cluster(), &shm};
   c.rank = c.cl.block_rank();
   c.ctas = c.cl.num_blocks();
-  const int row = blockIdx.x / c.ctas;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int row = blockIdx.x / c.ctas;
+  if (part != kAll) {  // the cluster's row among the part's (of every kThreads rows)
+    const int width = part == kFew ? few : kThreads, place = row % width, r = row / width * kThreads + threadIdx.x;
+    bool passes = false;
+    if (r < a.n_rows) {
+      const int k = a.top_k ? a.top_k[r] : 0;
+      passes = a.temperature[r] > 0.f && (k <= 0 || k > kShortK) &&
+               ((a.top_p && a.top_p[r] < 1.f) || k > 0 || !(a.min_p && a.min_p[r] > 0.f));
+    }
+    const int n_long = __syncthreads_count(passes);
+    const bool many = n_long > few;
+    // (many: the long ones first)
+    const bool first = r < a.n_rows && (part == kFew ? passes && !many : passes == many);
+    const bool second = r < a.n_rows && part == kRest && many && !passes;
+    const uint32_t those = __ballot_sync(0xffffffffu, first);
+    const uint32_t these = __ballot_sync(0xffffffffu, second);
+    if (lane == 0) shm.warp_sum[wid] = __popc(those), shm.scan[wid] = __popc(these);
+    __syncthreads();
+    const uint32_t below = (1u << lane) - 1;
+    int before = __popc(second ? these & below : those & below), all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int x = static_cast<int>(shm.warp_sum[w]), y = static_cast<int>(shm.scan[w]);
+      before += w < wid ? (second ? y : x) : 0;
+      before += second ? x : 0;
+      all += x + y;
+    }
+    if (place >= all) return;  // (the whole cluster)
+    if ((first || second) && before == place) shm.digit = r;
+    __syncthreads();
+    row = static_cast<int>(shm.digit);
+  }
   const int per = ((a.vocab + c.ctas - 1) / c.ctas + 7) & ~7;
   c.lo = min(a.vocab, c.rank * per);
   c.n = min(a.vocab, c.lo + per) - c.lo;
@@ -795,37 +830,62 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 }
 
 template <int T>
-cudaError_t launch(const SampleArgs& a, int ctas, cudaStream_t st) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, int part, int few) {
+  if (part == kFew) pdl_trigger();
+  sample_row<T>(a, part, few);
+  // (begun while the launch before runs: one CTA waits for that one's end, so that what follows waits for both)
+  if (part == kRest && blockIdx.x == 0) pdl_wait();
+}
+
+template <int T>
+cudaError_t launch(const SampleArgs& a, int rows, int ctas, int part, int few, cudaStream_t st) {
   static std::atomic<unsigned long long> done[2];
   cudaError_t e = set_smem_once(sample_kernel<T>, sizeof(Shared), done[0]);
   if (e != cudaSuccess) return e;
   e = set_attr_once(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done[1]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_rows * ctas);
+  cfg.gridDim = dim3(rows * ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = part == kRest ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, part, few);
+}
+
+template <int T>
+cudaError_t launch_rows(const SampleArgs& a, cudaStream_t st) {
+  // CTAs per row: slices of at most kSlice elements; more while the GPU holds all rows' CTAs at a time and a slice
+  // is more than 8192 elements.
+  int ctas = 1;
+  while ((a.vocab + ctas - 1) / ctas > kSlice - 8) ctas *= 2;
+  while (ctas < kMaxCtas && a.n_rows * ctas * 2 <= kWaveCtas * a.num_sms && a.vocab / ctas > 8192) ctas *= 2;
+  if (ctas == kMaxCtas || a.vocab / ctas <= 16384) return launch<T>(a, a.n_rows, ctas, kAll, 0, st);
+  // The rows of the long way set the call's time: where they are few (half the rows at most, and
+  // two and a half times what the GPU holds at once; of every kThreads rows) they begin first, with larger clusters; the others, for whom a large cluster only means more barriers, run
+  // beside them.  The device knows which rows they are: clusters without a row end at once.
+  // Measured (us), 248320 fp32 logits, clusters of four in one launch of two waves / this: 128 rows of mixed settings
+  // 181 / 149, all top-k 95 / 74, all top-p 394 / 378; 32 rows 98 / 78, 87 / 43, 210 / 134; 512 rows 455 / 367, 242 / 250,
+  // 1257 / 1261.
+  const int most = ctas < 4 ? 8 : 2 * ctas, groups = (a.n_rows + kThreads - 1) / kThreads;
+  const int few = std::max(1, std::min({5 * a.num_sms / most, a.n_rows / 2, kThreads}));
+  const cudaError_t e = launch<T>(a, groups * (a.n_rows < few ? a.n_rows : few), most, kFew, few, st);
+  return e != cudaSuccess ? e : launch<T>(a, a.n_rows, ctas, kRest, few, st);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
-  // CTAs per row: slices of at most kSlice elements; more while the rows' CTAs are at most four to an SM and a slice
-  // is more than 8192 elements
-  int ctas = 1;
-  while ((a.vocab + ctas - 1) / ctas > kSlice - 8) ctas *= 2;
-  while (ctas < kMaxCtas && a.n_rows * ctas * 2 <= kWaveCtas * a.num_sms && a.vocab / ctas > 8192) ctas *= 2;
-  if (a.type == 0) return launch<0>(a, ctas, st);
-  return a.type == 1 ? launch<1>(a, ctas, st) : launch<2>(a, ctas, st);
+  if (a.type == 0) return launch_rows<0>(a, st);
+  return a.type == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
 }
 
 }  // namespace df2

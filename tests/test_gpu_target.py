@@ -504,6 +504,53 @@ def test_sample_against_the_oracle(v, dtype):
     assert check_sample(x, t, k, p, m, u) <= n // 10
 
 
+def mixed_rows(n, v, wide, seed):
+    """Settings and logits of n rows, a share `wide` of them top-p without top-k."""
+    g = np.random.default_rng(seed)
+    x = torch.from_numpy((g.standard_normal((n, v)) * g.uniform(0.3, 3, (n, 1))).astype(np.float32)).cuda()
+    long = g.random(n) < wide
+    t = np.where(g.random(n) < 0.1, 0.0, g.uniform(0.5, 1.3, n))
+    k = np.where(long, 0, g.integers(1, 200, n))
+    p = np.where(long, g.uniform(0.3, 0.95, n), np.where(g.random(n) < 0.5, 1.0, 0.9))
+    m = np.where(g.random(n) < 0.5, 0.0, g.uniform(0, 0.1, n))
+    return x, t, k, p, m, np.minimum(g.random(n).astype(np.float32), np.float32(1 - 2.0 ** -24))
+
+
+@pytest.mark.parametrize("n,v", [(30, 140001), (128, 33000), (600, 17001)])
+@pytest.mark.parametrize("wide", [0.0, 0.05, 0.6, 1.0])
+def test_sample_many_rows(n, v, wide):
+    """Rows of a wide nucleus, none to all, among others that are not; more rows than a block has threads."""
+    assert check_sample(*mixed_rows(n, v, wide, n)) <= n // 10
+
+
+@pytest.mark.parametrize("wide", [0.1, 0.9])
+def test_sample_many_rows_in_a_graph(wide):
+    """What follows on the stream, eager or captured, sees every row's result."""
+    x, t, k, p, m, u = mixed_rows(128, 40000, wide, 3)
+    want = run_sample(x, t, k, p, m, u)
+    f = [torch.as_tensor(np.asarray(a), dtype=torch.float32).cuda() for a in (t, p, m, u)]
+    kk = torch.as_tensor(k, dtype=torch.int32).cuda()
+    token = torch.zeros(128, dtype=torch.int32, device="cuda")
+    kept = torch.zeros_like(x)
+
+    def step():
+        token.fill_(-9)
+        kept.fill_(5.0)
+        bd.dflash2_sample(x, f[0], kk, f[1], f[2], f[3], token, kept=kept)
+        return token.clone(), kept.clone()
+
+    eager = [step() for _ in range(10)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for got in eager:
+        assert (got[0].cpu().numpy() == want[0]).all() and (got[1].cpu().numpy() == want[2]).all()
+    for _ in range(3):
+        out[0].zero_()
+        graph.replay()
+        assert (out[0].cpu().numpy() == want[0]).all() and (out[1].cpu().numpy() == want[2]).all()
+
+
 def test_sample_equal_logits_and_borders():
     """Rows of one value, two values, the type's lowest value, -infinity, and single tokens left."""
     v = 9000
