@@ -7,7 +7,7 @@
 // Both directions are streams: a warp per token, 8 channels per lane and load, the keys' and
 // the values' loads issued together, amax by shuffles within the row's lanes, so each source
 // element is read once and each code written once.  Measured for 40,005 tokens of 8 heads of 128 (248 MB each
-// way): bf16 to e4m3 69 us (3.6 TB/s: instruction issue, 2.8 of 4 a clock, about 180 for 8 channels of a lane), back to
+// way): bf16 to e4m3 68 us (3.6 TB/s: instruction issue, 2.8 of 4 a clock, about 175 for 8 channels of a lane), back to
 // bf16 41 us (6.0 TB/s, 89% of a copy's rate).
 #include "common.cuh"
 #include "paged.h"
@@ -115,14 +115,17 @@ DF2_DEV uint2 codes8(const float (&x)[8], float s) {
   float inv;  // within 2^-23; s is at least 2^-126
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   const float up = inv * 1.000000476837158f, down = inv * 0.999999523162842f;
+  const float2 up2 = make_float2(up, up), down2 = make_float2(down, down);
   uint32_t w[2] = {0u, 0u}, differ = 0u;
   if constexpr (FMT == kKvInt8) {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded integer
     uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = __float_as_uint(fmaf(x[i], up, kMagic));
-      differ |= c[i] ^ __float_as_uint(fmaf(x[i], down, kMagic));
+    for (int i = 0; i < 8; i += 2) {
+      const float2 y = make_float2(x[i], x[i + 1]);
+      const float2 u = fma2(y, up2, make_float2(kMagic, kMagic)), d = fma2(y, down2, make_float2(kMagic, kMagic));
+      c[i] = __float_as_uint(u.x), c[i + 1] = __float_as_uint(u.y);
+      differ |= (c[i] ^ __float_as_uint(d.x)) | (c[i + 1] ^ __float_as_uint(d.y));
     }
     if (differ) {
 #pragma unroll
@@ -139,8 +142,9 @@ DF2_DEV uint2 codes8(const float (&x)[8], float s) {
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t c = pair(x[2 * i] * up, x[2 * i + 1] * up);
-      differ |= c ^ pair(x[2 * i] * down, x[2 * i + 1] * down);
+      const float2 y = make_float2(x[2 * i], x[2 * i + 1]), u = mul2(y, up2), d = mul2(y, down2);
+      const uint32_t c = pair(u.x, u.y);
+      differ |= c ^ pair(d.x, d.y);
       w[i >> 1] |= c << (16 * (i & 1));
     }
     if (differ) {
