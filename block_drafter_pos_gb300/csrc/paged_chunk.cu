@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   constexpr bool kBF = kQuant ? false : QBF;
   constexpr int NS = G::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[NS * 2 + G::kRing + 10];
+  __shared__ __align__(8) uint64_t bars[NS * 2 + G::kRing + 11];
   __shared__ uint32_t tmem_sh;
   __shared__ int poison_sh[G::kRing];  // by unit
   __shared__ long long tmp[kThreads / 32 + 1];
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* const sgen = smem_raw + (sbase - smem_u32(smem_raw));
   const uint32_t full = smem_u32(bars), empty = full + 8 * NS, info = empty + 8 * NS, s_full = info + 8 * G::kRing,
-                 p_full = s_full + 16, q_full = p_full + 32, o_done = q_full + 16;
+                 p_full = s_full + 16, q_full = p_full + 32, o_done = q_full + 16, all_done = o_done + 16;
   long long* const pre = reinterpret_cast<long long*>(sgen + G::kOffPre);
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       mbar_init_count(q_full + 8 * t, 4);
       mbar_init_count(o_done + 8 * t, 1);
     }
+    mbar_init_count(all_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_trigger();
@@ -831,11 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   __syncthreads();
   if (wid == 12) {
     if (lane == 0) {
-      // an extra commit covers whatever was issued; its barrier is one that nobody uses any more
-      mbar_init_count(info, 1);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      mma_commit(1, info);
-      mbar_wait(info, 0);
+      // an extra commit, on a barrier of its own, covers whatever was issued
+      mma_commit(1, all_done);
+      mbar_wait(all_done, 0);
     }
     __syncwarp();
     fence_after();
