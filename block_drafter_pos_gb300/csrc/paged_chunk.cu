@@ -196,7 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[NS * 2 + G::kRing + 11];
   __shared__ uint32_t tmem_sh;
-  __shared__ int poison_sh[G::kRing];  // by unit
+  // By unit: the number (from 1) of the last unit in the slot some of whose values are not finite.  Numbers only
+  // grow, so a row tile that is still at an older unit finds at worst a newer one's, and looks in vain.
+  __shared__ int poison_sh[G::kRing];
   __shared__ long long tmp[kThreads / 32 + 1];
   __shared__ float vmax_sh[2][4];
   __shared__ int flag_sh[2][4];
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           const float out_f = kQuant ? (whole ? inv * vref : vref) : (whole ? inv : 1.f);
           char* const po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
           float* const pp = a.part + slot * (a.s.rows * (D + 2)) + lr * D;
-          const bool poison = poison_sh[gunit % G::kRing] != 0;
+          const bool poison = *static_cast<volatile int*>(&poison_sh[gunit % G::kRing]) > gunit;
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
             float o[32];
@@ -741,10 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (piece_first) {
           if (j > 0) ++unit;
           vref = 0.f;
-          if (lt == 0) poison_sh[unit % G::kRing] = 0;
         }
         // (The slot's previous tile was eight tiles ago: operands up to that of tile j - 5 have been read, or this
-        // thread could not be here, so the weights of tile j - 5 and everything of earlier units are done.)
+        // thread could not be here, so the weights of tile j - 5 are done.)
         if constexpr (kQuant) {
           const float v = warp_max(vsv < INFINITY ? vsv : 0.f);
           if (lane == 0) vmax_sh[j & 1][wid - 8] = v;
@@ -768,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           // (a scale that is not finite counts as 0 here; the rows that see it add the products at the end)
           const bool finite = fabsf(vsv) < INFINITY;
           ks[128 + lt] = finite ? vsv * vinv : 0.f;
-          if (!finite) poison_sh[unit % G::kRing] = 1;
+          if (!finite) poison_sh[unit % G::kRing] = unit + 1;
           if (lt == 0) ks[256 + 5] = vref;
         }
         mbar_arrive(info + 8 * ring);
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
               found |= z.x != w.x || z.y != w.y || z.z != w.z || z.w != w.w;
               sts128(dst + x * kNext, z);
             }
-            if (found) poison_sh[unit_now % G::kRing] = 1;
+            if (found) poison_sh[unit_now % G::kRing] = unit_now + 1;
           } else {
 #pragma unroll
             for (int x0 = 0; x0 < kCount; x0 += kBatch) {
