@@ -16,7 +16,7 @@ def test_nonfinite_values_in_many_small_units(fmt):
     g = np.random.default_rng(4)
     new = [int(n) for n in g.choice([20, 40], 700)]            # 80 or 160 rows per KV head
     s = Setup(new, new, hq=8, hk=2, dim=64, page=16, fmt=fmt, seed=9)
-    q = s.queries("bf16")
+    q = s.queries(fmt)
     clean, _ = s.attend(q)
     hit = [r for r in range(700) if g.random() < 0.3]
     for r in hit:                                              # token 10 on see it, and KV head 0 only
