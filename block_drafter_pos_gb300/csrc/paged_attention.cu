@@ -19,8 +19,8 @@
 //    costing the third buffer.)
 //  * 16-bit caches feed mma.sync through ldmatrix.  8-bit codes are exact in fp16, so both
 //    products run on fp16 codes: the keys' scale multiplies the score, and the values'
-//    scale the weight, relative to the largest scale seen (so the fp16 weight cannot
-//    overflow and loses at most 2^-25 of the largest); the queries are rounded to fp16
+//    scale the weight, relative to a power of two near the largest scale that the row sees (so the fp16
+//    weight cannot overflow and loses at most 2^-25 of the largest); the queries are rounded to fp16
 //    after an exact power-of-two shift of their row.  A lane loads the codes as 16-byte
 //    pieces and the contraction order (keys) and the output columns (values) are permuted
 //    to match, so no code passes through shared memory twice.
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 
   uint32_t qf[kSteps][4];
   float o[NT][4];
-  float m0 = 0, m1 = 0, l0 = 0, l1 = 0, sc0 = 0, sc1 = 0, vref = 0, vinv = 0;
+  float m0 = 0, m1 = 0, l0 = 0, l1 = 0, sc0 = 0, sc1 = 0, vref0 = 0, vref1 = 0;
   int hi0 = 0, hi1 = 0, lo0 = 0, lo1 = 0, base = 0;       // visible keys of this thread's two rows
   int hi_min = 0, lo_max = 0;                             // keys in [lo_max, hi_min) are visible to every row
   bool mixed_rows = false;
@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 #pragma unroll
       for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
       m0 = m1 = -INFINITY;
-      l0 = l1 = vref = 0.f;
+      l0 = l1 = 0.f;
+      vref0 = vref1 = 0x1p-126f;
     }
 
     cp_wait<S - 2>();
@@ -455,20 +456,41 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     // a row that has seen nothing keeps weights of zero: 2^(-inf - 0)
     const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
     if constexpr (kQuant) {
-      // the values' reference: the largest finite scale of this warp's keys, raised when one exceeds 16 of it
-      float v = 0.f;
+      // the row's reference follows the largest finite scale of this warp's keys that the row sees, when that exceeds 16
+      // of it; where rows differ each looks at its own keys (one that it does not see costs it nothing)
+      float v0 = 0.f, v1 = 0.f;
+      if (masked && mixed_rows) {
 #pragma unroll
-      for (int i = 0; i < WK; i += 32) {
-        const float y = vsc[kw + i + lane];
-        v = y < INFINITY ? fmaxf(v, y) : v;
+        for (int t = 0; t < WK / 8; ++t) {
+          const float2 f = *reinterpret_cast<const float2*>(vsc + kw + 8 * t + 2 * q);
+          const float fx = f.x < INFINITY ? f.x : 0.f, fy = f.y < INFINITY ? f.y : 0.f;
+          if (z[t][0] != -INFINITY) v0 = fmaxf(v0, fx);
+          if (z[t][1] != -INFINITY) v0 = fmaxf(v0, fy);
+          if (z[t][2] != -INFINITY) v1 = fmaxf(v1, fx);
+          if (z[t][3] != -INFINITY) v1 = fmaxf(v1, fy);
+        }
+#pragma unroll
+        for (int of = 1; of <= 2; of <<= 1) {
+          v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, of));
+          v1 = fmaxf(v1, __shfl_xor_sync(0xffffffffu, v1, of));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < WK; i += 32) {
+          const float y = vsc[kw + i + lane];
+          v0 = y < INFINITY ? fmaxf(v0, y) : v0;
+        }
+        v0 = v1 = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v0)));  // (ordered as the floats from 0 are)
       }
-      if (__any_sync(0xffffffffu, v > 16.f * vref || (vref == 0.f && v > 0.f))) {
-        v = fmaxf(warp_max(v), 1.17549435e-38f);
-        const float f = vref / v;
-        vref = v;
-        vinv = 1.f / v;
-        f0 *= f;
-        f1 *= f;
+      if (v0 > 16.f * vref0) {
+        const float v = scale_reference(v0);
+        f0 *= vref0 * pow2_inverse(v);
+        vref0 = v;
+      }
+      if (v1 > 16.f * vref1) {
+        const float v = scale_reference(v1);
+        f1 *= vref1 * pow2_inverse(v);
+        vref1 = v;
       }
     }
     if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
@@ -481,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       }
     }
     // ---- weights and the values' product
+    const float vinv0 = pow2_inverse(vref0), vinv1 = pow2_inverse(vref1);
 #pragma unroll
     for (int t = 0; t < WK / 8; ++t) {
       const float p0 = ex2(z[t][0] - ref0), p1 = ex2(z[t][1] - ref0), p2 = ex2(z[t][2] - ref1), p3 = ex2(z[t][3] - ref1);
@@ -488,11 +511,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       l1 += p2 + p3;
       z[t][0] = p0, z[t][1] = p1, z[t][2] = p2, z[t][3] = p3;
       if constexpr (kQuant) {
-        float2 f = *reinterpret_cast<const float2*>(vsc + kw + 8 * t + 2 * q);
-        f.x *= vinv;
-        f.y *= vinv;
-        z[t][0] *= f.x, z[t][1] *= f.y;
-        z[t][2] *= f.x, z[t][3] *= f.y;
+        const float2 f = *reinterpret_cast<const float2*>(vsc + kw + 8 * t + 2 * q);
+        z[t][0] *= f.x * vinv0, z[t][1] *= f.y * vinv0;
+        z[t][2] *= f.x * vinv1, z[t][3] *= f.y * vinv1;
         if (masked) {  // (a masked position's scale may be anything)
           if (p0 == 0.f) z[t][0] = 0.f;
           if (p1 == 0.f) z[t][1] = 0.f;
@@ -604,9 +625,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     if (cc.unit_ends() || last) {
       if constexpr (kQuant) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[t][e] *= vref;
+        for (int t = 0; t < NT; ++t) {
+          o[t][0] *= vref0, o[t][1] *= vref0;
+          o[t][2] *= vref1, o[t][3] *= vref1;
+        }
       }
 #pragma unroll
       for (int of = 1; of <= 2; of <<= 1) {

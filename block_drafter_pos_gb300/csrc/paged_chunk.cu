@@ -18,8 +18,8 @@
 //  * Warps 9 - 11 bring the keys and values: cp.async of 16-byte pieces through the page table
 //    (any page size; its rows are looked up one tile ahead), or, for 8-bit caches, cp.async of the
 //    codes into a staging area from which the same thread writes them as exact fp16 values.  The
-//    keys' scale multiplies the score and the values' scale the weight, relative to a
-//    reference the loaders raise when a scale exceeds 16 of it.
+//    keys' scale multiplies the score and the values' scale the weight, relative to a power of
+//    two that a row raises when a scale that it sees exceeds 16 of it.
 //  * Every wait is bounded; one that gives up sets the requests' status and ends the CTA
 //    once its own copies and products are done.
 //
@@ -49,6 +49,10 @@ constexpr int kSoftRegs = 200, kOtherRegs = 56;  // 256 threads each: the 512 x 
 constexpr int kBN = kChunkBn;      // keys per tile
 constexpr int kM = 128;            // rows per tile
 constexpr float kGrow = 8.f;       // log2 of the largest weight
+// References of the values' scales in a wide tile (below).  A row's is at least 2^-112: weights over it, and sums of 128 of
+// them, stay finite, and what smaller values lose in fp16 weights is below 2^-126.  The tile's is at most 2^20, so that the
+// weights of rows with references from 2^-92 to 2^120 are summed over it.
+constexpr float kLeastRef = 0x1p-112f, kMostRef = 0x1p20f;
 
 template <int D, int FMT>
 struct ChunkGeo {
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   // grow, so a row tile that is still at an older unit finds at worst a newer one's, and looks in vain.
   __shared__ int poison_sh[G::kRing];
   __shared__ long long tmp[kThreads / 32 + 1];
-  __shared__ float vmax_sh[2][4];
+  __shared__ float vmax_sh[2][4], vmin_sh[2][4];
   __shared__ int flag_sh[2][4];
   static_assert(256 * (kSoftRegs + kOtherRegs) == kThreads * 128, "the register split");
   const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -312,6 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full + 8 * t);
     };
+    // The columns of the key tile at key0 that the row sees, one bit each.
+    auto visible = [&](int key0, int flags, const uint32_t* badw, unsigned long long& v0, unsigned long long& v1) {
+      v0 = columns_below(hi - key0) & ~columns_below(lo - key0);
+      v1 = columns_below(hi - key0 - 64) & ~columns_below(lo - key0 - 64);
+      if (a.s.causal == 2) {
+        const int d = um.base - key0;  // the column of the tree's first token
+        v0 &= columns_below(d) | columns_shifted(word, d);
+        v1 &= columns_below(d - 64) | columns_shifted(word, d - 64);
+      }
+      if (flags & 1) {
+        v0 &= ~(static_cast<unsigned long long>(badw[1]) << 32 | badw[0]);
+        v1 &= ~(static_cast<unsigned long long>(badw[3]) << 32 | badw[2]);
+      }
+    };
     enter(cc);
     while (cc.valid() && ok) {
       const int piece = cc.piece();
@@ -357,18 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         const bool masked = um.masked(key0) || (fl.x & 1);
         if (masked) {
-          // the columns that the row sees, one bit each
-          unsigned long long v0 = columns_below(hi - key0) & ~columns_below(lo - key0);
-          unsigned long long v1 = columns_below(hi - key0 - 64) & ~columns_below(lo - key0 - 64);
-          if (a.s.causal == 2) {
-            const int d = um.base - key0;  // the column of the tree's first token
-            v0 &= columns_below(d) | columns_shifted(word, d);
-            v1 &= columns_below(d - 64) | columns_shifted(word, d - 64);
-          }
-          if (fl.x & 1) {
-            v0 &= ~(static_cast<unsigned long long>(badw[1]) << 32 | badw[0]);
-            v1 &= ~(static_cast<unsigned long long>(badw[3]) << 32 | badw[2]);
-          }
+          unsigned long long v0, v1;
+          visible(key0, fl.x, badw, v0, v1);
           const uint32_t vw[4] = {static_cast<uint32_t>(v0), static_cast<uint32_t>(v0 >> 32), static_cast<uint32_t>(v1),
                                   static_cast<uint32_t>(v1 >> 32)};
 #pragma unroll
@@ -393,10 +401,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           m = mx;
           l *= f;
         }
+        // The values' scales are relative to the tile's reference, which is the unit's, and so is O: unless rows of the
+        // tile differ and a scale in it exceeds 16 of that.  Then (a wide tile) each row takes a reference of its
+        // own, at the largest scale that it sees, so that one it does not see costs it nothing; and it goes back to the unit's
+        // in the next tile, if that is not so far below that the weights there are nothing beside it.
+        float rowe = 0.f, rowi = 1.f;  // the tile's reference over the row's: its exponent, which the weights take, and the reciprocal
         if constexpr (kQuant) {
-          const float v = __int_as_float(fl.y);
-          if (j != 0 && v != vref) f *= vref / v;
-          vref = v;
+          const float tref = __int_as_float(fl.y);
+          if (j == 0) vref = tref;
+          if (vref != tref || (fl.x & 2)) {
+            float v = vref > 0x1p64f * tref ? vref : tref;
+            if (fl.x & 2) {
+              unsigned long long v0, v1;
+              visible(key0, fl.x, badw, v0, v1);
+              v = 0.f;
+#pragma unroll 1
+              for (int x = 0; x < 128; x += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(vf + x);
+                const uint32_t b = static_cast<uint32_t>((x < 64 ? v0 : v1) >> (x & 63));
+                v = fmaxf(v, fmaxf(fmaxf(b & 1 ? w.x : 0.f, b & 2 ? w.y : 0.f), fmaxf(b & 4 ? w.z : 0.f, b & 8 ? w.w : 0.f)));
+              }
+              v = scale_reference(fmaxf(v * tref, kLeastRef * fmaxf(tref, 1.f)));
+              if (j != 0 && v <= 16.f * vref) v = vref;
+            }
+            if (j != 0) f *= vref * pow2_inverse(v);
+            vref = v;
+            // (at less than 2^-60 no weight is above fp16's least, unless the factors are large)
+            const float r = fmaxf(tref * pow2_inverse(v), tref < kMostRef ? 0x1p-60f : 0x1p-126f);
+            rowe = pow2_exponent(r);
+            rowi = pow2_inverse(r);
+          }
         }
         if (__any_sync(0xffffffffu, f != 1.f)) {
           ok = mbar_wait(o_done + 8 * t, static_cast<uint32_t>((n - 1) & 1));
@@ -416,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
         }
         // ---- weights (a row that has seen nothing: 2^(-infinity)), announced by halves
-        const float mr = m == -INFINITY ? 0.f : -m;
+        const float mr0 = m == -INFINITY ? 0.f : -m, mr = kQuant ? mr0 + rowe : mr0;
         float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
         const float2 sc2 = make_float2(sc, sc), mr2 = make_float2(mr, mr);
 #pragma unroll
@@ -461,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           if (lane == 0) mbar_arrive(p_full + 8 * (2 * t + x));
         }
         acc0 = add2(acc0, acc1);
-        l += acc0.x + acc0.y;
+        l += (acc0.x + acc0.y) * (kQuant ? rowi : 1.f);
         ++n;
       }
       if (!ok) break;
@@ -572,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           fence_before();  // O has been read before this tile's next weights are announced
         }
         m = -INFINITY;
-        l = vref = 0.f;
+        l = 0.f;
       }
       ++gunit;
       gtile += piece;
@@ -691,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         l_first = lc.unit_ends();
         lc.next(a);
       };
-      float vref = 0.f, vinv = 0.f;
+      float vref = 0.f;
       look_up();
       // A thread copies piece ch of rows r0, r0 + kStep, ...: the swizzle's row bits are its own constant.
       constexpr int kPieces = D * (kQuant ? 1 : 2) / 16, kStep = kLoaders / kPieces, kCount = 128 / kStep;
@@ -742,13 +776,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         long long* o = offs + (j & 1) * 128;
         if (piece_first) {
           if (j > 0) ++unit;
-          vref = 0.f;
+          vref = 0x1p-126f;
         }
         // (The slot's previous tile was eight tiles ago: operands up to that of tile j - 5 have been read, or this
         // thread could not be here, so the weights of tile j - 5 are done.)
         if constexpr (kQuant) {
           const float v = warp_max(vsv < INFINITY ? vsv : 0.f);
-          if (lane == 0) vmax_sh[j & 1][wid - 8] = v;
+          // (keys outside the unit's range count as 0 there and not at all here)
+          const float w = -warp_max(vsv > 0.f && vsv < INFINITY ? -vsv : -0x1p126f);
+          if (lane == 0) vmax_sh[j & 1][wid - 8] = v, vmin_sh[j & 1][wid - 8] = w;
         }
         o[lt] = off;
         const uint32_t b = __ballot_sync(0xffffffffu, badv);
@@ -757,21 +793,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           flag_sh[j & 1][wid - 8] = b ? 1 : 0;
         }
         loaders_sync();
-        if (lt == 0) badw[4] = flag_sh[j & 1][0] | flag_sh[j & 1][1] | flag_sh[j & 1][2] | flag_sh[j & 1][3];
+        uint32_t flags = flag_sh[j & 1][0] | flag_sh[j & 1][1] | flag_sh[j & 1][2] | flag_sh[j & 1][3];  // 1: bad pages, 2: wide
         if constexpr (kQuant) {
           const float* vm = vmax_sh[j & 1];
           const float v = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
-          if (vref == 0.f || v > 16.f * vref) {
-            vref = fmaxf(v, 1.17549435e-38f);
-            vinv = 1.f / vref;
+          bool wide = false;
+          if (mixed) {
+            // (a unit's first: relative to the least scale in it)
+            const float* vl = vmin_sh[j & 1];
+            if (piece_first) vref = scale_reference(fminf(fminf(vl[0], vl[1]), fminf(vl[2], vl[3])));
+            wide = v > 16.f * vref;
+          } else if (piece_first || v > 16.f * vref) {
+            vref = scale_reference(v);
           }
+          const float tref = wide ? fminf(scale_reference(v), kMostRef) : vref;
           ks[lt] = ksv;
           // (a scale that is not finite counts as 0 here; the rows that see it add the products at the end)
           const bool finite = fabsf(vsv) < INFINITY;
-          ks[128 + lt] = finite ? vsv * vinv : 0.f;
+          ks[128 + lt] = finite ? vsv * pow2_inverse(tref) : 0.f;
           if (!finite) poison_sh[unit % G::kRing] = unit + 1;
-          if (lt == 0) ks[256 + 5] = vref;
+          if (lt == 0) ks[256 + 5] = tref;
+          if (wide) flags |= 2;
         }
+        if (lt == 0) badw[4] = flags;
         mbar_arrive(info + 8 * ring);
         const bool mixed_now = mixed;
         const int unit_now = unit;

@@ -95,4 +95,13 @@ DF2_DEV float pow2_shift(float x) {
   return ex == 0 || ex >= 254 ? 1.f : __uint_as_float((254u - ex) << 23);
 }
 
+// The values' reference: weights of an 8-bit cache are multiplied by their value's scale relative to it.  A power of
+// two, so that its reciprocal (pow2_inverse) and every change of it are exact: the one at a scale, within
+// [2^-126, 2^126].
+DF2_DEV float scale_reference(float v) {
+  return __uint_as_float(__float_as_uint(fminf(fmaxf(v, 0x1p-126f), 0x1p126f)) & 0x7F800000u);
+}
+DF2_DEV float pow2_inverse(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
+DF2_DEV float pow2_exponent(float x) { return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127); }
+
 }  // namespace df2

@@ -1,22 +1,25 @@
-"""Places where the target's side of a step can go wrong."""
-
+"""Places where the target's side of a step can go wrong: what a row does not see, calls whose ranges are
+partly bad, and decisions of the sampling that lie exactly on a border."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_target import Setup
+import block_drafter_pos_gb300 as bd
+from oracle import target as ot
+from test_gpu_target import DT, Setup, check_attention
 
 pytestmark = pytest.mark.gpu
 
+
 # ----------------------------------------------------------------------------- what a row does not see
 
-@pytest.mark.parametrize("fmt", ["bf16", "fp16"])
+@pytest.mark.parametrize("fmt", ["bf16", "fp16", "int8"])
 def test_nonfinite_values_in_many_small_units(fmt):
     """Units of one and of two row tiles after one another in a CTA, nonfinite values in some of them."""
     g = np.random.default_rng(4)
     new = [int(n) for n in g.choice([20, 40], 700)]            # 80 or 160 rows per KV head
     s = Setup(new, new, hq=8, hk=2, dim=64, page=16, fmt=fmt, seed=9)
-    q = s.queries(fmt)
+    q = s.queries("bf16" if fmt in ot.QMAX else fmt)
     clean, _ = s.attend(q)
     hit = [r for r in range(700) if g.random() < 0.3]
     for r in hit:                                              # token 10 on see it, and KV head 0 only
@@ -31,4 +34,102 @@ def test_nonfinite_values_in_many_small_units(fmt):
             at += n
         got = out.cpu()
         assert torch.isnan(got[seen].float()).all() and torch.equal(got[~seen], clean.cpu()[~seen])
+    s.close()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [8, 9, 140])
+@pytest.mark.parametrize("power", [14, 30, 100])
+def test_a_large_value_that_a_row_does_not_see(fmt, n, power):
+    """A later token's value 2^power times the others': the rows before it do not notice, nor do rows whose window has
+    left it (held to bounds over what they see), and the rows that see it are right."""
+    length, first = 200, 200 - n + n // 2
+    s = Setup([n], [length], hq=4, hk=2, fmt=fmt, seed=n)
+    q = s.queries("bf16")
+    clean, lse0 = s.attend(q)
+    narrow, _ = s.attend(q, window=3)
+    vals = [[x.copy() for x in s.vals[0]]]                     # of the rows that do not see it
+    hidden = torch.ones(n, dtype=torch.bool)
+    hidden[n // 2:n // 2 + 3] = False
+    s.gvs[int(s.table[0, first // 16]), first % 16, 1] *= 2.0 ** power
+    s.vals[0][1][first, 1] *= 2.0 ** power
+    out, lse = s.attend(q)
+    assert torch.equal(out[:, :2], clean[:, :2])
+    check_attention(s, q, out, lse)
+    check_attention(s, q, torch.cat([out[:n // 2], clean[n // 2:]]), torch.cat([lse[:n // 2], lse0[n // 2:]]), vals=vals)
+    out, _ = s.attend(q, window=3)
+    assert torch.equal(out[:, :2], narrow[:, :2])
+    check_attention(s, q, out, None, window=3)
+    narrow[hidden] = out[hidden]
+    check_attention(s, q, narrow, None, window=3, vals=vals)
+    s.close()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [6, 64])
+def test_a_large_value_in_another_branch(fmt, n):
+    """Written through the cache: a node's value 2^30 times the others' shows below it in the tree and nowhere else."""
+    s = Setup([n], [n + 100], hq=4, hk=2, fmt=fmt, seed=n)
+    g = np.random.default_rng(n)
+    words = [1]
+    for i in range(1, n):
+        words.append(words[int(g.integers(0, i))] | (1 << i))
+    words[1] = 3                                               # node 1 hangs on the root
+    tree = np.array(words, np.uint64)
+    below = torch.tensor([bool(w >> 1 & 1) for w in words])
+    t = torch.from_numpy(tree.view(np.int64)).cuda()
+    k, v = (torch.from_numpy(g.standard_normal((n, 2, 128)).astype(np.float32)).cuda() for _ in "kv")
+    q = s.queries("bf16")
+    got = []
+    for factor in (2.0 ** 30, 1.0):
+        v2 = v.clone()
+        v2[1] *= factor
+        bd.dflash2_paged_write(s.handle, s.cache, k, v2, s.begin, s.kv_len)
+        got.append(s.attend(q, tree_mask=t)[0])
+    for i, (x, fine) in enumerate(((k, s.vals[0][0]), (v, s.vals[0][1]))):
+        codes, scale = ot.quantise(x.cpu().numpy(), fmt)
+        fine[100:] = codes * scale[..., None].astype(np.float64)
+    assert below.any() and not below.all() and (got[0][below].float().abs().amax((1, 2)) > 1e3).all()
+    got[0][below] = got[1][below]
+    for out in got:
+        check_attention(s, q, out, None, tree=tree)
+    s.close()
+
+
+def test_rows_that_saw_a_large_value_before_a_small_one():
+    """Long contexts whose scales rise and fall by 2^12 from tile to tile, windows and prompts among them."""
+    for n, window in ((4, 0), (4, 300), (150, 0), (150, 300)):
+        s = Setup([n, n], [900, 1300], hq=4, hk=2, dim=64, page=32, fmt="e4m3", seed=n)
+        for r, length in enumerate(s.length):
+            f = np.exp2(12.0 * np.sin(np.arange(length) / 90.0)).astype(np.float32)
+            pos = np.arange(length)
+            pages = torch.from_numpy(s.table[r][pos // 32].astype(np.int64)).cuda()
+            s.gvs[pages, torch.from_numpy(pos % 32).cuda()] *= torch.from_numpy(f).cuda()[:, None]
+            s.vals[r][1] *= f[:, None, None].astype(np.float64)
+        q = s.queries("fp16")
+        out, lse = s.attend(q, window=window)
+        check_attention(s, q, out, lse, window=window)
+        s.close()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,length,window", [(7, 40, 0), (140, 140, 0), (140, 700, 33)])
+def test_value_rows_of_zeros(fmt, n, length, window):
+    """Rows of zeros have the least scale, next to scales of the ordinary size and of 2^-60 of it."""
+    s = Setup([n], [length], hq=4, hk=2, fmt=fmt, seed=n)
+    g = np.random.default_rng(n)
+    kind = g.integers(0, 3, length)
+    for p in range(length):
+        page, row = int(s.table[0, p // 16]), p % 16
+        if kind[p] == 0:
+            s.gv[page, row] = torch.zeros(2, 128).to(DT[fmt]).cuda()
+            s.gvs[page, row] = 2.0 ** -126
+            s.vals[0][1][p] = 0
+        elif kind[p] == 1:
+            s.gvs[page, row] *= 2.0 ** -60
+            s.vals[0][1][p] *= 2.0 ** -60
+    q = s.queries("bf16")
+    for causal in (True, False):
+        out, lse = s.attend(q, window=window, causal=causal)
+        check_attention(s, q, out, lse, causal=causal, window=window)
     s.close()
