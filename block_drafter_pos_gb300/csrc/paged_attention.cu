@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   uint32_t qf[kSteps][4];
   float o[NT][4];
   float m0 = 0, m1 = 0, l0 = 0, l1 = 0, sc0 = 0, sc1 = 0, vref0 = 0, vref1 = 0;
+  uint32_t nan0 = 0, nan1 = 0;  // channels of the two rows with a code of NaN that they see
   int hi0 = 0, hi1 = 0, lo0 = 0, lo1 = 0, base = 0;       // visible keys of this thread's two rows
   int hi_min = 0, lo_max = 0;                             // keys in [lo_max, hi_min) are visible to every row
   bool mixed_rows = false;
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
       vref0 = vref1 = 0x1p-126f;
+      nan0 = nan1 = 0;
     }
 
     cp_wait<S - 2>();
@@ -414,17 +416,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       z[t][0] *= sc0 * f.x, z[t][1] *= sc0 * f.y;
       z[t][2] *= sc1 * f.x, z[t][3] *= sc1 * f.y;
     }
+    auto sees = [&](int key, bool& v0, bool& v1) {  // this thread's two rows
+      v0 = key >= lo0 && key < hi0, v1 = key >= lo1 && key < hi1;
+      if (a.s.causal == 2 && key >= base) {
+        v0 = v0 && ((w0 >> ((key - base) & 63)) & 1ull);
+        v1 = v1 && ((w1 >> ((key - base) & 63)) & 1ull);
+      }
+    };
     if (masked) {
 #pragma unroll
       for (int t = 0; t < WK / 8; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int kk = kw + 8 * t + 2 * q + e, key = key0 + kk;
-          bool v0 = key >= lo0 && key < hi0, v1 = key >= lo1 && key < hi1;
-          if (a.s.causal == 2 && key >= base) {
-            v0 = v0 && ((w0 >> ((key - base) & 63)) & 1ull);
-            v1 = v1 && ((w1 >> ((key - base) & 63)) & 1ull);
-          }
+          const int kk = kw + 8 * t + 2 * q + e;
+          bool v0, v1;
+          sees(key0 + kk, v0, v1);
           if (any_bad && offs[sl_now * kBN + kk] < 0) v0 = v1 = false;
           z[t][e] = v0 ? z[t][e] : -INFINITY;
           z[t][2 + e] = v1 ? z[t][2 + e] : -INFINITY;
@@ -522,10 +528,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
     }
-    // 16-bit values may be infinities or NaN at positions that only some rows see: there the
-    // product takes zeros in their place, and each is added to the rows whose weight for it is not zero
+    // Values may be infinities or NaN (8 bits: codes of NaN) at positions that only some rows see: there the
+    // product takes zeros in their place, and each is added to the rows whose weight for it is not zero (8 bits: noted
+    // for the rows that see it)
     bool poison = false;
-    if constexpr (!kQuant) {
+    if constexpr (!kQuant || FMT == kKvE4m3) {
       if (masked && mixed_rows) {
         bool bad_v = false;
         constexpr uint32_t ex = kBF ? 0x7F80u : 0x7C00u;
@@ -533,9 +540,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           const uint4 w = lds16(vs + kw * G::kRowBytes + i * 16);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) bad_v |= (ww[u] & ex) == ex || ((ww[u] >> 16) & ex) == ex;
+          for (int u = 0; u < 4; ++u)
+            bad_v |= kQuant ? nan_codes(ww[u]) != 0 : (ww[u] & ex) == ex || ((ww[u] >> 16) & ex) == ex;
         }
-        poison = __any_sync(0xffffffffu, bad_v);
+        poison = kQuant ? __syncthreads_or(bad_v) != 0 : __any_sync(0xffffffffu, bad_v) != 0;
       }
     }
     if (poison) {
@@ -564,6 +572,34 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
             }
           }
         }
+      } else {
+        // this thread's channels, D / 8 from (D / 8) (2 q + e) on, in the rows that see them; then zeros in the codes' place
+#pragma unroll 1
+        for (int kk = kw; kk < kw + WK; ++kk) {
+          bool v0, v1;
+          sees(key0 + kk, v0, v1);
+#pragma unroll 1
+          for (int c = 0; c < NT / 2; ++c) {  // words
+            const int cw = q * (NT / 2) + c;
+            uint32_t x;
+            asm volatile("ld.shared.u32 %0, [%1];"
+                         : "=r"(x)
+                         : "r"(vs + kk * G::kRowBytes + (((cw >> 2) ^ (D == 128 ? kk & 6 : (kk >> 1) & 3)) << 4) + ((cw & 3) << 2))
+                         : "memory");
+            x = nan_codes(x) & 0x08040201u;
+            const uint32_t bits = ((x | x >> 8) | (x | x >> 8) >> 16) & 15u;
+            if (v0) nan0 |= bits << (4 * c);
+            if (v1) nan1 |= bits << (4 * c);
+          }
+        }
+        __syncthreads();
+        for (int i = tid; i < kBN * G::kChunks; i += kThreads) {
+          const uint4 w = lds16(vs + i * 16);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(vs + i * 16), "r"(w.x & ~nan_codes(w.x)),
+                       "r"(w.y & ~nan_codes(w.y)), "r"(w.z & ~nan_codes(w.z)), "r"(w.w & ~nan_codes(w.w))
+                       : "memory");
+        }
+        __syncthreads();
       }
     }
     {
@@ -628,6 +664,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         for (int t = 0; t < NT; ++t) {
           o[t][0] *= vref0, o[t][1] *= vref0;
           o[t][2] *= vref1, o[t][3] *= vref1;
+        }
+        if (FMT == kKvE4m3 && (nan0 | nan1)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if ((nan0 >> (e * NT + t)) & 1u) o[t][e] = NAN;
+              if ((nan1 >> (e * NT + t)) & 1u) o[t][2 + e] = NAN;
+            }
         }
       }
 #pragma unroll

@@ -544,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             tm_ld32(o_col + 32 * x, o);
             tm_wait_ld();
             if (poison && valid) {
-              // values that are not finite: the product had zeros there (16 bits: in tiles where rows differ;
-              // 8 bits: where the scale is not finite)
+              // values that are not finite: the product had zeros there (16 bits, and 8-bit codes of NaN: in tiles where
+              // rows differ; 8 bits: where the scale is not finite)
               const int first_i = cc.unit_t >= t_begin ? 0 : static_cast<int>(t_begin - cc.unit_t);
               for (int ti = first_i; ti <= i_last; ++ti) {
                 const int k0 = (cc.u.t0 + ti) * kBN;
@@ -557,11 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                   if (!paged_row(a.c, page, key % a.c.page_size, cc.h, &off, &so)) continue;
                   if constexpr (kQuant) {
                     const float vs = __ldg(a.c.v_scale + so);
-                    if (fabsf(vs) < INFINITY) continue;
+                    const bool fine = fabsf(vs) < INFINITY;
+                    if (fine && !(FMT == kKvE4m3 && old_um.mixed && old_um.masked(k0))) continue;
                     const uint32_t* v = reinterpret_cast<const uint32_t*>(a.c.v + off + 32 * x);
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
-                      const uint32_t w = __ldg(v + y);
+                      uint32_t w = __ldg(v + y);
+                      if (fine) w &= nan_codes(w);  // (of the other codes 0)
                       const float2 v0 = unpack2<false>(codes2<FMT, 0>(w)), v1 = unpack2<false>(codes2<FMT, 1>(w));
                       o[4 * y] += v0.x * vs, o[4 * y + 1] += v0.y * vs, o[4 * y + 2] += v1.x * vs, o[4 * y + 3] += v1.y * vs;
                     }
@@ -744,10 +746,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         const int use = idx / NS;
         return use == 0 || mbar_wait(empty + 8 * (idx % NS), static_cast<uint32_t>((use + 1) & 1));
       };
-      // 8-bit: this thread's codes of operand idx from the staging area to its slot
+      // 8-bit: this thread's codes of operand idx from the staging area to its slot; values that only some rows see without
+      // codes of NaN (the rows that see them add them at the end)
+      int tile = 0;                              // the tile looked up last; of it (bit 0) and those before:
+      uint32_t mixed_bits = 0, first_bits = 0;   // whether rows differ in it, and whether a unit (but the first) begins
       auto convert = [&](int idx) {
         if (!freed(idx)) return false;
         if constexpr (kQuant) {
+          const int age = tile - (idx >> 1);
+          const bool strip = FMT == kKvE4m3 && (idx & 1) && ((mixed_bits >> age) & 1u);
+          bool found = false;
           const uint32_t st = sbase + G::kOffStage + (idx % BUFS) * G::kStage + lt * 16;
           const uint32_t dst = sbase + G::kOffRing + (idx % NS) * G::kTile;
 #pragma unroll
@@ -755,12 +763,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             uint4 w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) w[x] = lds128(st + (x0 + x) * (kLoaders * 16));
+            if (strip) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint4 z = make_uint4(nan_codes(w[x].x), nan_codes(w[x].y), nan_codes(w[x].z), nan_codes(w[x].w));
+                found |= (z.x | z.y | z.z | z.w) != 0;
+                w[x] = make_uint4(w[x].x & ~z.x, w[x].y & ~z.y, w[x].z & ~z.z, w[x].w & ~z.w);
+              }
+            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const uint32_t d = dst + (x0 + x) * (kStep * 128);
               sts128(d + put0, make_uint4(codes2<FMT, 0>(w[x].x), codes2<FMT, 1>(w[x].x), codes2<FMT, 0>(w[x].y), codes2<FMT, 1>(w[x].y)));
               sts128(d + put1, make_uint4(codes2<FMT, 0>(w[x].z), codes2<FMT, 1>(w[x].z), codes2<FMT, 0>(w[x].w), codes2<FMT, 1>(w[x].w)));
             }
+          }
+          if (found) {
+            const int u = unit - __popc(first_bits & ((1u << age) - 1u));  // the tile's unit
+            poison_sh[u % G::kRing] = u + 1;
           }
         }
         landed(idx);
@@ -778,6 +798,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           if (j > 0) ++unit;
           vref = 0x1p-126f;
         }
+        tile = j;
+        mixed_bits = mixed_bits << 1 | (mixed ? 1u : 0u);
+        first_bits = first_bits << 1 | (piece_first && j > 0 ? 1u : 0u);
         // (The slot's previous tile was eight tiles ago: operands up to that of tile j - 5 have been read, or this
         // thread could not be here, so the weights of tile j - 5 are done.)
         if constexpr (kQuant) {

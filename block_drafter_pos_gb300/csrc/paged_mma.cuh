@@ -88,6 +88,9 @@ DF2_DEV uint32_t codes2(uint32_t w) {
   }
 }
 
+// Ones in the bytes of w that are e4m3 codes of NaN (0x7F and 0xFF).
+DF2_DEV uint32_t nan_codes(uint32_t w) { return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu; }
+
 // 2^-e with x in [2^e, 2^(e + 1)); 1 for zero, tiny and nonfinite x.  Rows of queries are brought to
 // fp16's range with it, exactly.
 DF2_DEV float pow2_shift(float x) {

@@ -133,3 +133,44 @@ def test_value_rows_of_zeros(fmt, n, length, window):
         out, lse = s.attend(q, window=window, causal=causal)
         check_attention(s, q, out, lse, causal=causal, window=window)
     s.close()
+
+
+@pytest.mark.parametrize("n", [8, 140])
+@pytest.mark.parametrize("byte", [0x7F, 0xFF])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_code_that_is_no_number(n, byte, dim):
+    """An e4m3 NaN code in a value reaches its channel in the rows that see it and nothing else; in a key, those rows."""
+    length, c = 200, 37
+    first = length - n + n // 2
+    s = Setup([n], [length], hq=4, hk=2, dim=dim, fmt="e4m3", seed=n)
+    q = s.queries("bf16")
+    clean, _ = s.attend(q)
+    page, row = int(s.table[0, first // 16]), first % 16
+    others = [i for i in range(dim) if i != c]
+    for window in (0, 5):
+        base = clean if window == 0 else s.attend(q, window=window)[0]
+        sees = torch.zeros(n, dtype=torch.bool)
+        sees[n // 2:n if window == 0 else n // 2 + window] = True
+        for pool in (s.gv, s.gk):
+            keep = pool[page, row, 1].clone()
+            codes = keep.view(torch.uint8).clone()
+            codes[c] = byte
+            pool[page, row, 1] = codes.view(DT["e4m3"])
+            out, _ = s.attend(q, window=window)
+            pool[page, row, 1] = keep
+            assert torch.equal(out[~sees], base[~sees]) and torch.equal(out[:, :2], base[:, :2])
+            late = out[sees][:, 2:]
+            if pool is s.gv:
+                assert torch.isnan(late[..., c].float()).all()
+                assert torch.equal(late[..., others], base[sees][:, 2:][..., others])
+            else:
+                assert torch.isnan(late.float()).all()
+    # in a position that every row sees: the channel of every row
+    far = 3
+    pool = s.gv[int(s.table[0, 0]), far, 1]
+    codes = pool.view(torch.uint8).clone()
+    codes[c] = byte
+    s.gv[int(s.table[0, 0]), far, 1] = codes.view(DT["e4m3"])
+    out, _ = s.attend(q)
+    assert torch.isnan(out[:, 2:, c].float()).all() and torch.equal(out[:, 2:][..., others], clean[:, 2:][..., others])
+    s.close()
