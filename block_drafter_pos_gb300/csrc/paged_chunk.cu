@@ -279,8 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       uint4 w[D / 8];
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) w[x] = valid ? __ldg(p + x) : make_uint4(0, 0, 0, 0);
-      const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;    // (the score's factor stays positive)
-      sc = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);      // (so that a masked score stays -infinity at a scale of 0)
+      // The score's factor stays above 0, so that a masked score stays -infinity: the query takes the scale's sign, and a
+      // scale of 0 itself.
+      const float sign = a.scale_log2 == 0.f ? 0.f : (a.scale_log2 < 0.f ? -1.f : 1.f);
+      sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
       if constexpr (kQuant) {
         float x = 0.f;
 #pragma unroll
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
         }
         const float f = pow2_shift(x);
-        sc /= f;
+        sc = fmaxf(sc / f, 0x1p-149f);
 #pragma unroll
         for (int y = 0; y < D / 8; ++y) {
           uint32_t ww[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
@@ -304,6 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
           w[y] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
         }
+      } else if (sign == 0.f) {
+#pragma unroll
+        for (int y = 0; y < D / 8; ++y)
+          w[y] = make_uint4(times_zero2<kBF>(w[y].x), times_zero2<kBF>(w[y].y), times_zero2<kBF>(w[y].z), times_zero2<kBF>(w[y].w));
       } else if (sign < 0.f) {
 #pragma unroll
         for (int y = 0; y < D / 8; ++y)

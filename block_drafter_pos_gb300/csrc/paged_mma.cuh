@@ -51,6 +51,13 @@ DF2_DEV uint32_t finite2(uint32_t w) {
   return w;
 }
 
+// Two 16-bit values times zero: NaN for infinities and NaN.
+template <bool BF>
+DF2_DEV uint32_t times_zero2(uint32_t w) {
+  constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
+  return ((w & ex) == ex ? 0x7FFFu : 0u) | (((w >> 16) & ex) == ex ? 0x7FFF0000u : 0u);
+}
+
 // Two fp32 values at a time (the packed fp32 instructions of this architecture).
 DF2_DEV float2 fma2(float2 a, float2 b, float2 c) {
   unsigned long long d;

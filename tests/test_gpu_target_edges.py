@@ -174,3 +174,34 @@ def test_a_code_that_is_no_number(n, byte, dim):
     out, _ = s.attend(q)
     assert torch.isnan(out[:, 2:, c].float()).all() and torch.equal(out[:, 2:][..., others], clean[:, 2:][..., others])
     s.close()
+
+
+@pytest.mark.parametrize("fmt,amp,q_amp", [("e4m3", 1.0, 2.0 ** -40), ("int8", 1.0, 2.0 ** -100), ("e4m3", 1.0, 1.0), ("bf16", 1e36, 1.0),
+                                           ("fp16", 1.0, 1.0)])
+@pytest.mark.parametrize("n", [5, 140])
+def test_a_scale_of_zero_weighs_all_alike(fmt, amp, q_amp, n):
+    s = Setup([n], [200], hq=4, hk=2, fmt=fmt, seed=n, amp=amp)
+    q = s.queries("fp16" if fmt == "fp16" else "bf16", amp=q_amp)
+    for scale in (0.0, -0.0):
+        out, lse = s.attend(q, scale=scale)
+        check_attention(s, q, out, lse, scale=0.0)
+    out, lse = s.attend(q, scale=0.0, causal=False)
+    check_attention(s, q, out, lse, scale=0.0, causal=False)
+    for scale in (-0.05, 2.0 ** -60) if amp == 1.0 else ():
+        out, lse = s.attend(q, scale=scale)
+        check_attention(s, q, out, lse, scale=scale)
+    s.close()
+
+
+def test_a_scale_of_zero_and_queries_that_are_not_finite():
+    for fmt in ("bf16", "int8"):
+        for n in (5, 140):
+            s = Setup([n], [200], hq=4, hk=2, fmt=fmt, seed=n)
+            q = s.queries("bf16").cuda()
+            clean, _ = s.attend(q, scale=0.0)
+            q[2, 1, 7], q[3, 0, 9] = float("inf"), float("nan")
+            out, _ = s.attend(q, scale=0.0)
+            bad = torch.zeros(n, 4, dtype=torch.bool)
+            bad[2, 1] = bad[3, 0] = True
+            assert torch.isnan(out[bad].float()).all() and torch.equal(out[~bad], clean[~bad])
+            s.close()
