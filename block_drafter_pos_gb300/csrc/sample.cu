@@ -770,18 +770,41 @@ DF2_DEV void sample_row(const SampleArgs& a, int part, int few) {
     stays = w >= floor_w;  // (a weight of zero may stay: it is then never drawn)
     return stays ? w : 0ull;
   };
+  // In place, a cut logit is then no longer what it was: which ones stay is noted, a bit each.
+  const bool noted = kept && !fill;
+  uint32_t* const stay_bits = &shm.piece[0][0];
+  static_assert(sizeof(shm.piece) * 8 >= kSlice, "a bit for every element of a slice");
   unsigned long long mine = 0;
-  for (int i0 = c.wlo + lane; i0 < c.whi; i0 += 256) {
-    float x[8];
+  if (!noted) {
+    for (int i0 = c.wlo + lane; i0 < c.whi; i0 += 256) {
+      float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = i0 + 32 * e < c.whi ? load1<T>(src, i0 + 32 * e) : -INFINITY;
+      for (int e = 0; e < 8; ++e) x[e] = i0 + 32 * e < c.whi ? load1<T>(src, i0 + 32 * e) : -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 8; ++e) {
+        bool stays;
+        mine += left(i0 + 32 * e, x[e], stays);
+        if (kept && i0 + 32 * e < c.whi) kept[i0 + 32 * e] = stays ? x[e] : kCut;
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int b0 = c.wlo; b0 < c.whi; b0 += 32) {
+      const int i = b0 + lane;
+      const float x = i < c.whi ? load1<T>(src, i) : -INFINITY;
       bool stays;
-      mine += left(i0 + 32 * e, x[e], stays);
-      if (kept && i0 + 32 * e < c.whi) kept[i0 + 32 * e] = stays ? x[e] : kCut;
+      mine += left(i, x, stays);
+      if (i < c.whi) kept[i] = stays ? x : kCut;
+      const uint32_t m = __ballot_sync(0xffffffffu, stays);
+      if (lane == 0) stay_bits[b0 >> 5] = m;
     }
   }
+  auto again = [&](int i) -> unsigned long long {
+    const float x = load1<T>(src, i);
+    if (noted) return (stay_bits[i >> 5] >> (i & 31)) & 1u ? weight(x, s, pw) : 0ull;
+    bool stays;
+    return left(i, x, stays);
+  };
   mine = put_total(c, mine);
   c.cl.sync();
   unsigned long long total = 0, before = 0;
@@ -807,15 +830,12 @@ DF2_DEV void sample_row(const SampleArgs& a, int part, int few) {
     const int lo = min(c.n, static_cast<int>(shm.digit) * wper), hi = min(c.n, lo + wper);
     const int each = (wper + kThreads - 1) / kThreads, i0 = lo + threadIdx.x * each;
     unsigned long long part = 0, all;
-    for (int e = 0; e < each; ++e) {
-      bool stays;
-      if (i0 + e < hi) part += left(i0 + e, load1<T>(src, i0 + e), stays);
-    }
+    for (int e = 0; e < each; ++e)
+      if (i0 + e < hi) part += again(i0 + e);
     from = shm.before + block_scan(&shm, part, all);
     if (holds(from, part)) {
       for (int e = 0; e < each && i0 + e < hi; ++e) {
-        bool stays;
-        const unsigned long long w = left(i0 + e, load1<T>(src, i0 + e), stays);
+        const unsigned long long w = again(i0 + e);
         if (holds(from, w)) {
           a.token[row] = c.lo + i0 + e;
           if (a.prob) a.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));

@@ -6,7 +6,7 @@ import torch
 
 import block_drafter_pos_gb300 as bd
 from oracle import target as ot
-from test_gpu_target import DT, Setup, check_attention
+from test_gpu_target import DT, Setup, check_attention, run_sample
 
 pytestmark = pytest.mark.gpu
 
@@ -205,3 +205,34 @@ def test_a_scale_of_zero_and_queries_that_are_not_finite():
             bad[2, 1] = bad[3, 0] = True
             assert torch.isnan(out[bad].float()).all() and torch.equal(out[~bad], clean[~bad])
             s.close()
+
+
+# ----------------------------------------------------------------------------- sampling
+
+def _in_place(x, t, k, p, m, u):
+    n = x.shape[0]
+    f = lambda a, d: torch.as_tensor(np.asarray(a), dtype=d).cuda()  # noqa: E731
+    y = x.clone()
+    token, prob = torch.full((n,), -9, dtype=torch.int32, device="cuda"), torch.full((n,), -9.0, device="cuda")
+    bd.dflash2_sample(y, f(t, torch.float32), f(k, torch.int32), f(p, torch.float32), f(m, torch.float32), f(u, torch.float32),
+                      token, prob=prob, kept=y)
+    torch.cuda.synchronize()
+    return token.cpu().numpy(), prob.cpu().numpy(), y.cpu().numpy()
+
+
+@pytest.mark.parametrize("n,v", [(24, 9001), (24, 70001), (200, 40000)])
+@pytest.mark.parametrize("t", [1.0, 1e6, 1e30, 3e38])
+def test_kept_in_place_of_wide_rows(n, v, t):
+    """Rows whose nucleus is wide: the kept logits take the logits' place, and the draw is the one of the logits."""
+    g = np.random.default_rng(v)
+    x = torch.from_numpy((g.standard_normal((n, v)) * 0.5).astype(np.float32)).cuda()
+    x[:, ::7] = float("-inf")
+    u = np.minimum(((np.arange(n) + 0.5) / n).astype(np.float32), np.float32(1 - 2.0 ** -24))
+    for k, p, m in ((0, 0.6, 0.0), (0, 1.0, 0.0), (5000, 0.7, 0.0), (5000, 1.0, 0.5), (60, 0.9, 0.0)):
+        args = ([t] * n, [k] * n, [p] * n, [m] * n, u)
+        want = run_sample(x, *args)
+        got = _in_place(x, *args)
+        assert (want[3] == 0).all() and (want[2] > -1e29).sum() < x.numel()
+        for a, c in zip(got, want):
+            np.testing.assert_array_equal(a, c)
+
