@@ -18,8 +18,22 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Request of packed row t and the row's position in its cache; false if the request's
-// range or length is out of bounds (status set) or no request holds the row.
+// Whether request r can be served: its range and its length are within bounds, and its new tokens within its length.
+DF2_DEV bool good_request(const PagedReq& q, int r, int& b0, int& b1, int& len) {
+  b0 = __ldg(q.begin + r), b1 = __ldg(q.begin + r + 1), len = __ldg(q.kv_len + r);
+  return paged_request_ok(q, b0, b1, len) && len >= b1 - b0;
+}
+
+// The first block flags the requests that cannot be served.
+DF2_DEV void flag_requests(const PagedReq& q) {
+  if (blockIdx.x != 0 || !q.status) return;
+  int b0, b1, len;
+  for (int r = threadIdx.x; r < q.n_req; r += kThreads)
+    if (!good_request(q, r, b0, b1, len)) q.status[r] = 1;  // DFLASH2_E_INVAL
+}
+
+// Request of packed row t and the row's position in its cache; false if no good request holds the row.  A whole warp
+// calls it for one row.
 DF2_DEV bool find_position(const PagedReq& q, int t, int& r, int& pos) {
   int lo = 0, hi = q.n_req;  // the last r with begin[r] <= t
   while (hi - lo > 1) {
@@ -27,12 +41,20 @@ DF2_DEV bool find_position(const PagedReq& q, int t, int& r, int& pos) {
     if (__ldg(q.begin + mid) <= t) lo = mid;
     else hi = mid;
   }
-  const int b0 = __ldg(q.begin + lo), b1 = __ldg(q.begin + lo + 1), len = __ldg(q.kv_len + lo);
+  int b0, b1, len;
   r = lo;
-  if (t < b0 || t >= b1) return false;
-  if (!paged_request_ok(q, b0, b1, len) || len < b1 - b0) {
-    if (q.status) q.status[lo] = 1;  // DFLASH2_E_INVAL
-    return false;
+  if (!good_request(q, r, b0, b1, len) || t < b0 || t >= b1) {
+    // a bad range may have misled the search: the first good request that holds the row
+    const int lane = threadIdx.x & 31;
+    uint32_t m = 0;
+    int r0 = -32;
+    while (m == 0 && (r0 += 32) < q.n_req) {
+      r = r0 + lane;
+      m = __ballot_sync(0xffffffffu, r < q.n_req && good_request(q, r, b0, b1, len) && t >= b0 && t < b1);
+    }
+    if (m == 0) return false;
+    r = r0 + __ffs(m) - 1;
+    good_request(q, r, b0, b1, len);
   }
   pos = len - (b1 - b0) + (t - b0);
   return true;
@@ -162,6 +184,7 @@ template <int D, int FMT, int T>
 __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ PagedMoveArgs a) {
   constexpr int kLanes = D / 8;  // of a row
   const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  flag_requests(a.rq);
   if (t >= a.rq.n_tokens) return;
   const char* const pk = a.k.p + t * a.k.token_stride * (T == kTF32 ? 4 : 2);
   const char* const pv = a.v.p + t * a.v.token_stride * (T == kTF32 ? 4 : 2);
@@ -245,6 +268,7 @@ template <int D, int FMT, int T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ PagedMoveArgs a) {
   constexpr int kLanes = D / 8;
   const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  flag_requests(a.rq);
   if (t >= a.rq.n_tokens) return;
   int r, pos;
   if (!find_position(a.rq, t, r, pos)) return;

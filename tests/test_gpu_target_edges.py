@@ -207,6 +207,56 @@ def test_a_scale_of_zero_and_queries_that_are_not_finite():
             s.close()
 
 
+# ----------------------------------------------------------------------------- calls
+
+
+@pytest.mark.parametrize("new,begin,tokens,length,want", [
+    ([8, 0, 4], [0, 30, 8, 12], 12, [20, 20, 20], [1, 1, 0]),      # one range past the rows, one reversed
+    ([4, 4, 4], [0, 4, 20, 24], 8, [20, 20, 20], [0, 1, 1]),       # two that end past the rows
+    ([4, 0, 4], [0, 4, 4, 8], 8, [20, -1, 20], [0, 1, 0]),         # a bad length of a request without tokens
+    ([4, 0, 4], [0, 4, 4, 8], 8, [20, 20, 33], [0, 0, 1]),         # past the page table's row
+    ([4, 4, 4], [-2, 2, 6, 10], 10, [20, 20, 20], [1, 0, 0]),      # before the rows
+])
+def test_calls_agree_about_bad_ranges(new, begin, tokens, length, want):
+    """Write, read and attention serve the same requests and flag the others."""
+    s = Setup(new, [20, 20, 20], hq=4, hk=2, dim=64, fmt="int8", page=16, seed=2)
+    b = torch.tensor(begin, dtype=torch.int32, device="cuda")
+    n = torch.tensor(length, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(2, tokens, 2, 64, generator=g, device="cuda")
+    status = torch.zeros(3, dtype=torch.int32, device="cuda")
+    bd.dflash2_paged_write(s.handle, s.cache, x[0], x[1], b, n, status=status)
+    assert status.tolist() == want
+    status.zero_()
+    y = torch.full_like(x, 7.0)
+    bd.dflash2_paged_read(s.handle, s.cache, y[0], y[1], b, n, status=status)
+    assert status.tolist() == want
+    status.zero_()
+    q = torch.randn(tokens, 4, 64, generator=g, device="cuda").bfloat16()
+    out = torch.full_like(q, 7.0)
+    bd.dflash2_paged_attention(s.handle, s.cache, q, out, b, n, max_new=tokens, max_len=32, scale=0.1, status=status)
+    assert status.tolist() == want
+    served = torch.zeros(tokens, dtype=torch.bool, device="cuda")
+    for r in range(3):
+        if want[r] == 0:
+            served[begin[r]:begin[r + 1]] = True
+    assert ((y - x).abs().amax((0, 2, 3))[served] < 0.05).all() and (y[:, ~served] == 7).all()
+    assert (out[~served] == 7).all() and not (out[served] == 7).all(-1).any()
+    s.close()
+
+
+def test_write_with_padding_rows():
+    """Rows behind the last request's (a captured call's padding) are left alone, and flag nothing."""
+    s = Setup([3, 2], [20, 9], hq=2, hk=2, dim=64, fmt="fp16", page=8, seed=3)
+    x = torch.randn(2, 40, 2, 64, device="cuda")
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    bd.dflash2_paged_write(s.handle, s.cache, x[0], x[1], s.begin, s.kv_len, status=status)
+    y = torch.full_like(x, 7.0)
+    bd.dflash2_paged_read(s.handle, s.cache, y[0], y[1], s.begin, s.kv_len, status=status)
+    assert not status.any() and torch.equal(y[:, :5], x[:, :5].half().float()) and (y[:, 5:] == 7).all()
+    s.close()
+
+
 # ----------------------------------------------------------------------------- sampling
 
 def _in_place(x, t, k, p, m, u):
