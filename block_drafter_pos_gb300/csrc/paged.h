@@ -48,6 +48,9 @@ DF2_HD inline bool paged_row(const PagedCache& c, int page, int row, int h, long
   return true;
 }
 
+// In the place of an offset where there is no row.  (Strides may be negative, so offsets may; this one no pool reaches.)
+constexpr long long kNoRow = -0x7FFFFFFFFFFFFFFFll - 1;
+
 // Whether a request's rows [b0, b1) and cache length are within the call's bounds.
 DF2_HD inline bool paged_request_ok(const PagedReq& q, int b0, int b1, int len) {
   return b0 >= 0 && b1 >= b0 && b1 <= q.n_tokens && b1 - b0 <= q.max_new && len >= 0 && len <= q.max_len;

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   PagedCursor oc;
   oc.start(a, pre, t_begin, t_end);
   PagedCursor cc = oc;  // the tile that is worked on
-  long long my_off = -1, my_soff = 0;
+  long long my_off = kNoRow, my_soff = 0;
   int my_bad = 0;
   int pg = 0, pg_row = 0, pg_h = 0, pg_r = 0;
   bool pg_in = false;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     oc.next(a);
   };
   auto resolve = [&]() {
-    my_off = -1;
+    my_off = kNoRow;
     my_bad = 0;
     if (pg_in && !paged_row(a.c, pg, pg_row, pg_h, &my_off, &my_soff)) {
       my_bad = 1;
@@ -237,8 +237,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     for (int i = 0; i < kCount; ++i) off[i] = o[i * kStep];
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const int bytes = off[i] >= 0 ? 16 : 0;
-      const long long byte = (off[i] >= 0 ? off[i] * (kQuant ? 1 : 2) : 0) + ch * 16;
+      const bool in = off[i] != kNoRow;
+      const int bytes = in ? 16 : 0;
+      const long long byte = (in ? off[i] * (kQuant ? 1 : 2) : 0) + ch * 16;
       cp_async16(dst + put_k + i * (kStep * G::kRowBytes), a.c.k + byte, bytes);
       cp_async16(dst + put_v + i * (kStep * G::kRowBytes), a.c.v + byte, bytes);
     }
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     resolve();
     put(j);
     soff_next = my_soff;
-    sval_next = my_off >= 0;
+    sval_next = my_off != kNoRow;
     __syncthreads();
     if (j < n_tiles) issue(j, j);
     cp_commit();
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   resolve();
   put(S - 1);
   soff_next = my_soff;
-  sval_next = my_off >= 0;
+  sval_next = my_off != kNoRow;
   fetch();  // tile S
 
   uint32_t qf[kSteps][4];
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           const int kk = kw + 8 * t + 2 * q + e;
           bool v0, v1;
           sees(key0 + kk, v0, v1);
-          if (any_bad && offs[sl_now * kBN + kk] < 0) v0 = v1 = false;
+          if (any_bad && offs[sl_now * kBN + kk] == kNoRow) v0 = v1 = false;
           z[t][e] = v0 ? z[t][e] : -INFINITY;
           z[t][2 + e] = v1 ? z[t][2 + e] : -INFINITY;
         }
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     sl_next = sl_next == S ? 0 : sl_next + 1;
     put(sl_next);
     soff_next = my_soff;
-    sval_next = my_off >= 0;
+    sval_next = my_off != kNoRow;
     sl_now = sl_now == S ? 0 : sl_now + 1;
     st_now = st_now == S - 1 ? 0 : st_now + 1;
     st_next = st_next == S - 1 ? 0 : st_next + 1;

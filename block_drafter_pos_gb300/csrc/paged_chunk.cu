@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       const int total = static_cast<int>(t_end - t_begin);
       UnitMask um;
       um.set(a.s, lc);
-      long long off = -1;
+      long long off = kNoRow;
       float ksv = 0.f, vsv = 0.f;
       bool badv = false, piece_first = true, mixed = false, l_first = true;
       int unit = 0;
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         const int key0 = (lc.u.t0 + lc.i) * kBN, key = key0 + lt;
         mixed = um.mixed && um.masked(key0);
         piece_first = l_first;
-        off = -1;
+        off = kNoRow;
         ksv = vsv = 0.f;
         badv = false;
         if (key >= lc.u.lo && key < lc.u.hi) {
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll 4
             for (int x = 0; x < kCount; ++x) {
               const long long of = o[r0 + x * kStep];
-              const uint4 w = of >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + of * 2)) : make_uint4(0, 0, 0, 0);
+              const uint4 w = of != kNoRow ? __ldg(reinterpret_cast<const uint4*>(pool + of * 2)) : make_uint4(0, 0, 0, 0);
               const uint4 z = make_uint4(finite2<kBF>(w.x), finite2<kBF>(w.y), finite2<kBF>(w.z), finite2<kBF>(w.w));
               found |= z.x != w.x || z.y != w.y || z.z != w.z || z.w != w.w;
               sts128(dst + x * kNext, z);
@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
               for (int x = 0; x < kBatch; ++x) of[x] = o[r0 + (x0 + x) * kStep];
 #pragma unroll
               for (int x = 0; x < kBatch; ++x)
-                cp_async16(dst + (x0 + x) * kNext, pool + (of[x] >= 0 ? of[x] * (kQuant ? 1 : 2) : 0), of[x] >= 0 ? 16 : 0);
+                cp_async16(dst + (x0 + x) * kNext, pool + (of[x] != kNoRow ? of[x] * (kQuant ? 1 : 2) : 0), of[x] != kNoRow ? 16 : 0);
             }
           }
           cp_commit();

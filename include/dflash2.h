@@ -520,7 +520,7 @@ typedef struct dflash2_paged_config {
 
 /* One layer's pools.  Element (page, row, head, channel) of k and of v is at
  * page * page_stride + row * token_stride + head * head_stride + channel (elements; any
- * order of pages, rows and heads).  k, v 16-byte aligned, strides whole 16 bytes.
+ * order of pages, rows and heads, either sign).  k, v 16-byte aligned, strides whole 16 bytes.
  * k_scale, v_scale: fp32, the same with scale_* strides and no channel (NULL with 16-bit
  * formats).  page_table int32 [n_req][table_stride], its first max_pages columns used. */
 typedef struct dflash2_paged_cache {

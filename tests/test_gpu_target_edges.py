@@ -1,5 +1,7 @@
 """Places where the target's side of a step can go wrong: what a row does not see, calls whose ranges are
 partly bad, and decisions of the sampling that lie exactly on a border."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -254,6 +256,42 @@ def test_write_with_padding_rows():
     y = torch.full_like(x, 7.0)
     bd.dflash2_paged_read(s.handle, s.cache, y[0], y[1], s.begin, s.kv_len, status=status)
     assert not status.any() and torch.equal(y[:, :5], x[:, :5].half().float()) and (y[:, 5:] == 7).all()
+    s.close()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("n", [1, 4, 140])
+def test_pages_and_rows_in_descending_order(fmt, n):
+    """Negative strides: the last page first, and a page's positions from its end."""
+    b = bd.binding
+    s = Setup([n], [300], hq=4, hk=2, dim=64, page=16, fmt=fmt, order="pch", seed=n)
+    q = s.queries("bf16").cuda()
+    want, _ = s.attend(q)
+    size, quant = (1, True) if fmt == "int8" else (2, False)
+    pages = s.gk.shape[0]
+    k, v = s.gk.flip(0, 1).contiguous(), s.gv.flip(0, 1).contiguous()
+    ks, vs = (t.flip(0, 1).contiguous() if quant else None for t in (s.gks, s.gvs))
+    token, page = 2 * 64, 16 * 2 * 64
+    end, send = ((pages - 1) * page + 15 * token) * size, ((pages - 1) * 32 + 15 * 2) * 4
+    at = lambda t, o: None if t is None else t.data_ptr() + o  # noqa: E731
+    c = b.PagedCache(at(k, end), at(v, end), at(ks, send), at(vs, send), s.gtable.data_ptr(), -page, -token, 64, -32, -2, 1,
+                     s.gtable.stride(0), pages, s.gtable.shape[1])
+    out = torch.full_like(q, 7.0)
+    rows = lambda t: b.Rows(t.data_ptr(), t.stride(0), t.stride(1), b.T_BF16, 0)  # noqa: E731
+    a = b.PagedAttentionArgs(1, n, n, 300, 1, 0, 64 ** -0.5, 0, s.begin.data_ptr(), s.kv_len.data_ptr(), rows(q), rows(out), None, None,
+                             None)
+    torch.cuda.synchronize()
+    assert bd.lib().dflash2_paged_attention(s.handle, ctypes.byref(c), ctypes.byref(a), None) == b.OK
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    x = torch.zeros(2, n, 2, 64, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    bd.dflash2_paged_read(s.handle, s.cache, y[0], y[1], s.begin, s.kv_len)
+    torch.cuda.synchronize()
+    assert bd.lib().dflash2_paged_read(s.handle, ctypes.byref(c), 1, n, s.begin.data_ptr(), s.kv_len.data_ptr(),
+                                       ctypes.byref(rows(x[0])), ctypes.byref(rows(x[1])), None, None) == b.OK
+    torch.cuda.synchronize()
+    assert torch.equal(x, y)
     s.close()
 
 
