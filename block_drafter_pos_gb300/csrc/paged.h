@@ -110,6 +110,11 @@ DF2_HD inline long long paged_head_tiles(const PagedShape& s, int n, int len) {
 // First tile of CTA c's run.
 DF2_HD inline long long paged_run_begin(long long c, long long C, long long T) { return c * T / C; }
 
+// Whether the run [t0, t1) has a tile of the request whose tiles are [first, next).
+DF2_HD inline bool paged_in_run(long long first, long long next, long long t0, long long t1) {
+  return first < next && first < t1 && next > t0;
+}
+
 struct PagedAttnArgs {
   PagedCache c;
   PagedReq rq;
@@ -120,7 +125,7 @@ struct PagedAttnArgs {
   float scale_log2;  // score scale * log2(e)
   float* part;       // partial results: slots of rows * head_dim outputs, then rows * (max, sum)
   // [CTAs][8]: the cut unit that begins in CTA c's run (request, KV head, row tile, last CTA and first slot, first
-  // row of the request, its new tokens), or -1
+  // row of the request, its new tokens), or -1; whether one of the CTA's waits gave up
   int* desc;
   unsigned* count;   // [CTAs] partials of that unit that have come (zero between calls)
   int ctas;

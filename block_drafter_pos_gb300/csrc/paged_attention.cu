@@ -818,12 +818,31 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   }
 }
 
-// Joins the partials of the units cut between CTAs, where the attention leaves that to a launch of its own.
-template <int D, bool QBF>
+// Flags every request with a tile in CTA c's run (a wait of that CTA gave up).
+DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
+  if (!a.rq.status) return;
+  auto tiles = [&](int r) {
+    int b0, n, len;
+    return paged_request(a.rq, r, b0, n, len) ? a.c.n_kv * paged_head_tiles(a.s, n, len) : 0ll;
+  };
+  long long T = 0, first = 0;
+  for (int r = 0; r < a.rq.n_req; ++r) T += tiles(r);
+  const long long C = T < gridDim.x ? T : gridDim.x;
+  for (int r = 0; r < a.rq.n_req; ++r) {
+    const long long next = first + tiles(r);
+    if (paged_in_run(first, next, paged_run_begin(c, C, T), paged_run_begin(c + 1, C, T))) a.rq.status[r] = 3;  // DFLASH2_E_CUDA
+    first = next;
+  }
+}
+
+// Joins the partials of the units cut between CTAs, where the attention leaves that to a launch of its own.  WAITS: of the
+// kernel for many rows, whose waits may give up.
+template <int D, bool QBF, bool WAITS>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
   pdl_wait();  // (launched while the attention still runs)
   const int4 d0 = *reinterpret_cast<const int4*>(a.desc + 8 * blockIdx.x);
-  const int2 d1 = *reinterpret_cast<const int2*>(a.desc + 8 * blockIdx.x + 4);
+  const int4 d1 = *reinterpret_cast<const int4*>(a.desc + 8 * blockIdx.x + 4);
+  if (WAITS && d1.z != 0 && blockIdx.y == 0 && threadIdx.x == 0) flag_run(a, blockIdx.x);
   if (d0.x < 0) return;
   for (int lr = blockIdx.y * 4 + (threadIdx.x >> 5); lr < a.s.rows; lr += 4 * gridDim.y)
     join_row<D, QBF>(a, d0.y, d0.z, blockIdx.x, d0.w >> 1, d0.w & 1, d1.x, d1.y, lr);
@@ -873,11 +892,14 @@ cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int 
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
   // a row per warp for units of 32 rows (four in turn took 2 to 3 us more), four for those of 256
   const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / 16);
+  auto combine = [&](auto kernel, auto kernel_waits) {
+    return launch_ex(a.s.rows == 32 ? kernel : kernel_waits, grid, dim3(128), 0, st, true, a);
+  };
   if (head_dim == 64)
-    return qtype == kTBf16 ? launch_ex(paged_combine_kernel<64, true>, grid, dim3(128), 0, st, true, a)
-                           : launch_ex(paged_combine_kernel<64, false>, grid, dim3(128), 0, st, true, a);
-  return qtype == kTBf16 ? launch_ex(paged_combine_kernel<128, true>, grid, dim3(128), 0, st, true, a)
-                         : launch_ex(paged_combine_kernel<128, false>, grid, dim3(128), 0, st, true, a);
+    return qtype == kTBf16 ? combine(paged_combine_kernel<64, true, false>, paged_combine_kernel<64, true, true>)
+                           : combine(paged_combine_kernel<64, false, false>, paged_combine_kernel<64, false, true>);
+  return qtype == kTBf16 ? combine(paged_combine_kernel<128, true, false>, paged_combine_kernel<128, true, true>)
+                         : combine(paged_combine_kernel<128, false, false>, paged_combine_kernel<128, false, true>);
 }
 
 }  // namespace df2

@@ -20,8 +20,8 @@
 //    codes into a staging area from which the same thread writes them as exact fp16 values.  The
 //    keys' scale multiplies the score and the values' scale the weight, relative to a power of
 //    two that a row raises when a scale that it sees exceeds 16 of it.
-//  * Every wait is bounded; one that gives up sets the requests' status and ends the CTA
-//    once its own copies and products are done.
+//  * Every wait is bounded; one that gives up marks the CTA and ends it once its own copies and
+//    products are done.  The kernel that joins partials flags the run's requests; rows whose partials never came are NaN.
 //
 // Measured: 4096 new tokens of 32 query heads over 32768 bf16 positions of 8 KV heads of 128 (2.06 TFLOP): 1.66 to
 // 1.72 ms, 1.2 PFLOP/s, 70% of the sustained cuBLAS rate, tensor pipe 52% active.  A 128-key tile takes about
@@ -235,9 +235,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   pdl_trigger();
   const long long T = paged_scan<kThreads>(a, pre, tmp);
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
-  if (tid == 0) a.desc[8 * c] = -1;
+  if (tid == 0) a.desc[8 * c] = -1, a.desc[8 * c + 6] = 0;
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
+  // Partials that never come (a wait that gives up) leave NaN in the rows they are joined into.
+  for (int i = tid; i < 2 * kChunkRows; i += kThreads) {
+    float* const p = a.part + (2 * c + i / kChunkRows) * (kChunkRows * (D + 2)) + kChunkRows * D;
+    reinterpret_cast<float2*>(p)[i % kChunkRows] = make_float2(NAN, NAN);
+  }
   if (wid == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_sh)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       gtile += piece;
       cc = nc;
     }
-    if (!ok && lane == 0 && a.rq.status) a.rq.status[cc.r] = 3;  // DFLASH2_E_CUDA
+    if (!ok && lane == 0) a.desc[8 * c + 6] = 1;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (wid == 12) {
@@ -693,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           break;
         }
       }
-      if (!ok && lane == 0 && a.rq.status) a.rq.status[cs.r] = 3;
+      if (!ok && lane == 0) a.desc[8 * c + 6] = 1;
     } else if (wid < 12) {
       // -------------------------------------------------------------- keys and values
       const int lt = tid - 256;
@@ -899,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if constexpr (kQuant) ok = convert(said++);
         else landed(said++);
       }
-      if (!ok && lt == 0 && a.rq.status) a.rq.status[lc.r] = 3;
+      if (!ok) a.desc[8 * c + 6] = 1;
     }
   }
   // every product has completed: its commits were waited for by the rows' last outputs, or (after an error) here

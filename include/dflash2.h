@@ -488,11 +488,16 @@ dflash2_status dflash2_debug_noalloc_inject_error(int32_t on);
  * p % page_size of page page_table[r][p / page_size].
  *
  * Errors found on the device go to status [n_req] (int32, or NULL), which the calls only
- * ever set to DFLASH2_E_INVAL and never clear: a token range outside the call's rows, a
+ * ever set to an error and never clear; DFLASH2_E_INVAL: a token range outside the call's rows, a
  * length outside the page table's row (or max_len), more new tokens than max_new, a page
  * id outside 0 .. n_pages - 1.  No address outside the pools is formed for them.  A
  * request with a bad range or length is skipped (its output rows keep what they held); a
  * bad page's rows are not written, read back as zeros, and are masked in the attention.
+ * token_begin ascends; a request that breaks this is one with a bad range, and a row that two
+ * good ranges hold goes to either.  kv_len[r] below n: write and read have no place for the first
+ * of the new tokens, and flag the request; to the attention those are tokens before position 0.
+ * The attention sets DFLASH2_E_CUDA if a wait inside a kernel gives up (a fault of the library
+ * or the device, none of the arguments): the request's rows are then not valid.
  * ------------------------------------------------------------------------------------ */
 
 /* Cache formats.  INT8 and E4M3 hold codes and one fp32 scale per (position, KV head) and
