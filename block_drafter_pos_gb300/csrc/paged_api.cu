@@ -46,6 +46,7 @@ PagedRows rows_of(const dflash2_rows& r) {
 dflash2_status check_cache(const dflash2_paged_handle* h, const dflash2_paged_cache* c, int32_t n_req) {
   if (!h || !c || n_req < 0) return DFLASH2_E_INVAL;
   if (n_req > h->cfg.max_requests) return DFLASH2_E_UNSUPPORTED;
+  if (n_req == 0) return DFLASH2_OK;  // (an empty batch's table has no address)
   const int size = kv_size(h->cfg.kv_format);
   if (!c->k || !c->v || !c->page_table || !aligned16(c->k) || !aligned16(c->v) || c->n_pages < 1 || c->max_pages < 1 ||
       c->table_stride < c->max_pages || !stride16(c->page_stride, size) || !stride16(c->token_stride, size) ||
@@ -86,7 +87,7 @@ dflash2_status move_rows(dflash2_paged_handle* h, const dflash2_paged_cache* cac
                          const dflash2_rows* v, int32_t* status, void* stream, bool write) {
   const dflash2_status s = check_cache(h, cache, n_req);
   if (s != DFLASH2_OK) return s;
-  if (n_tokens < 0 || !token_begin || !kv_len || !k || !v) return DFLASH2_E_INVAL;
+  if (n_tokens < 0 || !k || !v || (n_req > 0 && (!token_begin || !kv_len))) return DFLASH2_E_INVAL;
   if (n_tokens == 0 || n_req == 0) return DFLASH2_OK;
   if (!valid_rows(*k) || !valid_rows(*v) || k->type != v->type) return DFLASH2_E_INVAL;
   PagedMoveArgs a;
@@ -172,7 +173,7 @@ dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_pa
   const dflash2_paged_attention_args& x = *args;
   const dflash2_status s = check_cache(h, cache, x.n_req);
   if (s != DFLASH2_OK) return s;
-  if (x.n_tokens < 0 || x.max_new < 0 || x.max_len < 0 || !x.token_begin || !x.kv_len || x.window < 0 ||
+  if (x.n_tokens < 0 || x.max_new < 0 || x.max_len < 0 || (x.n_req > 0 && (!x.token_begin || !x.kv_len)) || x.window < 0 ||
       !isfinite(x.scale))
     return DFLASH2_E_INVAL;
   if (x.tree_mask && x.max_new > DFLASH2_PAGED_MAX_TREE) return DFLASH2_E_UNSUPPORTED;

@@ -295,6 +295,26 @@ def test_pages_and_rows_in_descending_order(fmt, n):
     s.close()
 
 
+def test_calls_without_requests_or_rows():
+    """An empty batch is no error and touches nothing."""
+    s = Setup([2], [20], hq=4, hk=2, dim=64, fmt="int8", page=16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    none, one = torch.zeros(0, **i32), torch.zeros(1, **i32)
+    x = torch.zeros(0, 2, 64, device="cuda")
+    y = torch.full((3, 2, 64), 7.0, device="cuda")
+    q = torch.full((3, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for table in (s.gtable[:0], torch.zeros(0, 0, **i32)):
+        cache = bd.paged_cache(s.gk, s.gv, table, s.gks, s.gvs)
+        for rows, qq in ((x, q[:0]), (y, q)):
+            bd.dflash2_paged_write(s.handle, cache, rows, rows, one, none)
+            bd.dflash2_paged_read(s.handle, cache, rows, rows, one, none)
+            bd.dflash2_paged_attention(s.handle, cache, qq, qq, one, none, max_new=0, max_len=0, scale=0.1)
+            bd.dflash2_paged_attention(s.handle, cache, qq, qq, one, none, max_new=3, max_len=20, scale=0.1)
+    torch.cuda.synchronize()
+    assert (y == 7).all() and (q == 7).all()
+    s.close()
+
+
 # ----------------------------------------------------------------------------- sampling
 
 def _in_place(x, t, k, p, m, u):

@@ -1,0 +1,18 @@
+"""Calls of the target's side that end on the host: empty batches, limits, and what the binding refuses.  No GPU."""
+import block_drafter_pos_gb300 as bd
+from test_target_host import P, FakeHandle, _attn, _cache, _rows
+
+b = bd.binding
+
+
+def test_an_empty_batch_needs_no_addresses():
+    """The lengths and the page table of no requests are empty tensors, whose address is 0."""
+    h, r = FakeHandle(), _rows()
+    for c in (_cache(page_table=None), _cache(page_table=None, max_pages=0, table_stride=0)):
+        for f in (bd.lib().dflash2_paged_write, bd.lib().dflash2_paged_read):
+            assert f(h.p, c, 0, 3, P, None, r, r, None, None) == b.OK
+            assert f(h.p, c, 0, 0, P, None, _rows(p=None), _rows(p=None), None, None) == b.OK
+            assert f(h.p, c, 0, -1, P, None, r, r, None, None) == b.E_INVAL
+        assert bd.lib().dflash2_paged_attention(h.p, c, _attn(n_req=0, kv_len=None), None) == b.OK
+        assert bd.lib().dflash2_paged_attention(h.p, c, _attn(n_req=0, kv_len=None, scale=float("nan")), None) == b.E_INVAL
+    assert bd.lib().dflash2_paged_attention(h.p, None, _attn(n_req=0), None) == b.E_INVAL
