@@ -64,6 +64,9 @@ struct PagedMoveArgs {
 cudaError_t launch_paged_write(const PagedMoveArgs& a, int head_dim, int fmt, cudaStream_t st);
 cudaError_t launch_paged_read(const PagedMoveArgs& a, int head_dim, int fmt, cudaStream_t st);
 
+// Longest cache of a request, and most rows (new tokens x group) of one: rounded up to a tile they stay in 32 bits.
+constexpr int kPagedMaxLen = 0x7FFFFFFF - 511, kPagedMaxRows = 0x7FFFFFFF - 511;
+
 // ------------------------------------------------------------------ attention schedule
 // The rows of a request are its (token, query head of one KV head) pairs, token-major:
 // row = i * group + g.  A unit is (request, KV head, tile of `rows` rows); it reads the

@@ -79,7 +79,7 @@ PagedCache cache_of(const dflash2_paged_handle* h, const dflash2_paged_cache* c)
 
 int capacity_of(const dflash2_paged_handle* h, const dflash2_paged_cache* c) {
   const int64_t cap = static_cast<int64_t>(c->max_pages) * h->cfg.page_size;
-  return static_cast<int>(std::min<int64_t>(cap, 0x7FFFFFFF));
+  return static_cast<int>(std::min<int64_t>(cap, kPagedMaxLen));
 }
 
 dflash2_status move_rows(dflash2_paged_handle* h, const dflash2_paged_cache* cache, int32_t n_req, int32_t n_tokens,
@@ -182,6 +182,8 @@ dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_pa
     return DFLASH2_E_INVAL;
   if (!quantised(h->cfg.kv_format) && x.q.type != (h->cfg.kv_format == DFLASH2_KV_BF16 ? DFLASH2_T_BF16 : DFLASH2_T_F16))
     return DFLASH2_E_INVAL;
+  if (static_cast<int64_t>(std::min(x.max_new, x.n_tokens)) * (h->cfg.n_q_heads / h->cfg.n_kv_heads) > kPagedMaxRows)
+    return DFLASH2_E_UNSUPPORTED;
   PagedAttnArgs a;
   memset(&a, 0, sizeof(a));
   a.c = cache_of(h, cache);

@@ -485,7 +485,8 @@ dflash2_status dflash2_debug_noalloc_inject_error(int32_t on);
  * rows token_begin[r] .. token_begin[r + 1] - 1 (int32 [n_req + 1], device), n of them.
  * kv_len[r] (int32 [n_req], device) is the length of its cache with the new tokens in
  * it: new token i is at position kv_len[r] - n + i.  Position p of request r is row
- * p % page_size of page page_table[r][p / page_size].
+ * p % page_size of page page_table[r][p / page_size].  A length is at most 2^31 - 512, whatever
+ * the page table's row has room for.
  *
  * Errors found on the device go to status [n_req] (int32, or NULL), which the calls only
  * ever set to an error and never clear; DFLASH2_E_INVAL: a token range outside the call's rows, a
@@ -581,7 +582,8 @@ dflash2_status dflash2_paged_read(dflash2_paged_handle* h, const dflash2_paged_c
 typedef struct dflash2_paged_attention_args {
   int32_t n_req;
   int32_t n_tokens;    /* rows of q, out, tree_mask, lse                                  */
-  int32_t max_new;     /* at least every request's number of new tokens (host bound)      */
+  int32_t max_new;     /* at least every request's number of new tokens (host bound); times the
+                        * query heads per KV head at most 2^31 - 512                      */
   int32_t max_len;     /* at least every request's kv_len (host bound)                    */
   int32_t causal;
   int32_t window;      /* 0: none                                                         */

@@ -16,3 +16,10 @@ def test_an_empty_batch_needs_no_addresses():
         assert bd.lib().dflash2_paged_attention(h.p, c, _attn(n_req=0, kv_len=None), None) == b.OK
         assert bd.lib().dflash2_paged_attention(h.p, c, _attn(n_req=0, kv_len=None, scale=float("nan")), None) == b.E_INVAL
     assert bd.lib().dflash2_paged_attention(h.p, None, _attn(n_req=0), None) == b.E_INVAL
+
+
+def test_more_rows_than_32_bits_count_are_refused():
+    """New tokens times the query heads of a KV head (4 here)."""
+    f, h, c = bd.lib().dflash2_paged_attention, FakeHandle(), _cache()
+    for n in (1 << 30, (1 << 31) - 1, (1 << 29) - 63):
+        assert f(h.p, c, _attn(n_tokens=n, max_new=n), None) == b.E_UNSUPPORTED

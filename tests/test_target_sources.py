@@ -26,12 +26,12 @@ def test_barriers_are_initialised_once(name):
     assert "mbar_init_count(" in before and "mbar_init_count(" not in after
 
 
-def _host_check(tmp_path, name):
+def _host_check(tmp_path, name, *flags):
     gxx, inc = shutil.which("g++"), "/usr/local/cuda/include"
     if gxx is None or not os.path.exists(os.path.join(inc, "cuda.h")):
         pytest.skip("g++ or the CUDA headers are missing")
     exe = str(tmp_path / "check")
-    subprocess.run([gxx, "-std=c++17", "-O2", "-I", CSRC, "-I", inc, os.path.join(ROOT, "tests", name), "-o", exe], check=True)
+    subprocess.run([gxx, "-std=c++17", "-O2", *flags, "-I", CSRC, "-I", inc, os.path.join(ROOT, "tests", name), "-o", exe], check=True)
     out = subprocess.run([exe], capture_output=True, text=True)
     assert out.returncode == 0 and out.stdout.startswith("ok "), out.stdout
 
@@ -39,6 +39,10 @@ def _host_check(tmp_path, name):
 def test_requests_of_a_run(tmp_path):
     """Those that a CTA flags when one of its waits gives up."""
     _host_check(tmp_path, "paged_run_check.cpp")
+
+
+def test_the_longest_caches_stay_in_32_bits(tmp_path):
+    _host_check(tmp_path, "paged_limits_check.cpp", "-fsanitize=signed-integer-overflow", "-fno-sanitize-recover")
 
 
 def test_a_wait_that_gives_up_spoils_its_whole_run():
