@@ -215,7 +215,7 @@ dflash2_status dflash2_sample(const dflash2_sample_args* args, void* stream) {
   if (x.vocab > kSampleMaxVocab || x.n_rows > (1 << 24)) return DFLASH2_E_UNSUPPORTED;
   if (x.n_rows == 0) return DFLASH2_OK;
   if (!x.logits || !x.temperature || !x.uniform || !x.token || (x.n_rows > 1 && x.row_stride < x.vocab) ||
-      (x.kept && x.n_rows > 1 && x.kept_stride < x.vocab))
+      (x.kept && x.n_rows > 1 && x.kept_stride < x.vocab) || reinterpret_cast<uintptr_t>(x.logits) % t_size(x.logits_type))
     return DFLASH2_E_INVAL;
   SampleArgs a;
   a.logits = x.logits;

@@ -599,7 +599,7 @@ typedef struct dflash2_paged_attention_args {
 dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_paged_cache* cache,
                                        const dflash2_paged_attention_args* args, void* stream);
 
-/* Truncated sampling of n_rows rows of logits [vocab] (type DFLASH2_T_*, row_stride
+/* Truncated sampling of n_rows rows of logits [vocab] (type DFLASH2_T_*, aligned to it, row_stride
  * elements apart) with the caller's uniforms.  Per row: weights w_i = exp((x_i - max x) / T);
  *   top_k > 0: the top_k largest logits stay (equal logits: smaller ids first);
  *   top_p < 1: in that order, id i stays while the weight before it is less than top_p

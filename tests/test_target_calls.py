@@ -1,4 +1,6 @@
 """Calls of the target's side that end on the host: empty batches, limits, and what the binding refuses.  No GPU."""
+import pytest
+
 import block_drafter_pos_gb300 as bd
 from test_target_host import P, FakeHandle, _attn, _cache, _rows
 
@@ -23,3 +25,9 @@ def test_more_rows_than_32_bits_count_are_refused():
     f, h, c = bd.lib().dflash2_paged_attention, FakeHandle(), _cache()
     for n in (1 << 30, (1 << 31) - 1, (1 << 29) - 63):
         assert f(h.p, c, _attn(n_tokens=n, max_new=n), None) == b.E_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kind,off", [(b.T_F32, 2), (b.T_F32, 1), (b.T_BF16, 1), (b.T_F16, 3)])
+def test_logits_off_their_types_alignment_are_refused(kind, off):
+    a = b.SampleArgs(2, 100, kind, 0, P + off, 100, P, P, P, P, P, P, P, 4 * P, 100, P)
+    assert bd.lib().dflash2_sample(a, None) == b.E_INVAL
