@@ -437,6 +437,8 @@ def dflash2_paged_create(cfg: PagedConfig) -> int:
 
 
 def dflash2_paged_destroy(h: int):
+    if h not in _paged_cfg:
+        raise _inval("dflash2_paged_destroy", "not a paged handle")
     _check(lib().dflash2_paged_destroy(h), "dflash2_paged_destroy")
     _paged_cfg.pop(h, None)
 

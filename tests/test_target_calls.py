@@ -31,3 +31,24 @@ def test_more_rows_than_32_bits_count_are_refused():
 def test_logits_off_their_types_alignment_are_refused(kind, off):
     a = b.SampleArgs(2, 100, kind, 0, P + off, 100, P, P, P, P, P, P, P, 4 * P, 100, P)
     assert bd.lib().dflash2_sample(a, None) == b.E_INVAL
+
+
+# ----------------------------------------------------------------------------- the binding
+
+def test_destroy_takes_live_handles_only(monkeypatch):
+    """A handle destroyed before, or no handle at all, does not reach the library."""
+    gone = []
+
+    class Lib:
+        @staticmethod
+        def dflash2_paged_destroy(h):
+            gone.append(h)
+            return b.OK
+
+    monkeypatch.setattr(b, "lib", lambda: Lib)
+    monkeypatch.setitem(b._paged_cfg, 4096, ((b.KV_INT8, 16, 2, 128), 8))
+    bd.dflash2_paged_destroy(4096)
+    for h in (4096, 4097, None):
+        with pytest.raises(bd.Dflash2Error):
+            bd.dflash2_paged_destroy(h)
+    assert gone == [4096]
