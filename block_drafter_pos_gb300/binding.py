@@ -355,30 +355,32 @@ def _calls():
     return _fast
 
 
-def _raw_stream(torch, stream) -> Optional[int]:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _raw_stream(what, torch, stream, dev: int) -> Optional[int]:
+    """The stream's handle; a launch goes to the current device, which has to be the tensors'."""
+    current = torch._C._cuda_getDevice()
+    if current != dev or (stream is not None and stream.device_index != dev):
+        raise _inval(what, f"the tensors are on device {dev}, which is not the current one or the stream's")
+    return torch._C._cuda_getCurrentRawStream(current) if stream is None else stream.cuda_stream
 
 
 def _inval(what: str, why: str):
     return Dflash2Error(E_INVAL, f"{what}: {why}")
 
 
-def _vector(what, name, t, dtype, n):
-    """Address of a contiguous CUDA tensor of n elements, or 0 for None."""
+def _vector(what, name, t, dtype, n, dev):
+    """Address of a contiguous tensor of n elements on CUDA device dev, or 0 for None."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        raise _inval(what, f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        raise _inval(what, f"{name} must be a contiguous tensor of {n} {dtype} on CUDA device {dev}")
     return t.data_ptr()
 
 
-def _rows(what, name, t, types, heads, dim):
+def _rows(what, name, t, types, heads, dim, dev):
     """The fields of dflash2_rows."""
     ty = types.get(t.dtype)
-    if ty is None or t.dim() != 3 or not t.is_cuda:
-        raise _inval(what, f"{name} must be a bf16, fp16 or fp32 CUDA tensor [tokens, {heads}, {dim}]")
+    if ty is None or t.dim() != 3 or t.get_device() != dev:
+        raise _inval(what, f"{name} must be a bf16, fp16 or fp32 tensor [tokens, {heads}, {dim}] on CUDA device {dev}")
     sh, st = t.shape, t.stride()
     if sh[1] != heads or sh[2] != dim or st[2] != 1:
         raise _inval(what, f"{name} must be [tokens, {heads}, {dim}] with contiguous channels")
@@ -393,7 +395,7 @@ def make_paged_config(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size:
 
 class PagedPool:
     """The cache structure of one layer (paged_cache makes it); it keeps the tensors alive."""
-    __slots__ = ("raw", "geometry", "n_req", "_keep")
+    __slots__ = ("raw", "geometry", "n_req", "device", "_keep")
 
 
 def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedPool:
@@ -406,18 +408,20 @@ def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedPool:
     if fmt is None or k.dim() != 4 or k.dtype is not v.dtype:
         raise _inval(what, "k and v must be pools of one type [pages, page_size, heads, head_dim]")
     sh, st = k.shape, k.stride()
-    if sh != v.shape or st != v.stride() or st[3] != 1 or not k.is_cuda or not v.is_cuda:
-        raise _inval(what, "k and v must be CUDA tensors of one shape and layout with contiguous channels")
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or page_table.stride(1) != 1:
-        raise _inval(what, "page_table must be an int32 CUDA tensor [requests, pages] with contiguous rows")
+    dev = k.get_device()
+    if sh != v.shape or st != v.stride() or st[3] != 1 or dev < 0 or v.get_device() != dev:
+        raise _inval(what, "k and v must be tensors of one shape and layout on one CUDA device, with contiguous channels")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.get_device() != dev or page_table.stride(1) != 1:
+        raise _inval(what, "page_table must be an int32 tensor [requests, pages] on the pools' device, with contiguous rows")
     c = PagedPool()
+    c.device = dev
     c.n_req, max_pages = page_table.shape
     ks = vs = 0
     ss = (0, 0, 0)
     if fmt >= KV_INT8:
         if k_scale is None or v_scale is None or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or \
-                k_scale.shape != sh[:3] or v_scale.shape != sh[:3] or not k_scale.is_cuda or not v_scale.is_cuda:
-            raise _inval(what, "8-bit pools need float32 scales [pages, page_size, heads]")
+                k_scale.shape != sh[:3] or v_scale.shape != sh[:3] or k_scale.get_device() != dev or v_scale.get_device() != dev:
+            raise _inval(what, "8-bit pools need float32 scales [pages, page_size, heads] on the pools' device")
         ss = k_scale.stride()
         if ss != v_scale.stride():
             raise _inval(what, "the scales must have one layout")
@@ -432,7 +436,8 @@ def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedPool:
 def dflash2_paged_create(cfg: PagedConfig) -> int:
     h = ctypes.c_void_p()
     _check(lib().dflash2_paged_create(ctypes.byref(cfg), ctypes.byref(h)), "dflash2_paged_create")
-    _paged_cfg[h.value] = ((cfg.kv_format, cfg.page_size, cfg.n_kv_heads, cfg.head_dim), cfg.n_q_heads)
+    _paged_cfg[h.value] = ((cfg.kv_format, cfg.page_size, cfg.n_kv_heads, cfg.head_dim), cfg.n_q_heads,
+                           _calls()[0]._C._cuda_getDevice())
     return h.value
 
 
@@ -444,18 +449,21 @@ def dflash2_paged_destroy(h: int):
 
 
 def _paged_check(what, torch, h, cache, token_begin, kv_len, status):
-    """The handle's geometry against the cache's; returns (geometry, query heads, requests, three addresses)."""
+    """The handle's geometry and device against the cache's; returns (geometry, query heads, requests, three addresses)."""
     g = _paged_cfg.get(h)
     if g is None:
         raise _inval(what, "not a paged handle")
     if cache.geometry != g[0]:
         raise _inval(what, "the pools are not of the handle's format, page size or heads")
+    dev = cache.device
+    if dev != g[2]:
+        raise _inval(what, f"the pools are on device {dev}, the handle on {g[2]}")
     n = kv_len.numel()
     if n > cache.n_req:
         raise _inval(what, "the page table has fewer rows than there are requests")
     i32 = torch.int32
-    return g[0], g[1], n, _vector(what, "token_begin", token_begin, i32, n + 1), \
-        _vector(what, "kv_len", kv_len, i32, n), _vector(what, "status", status, i32, n)
+    return g[0], g[1], n, _vector(what, "token_begin", token_begin, i32, n + 1, dev), \
+        _vector(what, "kv_len", kv_len, i32, n, dev), _vector(what, "status", status, i32, n, dev)
 
 
 def _paged_move(what, which, h, cache, k, v, token_begin, kv_len, status, stream):
@@ -463,9 +471,10 @@ def _paged_move(what, which, h, cache, k, v, token_begin, kv_len, status, stream
     g, _, n, begin, length, st = _paged_check(what, f[0], h, cache, token_begin, kv_len, status)
     if k.shape != v.shape or k.dtype is not v.dtype:
         raise _inval(what, "k and v must have one shape and type")
-    rk, rv = _rows(what, "k", k, f[1], g[2], g[3]), _rows(what, "v", v, f[1], g[2], g[3])
+    dev = cache.device
+    rk, rv = _rows(what, "k", k, f[1], g[2], g[3], dev), _rows(what, "v", v, f[1], g[2], g[3], dev)
     s = f[which](h, cache.raw, n, k.shape[0], begin, length, _PACK_ROWS.pack(*rk), _PACK_ROWS.pack(*rv), st,
-                 _raw_stream(f[0], stream))
+                 _raw_stream(what, f[0], stream, dev))
     if s:
         _check(s, what)
 
@@ -488,14 +497,15 @@ def dflash2_paged_attention(h, cache, q, out, token_begin, kv_len, max_new, max_
     f = _calls()
     torch = f[0]
     g, hq, n, begin, length, st = _paged_check(what, torch, h, cache, token_begin, kv_len, status)
-    rq, ro = _rows(what, "q", q, f[1], hq, g[3]), _rows(what, "out", out, f[1], hq, g[3])
+    dev = cache.device
+    rq, ro = _rows(what, "q", q, f[1], hq, g[3], dev), _rows(what, "out", out, f[1], hq, g[3], dev)
     tokens = q.shape[0]
     if out.shape[0] != tokens:
         raise _inval(what, "q and out must have the same rows")
     a = _PACK_ATTN.pack(n, tokens, max_new, max_len, 1 if causal else 0, window, scale, 0, begin, length, *rq, *ro,
-                        _vector(what, "tree_mask", tree_mask, torch.int64, tokens),
-                        _vector(what, "lse", lse, torch.float32, tokens * hq), st)
-    s = f[5](h, cache.raw, a, _raw_stream(torch, stream))
+                        _vector(what, "tree_mask", tree_mask, torch.int64, tokens, dev),
+                        _vector(what, "lse", lse, torch.float32, tokens * hq, dev), st)
+    s = f[5](h, cache.raw, a, _raw_stream(what, torch, stream, dev))
     if s:
         _check(s, what)
 
@@ -507,19 +517,20 @@ def dflash2_sample(logits, temperature, top_k, top_p, min_p, uniform, token, pro
     f = _calls()
     torch = f[0]
     ty = f[1].get(logits.dtype)
-    if ty is None or logits.dim() != 2 or logits.stride(1) != 1 or not logits.is_cuda:
+    dev = logits.get_device()
+    if ty is None or logits.dim() != 2 or logits.stride(1) != 1 or dev < 0:
         raise _inval(what, "logits must be a bf16, fp16 or fp32 CUDA tensor [rows, vocab] with contiguous rows")
     n, v = logits.shape
     i32, f32 = torch.int32, torch.float32
-    if kept is not None and (kept.dtype is not f32 or kept.shape != logits.shape or kept.stride(1) != 1 or not kept.is_cuda):
-        raise _inval(what, "kept must be a float32 CUDA tensor of the logits' shape with contiguous rows")
+    if kept is not None and (kept.dtype is not f32 or kept.shape != logits.shape or kept.stride(1) != 1 or kept.get_device() != dev):
+        raise _inval(what, "kept must be a float32 tensor of the logits' shape and device with contiguous rows")
     a = _PACK_SAMPLE.pack(n, v, ty, 0, logits.data_ptr(), logits.stride(0),
-                          _vector(what, "temperature", temperature, f32, n), _vector(what, "top_k", top_k, i32, n),
-                          _vector(what, "top_p", top_p, f32, n), _vector(what, "min_p", min_p, f32, n),
-                          _vector(what, "uniform", uniform, f32, n), _vector(what, "token", token, i32, n),
-                          _vector(what, "prob", prob, f32, n), 0 if kept is None else kept.data_ptr(),
-                          0 if kept is None else kept.stride(0), _vector(what, "status", status, i32, n))
-    s = f[6](a, _raw_stream(torch, stream))
+                          _vector(what, "temperature", temperature, f32, n, dev), _vector(what, "top_k", top_k, i32, n, dev),
+                          _vector(what, "top_p", top_p, f32, n, dev), _vector(what, "min_p", min_p, f32, n, dev),
+                          _vector(what, "uniform", uniform, f32, n, dev), _vector(what, "token", token, i32, n, dev),
+                          _vector(what, "prob", prob, f32, n, dev), 0 if kept is None else kept.data_ptr(),
+                          0 if kept is None else kept.stride(0), _vector(what, "status", status, i32, n, dev))
+    s = f[6](a, _raw_stream(what, torch, stream, dev))
     if s:
         _check(s, what)
 
