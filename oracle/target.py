@@ -77,26 +77,38 @@ def paged_attention(q, k, v, scale, see):
 def truncated_sample(x, temperature, top_k, top_p, min_p, u):
     """One row of logits -> (token, probability, stays [V], margin): margin is the smallest distance, in
     shares of the weight concerned, of any decision from its border (infinite where none is near)."""
+    token, prob, stays, cut, draw = truncated_sample_margins(x, temperature, top_k, top_p, min_p, u)
+    return token, prob, stays, min(cut, draw)
+
+
+def truncated_sample_margins(x, temperature, top_k, top_p, min_p, u):
+    """The same with two margins: of what stays, and of the draw.  Decisions without a rounding have none: the largest
+    logit's weight is 1; where every weight is 1 or too small to count, sums are whole numbers; and at u = 0 ids whose running
+    weight is 0 are passed over."""
     x = np.asarray(x, np.float64)
     order = np.argsort(-x, kind="stable")            # logit descending, id ascending
     v = len(x)
-    margin = np.inf
+    cut = draw = np.inf
     if temperature == 0:
         stays = np.zeros(v, bool)
         stays[order[0]] = True
-        return int(order[0]), 1.0, stays, margin
+        return int(order[0]), 1.0, stays, cut, draw
     xs = x[order]
     w = np.exp((xs - xs[0]) / float(temperature))
     n = top_k if 0 < top_k < v else v
     w[n:] = 0.0
+    whole = ((w == 1.0) | (w < 2.0 ** -80)).all()
+    if whole:
+        w = np.where(w == 1.0, 1.0, 0.0)
     keep = np.arange(v) < n
     if top_p < 1:
         total, run = w.sum(), np.cumsum(w)
         before = np.concatenate([[0.0], run[:-1]])
         keep &= (before < float(top_p) * total) | (np.arange(v) == 0)
-        margin = min(margin, np.abs(run - float(top_p) * total).min() / total)
+        if not whole:
+            cut = min(cut, np.abs(run - float(top_p) * total).min() / total)
     if min_p > 0:
-        margin = min(margin, np.abs(w[keep] - float(min_p)).min())
+        cut = min(cut, np.abs(w[keep & (w < 1.0)] - float(min_p)).min(initial=np.inf))
         keep &= w >= float(min_p)
     keep &= xs > -np.inf
     stays = np.zeros(v, bool)
@@ -106,5 +118,6 @@ def truncated_sample(x, temperature, top_k, top_p, min_p, u):
     cdf = np.cumsum(mass)
     goal = float(u) * cdf[-1]
     token = int(np.searchsorted(cdf, goal, side="right"))
-    margin = min(margin, np.abs(cdf - goal).min() / cdf[-1])
-    return token, mass[token] / cdf[-1], stays, margin
+    if not whole:
+        draw = np.abs(cdf[cdf > 0.0] - goal).min() / cdf[-1]
+    return token, mass[token] / cdf[-1], stays, cut, draw

@@ -8,7 +8,7 @@ import torch
 
 import block_drafter_pos_gb300 as bd
 from oracle import target as ot
-from test_gpu_target import DT, Setup, check_attention, run_sample
+from test_gpu_target import DT, MARGIN, Setup, check_attention, run_sample
 
 pytestmark = pytest.mark.gpu
 
@@ -344,3 +344,83 @@ def test_kept_in_place_of_wide_rows(n, v, t):
         for a, c in zip(got, want):
             np.testing.assert_array_equal(a, c)
 
+
+
+def _expect(x, k, p, m, u):
+    """Token, probability and what stays at T = 1, for rows whose weights are 1 or (below 2^-50 of that) nothing."""
+    order = np.argsort(-x, kind="stable")
+    top = order[x[order] == x.max()]
+    left = top[:k] if k > 0 else top
+    n = len(left)
+    if p < 1:
+        left = left[np.arange(n) < np.float64(np.float32(p)) * n]
+    left = np.sort(left)
+    pick = int(np.nonzero(np.arange(1, len(left) + 1) > np.float64(np.float32(u)) * len(left))[0][0])
+    return left[pick], 1.0 / len(left), left
+
+
+@pytest.mark.parametrize("v", [300, 9000, 100003])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_sample_decisions_that_lie_on_a_border(v, dtype):
+    """Weights that are equal to the bit: min_p = 1, u = 0 with the first ids cut, and top-p borders inside a group of
+    equal logits are exact decisions, with one right answer."""
+    x = np.full((8, v), -200.0, np.float32)
+    x[0] = 3.0                                                 # all equal
+    x[1, 1::2] = 1.0                                           # every other
+    x[2, 17:] = -4.0                                           # the first ids cut
+    x[3, -1] = 2.0                                             # the last alone
+    x[4, [5, v // 2, v - 2]] = 0.5
+    x[5, v // 3:] = float(torch.finfo(torch.bfloat16).min)     # the lowest of all, under the rest
+    x[6, :100] = -1e4
+    x[6, 100:] = -1e3
+    x[7, 40:290] = 0.0
+    xt = torch.from_numpy(x).to(DT[dtype]).cuda()
+    xd = xt.float().cpu().numpy()
+    for k, p, m in ((0, 1.0, 1.0), (7, 1.0, 1.0), (0, 0.5, 0.0), (0, 0.5, 1.0), (4, 0.5, 0.0), (4, 0.75, 1.0), (250, 0.5, 0.5),
+                    (2000, 0.25, 0.0), (1, 0.1, 1.0), (0, 0.125, 0.25)):
+        for u in (0.0, 0.25, 0.5, 0.75, 1 - 2.0 ** -24):
+            # (with top-k beyond the group of the largest, the other logits' weights are 0: they stay where only top-k cuts)
+            tok, prob, kept, status = run_sample(xt, [1.0] * 8, [k] * 8, [p] * 8, [m] * 8, [u] * 8)
+            assert (status == 0).all()
+            for r in range(8):
+                wt, wp, left = _expect(xd[r], k, p, m, u)
+                assert tok[r] == wt, (r, k, p, m, u, tok[r], wt)
+                assert abs(prob[r] - wp) <= wp * 2.0 ** -23
+                if p < 1 or m > 0:
+                    want = np.full(v, -1e30, np.float32)
+                    want[left] = xd[r][left]
+                    np.testing.assert_array_equal(kept[r], want, err_msg=str((r, k, p, m, u)))
+
+
+def test_sample_rows_of_few_values_leave_little_undecided():
+    """Rows of one, two and three values against the oracle, its two margins apart: what stays is compared wherever that
+    is decided, the draw wherever both are, and few of the rows are neither."""
+    v = 9000
+    x = torch.zeros(10, v)
+    x[1] = x[2] = torch.finfo(torch.float32).min
+    x[2, 17] = 3.0
+    x[3] = float("-inf")
+    x[3, [5, 8999]] = 1.0
+    x[4, ::2] = 1.0
+    x[5] = torch.linspace(-80, 80, v)
+    x[6, 4000] = 100.0
+    x[7] = float("-inf")
+    x[7, 8998] = -1e30
+    x[8] = -1e4
+    x[9] = torch.arange(v) % 3
+    xd, x = x.numpy().astype(np.float64), x.cuda()
+    f32 = lambda a: float(np.float32(a))  # noqa: E731
+    rows = cuts = draws = 0
+    for k, p, m in ((0, 1.0, 0.0), (7, 1.0, 0.0), (0, 0.5, 0.0), (4501, 0.7, 0.0), (1, 0.1, 1.0), (0, 1.0, 1.0), (v, 0.999, 1e-9)):
+        for t in (1.0, 0.05, 100.0):
+            for u in (0.0, 0.37, 1 - 2.0 ** -24):
+                tok, prob, kept, status = run_sample(x, [t] * 10, [k] * 10, [p] * 10, [m] * 10, [u] * 10)
+                assert (status == 0).all()
+                for r in range(10):
+                    wt, wp, stays, cut, draw = ot.truncated_sample_margins(xd[r], f32(t), k, f32(p), f32(m), f32(u))
+                    rows, cuts, draws = rows + 1, cuts + (cut < MARGIN), draws + (min(cut, draw) < MARGIN)
+                    if cut >= MARGIN:
+                        np.testing.assert_array_equal(kept[r], np.where(stays, xd[r].astype(np.float32), np.float32(-1e30)))
+                    if min(cut, draw) >= MARGIN:
+                        assert tok[r] == wt and abs(prob[r] - wp) <= wp * (2.0 ** -27 + 2.0 ** -24) + 2.0 ** -43
+    assert rows == 630 and cuts <= 6 and draws <= 22
