@@ -141,8 +141,11 @@ constexpr int kPagedMaxCtasPerSm = 2;
 constexpr int kChunkBn = 128;
 constexpr int kChunkRows = 256;
 // Most rows of a request for the kernel for few rows.  Above, one unit of the other reads the keys once where this one
-// would read them again for every 32 rows.  Measured (us; few rows / many), 16 requests over 8192 positions of 8 heads of
-// 128: 32 rows bf16 113 / 127, int8 109 / 141, e4m3 95 / 162; 64 rows (64-row units) 152 / 129, 175 / 143, 150 / 163.
+// would read them again for every 32 rows.  Measured (us; few rows / many; bf16, int8, e4m3), 16 requests over 8192
+// positions of 8 heads of 128: 32 rows 108 / 123, 105 / 147, 92 / 165; 64 rows 196 / 126, 187 / 150, 161 / 168.  Heads of
+// 64: 78 / 102, 73 / 111, 67 / 114; 142 / 103, 128 / 113, 117 / 116.  One KV head of 128: 25 / 29, 27 / 36, 26 / 38;
+// 36 / 34, 40 / 39, 38 / 41.  A window of 2048: 44 / 56, 43 / 57, 40 / 61; 64 / 59, 68 / 61, 62 / 65.  One request over
+// 16384: 27 / 31, 30 / 34, 29 / 36; 36 / 31, 38 / 35, 36 / 38.
 constexpr int kChunkMinRows = 32;
 // Scratch of the partials: two slots for each CTA, of 32 rows (two CTAs per SM) or 256.
 inline size_t paged_part_floats(int num_sms, int head_dim) {

@@ -25,11 +25,12 @@
 //    pieces and the contraction order (keys) and the output columns (values) are permuted
 //    to match, so no code passes through shared memory twice.
 //
-// Measured: 64 single tokens of 32 query heads over 8 KV heads' e4m3 caches, ragged to 16384 positions (1.34 GB): 257 us,
-// 5.2 TB/s, 77% of a copy's rate; DRAM moves 15% more than that, the scales' 32-byte sectors being read once per head.
+// Measured: 64 single tokens of 32 query heads over 8 KV heads' e4m3 caches, ragged to 16384 positions (1.34 GB): 256 to
+// 268 us by the GPU, 5.0 to 5.2 TB/s, 74 to 77% of a copy's rate; DRAM moves 15% more than that, the scales' 32-byte
+// sectors being read once per head.
 // 16 blocks of 8 over int8 caches ragged to 8192 (0.21 GB): 84 us, bound by the latency of 8 warps an SM
-// (3 us per tile of 128 keys; 0.44 instructions a scheduler and clock).  16 requests of 4 tokens over 8192 bf16 positions
-// (0.54 GB): 105 us, 5.1 TB/s.
+// (3 us per tile of 128 keys; 0.44 instructions a scheduler and clock).  16 requests over 8192 bf16 positions (0.54 GB):
+// of 4 tokens 105 us, 5.1 TB/s, of 8 (both row tiles) 108, 5.0 TB/s.
 #include "common.cuh"
 #include "paged_mma.cuh"
 #include "paged_sched.cuh"
@@ -342,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, of));
           xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, of));
         }
+        // (to fp16, the codes' exact type: exact from 2^-14 of the row's largest on, off by at most 2^-25 of that below)
         const float fa = pow2_shift(xa), fb = pow2_shift(xb);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
@@ -509,7 +511,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         o[t][3] *= f1;
       }
     }
-    // ---- weights and the values' product
+    // ---- weights and the values' product.  The sum takes the weights in fp32; the product rounds them once to its
+    // operands' type, which has to be the values' (bf16, or fp16 where the codes are), off by 2^-8 or 2^-11 of a weight at most.
+    // In two pieces they would cost the product twice.  Against 64 bits (relative error of the outputs, bf16 caches; that of
+    // rounding the output alone 0.0017): 0.0019 for a single token, 0.0023 for trees; 8 bits: 0.0017.
     const float vinv0 = pow2_inverse(vref0), vinv1 = pow2_inverse(vref1);
 #pragma unroll
     for (int t = 0; t < WK / 8; ++t) {

@@ -14,8 +14,8 @@
 //    2^8 (weights then stay below 2^8, within range of either 16-bit type, and the fp32 sums lose
 //    nothing), which after a unit's first tiles is rare; the tile's own warps do it.
 //  * While one tile's weights are being computed the tensor core works on the other's
-//    products: one thread of warp 8 issues O0, S0', O1, S1', ...
-//  * Warps 9 - 11 bring the keys and values: cp.async of 16-byte pieces through the page table
+//    products: one thread of warp 12 issues O0, S0', O1, S1', ...
+//  * Warps 8 - 11 bring the keys and values: cp.async of 16-byte pieces through the page table
 //    (any page size; its rows are looked up one tile ahead), or, for 8-bit caches, cp.async of the
 //    codes into a staging area from which the same thread writes them as exact fp16 values.  The
 //    keys' scale multiplies the score and the values' scale the weight, relative to a power of
@@ -23,12 +23,14 @@
 //  * Every wait is bounded; one that gives up marks the CTA and ends it once its own copies and
 //    products are done.  The kernel that joins partials flags the run's requests; rows whose partials never came are NaN.
 //
-// Measured: 4096 new tokens of 32 query heads over 32768 bf16 positions of 8 KV heads of 128 (2.06 TFLOP): 1.66 to
-// 1.72 ms, 1.2 PFLOP/s, 70% of the sustained cuBLAS rate, tensor pipe 52% active.  A 128-key tile takes about
+// Measured: 4096 new tokens of 32 query heads over 32768 bf16 positions of 8 KV heads of 128 (2.06 TFLOP): 1.68 to
+// 1.75 ms, 1.2 PFLOP/s, 69 to 72% of the sustained cuBLAS rate, tensor pipe 52% active.  A 128-key tile takes about
 // 3900 clocks where its products take 2048: a row tile's softmax (1700), the products of its weights and next scores
 // (1024) and the hand-offs between them follow one another, and two row tiles cover only part of each other.
-// Five chunks of 1501 tokens of 24 heads of 64 over e4m3 caches with a window of 2048: 235 us, bound by the softmax's
-// instructions (a scale and a factor for every key besides the exponential).
+// Five chunks of 1501 tokens of 24 heads of 64 over e4m3 caches with a window of 2048: 243 us, bound by the softmax's
+// instructions (a scale and a factor for every key besides the exponential; tensor pipe 18% active), 19 of them the join.
+// Under the launch's 128 registers 16-bit caches spill 12 bytes a thread and 8-bit ones 68 to 120 (read back: 72, and 240 to
+// 320).
 #include "common.cuh"
 #include "paged_mma.cuh"
 #include "paged_sched.cuh"
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             x = fmaxf(x, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
+        // (to fp16, the codes' exact type: exact from 2^-14 of the row's largest on, off by at most 2^-25 of that below)
         const float f = pow2_shift(x);
         sc = fmaxf(sc / f, 0x1p-149f);
 #pragma unroll
@@ -460,7 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             tm_st16(o_col + 16 * x, o);
           }
         }
-        // ---- weights (a row that has seen nothing: 2^(-infinity)), announced by halves
+        // ---- weights (a row that has seen nothing: 2^(-infinity)), announced by halves.  Rounded once, after their sum
+        // has taken them in fp32, to the product's operand type, which has to be the values': errors against 64 bits 0.0023
+        // with bf16 where the output's own rounding is 0.0017, 0.00029 with fp16 where that is 0.00021.
         const float mr0 = m == -INFINITY ? 0.f : -m, mr = kQuant ? mr0 + rowe : mr0;
         float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
         const float2 sc2 = make_float2(sc, sc), mr2 = make_float2(mr, mr);

@@ -894,7 +894,9 @@ cudaError_t launch_rows(const SampleArgs& a, cudaStream_t st) {
   // beside them.  The device knows which rows they are: clusters without a row end at once.
   // Measured (us), 248320 fp32 logits, clusters of four in one launch of two waves / this: 128 rows of mixed settings
   // 181 / 149, all top-k 95 / 74, all top-p 394 / 378; 32 rows 98 / 78, 87 / 43, 210 / 134; 512 rows 455 / 367, 242 / 250,
-  // 1257 / 1261.
+  // 1257 / 1261.  The same small clusters in one launch / this (another batch's settings; mixed, top-k, top-p): 128 rows of
+  // 248320 258 / 129, 71 / 75, 367 / 377, in bf16 270 / 152, 88 / 92, 374 / 384; 32 rows 101 / 83, 41 / 45, 132 / 137; 128
+  // rows of 131072 166 / 99, 52 / 56, 216 / 221; of 70000 101 / 71, 40 / 44, 134 / 139.
   const int most = ctas < 4 ? 8 : 2 * ctas, groups = (a.n_rows + kThreads - 1) / kThreads;
   const int few = std::max(1, std::min({5 * a.num_sms / most, a.n_rows / 2, kThreads}));
   const cudaError_t e = launch<T>(a, groups * (a.n_rows < few ? a.n_rows : few), most, kFew, few, st);

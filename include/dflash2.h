@@ -578,7 +578,11 @@ dflash2_status dflash2_paged_read(dflash2_paged_handle* h, const dflash2_paged_c
  * what they held.  Masked positions carry no
  * weight whatever they hold (NaN and infinities included).  q, out: bf16 or fp16, the
  * same type, which with a 16-bit cache is the cache's.  Scores, sums and products are
- * accumulated in fp32. */
+ * accumulated in fp32.  Before the product with the values each weight is rounded once, to
+ * the cache's type (off by at most 2^-8 of it for bf16, 2^-11 for fp16).  With an 8-bit cache the
+ * products run in fp16: the query's elements are exact down to 2^-14 of the row's largest and off by at
+ * most 2^-25 of that below, and the weights, times their value's scale, are off by at most 2^-11 of
+ * themselves or 2^-25 of the largest value scale that the row sees. */
 typedef struct dflash2_paged_attention_args {
   int32_t n_req;
   int32_t n_tokens;    /* rows of q, out, tree_mask, lse                                  */
