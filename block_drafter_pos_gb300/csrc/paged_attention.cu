@@ -19,8 +19,8 @@
 //    costing the third buffer.)
 //  * 16-bit caches feed mma.sync through ldmatrix.  8-bit codes are exact in fp16, so both
 //    products run on fp16 codes: the keys' scale multiplies the score, and the values'
-//    scale the weight, relative to a power of two near the largest scale that the row sees (so the fp16
-//    weight cannot overflow and loses at most 2^-25 of the largest); the queries are rounded to fp16
+//    scale the weight, relative to the largest that the row sees (so the fp16 weight
+//    cannot overflow and loses at most 2^-25 of the largest); the queries are rounded to fp16
 //    after an exact power-of-two shift of their row.  A lane loads the codes as 16-byte
 //    pieces and the contraction order (keys) and the output columns (values) are permuted
 //    to match, so no code passes through shared memory twice.
@@ -465,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     // a row that has seen nothing keeps weights of zero: 2^(-inf - 0)
     const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
     if constexpr (kQuant) {
-      // the row's reference follows the largest finite scale of this warp's keys that the row sees, when that exceeds 16
-      // of it; where rows differ each looks at its own keys (one that it does not see costs it nothing)
+      // the row's reference follows the largest finite scale of this warp's keys that the row sees; where rows differ each
+      // looks at its own keys (one that it does not see costs it nothing)
       float v0 = 0.f, v1 = 0.f;
       if (masked && mixed_rows) {
 #pragma unroll
@@ -491,14 +491,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
         v0 = v1 = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v0)));  // (ordered as the floats from 0 are)
       }
-      if (v0 > 16.f * vref0) {
+      if (v0 > kMostFactor * vref0) {
         const float v = scale_reference(v0);
-        f0 *= vref0 * pow2_inverse(v);
+        f0 *= vref0 * reciprocal(v);
         vref0 = v;
       }
-      if (v1 > 16.f * vref1) {
+      if (v1 > kMostFactor * vref1) {
         const float v = scale_reference(v1);
-        f1 *= vref1 * pow2_inverse(v);
+        f1 *= vref1 * reciprocal(v);
         vref1 = v;
       }
     }
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     // operands' type, which has to be the values' (bf16, or fp16 where the codes are), off by 2^-8 or 2^-11 of a weight at most.
     // In two pieces they would cost the product twice.  Against 64 bits (relative error of the outputs, bf16 caches; that of
     // rounding the output alone 0.0017): 0.0019 for a single token, 0.0023 for trees; 8 bits: 0.0017.
-    const float vinv0 = pow2_inverse(vref0), vinv1 = pow2_inverse(vref1);
+    const float vinv0 = reciprocal(vref0), vinv1 = reciprocal(vref1);
 #pragma unroll
     for (int t = 0; t < WK / 8; ++t) {
       const float p0 = ex2(z[t][0] - ref0), p1 = ex2(z[t][1] - ref0), p2 = ex2(z[t][2] - ref1), p3 = ex2(z[t][3] - ref1);

@@ -18,8 +18,8 @@
 //  * Warps 8 - 11 bring the keys and values: cp.async of 16-byte pieces through the page table
 //    (any page size; its rows are looked up one tile ahead), or, for 8-bit caches, cp.async of the
 //    codes into a staging area from which the same thread writes them as exact fp16 values.  The
-//    keys' scale multiplies the score and the values' scale the weight, relative to a power of
-//    two that a row raises when a scale that it sees exceeds 16 of it.
+//    keys' scale multiplies the score and the values' scale the weight, relative to a
+//    reference that is raised when a scale exceeds 128 of it (row by row where rows see different keys).
 //  * Every wait is bounded; one that gives up marks the CTA and ends it once its own copies and
 //    products are done.  The kernel that joins partials flags the run's requests; rows whose partials never came are NaN.
 //
@@ -408,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         x1 = fmaxf(fmaxf(x1, s[125]), x3);
         const float mx = fmaxf(fmaxf(fmaxf(x0, s[126]), s[127]), x1) * sc;
         float f = 1.f;  // O's factor
+        const bool fresh = j == 0 || m == -INFINITY;  // (nothing seen so far)
         if (j == 0) {
           m = mx;
         } else if (mx > m + kGrow) {
@@ -416,16 +417,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           l *= f;
         }
         // The values' scales are relative to the tile's reference, which is the unit's, and so is O: unless rows of the
-        // tile differ and a scale in it exceeds 16 of that.  Then (a wide tile) each row takes a reference of its
-        // own, at the largest scale that it sees, so that one it does not see costs it nothing; and it goes back to the unit's
-        // in the next tile, if that is not so far below that the weights there are nothing beside it.
+        // tile differ and its scales are too far apart for one.  Then (a wide tile) each row takes a reference of its
+        // own, the tile's by a power of two near a 16th of the largest scale that it sees, so that one it does not see costs it nothing;
+        // and it goes back to the unit's in the next tile, if that is not so far below that the weights there are nothing.
         float rowe = 0.f, rowi = 1.f;  // the tile's reference over the row's: its exponent, which the weights take, and the reciprocal
         if constexpr (kQuant) {
           const float tref = __int_as_float(fl.y);
-          if (j == 0) vref = tref;
+          if (fresh) vref = tref;
           if (vref != tref || (fl.x & 2)) {
-            float v = vref > 0x1p64f * tref ? vref : tref;
-            if (fl.x & 2) {
+            float v = tref, r = 1.f;
+            if (vref > 0x1p64f * tref) {  // (no weight is above fp16's least)
+              v = vref;
+              r = 0x1p-60f;
+            }
+            if ((fl.x & 2) && !(vref > 0x1p108f * tref)) {
               unsigned long long v0, v1;
               visible(key0, fl.x, badw, v0, v1);
               v = 0.f;
@@ -435,13 +440,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 const uint32_t b = static_cast<uint32_t>((x < 64 ? v0 : v1) >> (x & 63));
                 v = fmaxf(v, fmaxf(fmaxf(b & 1 ? w.x : 0.f, b & 2 ? w.y : 0.f), fmaxf(b & 4 ? w.z : 0.f, b & 8 ? w.w : 0.f)));
               }
-              v = scale_reference(fmaxf(v * tref, kLeastRef * fmaxf(tref, 1.f)));
-              if (j != 0 && v <= 16.f * vref) v = vref;
+              const float per = reciprocal(tref);
+              float rel = pow2_at(fmaxf(v * 0.0625f, kLeastRef * fmaxf(1.f, per)));
+              const float now = pow2_at(vref * per);
+              if (!fresh && v <= kMostFactor * now) rel = now;
+              v = tref * rel;
+              // (at less than 2^-60 no weight is above fp16's least, unless the factors are large)
+              r = fmaxf(pow2_inverse(rel), tref < kMostRef ? 0x1p-60f : 0x1p-126f);
             }
-            if (j != 0) f *= vref * pow2_inverse(v);
+            if (!fresh) f *= vref * reciprocal(v);
             vref = v;
-            // (at less than 2^-60 no weight is above fp16's least, unless the factors are large)
-            const float r = fmaxf(tref * pow2_inverse(v), tref < kMostRef ? 0x1p-60f : 0x1p-126f);
             rowe = pow2_exponent(r);
             rowi = pow2_inverse(r);
           }
@@ -743,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         l_first = lc.unit_ends();
         lc.next(a);
       };
-      float vref = 0.f;
+      float vref = 0.f, vinv = 0.f, seen_by_all = 0.f;
       look_up();
       // A thread copies piece ch of rows r0, r0 + kStep, ...: the swizzle's row bits are its own constant.
       constexpr int kPieces = D * (kQuant ? 1 : 2) / 16, kStep = kLoaders / kPieces, kCount = 128 / kStep;
@@ -810,10 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         float* ks = reinterpret_cast<float*>(sgen + G::kOffInfo + ring * G::kInfo);
         uint32_t* badw = reinterpret_cast<uint32_t*>(ks + 256);
         long long* o = offs + (j & 1) * 128;
-        if (piece_first) {
-          if (j > 0) ++unit;
-          vref = 0x1p-126f;
-        }
+        if (piece_first && j > 0) ++unit;
         tile = j;
         mixed_bits = mixed_bits << 1 | (mixed ? 1u : 0u);
         first_bits = first_bits << 1 | (piece_first && j > 0 ? 1u : 0u);
@@ -821,8 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         // thread could not be here, so the weights of tile j - 5 are done.)
         if constexpr (kQuant) {
           const float v = warp_max(vsv < INFINITY ? vsv : 0.f);
-          // (keys outside the unit's range count as 0 there and not at all here)
-          const float w = -warp_max(vsv > 0.f && vsv < INFINITY ? -vsv : -0x1p126f);
+          // (keys without a scale, outside the unit's range or on a bad page among them, count as 0 there and not at all here)
+          const float w = -warp_max(vsv > 0.f && vsv < INFINITY ? -vsv : -INFINITY);
           if (lane == 0) vmax_sh[j & 1][wid - 8] = v, vmin_sh[j & 1][wid - 8] = w;
         }
         o[lt] = off;
@@ -836,20 +841,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if constexpr (kQuant) {
           const float* vm = vmax_sh[j & 1];
           const float v = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
+          // The unit's reference is at most an 8th of a scale that all rows have seen (seen_by_all), or the least one of the
+          // unit's first tile, so that it is nowhere far above what a row has seen.  (That of a tile in which rows differ
+          // is a power of two: with which one a row's weights are multiplied, by the scales of keys that it does not see, is
+          // then nothing to it.)
           bool wide = false;
+          if (piece_first) seen_by_all = 0.f;
           if (mixed) {
-            // (a unit's first: relative to the least scale in it)
             const float* vl = vmin_sh[j & 1];
-            if (piece_first) vref = scale_reference(fminf(fminf(vl[0], vl[1]), fminf(vl[2], vl[3])));
-            wide = v > 16.f * vref;
-          } else if (piece_first || v > 16.f * vref) {
-            vref = scale_reference(v);
+            const float least = fminf(fminf(vl[0], vl[1]), fminf(vl[2], vl[3]));
+            if (piece_first) {
+              vref = pow2_at(least < INFINITY ? 0.125f * least : 0.f);
+              vinv = pow2_inverse(vref);
+            }
+            wide = v > kMostFactor * vref || (least < vref && seen_by_all < 8.f * vref);
+          } else {
+            seen_by_all = fmaxf(seen_by_all, v);
+            if (piece_first || v > kMostFactor * vref || seen_by_all < 8.f * vref) {
+              vref = scale_reference(seen_by_all);
+              vinv = 1.f / vref;
+            }
           }
-          const float tref = wide ? fminf(scale_reference(v), kMostRef) : vref;
+          const float tref = wide ? fminf(pow2_at(v * 0.0625f), kMostRef) : vref;
           ks[lt] = ksv;
           // (a scale that is not finite counts as 0 here; the rows that see it add the products at the end)
           const bool finite = fabsf(vsv) < INFINITY;
-          ks[128 + lt] = finite ? vsv * pow2_inverse(tref) : 0.f;
+          ks[128 + lt] = finite ? vsv * (wide ? pow2_inverse(tref) : vinv) : 0.f;
           if (!finite) poison_sh[unit % G::kRing] = unit + 1;
           if (lt == 0) ks[256 + 5] = tref;
           if (wide) flags |= 2;

@@ -105,12 +105,20 @@ DF2_DEV float pow2_shift(float x) {
   return ex == 0 || ex >= 254 ? 1.f : __uint_as_float((254u - ex) << 23);
 }
 
-// The values' reference: weights of an 8-bit cache are multiplied by their value's scale relative to it.  A power of
-// two, so that its reciprocal (pow2_inverse) and every change of it are exact: the one at a scale, within
-// [2^-126, 2^126].
-DF2_DEV float scale_reference(float v) {
-  return __uint_as_float(__float_as_uint(fminf(fmaxf(v, 0x1p-126f), 0x1p126f)) & 0x7F800000u);
+// The values' reference: weights of an 8-bit cache (at most 2^8) are multiplied by their value's scale relative to it.  It
+// begins at a 16th of a scale (whose value then has a factor of 16) and is raised when one exceeds 128 of it: so far up
+// fp16 holds the product, and down to 2^-25 of the largest scale or less it tells weights apart.  Within [2^-126, 2^126], so that its
+// reciprocal is a normal number.
+constexpr float kMostFactor = 128.f;
+DF2_DEV float in_reference_range(float x) { return fminf(fmaxf(x, 0x1p-126f), 0x1p126f); }
+DF2_DEV float scale_reference(float v) { return in_reference_range(v * 0.0625f); }
+DF2_DEV float reciprocal(float x) {  // within 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+// The power of two at x, within [2^-126, 2^126], and its exact reciprocal and exponent.
+DF2_DEV float pow2_at(float x) { return __uint_as_float(__float_as_uint(in_reference_range(x)) & 0x7F800000u); }
 DF2_DEV float pow2_inverse(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 DF2_DEV float pow2_exponent(float x) { return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127); }
 

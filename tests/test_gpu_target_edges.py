@@ -8,7 +8,7 @@ import torch
 
 import block_drafter_pos_gb300 as bd
 from oracle import target as ot
-from test_gpu_target import DT, MARGIN, Setup, check_attention, run_sample
+from test_gpu_target import DT, HALF, MARGIN, Setup, check_attention, run_sample
 
 pytestmark = pytest.mark.gpu
 
@@ -137,6 +137,119 @@ def test_value_rows_of_zeros(fmt, n, length, window):
     s.close()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,length,window", [(5, 300, 0), (140, 600, 300), (250, 250, 0), (200, 600, 0)])
+@pytest.mark.parametrize("what", ["zero", "bad page"])
+def test_first_tiles_without_a_scale(fmt, n, length, window, what):
+    """Scales of zero, or pages outside the pool, where a unit's keys begin: the rest keeps its weight.  (Enough requests
+    that a CTA has several tiles of a unit.)"""
+    s = Setup([n] * 20, [length] * 20, hq=8, hk=8, dim=64, fmt=fmt, seed=n)
+    q = s.queries("bf16")
+    begin = max(0, length - n - window + 1) // 128 * 128 if window else 0
+    for r in range(20):
+        if what == "zero":
+            for p in range(begin, begin + 128):
+                s.gvs[int(s.table[r, p // 16]), p % 16] = 0.0
+        else:
+            s.gtable[r, begin // 16:begin // 16 + 8] = -1
+        s.vals[r][1][begin:begin + 128] = 0
+    out, lse = s.attend(q, window=window)
+    see = ot.visible(n, length, True, window)
+    if what != "zero":
+        see[:, begin:begin + 128] = False
+    for r in (0, 7, 19):
+        k, v = s.vals[r]
+        part = slice(r * n, (r + 1) * n)
+        want, wl, spread, reach = ot.paged_attention(q.double().numpy()[part], k, v, 64 ** -0.5, see)
+        tol = HALF["bf16"] * np.abs(want) + 2.0 ** -10 * spread + 2.0 ** -20 * np.abs(v).max()
+        assert (np.abs(out[part].float().cpu().numpy() - want) <= tol).all()
+        assert np.array_equal(np.isneginf(lse[part].cpu().numpy()), np.isneginf(wl))
+    s.close()
+
+
+def _dense(s, q, r, at, see, scale):
+    """Request r's rows in 64 bits on the GPU: outputs, and for the bounds the weighted magnitudes, the largest visible
+    value and the largest score's magnitude."""
+    n = s.new[r]
+    k, v = (torch.from_numpy(x).cuda() for x in s.vals[r])
+    group = s.hq // s.hk
+    k, v = (x.repeat_interleave(group, 1).transpose(0, 1) for x in (k, v))                    # [hq, keys, dim]
+    see = torch.from_numpy(see).cuda()
+    z = q[at:at + n].cuda().double().transpose(0, 1) @ k.transpose(1, 2) * scale
+    reach = (q[at:at + n].cuda().double().abs().transpose(0, 1) @ k.abs().transpose(1, 2) * scale).masked_fill(~see, 0).amax(-1)
+    w = torch.softmax(z.masked_fill(~see, float("-inf")), -1).nan_to_num(0.0)
+    # (a position with a weight of zero adds nothing, whatever it holds; one with a weight adds what it holds)
+    bad = ~torch.isfinite(v)
+    out = w @ v.masked_fill(bad, 0.0)
+    hit = (see.to(v.dtype)[None].expand(s.hq, -1, -1) @ bad.to(v.dtype)) > 0
+    big = (see[None, :, :] & (v.masked_fill(bad, 0.0).abs().amax(-1) > 0)[:, None, :])
+    top = (big * v.masked_fill(bad, 0.0).abs().amax(-1)[:, None, :]).amax(-1)
+    return [x.transpose(0, 1) for x in (out, w @ v.masked_fill(bad, 0.0).abs(), hit)] + [x.T for x in (top, reach)]
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_spread_scales_over_many_tiles(seed):
+    """Value scales that differ by up to 2^80, zeros, scales and codes that are no numbers, windows, trees, blocks and prompts,
+    in runs of several tiles and units a CTA: every row against what it sees."""
+    g = np.random.default_rng(seed)
+    fmt = ["int8", "e4m3"][seed % 2]
+    kind = ["prompt", "prompt", "block", "tree"][seed // 2 % 4]
+    n_req = 24
+    lo, hi = {"prompt": (20, 260), "block": (2, 8), "tree": (10, 64)}[kind]
+    new = [int(x) for x in g.integers(lo, hi + 1, n_req)]
+    length = [n + int(g.integers(0, 900)) for n in new]
+    group = 4 if kind != "block" else int(g.choice([1, 4]))
+    s = Setup(new, length, hq=4 * group, hk=4, dim=[64, 128][seed // 8 % 2], page=16, fmt=fmt, seed=seed)
+    window = int(g.choice([0, 0, 40, 300]))
+    causal = bool(kind != "block" or g.random() < 0.5)
+    spread = float(g.choice([3, 12, 40, 80]))
+    tree = None
+    if kind == "tree":
+        words = []
+        for n in new:
+            w = [1]
+            for i in range(1, n):
+                w.append(w[int(g.integers(0, i))] | (1 << i))
+            words += w
+        tree = np.array(words, np.uint64)
+    for r, total in enumerate(length):
+        pos = np.arange(total)
+        pages, rows = torch.from_numpy(s.table[r][pos // 16].astype(np.int64)).cuda(), torch.from_numpy(pos % 16).cuda()
+        # plateaus of scales, single outliers, zeros
+        e = np.repeat(g.uniform(-spread / 2, spread / 2, total // 50 + 1), 50)[:total] if g.random() < 0.5 else np.zeros(total)
+        e = e + np.where(g.random(total) < 0.02, g.uniform(-spread / 2, spread / 2, total), 0)
+        f = np.where(g.random(total) < 0.02, 0.0, np.exp2(np.round(e)))
+        s.gvs[pages, rows] *= torch.from_numpy(f.astype(np.float32)).cuda()[:, None]
+        s.vals[r][1] *= f[:, None, None]
+        for p in np.nonzero(g.random(total) < 0.002)[0]:           # one head of a position
+            h, c = int(g.integers(0, 4)), int(g.integers(0, s.dim))
+            if g.random() < 0.5 or fmt == "int8":
+                s.gvs[int(s.table[r, p // 16]), p % 16, h] = float("nan")
+                s.vals[r][1][p, h] = np.nan
+            else:
+                codes = s.gv[int(s.table[r, p // 16]), p % 16, h].view(torch.uint8).clone()
+                codes[c] = 0x7F
+                s.gv[int(s.table[r, p // 16]), p % 16, h] = codes.view(DT["e4m3"])
+                s.vals[r][1][p, h, c] = np.nan
+    q = s.queries("bf16")
+    scale = s.dim ** -0.5
+    out, lse = s.attend(q, window=window, causal=causal, tree_mask=None if tree is None else torch.from_numpy(tree.view(np.int64)).cuda())
+    at = 0
+    for r, (n, total) in enumerate(zip(new, length)):
+        see = ot.visible(n, total, causal, window, None if tree is None else tree[at:at + n])
+        want, sums, hit, top, reach = _dense(s, q, r, at, see, scale)
+        got = out[at:at + n].double()
+        # the output's rounding, one of the weights, the scores' and exponentials', and weights next to a larger scale: half of
+        # fp16's least step times the reference, an 8th of the largest scale at most, for every key
+        rel = 2 * reach * (s.dim * 2.0 ** -24 + 2.0 ** -23) + 2.0 ** -21 + (total / 64 + 2) * 2.0 ** -22
+        tol = HALF["bf16"] * want.abs() + (HALF["fp16"] + 2 * rel[..., None]) * sums * 1.01 + total * 2.0 ** -28 * top[..., None] + 1e-30
+        assert torch.equal(torch.isnan(got), hit), f"request {r}: NaN pattern"
+        over = ((got - want).abs() > tol) & ~hit
+        assert not over.any(), (r, kind, spread, window, (got - want).abs()[over].max().item(), tol[over].min().item())
+        at += n
+    s.close()
+
+
 @pytest.mark.parametrize("n", [8, 140])
 @pytest.mark.parametrize("byte", [0x7F, 0xFF])
 @pytest.mark.parametrize("dim", [64, 128])
@@ -175,6 +288,28 @@ def test_a_code_that_is_no_number(n, byte, dim):
     s.gv[int(s.table[0, 0]), far, 1] = codes.view(DT["e4m3"])
     out, _ = s.attend(q)
     assert torch.isnan(out[:, 2:, c].float()).all() and torch.equal(out[:, 2:][..., others], clean[:, 2:][..., others])
+    s.close()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "bf16", "fp16"])
+@pytest.mark.parametrize("qt", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [1, 4, 16, 64])
+def test_one_key_is_its_value(fmt, qt, group):
+    """A softmax of one key weighs it 1: the output is the value, rounded once to the output's type.  (Above 32 rows per KV
+    head the weight that is rounded to 16 bits and the sum may stand for a power of two next to 1: two roundings.)"""
+    if fmt not in ot.QMAX and fmt != qt:
+        pytest.skip("a 16-bit cache takes queries of its own type")
+    s = Setup([1] * 40, [1] * 40, hq=2 * group, hk=2, fmt=fmt, seed=group, scale_spread=1e3)
+    out, lse = s.attend(s.queries(qt))
+    for r in range(40):
+        want = torch.from_numpy(s.vals[r][1][0].astype(np.float32)).to(DT[qt])      # [heads, channels]
+        got = out[r].cpu().view(2, group, 128)
+        if group <= 32:
+            assert torch.equal(got, want[:, None].expand(2, group, 128))
+        else:
+            v = torch.from_numpy(s.vals[r][1][0])[:, None]
+            weight = HALF["fp16" if fmt in ot.QMAX else fmt]
+            assert ((got.double() - v).abs() <= v.abs() * (HALF[qt] + weight) * 1.01 + 2.0 ** -25).all()
     s.close()
 
 
