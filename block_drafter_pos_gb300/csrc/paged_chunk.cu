@@ -27,9 +27,9 @@
 // 1.75 ms, 1.2 PFLOP/s, 69 to 72% of the sustained cuBLAS rate, tensor pipe 52% active.  A 128-key tile takes about
 // 3900 clocks where its products take 2048: a row tile's softmax (1700), the products of its weights and next scores
 // (1024) and the hand-offs between them follow one another, and two row tiles cover only part of each other.
-// Five chunks of 1501 tokens of 24 heads of 64 over e4m3 caches with a window of 2048: 243 us, bound by the softmax's
+// Five chunks of 1501 tokens of 24 heads of 64 over e4m3 caches with a window of 2048: 245 us, bound by the softmax's
 // instructions (a scale and a factor for every key besides the exponential; tensor pipe 18% active), 19 of them the join.
-// Under the launch's 128 registers 16-bit caches spill 12 bytes a thread and 8-bit ones 68 to 120 (read back: 72, and 240 to
+// Under the launch's 128 registers 16-bit caches spill 12 bytes a thread and 8-bit ones 92 to 128 (read back: 72, and 284 to
 // 320).
 #include "common.cuh"
 #include "paged_mma.cuh"
