@@ -418,9 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         // The values' scales are relative to the tile's reference, which is the unit's, and so is O: unless rows of the
         // tile differ and its scales are too far apart for one.  Then (a wide tile) each row takes a reference of its
-        // own, the tile's by a power of two near a 16th of the largest scale that it sees, so that one it does not see costs it nothing;
-        // and it goes back to the unit's in the next tile, if that is not so far below that the weights there are nothing.
-        float rowe = 0.f, rowi = 1.f;  // the tile's reference over the row's: its exponent, which the weights take, and the reciprocal
+        // own, the tile's by a power of two near a 16th of the largest scale that it sees, so that one it does not
+        // see costs it nothing; and it goes back to the unit's in the next tile, if that is not so far below that the
+        // weights there are nothing.
+        // The tile's reference over the row's: its exponent, which the weights take, and its reciprocal.
+        float rowe = 0.f, rowi = 1.f;
         if constexpr (kQuant) {
           const float tref = __int_as_float(fl.y);
           if (fresh) vref = tref;
