@@ -28,7 +28,7 @@
 // Measured: 64 single tokens of 32 query heads over 8 KV heads' e4m3 caches, ragged to 16384 positions (1.34 GB): 256 to
 // 268 us by the GPU, 5.0 to 5.2 TB/s, 74 to 77% of a copy's rate; DRAM moves 15% more than that, the scales' 32-byte
 // sectors being read once per head.
-// 16 blocks of 8 over int8 caches ragged to 8192 (0.21 GB): 84 us, bound by the latency of 8 warps an SM
+// 16 blocks of 8 over int8 caches ragged to 8192 (0.21 GB): 85 us, bound by the latency of 8 warps an SM
 // (3 us per tile of 128 keys; 0.44 instructions a scheduler and clock).  16 requests over 8192 bf16 positions (0.54 GB):
 // of 4 tokens 105 us, 5.1 TB/s, of 8 (both row tiles) 108, 5.0 TB/s.
 #include "common.cuh"
@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     const float vinv0 = reciprocal(vref0), vinv1 = reciprocal(vref1);
 #pragma unroll
     for (int t = 0; t < WK / 8; ++t) {
+      const bool h0 = z[t][0] == -INFINITY, h1 = z[t][1] == -INFINITY, h2 = z[t][2] == -INFINITY, h3 = z[t][3] == -INFINITY;
       const float p0 = ex2(z[t][0] - ref0), p1 = ex2(z[t][1] - ref0), p2 = ex2(z[t][2] - ref1), p3 = ex2(z[t][3] - ref1);
       l0 += p0 + p1;
       l1 += p2 + p3;
@@ -527,16 +528,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         z[t][0] *= f.x * vinv0, z[t][1] *= f.y * vinv0;
         z[t][2] *= f.x * vinv1, z[t][3] *= f.y * vinv1;
         if (masked) {  // (a masked position's scale may be anything)
-          if (p0 == 0.f) z[t][0] = 0.f;
-          if (p1 == 0.f) z[t][1] = 0.f;
-          if (p2 == 0.f) z[t][2] = 0.f;
-          if (p3 == 0.f) z[t][3] = 0.f;
+          if (h0) z[t][0] = 0.f;
+          if (h1) z[t][1] = 0.f;
+          if (h2) z[t][2] = 0.f;
+          if (h3) z[t][3] = 0.f;
         }
       }
     }
     // Values may be infinities or NaN (8 bits: codes of NaN) at positions that only some rows see: there the
-    // product takes zeros in their place, and each is added to the rows whose weight for it is not zero (8 bits: noted
-    // for the rows that see it)
+    // product takes zeros in their place, and each is added to the rows that see it, however small their weight (8 bits:
+    // noted for them)
     bool poison = false;
     if constexpr (!kQuant || FMT == kKvE4m3) {
       if (masked && mixed_rows) {
@@ -559,20 +560,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           for (int qq = 0; qq < 4; ++qq) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int src = (lane & ~3) | qq, row = kw + 8 * t + 2 * qq + e;
-              const float p0 = __shfl_sync(0xffffffffu, z[t][e], src), p1 = __shfl_sync(0xffffffffu, z[t][2 + e], src);
+              const int row = kw + 8 * t + 2 * qq + e;
+              bool v0, v1;
+              sees(key0 + row, v0, v1);
 #pragma unroll
               for (int d = 0; d < NT; ++d) {
                 uint32_t w;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vs + row * G::kRowBytes + ((d ^ (row & 7)) << 4) + 4 * q) : "memory");
                 const float2 v = unpack2<kBF>(w);
                 if (!isfinite(v.x)) {
-                  if (p0 != 0.f) o[d][0] += v.x;
-                  if (p1 != 0.f) o[d][2] += v.x;
+                  if (v0) o[d][0] += v.x;
+                  if (v1) o[d][2] += v.x;
                 }
                 if (!isfinite(v.y)) {
-                  if (p0 != 0.f) o[d][1] += v.y;
-                  if (p1 != 0.f) o[d][3] += v.y;
+                  if (v0) o[d][1] += v.y;
+                  if (v1) o[d][3] += v.y;
                 }
               }
             }

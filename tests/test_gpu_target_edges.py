@@ -313,6 +313,27 @@ def test_one_key_is_its_value(fmt, qt, group):
     s.close()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp16", "int8", "e4m3"])
+@pytest.mark.parametrize("n", [3, 8, 140])
+def test_values_that_are_not_finite_under_vanishing_weights(fmt, n):
+    """One-hot scores: a NaN value shows in every row that sees it, however small its weight, and in no other."""
+    length = 200
+    s = Setup([n], [length], hq=4, hk=2, fmt=fmt, seed=n)
+    q = s.queries("bf16" if fmt in ot.QMAX else fmt, amp=60.0)
+    clean, _ = s.attend(q, scale=1.0)
+    for first in (length - n, length - n + n // 2, length - 1, 5):
+        page, row = int(s.table[0, first // 16]), first % 16
+        pool = s.gv if s.gvs is None else s.gvs
+        keep = pool[page, row, 1].clone()
+        pool[page, row, 1] = float("nan")
+        out, _ = s.attend(q, scale=1.0)
+        pool[page, row, 1] = keep
+        sees = max(0, first - (length - n))
+        assert torch.isnan(out[sees:, 2:].float()).all() and torch.equal(out[:sees], clean[:sees])
+        assert torch.equal(out[:, :2], clean[:, :2])
+    s.close()
+
+
 @pytest.mark.parametrize("fmt,amp,q_amp", [("e4m3", 1.0, 2.0 ** -40), ("int8", 1.0, 2.0 ** -100), ("e4m3", 1.0, 1.0), ("bf16", 1e36, 1.0),
                                            ("fp16", 1.0, 1.0)])
 @pytest.mark.parametrize("n", [5, 140])
