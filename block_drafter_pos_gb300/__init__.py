@@ -10,4 +10,8 @@ from .binding import (  # noqa: F401
     dflash2_paged_create, dflash2_paged_destroy, dflash2_paged_write, dflash2_paged_read, dflash2_paged_attention,
     dflash2_sample, make_paged_config, paged_cache,
 )
+from .serving import (  # noqa: F401
+    RopePlan, PagePool, make_rope, page_pool, dflash2_rope, dflash2_paged_rope_write, dflash2_pages_resize, dflash2_pages_fork,
+    dflash2_pages_copy, dflash2_paged_keep, dflash2_paged_shared_bytes, dflash2_paged_attention_shared,
+)
 from .builder import build, LIB  # noqa: F401

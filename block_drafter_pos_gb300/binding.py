@@ -14,7 +14,7 @@ from typing import Dict, Optional
 from .builder import LIB
 
 MAX_LAYERS = 8
-OK, E_INVAL, E_NONFINITE, E_CUDA, E_UNSUPPORTED = 0, 1, 2, 3, 4
+OK, E_INVAL, E_NONFINITE, E_CUDA, E_UNSUPPORTED, E_NO_PAGES = 0, 1, 2, 3, 4, 5
 WEIGHTS_BF16, WEIGHTS_Q8G64 = 0, 1
 
 

@@ -21,7 +21,10 @@ ROOT = os.path.dirname(HERE)
 
 SOURCES = ["api.cu", "gemv.cu", "wide.cu", "glue.cu", "attention.cu", "lmhead.cu", "select.cu", "verify.cu", "noalloc.cu",
            "paged_api.cu", "paged_cache.cu", "paged_attention.cu",
-           "paged_chunk.cu", "sample.cu"]
+           "paged_chunk.cu", "sample.cu", "pages_api.cu", "pages.cu", "rope.cu"]
+# Compiled a second time with the flag, for attention over shared prefixes (paged_sched.cuh).
+SHARED_SOURCES = ["paged_attention.cu", "paged_chunk.cu"]
+SHARED_FLAG = "-DDF2_SHARED_PREFIX=1"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,16 +55,18 @@ def build(verbose: bool = False, force: bool = False) -> str:
     nvcc = nvcc_path()
     flags = _flags(verbose)
 
-    def compile_one(src):
-        obj = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
-        cmd = [nvcc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
+    def compile_one(job):
+        src, extra = job
+        obj = os.path.join(OUT_DIR, src.replace(".cu", "_shared.o" if extra else ".o"))
+        cmd = [nvcc] + flags + extra + ["-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
+    jobs = [(src, []) for src in SOURCES] + [(src, [SHARED_FLAG]) for src in SHARED_SOURCES]
+    with ThreadPoolExecutor(len(jobs)) as ex:
+        results = list(ex.map(compile_one, jobs))
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

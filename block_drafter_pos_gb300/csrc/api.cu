@@ -208,6 +208,7 @@ const char* dflash2_status_string(dflash2_status s) {
     case DFLASH2_E_NONFINITE: return "nonfinite logit or selector score";
     case DFLASH2_E_CUDA: return "CUDA error";
     case DFLASH2_E_UNSUPPORTED: return "unsupported geometry";
+    case DFLASH2_E_NO_PAGES: return "too few free pages";
     default: return "unknown status";
   }
 }

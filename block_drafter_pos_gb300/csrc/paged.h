@@ -88,13 +88,14 @@ struct UnitKeys {
 
 DF2_HD inline int paged_row_tiles(const PagedShape& s, int n) { return (n * s.group + s.rows - 1) / s.rows; }
 
-DF2_HD inline UnitKeys paged_unit_keys(const PagedShape& s, int n, int len, int qt) {
+// from: keys below it are not this unit's.
+DF2_HD inline UnitKeys paged_unit_keys(const PagedShape& s, int n, int len, int qt, int from = 0) {
   const int row1 = (qt + 1) * s.rows < n * s.group ? (qt + 1) * s.rows : n * s.group;
   const int p0 = len - n + qt * s.rows / s.group, p1 = len - n + (row1 - 1) / s.group;
   UnitKeys u;
   u.hi = s.causal == 1 ? p1 + 1 : len;
   if (u.hi < 0) u.hi = 0;
-  u.lo = s.window > 0 && p0 - s.window + 1 > 0 ? p0 - s.window + 1 : 0;
+  u.lo = s.window > 0 && p0 - s.window + 1 > from ? p0 - s.window + 1 : from;
   if (u.lo > u.hi) u.lo = u.hi;
   u.t0 = u.lo / s.bn;
   u.nt = (u.hi + s.bn - 1) / s.bn - u.t0;
@@ -103,10 +104,10 @@ DF2_HD inline UnitKeys paged_unit_keys(const PagedShape& s, int n, int len, int 
 }
 
 // Tiles of one KV head of a request.
-DF2_HD inline long long paged_head_tiles(const PagedShape& s, int n, int len) {
+DF2_HD inline long long paged_head_tiles(const PagedShape& s, int n, int len, int from = 0) {
   long long t = 0;
   const int nq = paged_row_tiles(s, n);
-  for (int qt = 0; qt < nq; ++qt) t += paged_unit_keys(s, n, len, qt).nt;
+  for (int qt = 0; qt < nq; ++qt) t += paged_unit_keys(s, n, len, qt, from).nt;
   return t;
 }
 
@@ -116,6 +117,28 @@ DF2_HD inline long long paged_run_begin(long long c, long long C, long long T) {
 // Whether the run [t0, t1) has a tile of the request whose tiles are [first, next).
 DF2_HD inline bool paged_in_run(long long first, long long next, long long t0, long long t1) {
   return first < next && first < t1 && next > t0;
+}
+
+// Requests in groups that share a prefix: two launches.  In the first the call's "requests" are the groups: their rows see all
+// of the prefix, and each row's result (outputs not divided by the sum, and maximum and sum) goes to the workspace.  In the
+// second they are the requests, with the keys behind the prefix, and what they write has the prefix's part in it.
+struct PagedGroups {
+  const int32_t* begin;   // [n_groups + 1]
+  const int32_t* prefix;  // [n_groups]
+  int n_groups, n_req;
+  int max_group, max_prefix;
+  int first;              // the first launch
+  float* joint;           // [n_tokens * query heads][head_dim], then as many (maximum, sum)
+};
+
+// Whether group g's requests [g0, g1) follow those of the group before and, the last's, end at the last request.  (Where one
+// does not, the whole call is refused: all of `begin` is trusted after that.)
+DF2_HD inline bool paged_group_in_order(const PagedGroups& s, int g, int g0, int g1) {
+  return g0 <= g1 && (g > 0 || g0 == 0) && (g < s.n_groups - 1 || g1 == s.n_req);
+}
+// Whether a group's prefix and rows [b0, b1) are within the call's bounds.
+DF2_HD inline bool paged_group_ok(const PagedGroups& s, const PagedReq& q, int prefix, int b0, int b1) {
+  return prefix >= 0 && prefix <= s.max_prefix && b0 >= 0 && b1 >= b0 && b1 <= q.n_tokens && b1 - b0 <= s.max_group;
 }
 
 struct PagedAttnArgs {
@@ -128,10 +151,12 @@ struct PagedAttnArgs {
   float scale_log2;  // score scale * log2(e)
   float* part;       // partial results: slots of rows * head_dim outputs, then rows * (max, sum)
   // [CTAs][8]: the cut unit that begins in CTA c's run (request, KV head, row tile, last CTA and first slot, first
-  // row of the request, its new tokens), or -1; whether one of the CTA's waits gave up
+  // row of the request, its new tokens), or -1; whether one of the CTA's waits gave up; with shared prefixes, whether
+  // the unit's rows have a part in the workspace
   int* desc;
   unsigned* count;   // [CTAs] partials of that unit that have come (zero between calls)
   int ctas;
+  PagedGroups g;     // with shared prefixes
 };
 
 // Rows of one unit of the kernel for few rows.
@@ -153,5 +178,8 @@ inline size_t paged_part_floats(int num_sms, int head_dim) {
 }
 cudaError_t launch_paged_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
+// The same kernels with a.g (both launches, one after the other).
+cudaError_t launch_shared_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
+cudaError_t launch_shared_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 
 }  // namespace df2

@@ -38,6 +38,7 @@
 namespace df2 {
 namespace {
 
+constexpr bool kShared = DF2_SHARED_PREFIX;
 constexpr int kThreads = 128;
 constexpr float kGrow = 8.f;  // a row's reference follows its maximum when that has grown by more than 2^8
 
@@ -97,7 +98,7 @@ struct Geo {
 // partials of CTAs c0 .. c1 (c0's in its slot `first`) are added in CTA order, eight at a time (their loads
 // together: what this costs is latency).
 template <int D, bool QBF>
-DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int slot0, int b0, int n, int lr) {
+DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int slot0, int b0, int n, int lr, bool joint) {
   const int R = a.s.rows, lane = threadIdx.x & 31, row = qt * R + lr;
   if (row >= n * a.s.group) return;
   const long long first = 2ll * c0 + slot0, stride = static_cast<long long>(R) * (D + 2);
@@ -142,8 +143,23 @@ DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int
           for (int e = 0; e < V; ++e) o[e] += x[i][e] * f;
         }
       }
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       const int i = row / a.s.group, head = h * a.s.group + row % a.s.group;
+      if constexpr (kShared) {
+        float* const j = joint_row<D>(a, b0 + i, head) + V * lane;
+        if (a.g.first) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) j[e] = o[e];
+          if (lane == 0) *joint_stat<D>(a, b0 + i, head) = make_float2(m, l);
+          return;
+        }
+        if (joint) {
+          const JointParts p(m, l, __ldcg(joint_stat<D>(a, b0 + i, head)));
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = o[e] * p.mine + __ldcg(j + e) * p.other;
+          inv = 1.f, m = p.m, l = p.l;
+        }
+      }
       char* po = a.out.p + ((b0 + i) * a.out.token_stride + head * a.out.head_stride + V * lane) * 2;
       if constexpr (V == 4)
         *reinterpret_cast<uint2*>(po) = make_uint2(pack2<QBF>(o[0] * inv, o[1] * inv), pack2<QBF>(o[2] * inv, o[3] * inv));
@@ -174,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   const int rg = wid % MT, kg = wid / MT;
 
   pdl_trigger();
-  const long long T = paged_scan<kThreads>(a, pre, tmp);
+  const long long T = paged_scan<kThreads, kShared>(a, pre, tmp);
   // (no empty runs: a cut unit's CTAs are then consecutive)
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
   if (MT > 1 && tid == 0) a.desc[8 * c] = -1;
@@ -183,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 
   // ---- the page rows of a tile: one key for each of the first kBN threads.  The page table is read (fetch)
   // one tile before its entries become offsets (resolve), so that its latency lies under a tile's work.
-  PagedCursor oc;
+  PagedCursor<kShared> oc;
   oc.start(a, pre, t_begin, t_end);
-  PagedCursor cc = oc;  // the tile that is worked on
+  PagedCursor<kShared> cc = oc;  // the tile that is worked on
   long long my_off = kNoRow, my_soff = 0;
   int my_bad = 0;
   int pg = 0, pg_row = 0, pg_h = 0, pg_r = 0;
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         pg_row = key - pi * a.c.page_size;
         pg_h = oc.h;
         pg_r = oc.r;
-        pg = __ldg(a.c.table + oc.r * a.c.table_stride + pi);
+        pg = __ldg(a.c.table + oc.table_row() * a.c.table_stride + pi);
       }
     }
     oc.next(a);
@@ -211,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     my_bad = 0;
     if (pg_in && !paged_row(a.c, pg, pg_row, pg_h, &my_off, &my_soff)) {
       my_bad = 1;
-      if (a.rq.status) a.rq.status[pg_r] = 1;  // DFLASH2_E_INVAL
+      paged_flag<kShared>(a, pg_r, 1);  // DFLASH2_E_INVAL
     }
   };
   auto put = [&](int slot) {  // into a slot of the offsets' ring
@@ -294,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       const bool va = ra < rows, vb = rb < rows;
       hi0 = va ? (a.s.causal == 1 ? min(cc.len, base + ia + 1) : cc.len) : 0;
       hi1 = vb ? (a.s.causal == 1 ? min(cc.len, base + ib + 1) : cc.len) : 0;
-      lo0 = a.s.window > 0 ? base + ia - a.s.window + 1 : 0;
-      lo1 = a.s.window > 0 ? base + ib - a.s.window + 1 : 0;
+      lo0 = a.s.window > 0 ? base + ia - a.s.window + 1 : cc.first_key();
+      lo1 = a.s.window > 0 ? base + ib - a.s.window + 1 : cc.first_key();
       if (a.s.causal == 2) {
         w0 = va ? __ldg(a.tree + cc.b0 + ia) : 0ull;
         w1 = vb ? __ldg(a.tree + cc.b0 + ib) : 0ull;
@@ -303,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       const int i_first = cc.qt * G::kRows / a.s.group;
       const int i_last = (min((cc.qt + 1) * G::kRows, rows) - 1) / a.s.group;
       hi_min = a.s.causal == 1 ? min(cc.len, base + i_first + 1) : (a.s.causal == 2 ? min(cc.len, base) : cc.len);
-      lo_max = a.s.window > 0 ? base + i_last - a.s.window + 1 : 0;
+      lo_max = a.s.window > 0 ? base + i_last - a.s.window + 1 : cc.first_key();
       mixed_rows = i_last > i_first || a.s.causal == 2;
       const char* pa = a.q.p + ((cc.b0 + ia) * a.q.token_stride + (cc.h * a.s.group + ra % a.s.group) * a.q.head_stride) * 2;
       const char* pb = a.q.p + ((cc.b0 + ib) * a.q.token_stride + (cc.h * a.s.group + rb % a.s.group) * a.q.head_stride) * 2;
@@ -751,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
           dd[4] = cc.b0;
           dd[5] = cc.n;
+          if constexpr (kShared) dd[7] = cc.from > 0;
           dd[0] = cc.r;
         }
 #pragma unroll
@@ -758,9 +775,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           const int lr = rg * 16 + g + 8 * hf, row = cc.qt * G::kRows + lr;
           if (row >= rows) continue;
           const float l = hf ? l1 : l0, m = hf ? m1 : m0;
-          if (whole) {
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (a NaN sum stays NaN)
+          if (whole && !(kShared && a.g.first)) {
+            float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (a NaN sum stays NaN)
             const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
+            float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+            if constexpr (kShared) {
+              if (cc.from > 0) {  // the prefix's part
+                const JointParts p(m, l, *joint_stat<D>(a, cc.b0 + i, head));
+                const float* const j = joint_row<D>(a, cc.b0 + i, head);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    o[t][2 * hf + e] = o[t][2 * hf + e] * p.mine + j[kQuant ? NT * (2 * q + e) + t : 8 * t + 2 * q + e] * p.other;
+                inv = 1.f;
+                lse = p.lse();
+              }
+            }
             char* po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
             if constexpr (!kQuant) {
 #pragma unroll
@@ -780,10 +811,17 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
                       pack2<QBF>(o[t + 6][2 * hf + e] * inv, o[t + 7][2 * hf + e] * inv));
             }
             if (a.lse && q == 0)
-              a.lse[static_cast<long long>(cc.b0 + i) * (a.c.n_kv * a.s.group) + head] =
-                  l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+              a.lse[static_cast<long long>(cc.b0 + i) * (a.c.n_kv * a.s.group) + head] = lse;
           } else {
             float* pp = a.part + slot * (G::kRows * (D + 2)) + lr * D;
+            float2* ps = reinterpret_cast<float2*>(a.part + slot * (G::kRows * (D + 2)) + G::kRows * D + 2 * lr);
+            if constexpr (kShared) {
+              if (whole) {
+                const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
+                pp = joint_row<D>(a, cc.b0 + i, head);
+                ps = joint_stat<D>(a, cc.b0 + i, head);
+              }
+            }
             if constexpr (!kQuant) {
 #pragma unroll
               for (int t = 0; t < NT; ++t)
@@ -796,8 +834,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
                   *reinterpret_cast<float4*>(pp + NT * (2 * q + e) + t) =
                       make_float4(o[t][2 * hf + e], o[t + 1][2 * hf + e], o[t + 2][2 * hf + e], o[t + 3][2 * hf + e]);
             }
-            if (q == 0)
-              *reinterpret_cast<float2*>(a.part + slot * (G::kRows * (D + 2)) + G::kRows * D + 2 * lr) = make_float2(m, l);
+            if (q == 0) *ps = make_float2(m, l);
           }
         }
       }
@@ -815,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
             __threadfence();
             const int slot0 = paged_run_begin(c0, C, T) == cc.unit_t ? 0 : 1;
             for (int lr = wid; lr < G::kRows; lr += kThreads / 32)
-              join_row<D, QBF>(a, cc.h, cc.qt, c0, c1, slot0, cc.b0, cc.n, lr);
+              join_row<D, QBF>(a, cc.h, cc.qt, c0, c1, slot0, cc.b0, cc.n, lr, cc.first_key() > 0);
           }
         }
       }
@@ -829,15 +866,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
   if (!a.rq.status) return;
   auto tiles = [&](int r) {
-    int b0, n, len;
-    return paged_request(a.rq, r, b0, n, len) ? a.c.n_kv * paged_head_tiles(a.s, n, len) : 0ll;
+    PagedWork w;
+    return paged_work<kShared>(a, r, w) && w.n > 0 ? a.c.n_kv * paged_head_tiles(a.s, w.n, w.len, w.from) : 0ll;
   };
   long long T = 0, first = 0;
   for (int r = 0; r < a.rq.n_req; ++r) T += tiles(r);
   const long long C = T < gridDim.x ? T : gridDim.x;
   for (int r = 0; r < a.rq.n_req; ++r) {
     const long long next = first + tiles(r);
-    if (paged_in_run(first, next, paged_run_begin(c, C, T), paged_run_begin(c + 1, C, T))) a.rq.status[r] = 3;  // DFLASH2_E_CUDA
+    if (paged_in_run(first, next, paged_run_begin(c, C, T), paged_run_begin(c + 1, C, T))) paged_flag<kShared>(a, r, 3);  // DFLASH2_E_CUDA
     first = next;
   }
 }
@@ -852,7 +889,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
   if (WAITS && d1.z != 0 && blockIdx.y == 0 && threadIdx.x == 0) flag_run(a, blockIdx.x);
   if (d0.x < 0) return;
   for (int lr = blockIdx.y * 4 + (threadIdx.x >> 5); lr < a.s.rows; lr += 4 * gridDim.y)
-    join_row<D, QBF>(a, d0.y, d0.z, blockIdx.x, d0.w >> 1, d0.w & 1, d1.x, d1.y, lr);
+    join_row<D, QBF>(a, d0.y, d0.z, blockIdx.x, d0.w >> 1, d0.w & 1, d1.x, d1.y, lr, d1.w != 0);
 }
 
 template <int D, int FMT, int MT, bool QBF>
@@ -891,10 +928,34 @@ cudaError_t launch_dim(PagedAttnArgs& a, int fmt, int qtype, int num_sms, cudaSt
 
 }  // namespace
 
-cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
+#if DF2_SHARED_PREFIX
+#define LAUNCH_ATTENTION launch_phase
+#define LAUNCH_CHUNK launch_shared_chunk
+static cudaError_t launch_phase(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
+
+cudaError_t launch_shared_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
+  if (a.g.max_prefix > 0) {
+    PagedAttnArgs p = a;
+    p.g.first = 1;
+    p.rq.n_req = a.g.n_groups;
+    p.rq.max_new = a.g.max_group;
+    p.rq.max_len = a.g.max_prefix;
+    p.s.causal = 0;
+    const cudaError_t e = launch_phase(p, head_dim, fmt, qtype, num_sms, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_phase(a, head_dim, fmt, qtype, num_sms, st);
+}
+
+static
+#else
+#define LAUNCH_ATTENTION launch_paged_attention
+#define LAUNCH_CHUNK launch_paged_chunk
+#endif
+cudaError_t LAUNCH_ATTENTION(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.rq.max_new) * a.s.group;
   cudaError_t e;
-  if (rows > kChunkMinRows) e = launch_paged_chunk(a, head_dim, fmt, qtype, num_sms, st);
+  if (rows > kChunkMinRows) e = LAUNCH_CHUNK(a, head_dim, fmt, qtype, num_sms, st);
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
   // a row per warp for units of 32 rows (four in turn took 2 to 3 us more), four for those of 256

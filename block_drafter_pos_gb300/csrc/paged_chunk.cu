@@ -45,6 +45,8 @@ using pipe::mbar_init_count;
 using pipe::mbar_wait;
 using pipe::smem_u32;
 
+constexpr bool kShared = DF2_SHARED_PREFIX;
+using Cursor = PagedCursor<kShared>;
 constexpr int kThreads = 512;
 constexpr int kLoaders = 128;
 constexpr int kSoftRegs = 200, kOtherRegs = 56;  // 256 threads each: the 512 x 128 of the launch
@@ -176,12 +178,12 @@ DF2_DEV void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 struct UnitMask {
   int base, hi_min, lo_max;
   bool mixed;  // rows differ (or a tree decides key by key)
-  DF2_DEV void set(const PagedShape& s, const PagedCursor& c) {
+  DF2_DEV void set(const PagedShape& s, const Cursor& c) {
     base = c.len - c.n;
     const int rows = c.n * s.group, i0 = c.qt * s.rows / s.group;
     const int i1 = (min((c.qt + 1) * s.rows, rows) - 1) / s.group;
     hi_min = s.causal == 1 ? min(c.len, base + i0 + 1) : (s.causal == 2 ? min(c.len, base) : c.len);
-    lo_max = s.window > 0 ? base + i1 - s.window + 1 : 0;
+    lo_max = s.window > 0 ? base + i1 - s.window + 1 : c.first_key();
     mixed = i1 > i0 || s.causal == 2;
   }
   DF2_DEV bool masked(int key0) const { return key0 < lo_max || key0 + kBN > hi_min; }
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_trigger();
-  const long long T = paged_scan<kThreads>(a, pre, tmp);
+  const long long T = paged_scan<kThreads, kShared>(a, pre, tmp);
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
   if (tid == 0) a.desc[8 * c] = -1, a.desc[8 * c + 6] = 0;
   if (c >= C) return;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     const int t = wid >> 2, lrow = tid & 127;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((wid & 3) * 32) << 16);
     const uint32_t s_col = lane_base + 128 * t, o_col = lane_base + 256 + 128 * t;
-    PagedCursor cc;
+    Cursor cc;
     cc.start(a, pre, t_begin, t_end);
     int n = 0, gtile = 0, gunit = 0;  // this row tile's key tiles so far; the run's key tiles and units
     float m = -INFINITY, l = 0.f, sc = 0.f, vref = 0.f;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     bool active = false;
     // This row's query of the cursor's unit into shared memory (the row tile's scores so far are complete, so
     // its former queries have been read), and what the row sees.
-    auto enter = [&](const PagedCursor& u) {
+    auto enter = [&](const Cursor& u) {
       const int rows = u.n * a.s.group - u.qt * a.s.rows;  // of the unit (may exceed it)
       active = t == 0 || rows > kM;
       um.set(a.s, u);
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       const bool valid = t * kM + lrow < rows;
       const int i = row / a.s.group, head = u.h * a.s.group + row % a.s.group;
       hi = valid ? (a.s.causal == 1 ? min(u.len, um.base + i + 1) : u.len) : 0;
-      lo = a.s.window > 0 ? max(um.base + i - a.s.window + 1, 0) : 0;
+      lo = a.s.window > 0 ? max(um.base + i - a.s.window + 1, 0) : u.first_key();
       if (a.s.causal == 2) word = valid ? __ldg(a.tree + u.b0 + i) : 0ull;
       const uint4* p = reinterpret_cast<const uint4*>(a.q.p + ((u.b0 + i) * a.q.token_stride + head * a.q.head_stride) * 2);
       uint4 w[D / 8];
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       }
       if (!ok) break;
       // ---- the end of the unit (or of the run): the next unit's queries first, then this one's outputs
-      PagedCursor nc = cc;
+      Cursor nc = cc;
       nc.skip(a, piece);
       {
         const int old_lo = lo, old_hi = hi;
@@ -537,9 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (was_active) {
           const int rows = cc.n * a.s.group - cc.qt * a.s.rows;
           const int i_last = cc.i + piece - 1;
-          const bool whole = cc.unit_t >= t_begin && i_last == cc.u.nt - 1;
+          const bool unit_whole = cc.unit_t >= t_begin && i_last == cc.u.nt - 1;
+          const bool whole = unit_whole && !(kShared && a.g.first);  // (its rows are done)
           const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
-          if (!whole && t == 0 && lrow == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
+          if (!unit_whole && t == 0 && lrow == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
             const long long cb = ((cc.unit_t + cc.u.nt) * C - 1) / T;
             int* dd = a.desc + 8 * c;
             dd[1] = cc.h;
@@ -547,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
             dd[4] = cc.b0;
             dd[5] = cc.n;
+            if constexpr (kShared) dd[7] = cc.from > 0;
             dd[0] = cc.r;
           }
           ok = mbar_wait(o_done + 8 * t, static_cast<uint32_t>((n - 1) & 1));
@@ -559,9 +563,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           const bool valid = lr < rows;
           const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
           const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (a NaN sum stays NaN)
-          const float out_f = kQuant ? (whole ? inv * vref : vref) : (whole ? inv : 1.f);
+          float out_f = kQuant ? (whole ? inv * vref : vref) : (whole ? inv : 1.f);
           char* const po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
-          float* const pp = a.part + slot * (a.s.rows * (D + 2)) + lr * D;
+          float* pp = a.part + slot * (a.s.rows * (D + 2)) + lr * D;
+          float2* ps = reinterpret_cast<float2*>(a.part + slot * (a.s.rows * (D + 2)) + a.s.rows * D + 2 * lr);
+          float other = 0.f;  // the factor of the prefix's part
+          if constexpr (kShared) {
+            if (unit_whole && valid) {
+              if (a.g.first) {
+                pp = joint_row<D>(a, cc.b0 + i, head);
+                ps = joint_stat<D>(a, cc.b0 + i, head);
+              } else if (cc.from > 0) {
+                const JointParts p(m, l, *joint_stat<D>(a, cc.b0 + i, head));
+                pp = joint_row<D>(a, cc.b0 + i, head);
+                out_f = kQuant ? p.mine * vref : p.mine;
+                other = p.other;
+                m = p.m, l = p.l;
+              }
+            }
+          }
           const bool poison = *static_cast<volatile int*>(&poison_sh[gunit % G::kRing]) > gunit;
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
@@ -578,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 if (!kQuant && !old_um.masked(k0)) continue;
                 for (int key = max(k0, old_lo); key < min(k0 + kBN, old_hi); ++key) {
                   if (a.s.causal == 2 && key >= old_um.base && !((old_word >> (key - old_um.base)) & 1ull)) continue;
-                  const int page = __ldg(a.c.table + cc.r * a.c.table_stride + key / a.c.page_size);
+                  const int page = __ldg(a.c.table + cc.table_row() * a.c.table_stride + key / a.c.page_size);
                   long long off, so;
                   if (!paged_row(a.c, page, key % a.c.page_size, cc.h, &off, &so)) continue;
                   if constexpr (kQuant) {
@@ -608,6 +628,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             if (valid) {
 #pragma unroll
               for (int y = 0; y < 32; ++y) o[y] *= out_f;
+              if constexpr (kShared) {
+                if (whole && cc.from > 0) {
+#pragma unroll
+                  for (int y = 0; y < 32; y += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(pp + 32 * x + y);
+                    o[y] += v.x * other, o[y + 1] += v.y * other, o[y + 2] += v.z * other, o[y + 3] += v.w * other;
+                  }
+                }
+              }
               if (whole) {
 #pragma unroll
                 for (int y = 0; y < 32; y += 8)
@@ -627,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 a.lse[static_cast<long long>(cc.b0 + i) * (a.c.n_kv * a.s.group) + head] =
                     l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
             } else {
-              *reinterpret_cast<float2*>(a.part + slot * (a.s.rows * (D + 2)) + a.s.rows * D + 2 * lr) = make_float2(m, l);
+              *ps = make_float2(m, l);
             }
           }
           __syncwarp();
@@ -647,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // -------------------------------------------------------------- products
       const uint32_t go = lane == 0 ? 1u : 0u;
       constexpr uint32_t id_s = instr(kBF, kBN, false), id_o = instr(kBF, D, true);
-      PagedCursor cs;  // the unit whose scores come next
+      Cursor cs;  // the unit whose scores come next
       cs.start(a, pre, t_begin, t_end);
       const int total = static_cast<int>(t_end - t_begin);
       int sn = 0, units = 0, left = cs.piece(), piece = left;  // tiles of that unit still to come
@@ -718,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // -------------------------------------------------------------- keys and values
       const int lt = tid - 256;
       long long* const offs = reinterpret_cast<long long*>(sgen + G::kOffOffs);
-      PagedCursor lc;
+      Cursor lc;
       lc.start(a, pre, t_begin, t_end);
       const int total = static_cast<int>(t_end - t_begin);
       UnitMask um;
@@ -738,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         badv = false;
         if (key >= lc.u.lo && key < lc.u.hi) {
           const int pi = key / a.c.page_size;
-          const int page = __ldg(a.c.table + lc.r * a.c.table_stride + pi);
+          const int page = __ldg(a.c.table + lc.table_row() * a.c.table_stride + pi);
           long long so;
           if (paged_row(a.c, page, key - pi * a.c.page_size, lc.h, &off, &so)) {
             if (kQuant) {
@@ -747,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             }
           } else {
             badv = true;
-            if (a.rq.status) a.rq.status[lc.r] = 1;  // DFLASH2_E_INVAL
+            paged_flag<kShared>(a, lc.r, 1);  // DFLASH2_E_INVAL
           }
         }
         l_first = lc.unit_ends();
@@ -979,7 +1008,11 @@ cudaError_t launch_dim(PagedAttnArgs& a, int fmt, int qtype, int num_sms, cudaSt
 
 }  // namespace
 
+#if DF2_SHARED_PREFIX
+cudaError_t launch_shared_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
+#else
 cudaError_t launch_paged_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
+#endif
   a.s.rows = kChunkRows;
   a.s.bn = kBN;
   return head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);

@@ -59,7 +59,8 @@ enum {
   DFLASH2_E_INVAL = 1,        /* bad argument: size, NULL pointer, alignment            */
   DFLASH2_E_NONFINITE = 2,    /* device status word: NaN/+inf logit or selector score   */
   DFLASH2_E_CUDA = 3,         /* CUDA launch or runtime error                           */
-  DFLASH2_E_UNSUPPORTED = 4   /* geometry or request count with no instantiated kernel  */
+  DFLASH2_E_UNSUPPORTED = 4,  /* geometry or request count with no instantiated kernel  */
+  DFLASH2_E_NO_PAGES = 5      /* device status word: the pool has too few free pages     */
 };
 
 enum { DFLASH2_WEIGHTS_BF16 = 0, DFLASH2_WEIGHTS_Q8G64 = 1 };
@@ -602,6 +603,151 @@ typedef struct dflash2_paged_attention_args {
 } dflash2_paged_attention_args;
 dflash2_status dflash2_paged_attention(dflash2_paged_handle* h, const dflash2_paged_cache* cache,
                                        const dflash2_paged_attention_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Serving many samples of one prompt: rotary positions, the pages of a pool that rows of one page
+ * table share, and attention of requests with a common prefix.
+ * ------------------------------------------------------------------------------------ */
+
+/* Rotary positions.  Pair i < rot_dim / 2 of a head's first rot_dim channels, (i, i + rot_dim / 2)
+ * or, interleaved, (2 i, 2 i + 1), is turned by position * f_i radians and multiplied by the
+ * amplitude; channels from rot_dim on pass unchanged.  With base_i = theta^(-2 i / rot_dim), all in FP64:
+ *   PLAIN    f_i = base_i;
+ *   LINEAR   f_i = base_i / factor;
+ *   YARN     f_i = base_i (1 - g_i) + base_i / factor g_i, g_i = (i - lo) / (hi - lo) within [0, 1] (0.001 in the
+ *            denominator's place if hi <= lo), where b(n) = rot_dim ln(original_len / (2 pi n)) / (2 ln theta),
+ *            lo = max(floor(b(beta_fast)), 0), hi = min(ceil(b(beta_slow)), rot_dim - 1);
+ *   TABLE    f_i = table[i] (a host array; theta and factor are not looked at).
+ * amplitude 0: 0.1 ln(factor) + 1 for YARN, else 1. */
+enum { DFLASH2_ROPE_PLAIN = 0, DFLASH2_ROPE_LINEAR = 1, DFLASH2_ROPE_YARN = 2, DFLASH2_ROPE_TABLE = 3 };
+#define DFLASH2_ROPE_MAX_DIM 256
+
+typedef struct dflash2_rope_config {
+  int32_t rot_dim;       /* a multiple of 16, at most DFLASH2_ROPE_MAX_DIM             */
+  int32_t interleaved;   /* 0 or 1                                                      */
+  int32_t scaling;       /* DFLASH2_ROPE_*                                              */
+  int32_t original_len;  /* YARN: positions the model was trained on                    */
+  double theta;          /* above 1                                                     */
+  double factor;         /* LINEAR: above 0; YARN: at least 1                           */
+  double beta_fast, beta_slow; /* YARN: turns in original_len, above 0; 0: 32 and 1     */
+  double amplitude;      /* not negative                                                */
+  const double* table;   /* TABLE: [rot_dim / 2], finite, within +-2^20                 */
+} dflash2_rope_config;
+
+/* The plan: a plain host structure, copied into each call (nothing on the device; used from any thread). */
+typedef struct dflash2_rotation {
+  int32_t rot_dim, interleaved;
+  float amplitude;
+  int32_t reserved;
+  uint64_t turns[DFLASH2_ROPE_MAX_DIM / 2]; /* f_i / (2 pi) as a fraction of 2^64 */
+} dflash2_rotation;
+
+/* Computes a plan (host only).  The angle of a position p is p * turns[i] modulo 2^64, exact for every int32
+ * position up to the rounding of f_i in FP64. */
+dflash2_status dflash2_rope_plan(const dflash2_rope_config* cfg, dflash2_rotation* out);
+
+/* Turns rows x [n_tokens][x_heads][head_dim] into out, and in the same launch k [n_tokens][k_heads][head_dim] into
+ * k_out (k_heads 0: none).  positions int32 [n_tokens], any value.  inverse != 0: by the opposite angle with the same
+ * amplitude, which takes the gradient of out back to that of x.  head_dim: a multiple of 8 from rot_dim to 1024.
+ * Each output is x, cosine and sine in fp32, rounded once.  x and out have one type; out may be x
+ * itself (the same address and strides), any other overlap of their address ranges is refused. */
+dflash2_status dflash2_rope(const dflash2_rotation* rope, int32_t n_tokens, int32_t head_dim, int32_t x_heads,
+                            const dflash2_rows* x, const dflash2_rows* out, int32_t k_heads, const dflash2_rows* k,
+                            const dflash2_rows* k_out, const int32_t* positions, int32_t inverse, void* stream);
+
+/* dflash2_paged_write of the turned keys, and the turned queries (n_q_heads heads) into q_out: k is turned in fp32
+ * and rounded once, to the cache's format; v is written as it is.  Tokens are turned by their positions in the
+ * cache, or by positions[row] (int32 [n_tokens]; a draft tree's nodes by their depths).  q NULL: keys and values
+ * only.  q, k, v, q_out have one type; q_out may be q itself.  rot_dim at most head_dim.  Rows of a request that is
+ * out of bounds keep what they held, q_out's too; a bad page's queries are turned. */
+dflash2_status dflash2_paged_rope_write(dflash2_paged_handle* h, const dflash2_rotation* rope,
+                                        const dflash2_paged_cache* cache, int32_t n_req, int32_t n_tokens,
+                                        const int32_t* token_begin, const int32_t* kv_len, const int32_t* positions,
+                                        const dflash2_rows* q, const dflash2_rows* q_out, const dflash2_rows* k,
+                                        const dflash2_rows* v, int32_t* status, void* stream);
+
+/* The pages of a pool, shared by the rows of one page table (all layers' pools go by the same ids).
+ * ref int32 [n_pages]: how many rows of the table hold the page; 0: free.  A program begins with zeros, and rows
+ * of length 0.  Row r holds the pages of its first ceil(kv_len[r] / page_size) columns.  The calls below keep
+ * this; each reads and changes it on the device, in stream order. */
+#define DFLASH2_PAGES_MAX (1 << 22)
+typedef struct dflash2_page_pool {
+  int32_t* ref;
+  int32_t* page_table;  /* [n_rows][table_stride], its first max_pages columns used */
+  int64_t table_stride;
+  int32_t n_pages;      /* at most DFLASH2_PAGES_MAX */
+  int32_t n_rows;       /* at most DFLASH2_PAGED_MAX_REQUESTS */
+  int32_t max_pages;
+  int32_t page_size;
+} dflash2_page_pool;
+
+/* Brings every row from kv_len[r] to new_len[r] positions (int32 [n_rows]) and kv_len[r] to new_len[r].
+ * A shorter row gives the pages past its end back (their columns become -1; a page without holders is free to the
+ * next call, not to this one).  A longer one takes pages, by row and then by column, the lowest free ids first.  Where
+ * it would write to a page that other rows hold too (its last page, partly filled), it takes a page in that one's
+ * place, gives that one back, and notes the copy; but if all holders of the page grow in this call, the first
+ * row keeps it.
+ *   copies int32 [3][n_rows], written: the page to copy from, the page to copy to, and how many of its first
+ *     positions (-1, -1, 0: none), for dflash2_pages_copy, which every layer's pools need before the next change.
+ *   status int32 [n_rows] or NULL, set to an error, never cleared: DFLASH2_E_INVAL (a negative length, one past
+ *     max_pages pages, a page id outside the pool or a held page that counts no holder); DFLASH2_E_NO_PAGES (the row, or one
+ *     before it that takes pages, needs more than are left; it keeps its length and its pages).  Such a row takes nothing. */
+dflash2_status dflash2_pages_resize(const dflash2_page_pool* pool, int32_t* kv_len, const int32_t* new_len,
+                                    int32_t* copies, int32_t* status, void* stream);
+
+/* Row child[i] becomes another holder of all pages of row parent[i], with its length (int32 [n_fork]; n_fork at most
+ * DFLASH2_PAGED_MAX_REQUESTS).  No page is taken or copied: dflash2_pages_resize does that once either row grows.
+ *   status int32 [n_fork] or NULL: DFLASH2_E_INVAL, and nothing done for the pair, where a row is outside the table,
+ *     the child's length is not 0, the child is a child twice or a parent too, or the parent's length or a page of
+ *     it is out of bounds. */
+dflash2_status dflash2_pages_fork(const dflash2_page_pool* pool, int32_t n_fork, const int32_t* parent,
+                                  const int32_t* child, int32_t* kv_len, int32_t* status, void* stream);
+
+/* Copies the first copies[2][i] positions of page copies[0][i] to page copies[1][i] (int32 [3][n]), keys, values
+ * and scales, in each of n_caches pools of the handle's geometry (host array; page tables are not looked at).  An
+ * entry with a negative page is passed over; one outside the pool, or with more positions than a page has, is
+ * flagged in status [n] (or NULL) as DFLASH2_E_INVAL and not done.  A page copied to must be named once. */
+dflash2_status dflash2_pages_copy(dflash2_paged_handle* h, int32_t n_caches, const dflash2_paged_cache* caches,
+                                  int32_t n, const int32_t* copies, int32_t* status, void* stream);
+
+/* Keeps some of the newest tokens of each request (the accepted path of a draft tree) and moves them
+ * together: new token keep[r][j] (of the n = token_begin[r + 1] - token_begin[r] that end at kv_len[r]) goes to the place of
+ * new token j, j < n_keep[r], in each of n_caches pools (host array; codes and scales as they are).  keep int32
+ * [n_req][keep_stride], each row's first n_keep[r] <= max_keep entries ascending.  n at most DFLASH2_PAGED_MAX_TREE.
+ *   kv_out int32 [n_req] or NULL: kv_len - n + n_keep (kv_len for a request out of bounds); not kv_len itself.
+ *   status [n_req] or NULL: DFLASH2_E_INVAL as for dflash2_paged_write, or for n_keep or keep out of bounds; nothing
+ *     of such a request is moved.  A bad page in one layer stops the request in that layer alone. */
+dflash2_status dflash2_paged_keep(dflash2_paged_handle* h, int32_t n_caches, const dflash2_paged_cache* caches,
+                                  int32_t n_req, const int32_t* token_begin, const int32_t* kv_len,
+                                  const int32_t* keep, int64_t keep_stride, int32_t max_keep, const int32_t* n_keep,
+                                  int32_t* kv_out, int32_t* status, void* stream);
+
+/* dflash2_paged_attention where consecutive requests share a prefix: with x.window 0, the same outputs up to
+ * rounding, the prefix's keys and values read once for the group instead of once for each of its requests.
+ *   group_begin int32 [n_groups + 1] (device): group g is requests group_begin[g] .. group_begin[g + 1] - 1,
+ *     ascending from 0 to x.n_req (if it does not, every request is flagged and nothing is written).
+ *   prefix_len int32 [n_groups] (device): positions below it hold the same keys and values for every request of
+ *     the group; they are read through the page table's row of its first request.  0: nothing is shared.  At most
+ *     kv_len - n of each of its requests.
+ *   max_group, max_prefix: at least every group's number of new tokens and prefix_len (host bounds).
+ *   workspace: dflash2_paged_shared_bytes(h, x.n_tokens) bytes, 16-byte aligned, used by one call at a time.
+ * A group whose prefix or rows break these bounds is skipped and all its requests are flagged, as they are for a bad page of
+ * its prefix (which is masked); a request that does is skipped and flagged alone.  A row that two good ranges hold is
+ * not valid.  The largest group's rows (max_group times query heads per KV head) end at 2^31 - 512. */
+typedef struct dflash2_paged_shared_args {
+  dflash2_paged_attention_args x;
+  int32_t n_groups;
+  int32_t max_group;
+  int32_t max_prefix;
+  int32_t reserved;
+  const int32_t* group_begin;
+  const int32_t* prefix_len;
+  void* workspace;
+  int64_t workspace_bytes;
+} dflash2_paged_shared_args;
+int64_t dflash2_paged_shared_bytes(const dflash2_paged_handle* h, int32_t n_tokens);
+dflash2_status dflash2_paged_attention_shared(dflash2_paged_handle* h, const dflash2_paged_cache* cache,
+                                              const dflash2_paged_shared_args* args, void* stream);
 
 /* Truncated sampling of n_rows rows of logits [vocab] (type DFLASH2_T_*, aligned to it, row_stride
  * elements apart) with the caller's uniforms.  Per row: weights w_i = exp((x_i - max x) / T);
