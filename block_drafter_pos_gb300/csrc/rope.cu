@@ -56,40 +56,97 @@ DF2_DEV void turn_item(float (&lo)[8], float (&hi)[8], const float4* table, int 
 }
 
 // One item of a head: 16 turned channels (j < items), or up to 16 of those behind them.
-template <int T, bool IL>
-struct Item {
-  float lo[8], hi[8];
+struct Span {
   int first, second;  // channels (second < 0: none)
-  DF2_DEV void at(int rot, int dim, int items, int j) {
-    if (j < items) {
-      first = IL ? 16 * j : 8 * j;
-      second = IL ? first + 8 : first + (rot >> 1);
+  bool turned;
+  template <bool IL>
+  static DF2_DEV Span of(int rot, int dim, int items, int j) {
+    Span s;
+    s.turned = j < items;
+    if (s.turned) {
+      s.first = IL ? 16 * j : 8 * j;
+      s.second = IL ? s.first + 8 : s.first + (rot >> 1);
     } else {
-      first = rot + 16 * (j - items);
-      second = first + 8 < dim ? first + 8 : -1;
+      s.first = rot + 16 * (j - items);
+      s.second = s.first + 8 < dim ? s.first + 8 : -1;
+    }
+    return s;
+  }
+};
+// 8 channels as they lie in memory.
+template <int T>
+struct Raw {
+  uint4 w[T == kTF32 ? 2 : 1];
+  DF2_DEV void load(const char* p, long long off) {
+    const uint4* s = reinterpret_cast<const uint4*>(p + off * (T == kTF32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (T == kTF32 ? 2 : 1); ++i) w[i] = s[i];
+  }
+  DF2_DEV void store(char* p, long long off) const {
+    uint4* d = reinterpret_cast<uint4*>(p + off * (T == kTF32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (T == kTF32 ? 2 : 1); ++i) d[i] = w[i];
+  }
+  DF2_DEV void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < (T == kTF32 ? 2 : 1); ++i) {
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (T == kTF32) {
+          x[4 * i + e] = __uint_as_float(v[e]);
+        } else {
+          const float2 f = unpack2<T == kTBf16>(v[e]);
+          x[2 * e] = f.x, x[2 * e + 1] = f.y;
+        }
+      }
     }
   }
-  DF2_DEV void load(const char* p, long long row) {
-    load8<T>(p, row + first, lo);
-    if (second >= 0) load8<T>(p, row + second, hi);
-  }
-  DF2_DEV void store(char* p, long long row) const {
-    store8<T>(p, row + first, lo);
-    if (second >= 0) store8<T>(p, row + second, hi);
+  DF2_DEV void put(const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < (T == kTF32 ? 2 : 1); ++i) {
+      if constexpr (T == kTF32)
+        w[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
+      else
+        w[i] = make_uint4(pack2<T == kTBf16>(x[0], x[1]), pack2<T == kTBf16>(x[2], x[3]), pack2<T == kTBf16>(x[4], x[5]),
+                          pack2<T == kTBf16>(x[6], x[7]));
+    }
   }
 };
 
-struct Quotient {  // n / d for n and d up to 2^16 (the magic number is off by less than d / 2^32)
-  uint32_t magic;
-  __host__ explicit Quotient(int d) : magic(static_cast<uint32_t>((0x100000000ull + d - 1) / d)), d(d) {}
-  DF2_DEV int of(int n) const { return d == 1 ? n : static_cast<int>(__umulhi(n, magic)); }
-  int d;
-};
-
-// A CTA turns `per` tokens.  Its items are numbered by token, then x's heads and k's, then along the head.
+// The item of tokens t, t + 1, ... (`n` of them, at most kTogether; those whose bit in `live` is not set are passed over): their
+// loads are in flight together.
+constexpr int kTogether = 4;
 template <int T, bool IL>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int per, Quotient by_token,
-                                                        Quotient by_xhead, Quotient by_khead) {
+DF2_DEV void turn_tokens(const PagedRows& x, const PagedRows& y, long long t, int h, const Span& s, int n, uint32_t live,
+                         const float4* table, int items, int j) {
+  Raw<T> lo[kTogether], hi[kTogether];
+  const long long from = t * x.token_stride + h * x.head_stride, to = t * y.token_stride + h * y.head_stride;
+#pragma unroll
+  for (int e = 0; e < kTogether; ++e)
+    if (e < n && (live >> e & 1)) {
+      lo[e].load(x.p, from + e * x.token_stride + s.first);
+      if (s.second >= 0) hi[e].load(x.p, from + e * x.token_stride + s.second);
+    }
+#pragma unroll
+  for (int e = 0; e < kTogether; ++e)
+    if (e < n && (live >> e & 1)) {
+      if (s.turned) {
+        float a[8], b[8];
+        lo[e].get(a);
+        hi[e].get(b);
+        turn_item<IL>(a, b, table + e * 4 * items, items, j);
+        lo[e].put(a);
+        hi[e].put(b);
+      }
+      lo[e].store(y.p, to + e * y.token_stride + s.first);
+      if (s.second >= 0) hi[e].store(y.p, to + e * y.token_stride + s.second);
+    }
+}
+
+// A CTA turns `per` tokens.  A thread takes an item (numbered by x's heads and k's, then along the head) of up to four tokens at a time.
+template <int T, bool IL>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int per, int x_each, int k_each) {
   extern __shared__ float4 table[];  // [per][4][items]
   const int items = a.plan.rot >> 4, pairs = a.plan.rot >> 1;
   const int t0 = blockIdx.x * per, n = min(per, a.n_tokens - t0);
@@ -98,70 +155,37 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     put_turn(table + t * 4 * items, items, i - t * pairs, turn_of(a.plan, i - t * pairs, __ldg(a.positions + t0 + t)));
   }
   __syncthreads();
-  const int x_items = a.x_heads * by_xhead.d;
-  struct Place {
-    const char* src;
-    char* dst;
-    long long from, to;
-    int t, j;
-  };
-  auto place = [&](int i, Item<T, IL>& it) {
-    Place p;
-    p.t = by_token.of(i);
-    int o = i - p.t * by_token.d;
+  const int x_items = a.x_heads * x_each, token = x_items + a.k_heads * k_each, groups = (n + kTogether - 1) / kTogether;
+  for (int i = blockIdx.y * kThreads + threadIdx.x; i < token * groups; i += kThreads * gridDim.y) {
+    const int g = i / token;
+    int o = i - g * token;
     const bool x = o < x_items;
     if (!x) o -= x_items;
-    const int h = x ? by_xhead.of(o) : by_khead.of(o);
-    p.j = o - h * (x ? by_xhead.d : by_khead.d);
-    const PagedRows &s = x ? a.x : a.k, &d = x ? a.y : a.ky;
-    p.src = s.p, p.dst = d.p;
-    p.from = (t0 + p.t) * s.token_stride + h * s.head_stride;
-    p.to = (t0 + p.t) * d.token_stride + h * d.head_stride;
-    it.at(a.plan.rot, a.dim, items, p.j);
-    return p;
-  };
-  const int total = n * by_token.d;
-  for (int i = blockIdx.y * kThreads + threadIdx.x; i < total; i += 2 * kThreads * gridDim.y) {
-    Item<T, IL> u[2];
-    Place p[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int ie = i + e * kThreads * static_cast<int>(gridDim.y);
-      p[e].t = -1;
-      if (ie < total) {
-        p[e] = place(ie, u[e]);
-        u[e].load(p[e].src, p[e].from);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (p[e].t < 0) continue;
-      if (p[e].j < items) turn_item<IL>(u[e].lo, u[e].hi, table + p[e].t * 4 * items, items, p[e].j);
-      u[e].store(p[e].dst, p[e].to);
-    }
+    const int each = x ? x_each : k_each, h = o / each, j = o - h * each;
+    turn_tokens<T, IL>(x ? a.x : a.k, x ? a.y : a.ky, t0 + g * kTogether, h, Span::of<IL>(a.plan.rot, a.dim, items, j),
+                       n - g * kTogether, 15u, table + g * kTogether * 4 * items, items, j);
   }
 }
 
 template <int T>
 cudaError_t launch_rows(const RopeArgs& a, int num_sms, cudaStream_t st) {
   const int items = a.plan.rot >> 4, rest = (a.dim - a.plan.rot + 15) >> 4;
-  const Quotient xh(items + (a.x_copy ? rest : 0)), kh(items + (a.k_copy ? rest : 0));
-  const int token = a.x_heads * xh.d + a.k_heads * kh.d;
-  // about 8 items a thread while that leaves two CTAs an SM; below, a token a CTA, its items split over up to 4
-  int per = std::max(1, std::min({16, 8 * kThreads / token, a.n_tokens / (2 * num_sms)}));
+  const int x_each = items + (a.x_copy ? rest : 0), k_each = items + (a.k_copy ? rest : 0);
+  const int token = a.x_heads * x_each + a.k_heads * k_each;
+  // 8 tokens a CTA, or 16 of few items, while that leaves two CTAs an SM; below, a token a CTA, its items split over up to 4
+  const int per = a.n_tokens >= 16 * num_sms ? (token <= kThreads ? 16 : 8) : std::max(1, std::min(kTogether, a.n_tokens / (2 * num_sms)));
   const int ctas = (a.n_tokens + per - 1) / per;
-  const int split = ctas >= num_sms ? 1 : std::max(1, std::min(4, (token + 2 * kThreads - 1) / (2 * kThreads)));
+  const int split = ctas >= num_sms ? 1 : std::max(1, std::min(4, (token + kThreads - 1) / kThreads));
   const size_t smem = static_cast<size_t>(per) * 4 * items * sizeof(float4);
-  const Quotient tok(token);
-  if (a.plan.interleaved) rope_kernel<T, true><<<dim3(ctas, split), kThreads, smem, st>>>(a, per, tok, xh, kh);
-  else rope_kernel<T, false><<<dim3(ctas, split), kThreads, smem, st>>>(a, per, tok, xh, kh);
+  if (a.plan.interleaved) rope_kernel<T, true><<<dim3(ctas, split), kThreads, smem, st>>>(a, per, x_each, k_each);
+  else rope_kernel<T, false><<<dim3(ctas, split), kThreads, smem, st>>>(a, per, x_each, k_each);
   return cudaGetLastError();
 }
 
 // 8 tokens a CTA.  blockIdx.y = 0: their keys and values, a warp per token, as dflash2_paged_write stores them; the
 // others: a share of the query heads each.
 template <int D, int FMT, int T>
-__global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_constant__ RopeWriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rope_write_kernel(const __grid_constant__ RopeWriteArgs a) {
   constexpr int kTokens = kThreads / 32, kLanes = D / 8, kMaxItems = D / 16;
   __shared__ float4 table[kTokens][4 * kMaxItems];
   __shared__ int good[kTokens];
@@ -173,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_const
   const bool found = t < m.rq.n_tokens && find_position(m.rq, t, r, pos);
   if (found) {
     const int p = a.positions ? __ldg(a.positions + t) : pos;
-    for (int i = lane; i < half; i += 32) put_turn(table[wid], items, i, turn_of(a.plan, i, p));
+    for (int i = lane; i < half; i += 32) put_turn(table[wid], kMaxItems, i, turn_of(a.plan, i, p));
   }
   if (lane == 0) good[wid] = found;
   if (blockIdx.y > 0) {
@@ -182,19 +206,15 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_const
     const int h0 = static_cast<int>(static_cast<long long>(a.q_heads) * (blockIdx.y - 1) / (gridDim.y - 1));
     const int h1 = static_cast<int>(static_cast<long long>(a.q_heads) * blockIdx.y / (gridDim.y - 1));
     const int per_token = (h1 - h0) * per_head;
+    uint32_t live = 0;
+#pragma unroll
+    for (int w = 0; w < kTokens; ++w) live |= (good[w] ? 1u : 0u) << w;
     auto turn = [&](auto il) {
       constexpr bool IL = decltype(il)::value;
-      for (int w = 0; w < kTokens; ++w) {
-        if (!good[w]) continue;
-        const long long row = blockIdx.x * kTokens + w;
-        for (int i = threadIdx.x; i < per_token; i += kThreads) {
-          const int h = i / per_head, j = i - h * per_head;
-          Item<T, IL> u;
-          u.at(rot, D, items, j);
-          u.load(a.q.p, row * a.q.token_stride + (h0 + h) * a.q.head_stride);
-          if (j < items) turn_item<IL>(u.lo, u.hi, table[w], items, j);
-          u.store(a.y.p, row * a.y.token_stride + (h0 + h) * a.y.head_stride);
-        }
+      for (int i = threadIdx.x; i < per_token * (kTokens / kTogether); i += kThreads) {
+        const int g = i / per_token, o = i - g * per_token, h = o / per_head, j = o - h * per_head;
+        turn_tokens<T, IL>(a.q, a.y, static_cast<long long>(blockIdx.x) * kTokens + g * kTogether, h0 + h, Span::of<IL>(rot, D, items, j),
+                           kTogether, live >> (g * kTogether), table[g * kTogether], kMaxItems, j);
       }
     };
     if (a.plan.interleaved) turn(std::true_type{});
@@ -216,10 +236,10 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_const
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       if (a.plan.interleaved) {
-        const float4 q = table[wid][(2 * (ch >> 3 & 1) + (w & 1)) * items + (ch >> 4)];
+        const float4 q = table[wid][(2 * (ch >> 3 & 1) + (w & 1)) * kMaxItems + (ch >> 4)];
         if (w < 2) cs[2 * w] = q.x, sn[2 * w] = q.y, cs[2 * w + 1] = q.z, sn[2 * w + 1] = q.w;
       } else {
-        const float4 q = table[wid][w * items + ((upper ? partner : ch) >> 3)];
+        const float4 q = table[wid][w * kMaxItems + ((upper ? partner : ch) >> 3)];
         cs[2 * w] = q.x, sn[2 * w] = upper ? q.y : -q.y, cs[2 * w + 1] = q.z, sn[2 * w + 1] = upper ? q.w : -q.w;
       }
     }
