@@ -78,6 +78,8 @@ DF2_DEV long long block_scan(long long v, long long* tmp, long long& total) {
   return before;
 }
 
+constexpr int kSlots = 2 * kResizeThreads;  // (never more than half full)
+static_assert(kSlots == 1 << 11, "the slot's bits of a product");
 struct ResizeShared {
   long long tmp[33];
   int first[kResizeThreads + 1];  // rank of the first page a row takes (at most 2^30)
@@ -85,6 +87,7 @@ struct ResizeShared {
   int tail[kResizeThreads];       // the last page, partly filled, of a row that grows; -1: none
   int what[kResizeThreads];       // bits below
   int served;                     // pages that rows take
+  int key[kSlots], same[kSlots], least[kSlots];  // rows with the tail `key`: how many, and the first
 };
 constexpr int kGood = 1, kRenews = 2, kServed = 4;
 
@@ -118,18 +121,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kResizeThread
     }
   }
   s.tail[tid] = tail;
+  for (int i = tid; i < kSlots; i += kResizeThreads) s.key[i] = -1, s.same[i] = 0, s.least[i] = kResizeThreads;
   if (tid == 0) s.served = 0;
   __syncthreads();
+  // rows with one tail meet in a slot of a small table, where they are counted
+  int slot = -1;
   if (tail >= 0 && holders > 1) {
-    int same = 0;
-    bool first = true;
-    for (int r = 0; r < p.n_rows; ++r) {
-      if (s.tail[r] != tail) continue;
-      ++same;
-      first = first && r >= tid;
+    slot = static_cast<int>((static_cast<uint32_t>(tail) * 2654435761u) >> 21);
+    for (;; slot = (slot + 1) & (kSlots - 1)) {
+      const int k = atomicCAS(&s.key[slot], -1, tail);
+      if (k == -1 || k == tail) break;
     }
-    if (!first || same < holders) what |= kRenews, ++want, --col;
+    atomicAdd(&s.same[slot], 1);
+    atomicMin(&s.least[slot], tid);
   }
+  __syncthreads();
+  if (slot >= 0 && (s.least[slot] != tid || s.same[slot] < holders)) what |= kRenews, ++want, --col;
   long long total;
   const long long before = block_scan(want, s.tmp, total);
   s.first[tid] = static_cast<int>(min(before, 1ll << 30));
@@ -223,11 +230,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kResizeThread
     const bool done = (w & kGood) && (w & kServed);
     bool fine = true;
     if (done && len < old) {
-      for (int c = pages_of(len, p.page_size) + lane; c < pages_of(old, p.page_size); c += 32) {
-        int32_t* const entry = p.table + r * p.table_stride + c;
-        const int page = *entry;
-        *entry = -1;
-        fine = fine && in_pool(p, page) && give_back(p, page);
+      // (eight columns a lane in flight: what this costs is the latency of the loads and of the counts)
+      const int end = pages_of(old, p.page_size);
+      int32_t* const row = p.table + r * p.table_stride;
+      for (int c = pages_of(len, p.page_size) + lane; c < end; c += 8 * 32) {
+        int page[8], had[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) page[i] = c + 32 * i < end ? row[c + 32 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) had[i] = in_pool(p, page[i]) ? atomicSub(p.ref + page[i], 1) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (c + 32 * i >= end) continue;
+          row[c + 32 * i] = -1;
+          if (had[i] >= 1) continue;
+          fine = false;
+          if (in_pool(p, page[i])) atomicAdd(p.ref + page[i], 1);
+        }
       }
     }
     fine = __all_sync(0xffffffffu, fine);
