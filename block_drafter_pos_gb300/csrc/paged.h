@@ -119,15 +119,17 @@ DF2_HD inline bool paged_in_run(long long first, long long next, long long t0, l
   return first < next && first < t1 && next > t0;
 }
 
-// Requests in groups that share a prefix: two launches.  In the first the call's "requests" are the groups: their rows see all
-// of the prefix, and each row's result (outputs not divided by the sum, and maximum and sum) goes to the workspace.  In the
-// second they are the requests, with the keys behind the prefix, and what they write has the prefix's part in it.
+// Requests in groups that share a prefix: two launches.  In the first the call's "requests" are the groups of more than one: their
+// rows see all of the prefix, and each row's result (outputs not divided by the sum, and maximum and sum) goes to the
+// workspace.  In the second they are the requests, with the keys behind the prefix, and what they write has the prefix's
+// part in it.  Or (`apart`) one launch of the requests, each with all its keys.
 struct PagedGroups {
   const int32_t* begin;   // [n_groups + 1]
   const int32_t* prefix;  // [n_groups]
   int n_groups, n_req;
   int max_group, max_prefix;
-  int first;              // the first launch
+  int first, second;      // the first launch, or a second after one
+  int apart;
   float* joint;           // [n_tokens * query heads][head_dim], then as many (maximum, sum)
 };
 

@@ -193,7 +193,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   const long long T = paged_scan<kThreads, kShared>(a, pre, tmp);
   // (no empty runs: a cut unit's CTAs are then consecutive)
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
-  if (MT > 1 && tid == 0) a.desc[8 * c] = -1;
+  if constexpr (kShared) {
+    // The second launch may begin while the first still runs: what that one writes (and what it reads of the handle's
+    // scratch) is touched after a wait, here or at the end of the run's first unit.
+    if (c >= C) {
+      pdl_wait();
+      if (MT > 1 && tid == 0) a.desc[8 * c] = -1;
+    }
+  } else if (MT > 1 && tid == 0) {
+    a.desc[8 * c] = -1;
+  }
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
 
@@ -217,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         pg_row = key - pi * a.c.page_size;
         pg_h = oc.h;
         pg_r = oc.r;
-        pg = __ldg(a.c.table + oc.table_row() * a.c.table_stride + pi);
+        pg = __ldg(a.c.table + oc.table_row(key) * a.c.table_stride + pi);
       }
     }
     oc.next(a);
@@ -297,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   bool mixed_rows = false;
   unsigned long long w0 = 0, w1 = 0;
   bool fresh = true;
+  [[maybe_unused]] bool waited = false;
   int st_now = 0, st_next = S - 1;       // stages of tiles j and j + S - 1
   int sl_now = 0, sl_next = S - 1;       // offset slots of the same (ring of S + 1); tile j + S takes the one after
 
@@ -683,6 +693,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     // ---- end of the unit or of the run: join the key groups, write
     const bool last = j == n_tiles - 1;
     if (cc.unit_ends() || last) {
+      if constexpr (kShared) {
+        if (!waited) {
+          pdl_wait();
+          if (MT > 1 && tid == 0) a.desc[8 * c] = -1;
+          waited = true;
+        }
+      }
       if constexpr (kQuant) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -905,6 +922,7 @@ cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   const long long rt = (static_cast<long long>(a.rq.max_new) * a.s.group + G::kRows - 1) / G::kRows;
   const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + G::kBN - 1) / G::kBN + 1);
   a.ctas = static_cast<int>(most < static_cast<long long>(num_sms) * per_sm ? most : num_sms * per_sm);
+  if (kShared) return launch_ex(paged_attn_kernel<D, FMT, MT, QBF>, dim3(a.ctas), dim3(kThreads), smem, st, a.g.second != 0, a);
   paged_attn_kernel<D, FMT, MT, QBF><<<a.ctas, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -934,7 +952,8 @@ cudaError_t launch_dim(PagedAttnArgs& a, int fmt, int qtype, int num_sms, cudaSt
 static cudaError_t launch_phase(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 
 cudaError_t launch_shared_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
-  if (a.g.max_prefix > 0) {
+  a.g.apart = a.g.max_prefix == 0 || a.g.n_groups == a.g.n_req;
+  if (!a.g.apart) {
     PagedAttnArgs p = a;
     p.g.first = 1;
     p.rq.n_req = a.g.n_groups;
@@ -943,6 +962,7 @@ cudaError_t launch_shared_attention(PagedAttnArgs& a, int head_dim, int fmt, int
     p.s.causal = 0;
     const cudaError_t e = launch_phase(p, head_dim, fmt, qtype, num_sms, st);
     if (e != cudaSuccess) return e;
+    a.g.second = 1;
   }
   return launch_phase(a, head_dim, fmt, qtype, num_sms, st);
 }
@@ -959,7 +979,7 @@ cudaError_t LAUNCH_ATTENTION(PagedAttnArgs& a, int head_dim, int fmt, int qtype,
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
   // a row per warp for units of 32 rows (four in turn took 2 to 3 us more), four for those of 256
-  const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / 16);
+  const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / (kShared ? 4 : 16));
   auto combine = [&](auto kernel, auto kernel_waits) {
     return launch_ex(a.s.rows == 32 ? kernel : kernel_waits, grid, dim3(128), 0, st, true, a);
   };

@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   pdl_trigger();
   const long long T = paged_scan<kThreads, kShared>(a, pre, tmp);
   const long long C = T < gridDim.x ? T : gridDim.x, c = blockIdx.x;
+  if (kShared) pdl_wait();  // (a second launch may begin while the first still uses the scratch)
   if (tid == 0) a.desc[8 * c] = -1, a.desc[8 * c + 6] = 0;
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 if (!kQuant && !old_um.masked(k0)) continue;
                 for (int key = max(k0, old_lo); key < min(k0 + kBN, old_hi); ++key) {
                   if (a.s.causal == 2 && key >= old_um.base && !((old_word >> (key - old_um.base)) & 1ull)) continue;
-                  const int page = __ldg(a.c.table + cc.table_row() * a.c.table_stride + key / a.c.page_size);
+                  const int page = __ldg(a.c.table + cc.table_row(key) * a.c.table_stride + key / a.c.page_size);
                   long long off, so;
                   if (!paged_row(a.c, page, key % a.c.page_size, cc.h, &off, &so)) continue;
                   if constexpr (kQuant) {
@@ -767,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         badv = false;
         if (key >= lc.u.lo && key < lc.u.hi) {
           const int pi = key / a.c.page_size;
-          const int page = __ldg(a.c.table + lc.table_row() * a.c.table_stride + pi);
+          const int page = __ldg(a.c.table + lc.table_row(key) * a.c.table_stride + pi);
           long long so;
           if (paged_row(a.c, page, key - pi * a.c.page_size, lc.h, &off, &so)) {
             if (kQuant) {
@@ -991,6 +992,7 @@ cudaError_t launch_one(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   const long long rt = (static_cast<long long>(a.rq.max_new) * a.s.group + kChunkRows - 1) / kChunkRows;
   const long long most = static_cast<long long>(a.rq.n_req) * a.c.n_kv * rt * ((a.rq.max_len + kBN - 1) / kBN + 1);
   a.ctas = static_cast<int>(most < num_sms ? most : num_sms);
+  if (kShared) return launch_ex(paged_chunk_kernel<D, FMT, QBF>, dim3(a.ctas), dim3(kThreads), smem, st, a.g.second != 0, a);
   paged_chunk_kernel<D, FMT, QBF><<<a.ctas, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }

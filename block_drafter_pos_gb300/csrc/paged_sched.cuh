@@ -30,11 +30,12 @@ struct PagedWork {
   int b0, n, len;  // its rows and keys; n = 0: nothing to do
   int from;        // its first key
   int row;         // its row of the page table
+  int head, head_row;  // the row that holds the keys below `head`
 };
 template <bool SHARED>
 DF2_DEV bool paged_work(const PagedAttnArgs& a, int r, PagedWork& w) {
-  w.from = 0;
-  w.row = r;
+  w.from = w.head = 0;
+  w.row = w.head_row = r;
   if constexpr (!SHARED) {
     return paged_request(a.rq, r, w.b0, w.n, w.len);
   } else {
@@ -53,7 +54,7 @@ DF2_DEV bool paged_work(const PagedAttnArgs& a, int r, PagedWork& w) {
     const int b0 = __ldg(a.rq.begin + g0), b1 = __ldg(a.rq.begin + g1);
     if (!paged_group_ok(a.g, a.rq, prefix, b0, b1)) return false;
     if (a.g.first) {
-      if (prefix == 0) return true;  // (its rows have no part of a prefix)
+      if (prefix == 0 || g1 - g0 == 1) return true;  // (its rows have no part of a prefix)
       w.b0 = b0, w.n = b1 - b0, w.len = prefix, w.row = g0;
       return true;
     }
@@ -61,7 +62,9 @@ DF2_DEV bool paged_work(const PagedAttnArgs& a, int r, PagedWork& w) {
     if (!paged_request(a.rq, r, own.b0, own.n, own.len) || own.b0 < b0 || own.b0 + own.n > b1 ||
         own.len - own.n < prefix)
       return false;
-    w.b0 = own.b0, w.n = own.n, w.len = own.len, w.from = prefix;
+    w.b0 = own.b0, w.n = own.n, w.len = own.len;
+    if (a.g.apart || g1 - g0 == 1) w.head = prefix, w.head_row = g0;
+    else w.from = prefix;
     return true;
   }
 }
@@ -127,19 +130,19 @@ struct PagedCursor {
   long long t, t1;
   int r, h, qt;        // the unit
   int b0, n, len;      // its request
-  int from, row;       // (SHARED)
+  int from, row, head, head_row;  // (SHARED)
   UnitKeys u;
   int i;               // tile within the unit (0 .. u.nt - 1)
   long long unit_t;    // the unit's first tile in the launch's numbering
 
   DF2_DEV bool valid() const { return t < t1; }
-  DF2_DEV int table_row() const { return SHARED ? row : r; }
+  DF2_DEV int table_row(int key) const { return SHARED ? (key < head ? head_row : row) : r; }
   DF2_DEV int first_key() const { return SHARED ? from : 0; }
   DF2_DEV void request(const PagedAttnArgs& a) {
     if constexpr (SHARED) {
       PagedWork w;
       paged_work<true>(a, r, w);
-      b0 = w.b0, n = w.n, len = w.len, from = w.from, row = w.row;
+      b0 = w.b0, n = w.n, len = w.len, from = w.from, row = w.row, head = w.head, head_row = w.head_row;
     } else {
       paged_request(a.rq, r, b0, n, len);
     }

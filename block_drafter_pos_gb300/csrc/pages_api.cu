@@ -269,8 +269,13 @@ dflash2_status dflash2_paged_attention_shared(dflash2_paged_handle* h, const dfl
   const int max_group = std::min(x.max_group, x.x.n_tokens);
   if (static_cast<int64_t>(max_group) * a.s.group > kPagedMaxRows) return DFLASH2_E_UNSUPPORTED;
   if (!x.workspace || !aligned16(x.workspace) || x.workspace_bytes < dflash2_paged_shared_bytes(h, x.x.n_tokens)) return DFLASH2_E_INVAL;
-  a.g = PagedGroups{x.group_begin, x.prefix_len, x.n_groups, x.x.n_req, max_group, std::min(x.max_prefix, capacity_of(h, cache)),
-                    0, static_cast<float*>(x.workspace)};
+  a.g.begin = x.group_begin;
+  a.g.prefix = x.prefix_len;
+  a.g.n_groups = x.n_groups;
+  a.g.n_req = x.x.n_req;
+  a.g.max_group = max_group;
+  a.g.max_prefix = std::min(x.max_prefix, capacity_of(h, cache));
+  a.g.joint = static_cast<float*>(x.workspace);
   const cudaError_t e = launch_shared_attention(a, h->cfg.head_dim, h->cfg.kv_format, x.x.q.type, h->num_sms,
                                                 static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DFLASH2_OK : DFLASH2_E_CUDA;
