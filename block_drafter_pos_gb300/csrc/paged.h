@@ -129,9 +129,18 @@ struct PagedGroups {
   int n_groups, n_req;
   int max_group, max_prefix;
   int first, second;      // the first launch, or a second after one
-  int apart;
+  int apart;              // (before the launch: the caller's choice)
   float* joint;           // [n_tokens * query heads][head_dim], then as many (maximum, sum)
 };
+
+enum { kSharedAuto = 0, kSharedTogether = 1, kSharedApart = 2 };
+// Apart, the requests behind a group's first one read its prefix again, mostly from L2; together, there is a launch more, a
+// join of its partials, and a part to fetch for every row.  Bytes read again where the two meet, or fewer: for units of 16 rows, twice
+// that for wider ones.  Measured (us; together / apart), 8 KV
+// heads of 128, single tokens over bf16 caches: 4 requests over 8192 positions 30 / 28, 16 over 2048 30 / 29, 64 over 512 39 / 33, over
+// 1024 40 / 50; e4m3: 16 over 4096 38 / 38, 64 over 1024 47 / 45; blocks of 8: bf16 16 over 4096 59 / 56, 64 over 1024 72 / 63, over
+// 2048 78 / 105, e4m3 64 over 2048 98 / 98.
+constexpr long long kApartBytes = 1ll << 27;
 
 // Whether group g's requests [g0, g1) follow those of the group before and, the last's, end at the last request.  (Where one
 // does not, the whole call is refused: all of `begin` is trusted after that.)

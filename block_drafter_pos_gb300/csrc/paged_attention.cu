@@ -103,6 +103,23 @@ DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int
   if (row >= n * a.s.group) return;
   const long long first = 2ll * c0 + slot0, stride = static_cast<long long>(R) * (D + 2);
   constexpr int V = D / 32;  // channels per lane
+  // (the prefix's part, its loads under the others')
+  float2 prefix_stat = make_float2(0.f, 0.f);
+  float prefix_o[V] = {};
+  if constexpr (kShared) {
+    if (joint) {
+      const int token = b0 + row / a.s.group, head = h * a.s.group + row % a.s.group;
+      const float* const j = joint_row<D>(a, token, head) + V * lane;
+      prefix_stat = __ldcg(joint_stat<D>(a, token, head));
+      if constexpr (V == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(j));
+        prefix_o[0] = v.x, prefix_o[1] = v.y, prefix_o[2] = v.z, prefix_o[3] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(j));
+        prefix_o[0] = v.x, prefix_o[1] = v.y;
+      }
+    }
+  }
       float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = 0.f;
@@ -146,17 +163,17 @@ DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int
       float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       const int i = row / a.s.group, head = h * a.s.group + row % a.s.group;
       if constexpr (kShared) {
-        float* const j = joint_row<D>(a, b0 + i, head) + V * lane;
         if (a.g.first) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) j[e] = o[e];
+          float* const j = joint_row<D>(a, b0 + i, head) + V * lane;
+          if constexpr (V == 4) *reinterpret_cast<float4*>(j) = make_float4(o[0], o[1], o[2], o[3]);
+          else *reinterpret_cast<float2*>(j) = make_float2(o[0], o[1]);
           if (lane == 0) *joint_stat<D>(a, b0 + i, head) = make_float2(m, l);
           return;
         }
         if (joint) {
-          const JointParts p(m, l, __ldcg(joint_stat<D>(a, b0 + i, head)));
+          const JointParts p(m, l, prefix_stat);
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = o[e] * p.mine + __ldcg(j + e) * p.other;
+          for (int e = 0; e < V; ++e) o[e] = o[e] * p.mine + prefix_o[e] * p.other;
           inv = 1.f, m = p.m, l = p.l;
         }
       }
@@ -952,7 +969,11 @@ cudaError_t launch_dim(PagedAttnArgs& a, int fmt, int qtype, int num_sms, cudaSt
 static cudaError_t launch_phase(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 
 cudaError_t launch_shared_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
-  a.g.apart = a.g.max_prefix == 0 || a.g.n_groups == a.g.n_req;
+  const bool bits16 = fmt == kKvBf16 || fmt == kKvF16;
+  const long long position = 2ll * a.c.n_kv * (bits16 ? 2 * head_dim : head_dim + 4);
+  const long long again = static_cast<long long>(a.g.n_req - a.g.n_groups) * a.g.max_prefix * position;
+  const long long most = static_cast<long long>(a.rq.max_new) * a.s.group <= 16 ? kApartBytes : 2 * kApartBytes;
+  a.g.apart = a.g.max_prefix == 0 || a.g.apart == kSharedApart || (a.g.apart == kSharedAuto && again <= most);
   if (!a.g.apart) {
     PagedAttnArgs p = a;
     p.g.first = 1;

@@ -12,7 +12,10 @@
 
 using namespace df2;
 
-static_assert(DFLASH2_ROPE_MAX_DIM == 2 * kRopeMaxPairs && DFLASH2_PAGED_MAX_TREE == kKeepMax, "the header's limits");
+static_assert(DFLASH2_ROPE_MAX_DIM == 2 * kRopeMaxPairs && DFLASH2_PAGED_MAX_TREE == kKeepMax &&
+                  int(DFLASH2_SHARED_AUTO) == int(kSharedAuto) && int(DFLASH2_SHARED_TOGETHER) == int(kSharedTogether) &&
+                  int(DFLASH2_SHARED_APART) == int(kSharedApart),
+              "the header's limits and enumerations");
 
 namespace {
 
@@ -262,7 +265,9 @@ dflash2_status dflash2_paged_attention_shared(dflash2_paged_handle* h, const dfl
   bool empty = false;
   const dflash2_status s = attention_args(h, cache, x.x, &a, &empty);
   if (s != DFLASH2_OK) return s;
-  if (x.n_groups < 0 || x.max_group < 0 || x.max_prefix < 0 || x.x.window != 0) return DFLASH2_E_INVAL;
+  if (x.n_groups < 0 || x.max_group < 0 || x.max_prefix < 0 || x.x.window != 0 || x.how < DFLASH2_SHARED_AUTO ||
+      x.how > DFLASH2_SHARED_APART)
+    return DFLASH2_E_INVAL;
   if (x.n_groups > DFLASH2_PAGED_MAX_REQUESTS) return DFLASH2_E_UNSUPPORTED;
   if (empty) return DFLASH2_OK;
   if (x.n_groups < 1 || !x.group_begin || !x.prefix_len) return DFLASH2_E_INVAL;
@@ -275,6 +280,7 @@ dflash2_status dflash2_paged_attention_shared(dflash2_paged_handle* h, const dfl
   a.g.n_req = x.x.n_req;
   a.g.max_group = max_group;
   a.g.max_prefix = std::min(x.max_prefix, capacity_of(h, cache));
+  a.g.apart = x.how;
   a.g.joint = static_cast<float*>(x.workspace);
   const cudaError_t e = launch_shared_attention(a, h->cfg.head_dim, h->cfg.kv_format, x.x.q.type, h->num_sms,
                                                 static_cast<cudaStream_t>(stream));

@@ -12,6 +12,7 @@ from .binding import _check, _inval, _raw_stream, _rows, _vector
 ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN, ROPE_TABLE = 0, 1, 2, 3
 ROPE_MAX_DIM = 256
 _SCALING = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "yarn": ROPE_YARN, "table": ROPE_TABLE}
+_HOW = {"auto": 0, "together": 1, "apart": 2}
 _PACK_POOL = struct.Struct("@2Pq4i")
 _PACK_SHARED = struct.Struct("@4i3Pq")      # behind the attention's arguments
 
@@ -249,10 +250,12 @@ def dflash2_paged_shared_bytes(h, n_tokens: int) -> int:
 
 
 def dflash2_paged_attention_shared(h, cache, q, out, token_begin, kv_len, group_begin, prefix_len, workspace, max_new, max_len,
-                                   max_group, max_prefix, scale, causal=True, tree_mask=None, lse=None, status=None, stream=None):
+                                   max_group, max_prefix, scale, causal=True, tree_mask=None, lse=None, status=None, how="auto",
+                                   stream=None):
     """dflash2_paged_attention where requests group_begin[g] .. group_begin[g + 1] - 1 (int32 [groups + 1]) share their first
-    prefix_len[g] positions (int32 [groups]), whose keys and values are read once for the group, through its first request's
-    row of the page table.  workspace: uint8 [dflash2_paged_shared_bytes(h, tokens)]."""
+    prefix_len[g] positions (int32 [groups]), whose keys and values are read through its first request's
+    row of the page table.  workspace: uint8 [dflash2_paged_shared_bytes(h, tokens)].
+    how: "together", "apart" or "auto"."""
     what = "dflash2_paged_attention_shared"
     f, torch = _calls(), _b._calls()[0]
     types, i32 = f["types"], torch.int32
@@ -266,7 +269,9 @@ def dflash2_paged_attention_shared(h, cache, q, out, token_begin, kv_len, group_
     a = _b._PACK_ATTN.pack(n, tokens, max_new, max_len, 1 if causal else 0, 0, scale, 0, begin, length, *rq, *ro,
                            _vector(what, "tree_mask", tree_mask, torch.int64, tokens, dev),
                            _vector(what, "lse", lse, torch.float32, tokens * hq, dev), st)
-    a += _PACK_SHARED.pack(groups, max_group, max_prefix, 0, _vector(what, "group_begin", group_begin, i32, groups + 1, dev),
+    if how not in _HOW:
+        raise _inval(what, f"how must be one of {', '.join(_HOW)}")
+    a += _PACK_SHARED.pack(groups, max_group, max_prefix, _HOW[how], _vector(what, "group_begin", group_begin, i32, groups + 1, dev),
                            _vector(what, "prefix_len", prefix_len, i32, groups, dev), _vector(what, "workspace", workspace, torch.uint8, room, dev), room)
     s = f["shared"](h, cache.raw, a, _raw_stream(what, torch, stream, dev))
     if s:

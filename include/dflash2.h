@@ -723,7 +723,7 @@ dflash2_status dflash2_paged_keep(dflash2_paged_handle* h, int32_t n_caches, con
                                   int32_t* kv_out, int32_t* status, void* stream);
 
 /* dflash2_paged_attention where consecutive requests share a prefix: with x.window 0, the same outputs up to
- * rounding, the prefix's keys and values read once for the group instead of once for each of its requests.
+ * rounding, the prefix's keys and values read once for the group.
  *   group_begin int32 [n_groups + 1] (device): group g is requests group_begin[g] .. group_begin[g + 1] - 1,
  *     ascending from 0 to x.n_req (if it does not, every request is flagged and nothing is written).
  *   prefix_len int32 [n_groups] (device): positions below it hold the same keys and values for every request of
@@ -731,15 +731,19 @@ dflash2_status dflash2_paged_keep(dflash2_paged_handle* h, int32_t n_caches, con
  *     kv_len - n of each of its requests.
  *   max_group, max_prefix: at least every group's number of new tokens and prefix_len (host bounds).
  *   workspace: dflash2_paged_shared_bytes(h, x.n_tokens) bytes, 16-byte aligned, used by one call at a time.
+ *   how: TOGETHER reads a prefix once for its group, in a launch of its own; APART lets each request read it, in one
+ *     launch, which is faster while what is read again is little (and stays in the L2 cache).  AUTO chooses by the bytes that
+ *     x.n_req - n_groups requests read again of max_prefix positions.
  * A group whose prefix or rows break these bounds is skipped and all its requests are flagged, as they are for a bad page of
  * its prefix (which is masked); a request that does is skipped and flagged alone.  A row that two good ranges hold is
  * not valid.  The largest group's rows (max_group times query heads per KV head) end at 2^31 - 512. */
+enum { DFLASH2_SHARED_AUTO = 0, DFLASH2_SHARED_TOGETHER = 1, DFLASH2_SHARED_APART = 2 };
 typedef struct dflash2_paged_shared_args {
   dflash2_paged_attention_args x;
   int32_t n_groups;
   int32_t max_group;
   int32_t max_prefix;
-  int32_t reserved;
+  int32_t how;           /* DFLASH2_SHARED_* */
   const int32_t* group_begin;
   const int32_t* prefix_len;
   void* workspace;

@@ -443,6 +443,7 @@ class SharedSetup(Setup):
         kw.setdefault("max_group", self.max_group)
         kw.setdefault("max_prefix", max(self.prefix + [0]))
         kw.setdefault("scale", self.dim ** -0.5)
+        kw.setdefault("how", "together")
         bd.dflash2_paged_attention_shared(self.handle, self.cache, q, out, self.begin, self.kv_len, self.group_begin, self.prefix_len,
                                           self.work, max_new=max(self.new + [1]), max_len=max(self.length + [1]), lse=lse, status=status, **kw)
         torch.cuda.synchronize()
@@ -468,27 +469,42 @@ CASES = [  # sizes of groups, prefixes, new tokens, own keys
 @pytest.mark.parametrize("fmt,qtype", [("bf16", "bf16"), ("fp16", "fp16"), ("int8", "bf16"), ("e4m3", "fp16")])
 @pytest.mark.parametrize("hq,hk,dim,page,order", [(4, 2, 128, 16, "phc"), (3, 1, 64, 24, "hpc"), (16, 2, 128, 7, "pch")])
 @pytest.mark.parametrize("case", range(len(CASES)))
-def test_shared_attention(case, hq, hk, dim, page, order, fmt, qtype):
+@pytest.mark.parametrize("how", ["together", "apart"])
+def test_shared_attention(how, case, hq, hk, dim, page, order, fmt, qtype):
     sizes, prefix, new, own = CASES[case]
     pre = [p for n, p in zip(sizes, prefix) for _ in range(n)]
     s = SharedSetup(new, [p + n for p, n in zip(pre, own)], hq=hq, hk=hk, dim=dim, page=page, order=order, fmt=fmt,
                     seed=case + dim).share(sizes, prefix)
     q = s.queries(qtype, amp=2.0)
     status = torch.zeros(len(new), dtype=torch.int32, device="cuda")
-    out, lse = s.attend_shared(q, status=status)
+    out, lse = s.attend_shared(q, status=status, how=how)
     assert not status.any()
     check_shared(s, q, out, lse)
-    again, lse2 = s.attend_shared(q)                       # the same bits, whatever the workspace held
+    again, lse2 = s.attend_shared(q, how=how)              # the same bits, whatever the workspace held
     assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
     if case in (0, 3):
-        check_shared(s, q, *s.attend_shared(q, causal=False), causal=False)
-        check_shared(s, q, *s.attend_shared(q, scale=-0.3), scale=-0.3)
+        check_shared(s, q, *s.attend_shared(q, causal=False, how=how), causal=False)
+        check_shared(s, q, *s.attend_shared(q, scale=-0.3, how=how), scale=-0.3)
     s.close()
+
+
+def test_shared_attention_chooses_by_the_bytes():
+    """On either side of the border the call's bits are those of the way it names: 16 requests over 4 KB positions, 32768 read
+    again; the border is 128 MiB for 16 rows and 256 MiB above."""
+    for new, prefix, way in ((1, 2184, "apart"), (1, 2185, "together"), (8, 4369, "apart"), (8, 4370, "together")):
+        s = SharedSetup([new] * 16, [prefix + new + 3 * r for r in range(16)], hq=32, hk=8, page=64, seed=prefix).share([16], [prefix])
+        assert (15 * prefix * 4096 <= (1 << 27 if new == 1 else 1 << 28)) == (way == "apart")
+        q = s.queries("bf16")
+        ways = {w: s.attend_shared(q, how=w)[1] for w in ("auto", "together", "apart")}
+        assert not torch.equal(ways["together"], ways["apart"])              # (joined in another order)
+        assert torch.equal(ways["auto"], ways[way])
+        s.close()
 
 
 @pytest.mark.parametrize("fmt,qtype", [("bf16", "bf16"), ("e4m3", "bf16")])
 @pytest.mark.parametrize("nodes", [3, 33, 64])
-def test_shared_attention_of_trees(fmt, qtype, nodes):
+@pytest.mark.parametrize("how", ["together", "apart"])
+def test_shared_attention_of_trees(how, fmt, qtype, nodes):
     """Tree masks; words without a bit leave a row with the prefix alone, or, without a prefix, with nothing."""
     sizes, prefix = [3, 2], [90, 0]
     new, own = [nodes] * 5, [nodes + 4, nodes, nodes + 70, nodes, nodes]
@@ -497,7 +513,7 @@ def test_shared_attention_of_trees(fmt, qtype, nodes):
     tree = np.array([int(g.integers(0, 1 << 63)) | 1 << i for _ in range(5) for i in range(nodes)], np.uint64)
     tree[2] = tree[nodes + 1] = tree[3 * nodes] = 0
     q = s.queries(qtype)
-    out, lse = s.attend_shared(q, tree_mask=torch.from_numpy(tree.view(np.int64)).cuda())
+    out, lse = s.attend_shared(q, tree_mask=torch.from_numpy(tree.view(np.int64)).cuda(), how=how)
     check_shared(s, q, out, lse, tree=tree)
     assert not out[3 * nodes].any() and bool((lse[3 * nodes] == -float("inf")).all())
     s.close()
@@ -517,7 +533,8 @@ def test_shared_attention_is_the_single_call():
     s.close()
 
 
-def test_shared_attention_flags_bad_groups_and_requests():
+@pytest.mark.parametrize("how", ["together", "apart"])
+def test_shared_attention_flags_bad_groups_and_requests(how):
     """A group or a request that breaks its bounds is flagged and its rows stay; the others are served."""
     sizes, prefix = [2, 2, 2], [100, 50, 70]
     new, length = [3] * 6, [110, 120, 60, 53, 90, 100]
@@ -528,7 +545,7 @@ def test_shared_attention_flags_bad_groups_and_requests():
         return s, q, torch.full_like(q, 7).cuda(), torch.zeros(6, dtype=torch.int32, device="cuda")
 
     def look(s, q, out, status, bad, **kw):
-        out, lse = s.attend_shared(q, out=out, status=status, **kw)
+        out, lse = s.attend_shared(q, out=out, status=status, how=how, **kw)
         assert status.tolist() == [int(r in bad) for r in range(6)]
         for r in range(6):
             rows = out[3 * r:3 * r + 3]
@@ -564,7 +581,8 @@ def test_shared_attention_flags_bad_groups_and_requests():
     look(s, *x, bad=[4, 5])
 
 
-def test_shared_attention_masks_bad_pages():
+@pytest.mark.parametrize("how", ["together", "apart"])
+def test_shared_attention_masks_bad_pages(how):
     """A bad page of the prefix is masked for the whole group, which is flagged; one behind it for its request."""
     sizes, prefix = [3, 1], [64, 0]
     s = SharedSetup([2] * 4, [90, 100, 70, 20], fmt="e4m3", page=16).share(sizes, prefix)
@@ -572,7 +590,7 @@ def test_shared_attention_masks_bad_pages():
     s.gtable[1, 5] = -1
     q = s.queries("bf16")
     status = torch.zeros(4, dtype=torch.int32, device="cuda")
-    out, lse = s.attend_shared(q, status=status)
+    out, lse = s.attend_shared(q, status=status, how=how)
     assert status.tolist() == [1, 1, 1, 0]
     qd = q.double().numpy()
     for r in range(4):
@@ -588,7 +606,8 @@ def test_shared_attention_masks_bad_pages():
     s.close()
 
 
-def test_shared_attention_of_values_that_are_not_finite():
+@pytest.mark.parametrize("how", ["together", "apart"])
+def test_shared_attention_of_values_that_are_not_finite(how):
     """In the prefix they show in the group's rows alone; behind it in the rows that see them; in masked places nowhere."""
     s = SharedSetup([2, 2, 2], [200, 210, 40], fmt="bf16", page=16).share([2, 1], [128, 0])
     s.gv[int(s.table[0, 3]), 2, 1, 5] = float("inf")                # position 50 of the prefix
@@ -596,7 +615,7 @@ def test_shared_attention_of_values_that_are_not_finite():
     s.gv[int(s.table[1, 209 // 16]), 209 % 16, 0, 9] = float("nan")  # the newest token of request 1
     s.vals[1][1][209, 0, 9] = np.nan
     q = s.queries("bf16")
-    out, lse = s.attend_shared(q)
+    out, lse = s.attend_shared(q, how=how)
     bad = [tuple(x) for x in (~torch.isfinite(out)).nonzero().tolist()]
     assert {(t, h) for t, h, c in bad if c == 5} == {(t, h) for t in range(4) for h in (2, 3)}
     assert {(t, h, c) for t, h, c in bad if c != 5} == {(3, h, 9) for h in (0, 1)}
@@ -638,7 +657,7 @@ def test_captured_calls_replay_on_new_contents():
             bd.dflash2_rope(s.plan, s.q, s.turned, s.pos)
             bd.dflash2_pages_resize(s.pages.pool, s.pages.kv, s.lens, s.pages.copies)
             bd.dflash2_paged_attention_shared(s.handle, s.cache, s.turned, s.out, s.begin, s.kv_len, s.group_begin, s.prefix_len, s.work,
-                                              max_new=2, max_len=400, max_group=12, max_prefix=300, scale=0.1)
+                                              max_new=2, max_len=400, max_group=12, max_prefix=300, scale=0.1, how="together")
         step()
         torch.cuda.synchronize()
         s.graph = torch.cuda.CUDAGraph()
@@ -665,7 +684,7 @@ def test_captured_calls_replay_on_new_contents():
             assert torch.equal(turned, s.turned)
             out = torch.empty_like(s.out)
             bd.dflash2_paged_attention_shared(s.handle, s.cache, turned, out, s.begin, s.kv_len, s.group_begin, s.prefix_len, s.work,
-                                              max_new=2, max_len=400, max_group=12, max_prefix=300, scale=0.1)
+                                              max_new=2, max_len=400, max_group=12, max_prefix=300, scale=0.1, how="together")
             # the same bits (the shorter second prefix uncovers rows of NaN in its second request)
             assert torch.equal(out.view(torch.int16), s.out.view(torch.int16)) and s.kv_len.tolist() == now
             assert bool(torch.isfinite(s.out[:10]).all())
@@ -685,7 +704,7 @@ def test_calls_on_another_stream():
         torch.cuda._sleep(20_000_000)
         late.copy_(q)
     bd.dflash2_paged_attention_shared(s.handle, s.cache, late, out, s.begin, s.kv_len, s.group_begin, s.prefix_len, s.work, max_new=1,
-                                      max_len=400, max_group=8, max_prefix=384, scale=s.dim ** -0.5, stream=side)
+                                      max_len=400, max_group=8, max_prefix=384, scale=s.dim ** -0.5, stream=side, how="together")
     side.synchronize()
     assert torch.equal(out, want)
     s.close()

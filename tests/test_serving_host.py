@@ -224,9 +224,9 @@ def test_copy_and_keep_refuse_bad_arguments():
     assert keep(h.p, 2, _two(page_table=None), 0, None, None, None, 4, 4, None, None, None, None) == b.OK
 
 
-def _shared(tokens=4, groups=1, max_group=4, max_prefix=16, begin=P, prefix=P, work=P, size=1 << 40, **kw):
+def _shared(tokens=4, groups=1, max_group=4, max_prefix=16, begin=P, prefix=P, work=P, size=1 << 40, how=0, **kw):
     a = _attn(n_tokens=tokens, **kw)
-    return bytes(a) + sv._PACK_SHARED.pack(groups, max_group, max_prefix, 0, begin or 0, prefix or 0, work or 0, size)
+    return bytes(a) + sv._PACK_SHARED.pack(groups, max_group, max_prefix, how, begin or 0, prefix or 0, work or 0, size)
 
 
 def test_shared_attention_refuses_bad_arguments():
@@ -241,7 +241,7 @@ def test_shared_attention_refuses_bad_arguments():
         assert f(h.p, c, _shared(q=_rows(**kw)), None) == b.E_INVAL, kw
         assert f(h.p, c, _shared(out=_rows(**kw)), None) == b.E_INVAL, kw
     for kw in (dict(window=1), dict(groups=-1), dict(groups=0), dict(max_group=-1), dict(max_prefix=-1), dict(begin=None),
-               dict(prefix=None), dict(work=None), dict(work=P + 8), dict(size=need - 1), dict(scale=NAN), dict(max_len=-1)):
+               dict(prefix=None), dict(how=-1), dict(how=3), dict(work=None), dict(work=P + 8), dict(size=need - 1), dict(scale=NAN), dict(max_len=-1)):
         assert f(h.p, c, _shared(**kw), None) == b.E_INVAL, kw
     assert f(h.p, c, _shared(groups=1025), None) == b.E_UNSUPPORTED
     assert f(h.p, c, _shared(n_req=5), None) == b.E_UNSUPPORTED
@@ -376,6 +376,10 @@ def test_unknown_handles_are_refused(calls):
         bd.dflash2_pages_copy(4097, [c], Stub(0, I32, 3, 3))
     with pytest.raises(bd.Dflash2Error):
         bd.dflash2_paged_shared_bytes(None, 4)
+    with pytest.raises(bd.Dflash2Error, match="how"):
+        t = {k: Stub(0, *v) for k, v in TENSORS.items()}
+        bd.dflash2_paged_attention_shared(4096, c, t["x"], t["out"], t["begin"], t["kv_len"], t["group_begin"], t["prefix"], t["work"], 6,
+                                          64, 6, 16, 0.1, how="other")
 
 
 # ----------------------------------------------------------------------------- the oracle's pins
