@@ -21,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 
 SOURCES = ["api.cu", "gemv.cu", "wide.cu", "glue.cu", "attention.cu", "lmhead.cu", "select.cu", "verify.cu", "noalloc.cu",
            "paged_api.cu", "paged_cache.cu", "paged_attention.cu",
-           "paged_chunk.cu", "sample.cu", "pages_api.cu", "pages.cu", "rope.cu"]
+           "paged_chunk.cu", "sample.cu", "paged_prefix.cu", "pages_api.cu", "pages.cu", "rope.cu"]
 # Compiled a second time with the flag, for attention over shared prefixes (paged_sched.cuh).
 SHARED_SOURCES = ["paged_attention.cu", "paged_chunk.cu"]
 SHARED_FLAG = "-DDF2_SHARED_PREFIX=1"

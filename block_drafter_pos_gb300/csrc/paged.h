@@ -189,7 +189,8 @@ inline size_t paged_part_floats(int num_sms, int head_dim) {
 }
 cudaError_t launch_paged_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 cudaError_t launch_paged_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
-// The same kernels with a.g (both launches, one after the other).
+// The same with a.g (both launches, one after the other); the first launch's kernel for many rows.
+cudaError_t launch_shared_prefix(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 cudaError_t launch_shared_chunk(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 cudaError_t launch_shared_attention(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st);
 

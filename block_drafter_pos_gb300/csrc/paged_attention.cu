@@ -996,7 +996,8 @@ static
 cudaError_t LAUNCH_ATTENTION(PagedAttnArgs& a, int head_dim, int fmt, int qtype, int num_sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.rq.max_new) * a.s.group;
   cudaError_t e;
-  if (rows > kChunkMinRows) e = LAUNCH_CHUNK(a, head_dim, fmt, qtype, num_sms, st);
+  if (kShared && a.g.first && rows > kChunkMinRows) e = launch_shared_prefix(a, head_dim, fmt, qtype, num_sms, st);
+  else if (rows > kChunkMinRows) e = LAUNCH_CHUNK(a, head_dim, fmt, qtype, num_sms, st);
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
   // a row per warp for units of 32 rows (four in turn took 2 to 3 us more), four for those of 256
