@@ -296,22 +296,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 
   const int n_tiles = static_cast<int>(t_end - t_begin);
   // prologue: tiles 0 .. S - 2 in flight, the offsets of tile S - 1 looked up
-#pragma unroll
-  for (int j = 0; j < S - 1; ++j) {
+#pragma unroll 1  // (code that runs once is fetched once)
+  for (int j = 0; j < S; ++j) {
     fetch();
     resolve();
     put(j);
     soff_next = my_soff;
     sval_next = my_off != kNoRow;
+    if (j == S - 1) break;
     __syncthreads();
     if (j < n_tiles) issue(j, j);
     cp_commit();
   }
-  fetch();
-  resolve();
-  put(S - 1);
-  soff_next = my_soff;
-  sval_next = my_off != kNoRow;
   fetch();  // tile S
 
   uint32_t qf[kSteps][4];
@@ -1000,8 +996,9 @@ cudaError_t LAUNCH_ATTENTION(PagedAttnArgs& a, int head_dim, int fmt, int qtype,
   else if (rows > kChunkMinRows) e = LAUNCH_CHUNK(a, head_dim, fmt, qtype, num_sms, st);
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
-  // a row per warp for units of 32 rows (four in turn took 2 to 3 us more), four for those of 256
-  const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / (kShared ? 4 : 16));
+  // a row per warp for units of 32 rows (four in turn took 2 to 3 us more) and for a prefix's, which are cut into many pieces
+  // (four in turn 24 us against 12, 64 tokens over 32768); four for the others of 256
+  const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / (kShared && a.g.first ? 4 : 16));
   auto combine = [&](auto kernel, auto kernel_waits) {
     return launch_ex(a.s.rows == 32 ? kernel : kernel_waits, grid, dim3(128), 0, st, true, a);
   };

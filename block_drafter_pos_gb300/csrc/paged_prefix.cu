@@ -38,6 +38,13 @@ struct Geo : ChunkGeo<D, FMT> {
   static constexpr int kFixed = kOffPre + 1024;
 };
 
+// A whole sector (32 bytes, aligned) from a thread, whose row is another line than its neighbours'.
+DF2_DEV void store32(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
+               "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 template <int D, int FMT, bool QBF>
 __global__ void __launch_bounds__(kThreads, 1) paged_prefix_kernel(const __grid_constant__ PagedAttnArgs a) {
   using G = Geo<D, FMT>;
@@ -342,8 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefix_kernel(const __grid_
             }
             if (valid) {
 #pragma unroll
-              for (int y = 0; y < 32; y += 4)
-                *reinterpret_cast<float4*>(pp + 32 * x + y) = make_float4(o[y] * out_f, o[y + 1] * out_f, o[y + 2] * out_f, o[y + 3] * out_f);
+              for (int y = 0; y < 32; ++y) o[y] *= out_f;
+#pragma unroll
+              for (int y = 0; y < 32; y += 8) store32(pp + 32 * x + y, o + y);
             }
           }
           if (valid) *ps = make_float2(m, l);

@@ -273,7 +273,7 @@ dflash2_status dflash2_paged_attention_shared(dflash2_paged_handle* h, const dfl
   if (x.n_groups < 1 || !x.group_begin || !x.prefix_len) return DFLASH2_E_INVAL;
   const int max_group = std::min(x.max_group, x.x.n_tokens);
   if (static_cast<int64_t>(max_group) * a.s.group > kPagedMaxRows) return DFLASH2_E_UNSUPPORTED;
-  if (!x.workspace || !aligned16(x.workspace) || x.workspace_bytes < dflash2_paged_shared_bytes(h, x.x.n_tokens)) return DFLASH2_E_INVAL;
+  if (!x.workspace || (reinterpret_cast<uintptr_t>(x.workspace) & 31u) != 0 || x.workspace_bytes < dflash2_paged_shared_bytes(h, x.x.n_tokens)) return DFLASH2_E_INVAL;
   a.g.begin = x.group_begin;
   a.g.prefix = x.prefix_len;
   a.g.n_groups = x.n_groups;

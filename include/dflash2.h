@@ -730,7 +730,7 @@ dflash2_status dflash2_paged_keep(dflash2_paged_handle* h, int32_t n_caches, con
  *     the group; they are read through the page table's row of its first request.  0: nothing is shared.  At most
  *     kv_len - n of each of its requests.
  *   max_group, max_prefix: at least every group's number of new tokens and prefix_len (host bounds).
- *   workspace: dflash2_paged_shared_bytes(h, x.n_tokens) bytes, 16-byte aligned, used by one call at a time.
+ *   workspace: dflash2_paged_shared_bytes(h, x.n_tokens) bytes, 32-byte aligned, used by one call at a time.
  *   how: TOGETHER reads a prefix once for its group, in a launch of its own; APART lets each request read it, in one
  *     launch, which is faster while what is read again is little (and stays in the L2 cache).  AUTO chooses by the bytes that
  *     x.n_req - n_groups requests read again of max_prefix positions.

@@ -241,7 +241,7 @@ def test_shared_attention_refuses_bad_arguments():
         assert f(h.p, c, _shared(q=_rows(**kw)), None) == b.E_INVAL, kw
         assert f(h.p, c, _shared(out=_rows(**kw)), None) == b.E_INVAL, kw
     for kw in (dict(window=1), dict(groups=-1), dict(groups=0), dict(max_group=-1), dict(max_prefix=-1), dict(begin=None),
-               dict(prefix=None), dict(how=-1), dict(how=3), dict(work=None), dict(work=P + 8), dict(size=need - 1), dict(scale=NAN), dict(max_len=-1)):
+               dict(prefix=None), dict(how=-1), dict(how=3), dict(work=None), dict(work=P + 16), dict(size=need - 1), dict(scale=NAN), dict(max_len=-1)):
         assert f(h.p, c, _shared(**kw), None) == b.E_INVAL, kw
     assert f(h.p, c, _shared(groups=1025), None) == b.E_UNSUPPORTED
     assert f(h.p, c, _shared(n_req=5), None) == b.E_UNSUPPORTED
