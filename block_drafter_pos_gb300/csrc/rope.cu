@@ -114,22 +114,23 @@ struct Raw {
   }
 };
 
-// The item of tokens t, t + 1, ... (`n` of them, at most kTogether; those whose bit in `live` is not set are passed over): their
+// The item of tokens t, t + 1, ... (`n` of them, at most kTogether<T>; those whose bit in `live` is not set are passed over): their
 // loads are in flight together.
-constexpr int kTogether = 4;
+template <int T>
+constexpr int kTogether = T == kTF32 ? 2 : 4;
 template <int T, bool IL>
 DF2_DEV void turn_tokens(const PagedRows& x, const PagedRows& y, long long t, int h, const Span& s, int n, uint32_t live,
                          const float4* table, int items, int j) {
-  Raw<T> lo[kTogether], hi[kTogether];
+  Raw<T> lo[kTogether<T>], hi[kTogether<T>];
   const long long from = t * x.token_stride + h * x.head_stride, to = t * y.token_stride + h * y.head_stride;
 #pragma unroll
-  for (int e = 0; e < kTogether; ++e)
+  for (int e = 0; e < kTogether<T>; ++e)
     if (e < n && (live >> e & 1)) {
       lo[e].load(x.p, from + e * x.token_stride + s.first);
       if (s.second >= 0) hi[e].load(x.p, from + e * x.token_stride + s.second);
     }
 #pragma unroll
-  for (int e = 0; e < kTogether; ++e)
+  for (int e = 0; e < kTogether<T>; ++e)
     if (e < n && (live >> e & 1)) {
       if (s.turned) {
         float a[8], b[8];
@@ -144,7 +145,8 @@ DF2_DEV void turn_tokens(const PagedRows& x, const PagedRows& y, long long t, in
     }
 }
 
-// A CTA turns `per` tokens.  A thread takes an item (numbered by x's heads and k's, then along the head) of up to four tokens at a time.
+// A CTA turns `per` tokens.  A thread takes an item (numbered by x's heads and k's, then along the head) of
+// up to four tokens at a time.
 template <int T, bool IL>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int per, int x_each, int k_each) {
   extern __shared__ float4 table[];  // [per][4][items]
@@ -155,15 +157,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     put_turn(table + t * 4 * items, items, i - t * pairs, turn_of(a.plan, i - t * pairs, __ldg(a.positions + t0 + t)));
   }
   __syncthreads();
-  const int x_items = a.x_heads * x_each, token = x_items + a.k_heads * k_each, groups = (n + kTogether - 1) / kTogether;
+  const int x_items = a.x_heads * x_each, token = x_items + a.k_heads * k_each, groups = (n + kTogether<T> - 1) / kTogether<T>;
   for (int i = blockIdx.y * kThreads + threadIdx.x; i < token * groups; i += kThreads * gridDim.y) {
     const int g = i / token;
     int o = i - g * token;
     const bool x = o < x_items;
     if (!x) o -= x_items;
     const int each = x ? x_each : k_each, h = o / each, j = o - h * each;
-    turn_tokens<T, IL>(x ? a.x : a.k, x ? a.y : a.ky, t0 + g * kTogether, h, Span::of<IL>(a.plan.rot, a.dim, items, j),
-                       n - g * kTogether, 15u, table + g * kTogether * 4 * items, items, j);
+    turn_tokens<T, IL>(x ? a.x : a.k, x ? a.y : a.ky, t0 + g * kTogether<T>, h, Span::of<IL>(a.plan.rot, a.dim, items, j),
+                       n - g * kTogether<T>, (1u << kTogether<T>) - 1u, table + g * kTogether<T> * 4 * items, items, j);
   }
 }
 
@@ -173,7 +175,7 @@ cudaError_t launch_rows(const RopeArgs& a, int num_sms, cudaStream_t st) {
   const int x_each = items + (a.x_copy ? rest : 0), k_each = items + (a.k_copy ? rest : 0);
   const int token = a.x_heads * x_each + a.k_heads * k_each;
   // 8 tokens a CTA, or 16 of few items, while that leaves two CTAs an SM; below, a token a CTA, its items split over up to 4
-  const int per = a.n_tokens >= 16 * num_sms ? (token <= kThreads ? 16 : 8) : std::max(1, std::min(kTogether, a.n_tokens / (2 * num_sms)));
+  const int per = a.n_tokens >= 16 * num_sms ? (token <= kThreads ? 16 : 8) : std::max(1, std::min(kTogether<T>, a.n_tokens / (2 * num_sms)));
   const int ctas = (a.n_tokens + per - 1) / per;
   const int split = ctas >= num_sms ? 1 : std::max(1, std::min(4, (token + kThreads - 1) / kThreads));
   const size_t smem = static_cast<size_t>(per) * 4 * items * sizeof(float4);
@@ -182,17 +184,19 @@ cudaError_t launch_rows(const RopeArgs& a, int num_sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// 8 tokens a CTA.  blockIdx.y = 0: their keys and values, a warp per token, as dflash2_paged_write stores them; the
-// others: a share of the query heads each.
+// 8 tokens to `parts` CTAs.  The first: their keys and values, a warp per token, as dflash2_paged_write stores them; the
+// others: a share of the query heads each.  (The CTAs of a token follow one another, so that those bound by the quantisation's
+// instructions run beside those bound by memory.)
 template <int D, int FMT, int T>
-__global__ void __launch_bounds__(kThreads, 3) rope_write_kernel(const __grid_constant__ RopeWriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_write_kernel(const __grid_constant__ RopeWriteArgs a, int parts) {
   constexpr int kTokens = kThreads / 32, kLanes = D / 8, kMaxItems = D / 16;
   __shared__ float4 table[kTokens][4 * kMaxItems];
   __shared__ int good[kTokens];
   const PagedMoveArgs& m = a.move;
-  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x * kTokens + wid;
+  const int block = blockIdx.x / parts, part = blockIdx.x - block * parts;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, t = block * kTokens + wid;
   const int rot = a.plan.rot, items = rot >> 4, half = rot >> 1;
-  if (blockIdx.y == 0) flag_requests(m.rq);
+  if (part == 0) flag_requests(m.rq);
   int r = 0, pos = 0;
   const bool found = t < m.rq.n_tokens && find_position(m.rq, t, r, pos);
   if (found) {
@@ -200,21 +204,21 @@ __global__ void __launch_bounds__(kThreads, 3) rope_write_kernel(const __grid_co
     for (int i = lane; i < half; i += 32) put_turn(table[wid], kMaxItems, i, turn_of(a.plan, i, p));
   }
   if (lane == 0) good[wid] = found;
-  if (blockIdx.y > 0) {
+  if (part > 0) {
     __syncthreads();
     const int per_head = items + (a.q_copy ? (D - rot + 15) >> 4 : 0);
-    const int h0 = static_cast<int>(static_cast<long long>(a.q_heads) * (blockIdx.y - 1) / (gridDim.y - 1));
-    const int h1 = static_cast<int>(static_cast<long long>(a.q_heads) * blockIdx.y / (gridDim.y - 1));
+    const int h0 = static_cast<int>(static_cast<long long>(a.q_heads) * (part - 1) / (parts - 1));
+    const int h1 = static_cast<int>(static_cast<long long>(a.q_heads) * part / (parts - 1));
     const int per_token = (h1 - h0) * per_head;
     uint32_t live = 0;
 #pragma unroll
     for (int w = 0; w < kTokens; ++w) live |= (good[w] ? 1u : 0u) << w;
     auto turn = [&](auto il) {
       constexpr bool IL = decltype(il)::value;
-      for (int i = threadIdx.x; i < per_token * (kTokens / kTogether); i += kThreads) {
+      for (int i = threadIdx.x; i < per_token * (kTokens / kTogether<T>); i += kThreads) {
         const int g = i / per_token, o = i - g * per_token, h = o / per_head, j = o - h * per_head;
-        turn_tokens<T, IL>(a.q, a.y, static_cast<long long>(blockIdx.x) * kTokens + g * kTogether, h0 + h, Span::of<IL>(rot, D, items, j),
-                           kTogether, live >> (g * kTogether), table[g * kTogether], kMaxItems, j);
+        turn_tokens<T, IL>(a.q, a.y, static_cast<long long>(block) * kTokens + g * kTogether<T>, h0 + h, Span::of<IL>(rot, D, items, j),
+                           kTogether<T>, live >> (g * kTogether<T>), table[g * kTogether<T>], kMaxItems, j);
       }
     };
     if (a.plan.interleaved) turn(std::true_type{});
@@ -228,48 +232,48 @@ __global__ void __launch_bounds__(kThreads, 3) rope_write_kernel(const __grid_co
   const char* const pk = m.k.p + t * m.k.token_stride * (T == kTF32 ? 4 : 2);
   const char* const pv = m.v.p + t * m.v.token_stride * (T == kTF32 ? 4 : 2);
   const int pieces = m.c.n_kv * kLanes, ch = (lane % kLanes) * 8;
-  // this lane's channels' partners and turns, the same in every head
-  const bool turned = ch < rot, upper = ch >= half;
+  // this lane's channels' partners, the same in every head
+  const bool turned = ch < rot, upper = ch >= half, il = a.plan.interleaved;
   const int partner = upper ? ch - half : ch + half;
-  float cs[8], sn[8];
-  if (turned) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (a.plan.interleaved) {
-        const float4 q = table[wid][(2 * (ch >> 3 & 1) + (w & 1)) * kMaxItems + (ch >> 4)];
-        if (w < 2) cs[2 * w] = q.x, sn[2 * w] = q.y, cs[2 * w + 1] = q.z, sn[2 * w + 1] = q.w;
-      } else {
-        const float4 q = table[wid][w * kMaxItems + ((upper ? partner : ch) >> 3)];
-        cs[2 * w] = q.x, sn[2 * w] = upper ? q.y : -q.y, cs[2 * w + 1] = q.z, sn[2 * w + 1] = upper ? q.w : -q.w;
-      }
-    }
-  }
+  const float4* const turns = table[wid] + (il ? 2 * (ch >> 3 & 1) * kMaxItems + (ch >> 4) : (upper ? partner : ch) >> 3);
   for (int p0 = 0; p0 < pieces; p0 += 64) {
-    float x[2][2][8], b[2][8];
+    Raw<T> k[2], b[2], v[2];
     int h[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int p = p0 + 32 * i + lane;
       h[i] = p < pieces ? p / kLanes : 0;  // (idle lanes redo head 0 and store nothing)
-      load8<T>(pk, h[i] * m.k.head_stride + ch, x[i][0]);
-      if (turned && !a.plan.interleaved) load8<T>(pk, h[i] * m.k.head_stride + partner, b[i]);
-      load8<T>(pv, h[i] * m.v.head_stride + ch, x[i][1]);
+      k[i].load(pk, h[i] * m.k.head_stride + ch);
+      if (turned && !il) b[i].load(pk, h[i] * m.k.head_stride + partner);
+      v[i].load(pv, h[i] * m.v.head_stride + ch);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool in = p0 + 32 * i + lane < pieces;
       const long long o = off + h[i] * m.c.head_stride + ch, so = soff + h[i] * m.c.s_head_stride;
-      if (turned) {
-        if (a.plan.interleaved) {
+      float x[8];
+      k[i].get(x);
+      if (turned && il) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) turn2(x[i][0][2 * e], x[i][0][2 * e + 1], cs[e], sn[e]);
-        } else {
+        for (int w = 0; w < 2; ++w) {
+          const float4 t4 = turns[w * kMaxItems];
+          turn2(x[4 * w], x[4 * w + 1], t4.x, t4.y);
+          turn2(x[4 * w + 2], x[4 * w + 3], t4.z, t4.w);
+        }
+      } else if (turned) {
+        float y[8];
+        b[i].get(y);
+        const float sign = upper ? 1.f : -1.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][0][e] = x[i][0][e] * cs[e] + b[i][e] * sn[e];
+        for (int w = 0; w < 4; ++w) {
+          const float4 t4 = turns[w * kMaxItems];
+          x[2 * w] = x[2 * w] * t4.x + y[2 * w] * (sign * t4.y);
+          x[2 * w + 1] = x[2 * w + 1] * t4.z + y[2 * w + 1] * (sign * t4.w);
         }
       }
-      put8<D, FMT, kTF32>(m.c, 0, o, so, ch, in, x[i][0]);
-      put8<D, FMT, T>(m.c, 1, o, so, ch, in, x[i][1]);
+      put8<D, FMT, kTF32>(m.c, 0, o, so, ch, in, x);
+      v[i].get(x);
+      put8<D, FMT, T>(m.c, 1, o, so, ch, in, x);
     }
   }
 }
@@ -279,11 +283,12 @@ cudaError_t launch_write(const RopeWriteArgs& a, int num_sms, cudaStream_t st) {
   const int ctas = (a.move.rq.n_tokens + kThreads / 32 - 1) / (kThreads / 32);
   // few tokens: their query heads over more CTAs
   const int split = a.q.p ? std::max(1, std::min({8, a.q_heads, 2 * num_sms / ctas})) : 0;
-  const dim3 grid(ctas, 1 + split);
+  const int parts = 1 + split;
+  const dim3 grid(static_cast<unsigned>(ctas) * parts);
   switch (a.move.k.type) {
-    case kTBf16: rope_write_kernel<D, FMT, kTBf16><<<grid, kThreads, 0, st>>>(a); break;
-    case kTF16: rope_write_kernel<D, FMT, kTF16><<<grid, kThreads, 0, st>>>(a); break;
-    default: rope_write_kernel<D, FMT, kTF32><<<grid, kThreads, 0, st>>>(a); break;
+    case kTBf16: rope_write_kernel<D, FMT, kTBf16><<<grid, kThreads, 0, st>>>(a, parts); break;
+    case kTF16: rope_write_kernel<D, FMT, kTF16><<<grid, kThreads, 0, st>>>(a, parts); break;
+    default: rope_write_kernel<D, FMT, kTF32><<<grid, kThreads, 0, st>>>(a, parts); break;
   }
   return cudaGetLastError();
 }
