@@ -174,8 +174,10 @@ cudaError_t launch_rows(const RopeArgs& a, int num_sms, cudaStream_t st) {
   const int items = a.plan.rot >> 4, rest = (a.dim - a.plan.rot + 15) >> 4;
   const int x_each = items + (a.x_copy ? rest : 0), k_each = items + (a.k_copy ? rest : 0);
   const int token = a.x_heads * x_each + a.k_heads * k_each;
-  // 8 tokens a CTA, or 16 of few items, while that leaves two CTAs an SM; below, a token a CTA, its items split over up to 4
-  const int per = a.n_tokens >= 16 * num_sms ? (token <= kThreads ? 16 : 8) : std::max(1, std::min(kTogether<T>, a.n_tokens / (2 * num_sms)));
+  // about eight CTAs an SM (9001 tokens of 112 items: with four 27 us, with eight 23), of whole groups of tokens, up to 8 tokens or
+  // 16 of few items; a token a CTA where there are few, its items split over up to 4
+  const int most = token <= kThreads ? 16 : 8, share = a.n_tokens / (8 * num_sms);
+  const int per = share >= most ? most : share >= 4 ? share & ~3 : std::max(1, share);
   const int ctas = (a.n_tokens + per - 1) / per;
   const int split = ctas >= num_sms ? 1 : std::max(1, std::min(4, (token + kThreads - 1) / kThreads));
   const size_t smem = static_cast<size_t>(per) * 4 * items * sizeof(float4);
