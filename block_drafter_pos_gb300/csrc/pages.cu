@@ -27,11 +27,11 @@ DF2_DEV bool give_back(const PagePool& p, int page) {
 }
 
 // ------------------------------------------------------------------ taking and giving back
-// A cluster of 8 CTAs.  Every CTA works out what each row wants (a thread per row).  The counts are read in chunks of
+// A cluster of 16 CTAs (of 8: 256 samples freed, forked and grown 43 us against 41).  Every CTA works out what each row wants (a thread per row).  The counts are read in chunks of
 // 1024 pages, a warp each, dealt to the CTAs in turn; each keeps its chunks' free pages as bits and tells all
 // CTAs how many they are.  After the cluster's barrier nothing is read any more that the call changes: each warp hands its
 // chunks' free pages to the rows that their ranks fall to, and rows give back what they no longer hold.
-constexpr int kCluster = 8, kResizeThreads = 1024, kChunk = 1024;
+constexpr int kCluster = 16, kResizeThreads = 1024, kChunk = 1024;
 
 DF2_DEV uint32_t cluster_rank() {
   uint32_t r;
@@ -91,8 +91,7 @@ struct ResizeShared {
 };
 constexpr int kGood = 1, kRenews = 2, kServed = 4;
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kResizeThreads, 1)
-    resize_kernel(const __grid_constant__ PagesResizeArgs a) {
+__global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_constant__ PagesResizeArgs a) {
   extern __shared__ __align__(16) char smem[];
   ResizeShared& s = *reinterpret_cast<ResizeShared*>(smem);
   const PagePool& p = a.p;
@@ -411,11 +410,24 @@ size_t resize_smem(int n_pages) {
 }  // namespace
 
 cudaError_t launch_pages_resize(const PagesResizeArgs& a, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = set_smem_once(resize_kernel, static_cast<int>(resize_smem(1 << 22)), done);
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = set_smem_once(resize_kernel, static_cast<int>(resize_smem(1 << 22)), done[0]);
   if (e != cudaSuccess) return e;
-  resize_kernel<<<kCluster, kResizeThreads, resize_smem(a.p.n_pages), st>>>(a);
-  return cudaGetLastError();
+  e = set_attr_once(resize_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done[1]);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kResizeThreads);
+  cfg.dynamicSmemBytes = resize_smem(a.p.n_pages);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, resize_kernel, a);
 }
 
 cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t st) {
