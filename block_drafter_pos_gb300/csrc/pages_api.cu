@@ -118,9 +118,11 @@ dflash2_status dflash2_rope_plan(const dflash2_rope_config* cfg, dflash2_rotatio
     if (!(fabs(f) <= 1048576.0)) return DFLASH2_E_INVAL;
     rate[i] = f;
   }
+  const float amplitude = static_cast<float>(c.amplitude > 0 ? c.amplitude : (yarn ? 0.1 * log(c.factor) + 1 : 1.0));
+  if (!isfinite(amplitude)) return DFLASH2_E_INVAL;
   out->rot_dim = c.rot_dim;
   out->interleaved = c.interleaved;
-  out->amplitude = static_cast<float>(c.amplitude > 0 ? c.amplitude : (yarn ? 0.1 * log(c.factor) + 1 : 1.0));
+  out->amplitude = amplitude;
   for (int i = 0; i < c.rot_dim / 2; ++i) {
     const double t = rate[i] / (2 * pi), f = t - floor(t);  // [0, 1] (1 for a tiny negative rate: no turn)
     const double high = floor(f * 4294967296.0);

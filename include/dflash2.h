@@ -650,7 +650,8 @@ dflash2_status dflash2_rope_plan(const dflash2_rope_config* cfg, dflash2_rotatio
  * k_out (k_heads 0: none).  positions int32 [n_tokens], any value.  inverse != 0: by the opposite angle with the same
  * amplitude, which takes the gradient of out back to that of x.  head_dim: a multiple of 8 from rot_dim to 1024.
  * Each output is x, cosine and sine in fp32, rounded once.  x and out have one type; out may be x
- * itself (the same address and strides), any other overlap of their address ranges is refused. */
+ * itself (the same address and strides), any other overlap of their address ranges is refused; out is apart from k
+ * and k_out from x. */
 dflash2_status dflash2_rope(const dflash2_rotation* rope, int32_t n_tokens, int32_t head_dim, int32_t x_heads,
                             const dflash2_rows* x, const dflash2_rows* out, int32_t k_heads, const dflash2_rows* k,
                             const dflash2_rows* k_out, const int32_t* positions, int32_t inverse, void* stream);

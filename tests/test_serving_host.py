@@ -34,7 +34,7 @@ NAN, INF = float("nan"), float("inf")
 BAD_PLANS = [(dict(rot_dim=0), "E_INVAL"), (dict(rot_dim=-16), "E_INVAL"), (dict(rot_dim=24), "E_UNSUPPORTED"),
              (dict(rot_dim=272), "E_UNSUPPORTED"), (dict(interleaved=2), "E_INVAL"), (dict(scaling=4), "E_INVAL"),
              (dict(scaling=-1), "E_INVAL"), (dict(theta=1.0), "E_INVAL"), (dict(theta=NAN), "E_INVAL"), (dict(theta=INF), "E_INVAL"),
-             (dict(amplitude=-1.0), "E_INVAL"), (dict(amplitude=NAN), "E_INVAL"),
+             (dict(amplitude=-1.0), "E_INVAL"), (dict(amplitude=NAN), "E_INVAL"), (dict(amplitude=1e39), "E_INVAL"),
              (dict(scaling=1, factor=0.0), "E_INVAL"), (dict(scaling=1, factor=-2.0), "E_INVAL"), (dict(scaling=1, factor=1e-9), "E_INVAL"),
              (dict(scaling=2, factor=0.5, original_len=9), "E_INVAL"), (dict(scaling=2, factor=2.0), "E_INVAL"),
              (dict(scaling=2, factor=2.0, original_len=9, beta_fast=NAN), "E_INVAL"),
