@@ -403,19 +403,19 @@ def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedPool:
     the first three dimensions, the same for both), scales [pages, page_size, n_kv_heads]
     (8-bit pools) and page_table int32 [requests, pages of a request]."""
     what = "paged_cache"
-    torch, _, formats = _calls()[:3]
-    fmt = formats.get(k.dtype)
-    if fmt is None or k.dim() != 4 or k.dtype is not v.dtype:
+    f = _calls()
+    ty, sh, st, dev = k.dtype, k.shape, k.stride(), k.get_device()
+    fmt = f[2].get(ty)
+    if fmt is None or len(sh) != 4 or v.dtype is not ty:
         raise _inval(what, "k and v must be pools of one type [pages, page_size, heads, head_dim]")
-    sh, st = k.shape, k.stride()
-    dev = k.get_device()
     if sh != v.shape or st != v.stride() or st[3] != 1 or dev < 0 or v.get_device() != dev:
         raise _inval(what, "k and v must be tensors of one shape and layout on one CUDA device, with contiguous channels")
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.get_device() != dev or page_table.stride(1) != 1:
+    torch, rows, along = f[0], page_table.shape, page_table.stride()
+    if page_table.dtype is not torch.int32 or len(rows) != 2 or page_table.get_device() != dev or along[1] != 1:
         raise _inval(what, "page_table must be an int32 tensor [requests, pages] on the pools' device, with contiguous rows")
     c = PagedPool()
     c.device = dev
-    c.n_req, max_pages = page_table.shape
+    c.n_req, max_pages = rows
     ks = vs = 0
     ss = (0, 0, 0)
     if fmt >= KV_INT8:
@@ -427,7 +427,7 @@ def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> PagedPool:
             raise _inval(what, "the scales must have one layout")
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     c.raw = _PACK_CACHE.pack(k.data_ptr(), v.data_ptr(), ks, vs, page_table.data_ptr(), st[0], st[1], st[2], *ss,
-                             page_table.stride(0) if c.n_req > 1 else max_pages, sh[0], max_pages)
+                             along[0] if c.n_req > 1 else max_pages, sh[0], max_pages)
     c.geometry = (fmt, sh[1], sh[2], sh[3])
     c._keep = (k, v, page_table, k_scale, v_scale)
     return c

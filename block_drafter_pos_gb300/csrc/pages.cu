@@ -3,7 +3,9 @@
 //
 // State is the number of holders of each page, nothing else: a page without one is free, and the lowest free ids go
 // first, so the result does not depend on the order of the device's work, and pages taken and given back leave the
-// state as it was.  These are latencies, not bytes: each call is one launch.
+// state as it was.  These are latencies, not bytes: each call is one launch.  Measured (us, profiled alone): eight rows
+// of 63 pages grown and forked 9 and 4; 264 rows over 118,000 pages grown by 44 pages each 16, forked (256,000 holders) 7, freed 28;
+// 255 tails of pages of one head copied 5.  Kept nodes of 48 trees in 16 layers (54 MB) 10 us, 5.3 TB/s.
 #include <algorithm>
 
 #include "common.cuh"
@@ -27,10 +29,11 @@ DF2_DEV bool give_back(const PagePool& p, int page) {
 }
 
 // ------------------------------------------------------------------ taking and giving back
-// A cluster of 16 CTAs (of 8: 256 samples freed, forked and grown 43 us against 41).  Every CTA works out what each row wants (a thread per row).  The counts are read in chunks of
-// 1024 pages, a warp each, dealt to the CTAs in turn; each keeps its chunks' free pages as bits and tells all
-// CTAs how many they are.  After the cluster's barrier nothing is read any more that the call changes: each warp hands its
-// chunks' free pages to the rows that their ranks fall to, and rows give back what they no longer hold.
+// A cluster of 16 CTAs (of 8: 256 samples freed, forked and grown 43 us against 41).  Every CTA works out what each row
+// wants (a thread per row).  The counts are read in chunks of 1024 pages, a warp each, dealt to the CTAs in turn; each keeps its
+// chunks' free pages as bits and tells all CTAs how many they are.  After the cluster's barrier nothing is read any more that
+// the call changes: each warp hands its chunks' free pages to the rows that their ranks fall to, and rows give back what
+// they no longer hold.
 constexpr int kCluster = 16, kResizeThreads = 1024, kChunk = 1024;
 
 DF2_DEV uint32_t cluster_rank() {

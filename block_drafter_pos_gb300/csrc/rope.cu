@@ -7,7 +7,12 @@
 //
 // Both kernels are streams: a token's cosines and sines are computed once into shared memory and serve all its heads,
 // and an item is 16 channels of a head (8 pairs), two 16-byte loads and stores of 16-bit types.  The table is in
-// quarters of an item, so that neighbouring items' 16-byte reads are neighbours too.
+// quarters of an item, so that neighbouring items' 16-byte reads are neighbours too.  A thread has the same item of four tokens
+// (of fp32, two) in flight: 32768 tokens of 32 + 8 bf16 heads of 128 (671 MB) 98 us, 6.8 TB/s, the rate of a copy; an item at a time 116.
+// 9001 tokens of 28 fp32 heads of 64, 16 channels turned (129 MB): 23 us, 5.6 TB/s.
+//
+// Into the cache: 30,005 tokens, 64 of 128 channels turned, bf16 to e4m3 (678 MB) 114 us, 5.9 TB/s; the quantisation's
+// instructions (65% of the issue slots) run beside the queries' bytes.  64 tokens: 5 us.
 #include <algorithm>
 #include <type_traits>
 
