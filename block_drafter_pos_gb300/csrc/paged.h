@@ -135,12 +135,13 @@ struct PagedGroups {
 
 enum { kSharedAuto = 0, kSharedTogether = 1, kSharedApart = 2 };
 // Apart, the requests behind a group's first one read its prefix again, mostly from L2; together, there is a launch more, a
-// join of its partials, and a part to fetch for every row.  Bytes read again where the two meet, or fewer: for units of 16 rows, twice
-// that for wider ones.  Measured (us; together / apart), 8 KV
-// heads of 128, single tokens over bf16 caches: 4 requests over 8192 positions 30 / 28, 16 over 2048 30 / 29, 64 over 512 39 / 33, over
-// 1024 40 / 50; e4m3: 16 over 4096 38 / 38, 64 over 1024 47 / 45; blocks of 8: bf16 16 over 4096 59 / 56, 64 over 1024 72 / 63, over
-// 2048 78 / 105, e4m3 64 over 2048 98 / 98.
-constexpr long long kApartBytes = 1ll << 27;
+// join of its partials, and a part to fetch for every row.  Bytes read again where the two meet: for units of 16 rows, twice
+// that for wider ones.  Measured (us; together / apart), 8 KV heads of 128, 4 KB a position in bf16 and 2.1 in e4m3, single tokens: bf16
+// 4 requests over 8192 positions 32 / 29, 8 over 4096 29 / 29, 16 over 1024 24 / 21, over 2048 27 / 29, 64 over 512 34 / 33, over 1024
+// 35 / 50; e4m3 4 over 16384 38 / 37, 16 over 2048 31 / 26, over 4096 33 / 38, 64 over 512 41 / 36, over 1024 42 / 45.  Blocks of 8:
+// bf16 16 over 2048 42 / 35, over 4096 51 / 56, 64 over 1024 64 / 64; e4m3 16 over 4096 60 / 53, over 8192 70 / 88, 64 over 1024
+// 80 / 66, over 2048 88 / 99.
+constexpr long long kApartBytes = 100ll << 20;
 
 // Whether group g's requests [g0, g1) follow those of the group before and, the last's, end at the last request.  (Where one
 // does not, the whole call is refused: all of `begin` is trusted after that.)

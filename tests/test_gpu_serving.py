@@ -489,11 +489,11 @@ def test_shared_attention(how, case, hq, hk, dim, page, order, fmt, qtype):
 
 
 def test_shared_attention_chooses_by_the_bytes():
-    """On either side of the border the call's bits are those of the way it names: 16 requests over 4 KB positions, 32768 read
-    again; the border is 128 MiB for 16 rows and 256 MiB above."""
-    for new, prefix, way in ((1, 2184, "apart"), (1, 2185, "together"), (8, 4369, "apart"), (8, 4370, "together")):
+    """On either side of the border the call's bits are those of the way it names: 15 requests read positions of 4 KB again;
+    the border is 100 MiB for 16 rows and 200 MiB above."""
+    for new, prefix, way in ((1, 1706, "apart"), (1, 1707, "together"), (8, 3413, "apart"), (8, 3414, "together")):
         s = SharedSetup([new] * 16, [prefix + new + 3 * r for r in range(16)], hq=32, hk=8, page=64, seed=prefix).share([16], [prefix])
-        assert (15 * prefix * 4096 <= (1 << 27 if new == 1 else 1 << 28)) == (way == "apart")
+        assert (15 * prefix * 4096 <= (100 << 20 if new == 1 else 200 << 20)) == (way == "apart")
         q = s.queries("bf16")
         ways = {w: s.attend_shared(q, how=w)[1] for w in ("auto", "together", "apart")}
         assert not torch.equal(ways["together"], ways["apart"])              # (joined in another order)

@@ -420,3 +420,13 @@ def test_oracle_pages_by_hand():
     assert os_.pages_resize(table, ref, kv, [9, 16, 16], 4)[1] == [5, 0, 0] and kv == [8, 16, 16]
     assert os_.pages_resize(table, ref, kv, [0, 0, 0], 4)[1] == [0, 0, 0] and not any(ref) and table == [[-1] * 4] * 3
     assert os_.pages_fork(table, ref, kv, [0, 0, 1, 2], [1, 1, 2, 0], 4) == [1, 1, 1, 1]
+
+
+def test_a_wait_that_gives_up_spoils_its_run():
+    """Every role of the prefix's kernel marks its CTA, and partials that never come are NaN; the joining kernel flags a run's groups."""
+    csrc = os.path.join(ROOT, "block_drafter_pos_gb300", "csrc")
+    text, sched = (open(os.path.join(csrc, n)).read() for n in ("paged_prefix.cu", "paged_sched.cuh"))
+    assert text.count("a.desc[8 * c + 6] = 1;") == 4 and text.count("a.desc[8 * c + 6] = 0;") == 1
+    assert text.index("make_float2(NAN, NAN)") < text.index("tcgen05.alloc") and "paged_flag<kShared>(a, r, 3)" in open(
+        os.path.join(csrc, "paged_attention.cu")).read()
+    assert "for (int x = __ldg(a.g.begin + r); x < __ldg(a.g.begin + r + 1); ++x) a.rq.status[x] = what;" in sched
