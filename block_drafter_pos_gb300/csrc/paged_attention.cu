@@ -87,17 +87,16 @@ struct Geo {
   static constexpr int kKG = 4 / MT;                   // key groups (a warp: one row tile, one group)
   static constexpr int kWK = kBN / kKG;                // keys of a warp
   static constexpr int kNT = D / 8;                    // output column tiles
-  static constexpr int kMergeCols = kNT / 4;           // column tiles joined at a time
-  static constexpr int kMerge = (kKG - 1) * MT * kMergeCols * 4 * 32 * 4;
+  static_assert((kKG - 1) * MT * kNT * 4 * 32 * 4 <= kStage, "the key groups are joined in a tile's buffer");
   static constexpr int kStat = 4 * 32 * 16;
   static constexpr int kOff = (kStages + 1) * kBN * 8 + (kStages + 1) * 16 + 64;
-  static constexpr int kFixed = kStages * kStage + kMerge + kStat + kOff;
+  static constexpr int kFixed = kStages * kStage + kStat + kOff;
 };
 
 // One warp joins row lr of a cut unit (KV head h, row tile qt of the request with rows b0 .. b0 + n - 1 new tokens): the
-// partials of CTAs c0 .. c1 (c0's in its slot `first`) are added in CTA order, eight at a time (their loads
+// partials of CTAs c0 .. c1 (c0's in its slot `first`) are added in CTA order, B at a time (their loads
 // together: what this costs is latency).
-template <int D, bool QBF>
+template <int D, bool QBF, int B>
 DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int slot0, int b0, int n, int lr, bool joint) {
   const int R = a.s.rows, lane = threadIdx.x & 31, row = qt * R + lr;
   if (row >= n * a.s.group) return;
@@ -123,11 +122,11 @@ DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int
       float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = 0.f;
-      for (int c = c0; c <= c1; c += 8) {
-        float2 st[8];
-        float x[8][V];
+      for (int c = c0; c <= c1; c += B) {
+        float2 st[B];
+        float x[B][V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < B; ++i) {
           st[i] = make_float2(-INFINITY, 0.f);
           if (c + i <= c1) {
             const float* p = a.part + (c + i == c0 ? first : 2ll * (c + i)) * stride;
@@ -146,14 +145,14 @@ DF2_DEV void join_row(const PagedAttnArgs& a, int h, int qt, int c0, int c1, int
         }
         float top = m;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, st[i].x);
+        for (int i = 0; i < B; ++i) top = fmaxf(top, st[i].x);
         const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(m - ref);
         m = top;
         l *= f0;
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] *= f0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < B; ++i) {
           const float f = ex2(st[i].x - ref);
           l += st[i].y * f;
 #pragma unroll
@@ -196,9 +195,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   constexpr int kSteps = D / 16;
   extern __shared__ __align__(128) char sm[];
   const uint32_t ring = smem_addr(sm);
-  float* const merge = reinterpret_cast<float*>(sm + S * G::kStage);
-  float4* const stat = reinterpret_cast<float4*>(sm + S * G::kStage + G::kMerge);
-  long long* const offs = reinterpret_cast<long long*>(sm + S * G::kStage + G::kMerge + G::kStat);  // [S + 1][kBN]
+  float4* const stat = reinterpret_cast<float4*>(sm + S * G::kStage);
+  long long* const offs = reinterpret_cast<long long*>(sm + S * G::kStage + G::kStat);  // [S + 1][kBN]
   int* const badp = reinterpret_cast<int*>(offs + (S + 1) * kBN);                                    // [S + 1][4]
   long long* const tmp = reinterpret_cast<long long*>(badp + (S + 1) * 4);
   unsigned* const last_sh = reinterpret_cast<unsigned*>(tmp + 7);
@@ -695,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       }
     }
 
+    const int st_read = st_now;
     sl_next = sl_next == S ? 0 : sl_next + 1;
     put(sl_next);
     soff_next = my_soff;
@@ -762,27 +761,24 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
         m0 = y0;
         m1 = y1;
+        // (through the tile's own buffer, which all have read)
+        float* const merge = reinterpret_cast<float*>(sm + st_read * G::kStage);
+        if (kg > 0) {
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          constexpr int MC = G::kMergeCols;
-          if (part) __syncthreads();
-          if (kg > 0) {
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < MC; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) merge[((((kg - 1) * MT + rg) * MC + t) * 4 + e) * 32 + lane] = o[part * MC + t][e];
-          }
-          __syncthreads();
-          if (kg == 0) {
-#pragma unroll
-            for (int i = 0; i < KG - 1; ++i)
-#pragma unroll
-              for (int t = 0; t < MC; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[part * MC + t][e] += merge[(((i * MT + rg) * MC + t) * 4 + e) * 32 + lane];
-          }
+            for (int e = 0; e < 4; ++e) merge[((((kg - 1) * MT + rg) * NT + t) * 4 + e) * 32 + lane] = o[t][e];
         }
-        // the buffers are next written after the next tile's barrier
+        __syncthreads();
+        if (kg == 0) {
+#pragma unroll
+          for (int i = 0; i < KG - 1; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][e] += merge[(((i * MT + rg) * NT + t) * 4 + e) * 32 + lane];
+        }
+        // the buffer is next written after the next tile's barrier
       }
       if (kg == 0) {
         const int rows = cc.n * a.s.group;
@@ -882,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
             __threadfence();
             const int slot0 = paged_run_begin(c0, C, T) == cc.unit_t ? 0 : 1;
             for (int lr = wid; lr < G::kRows; lr += kThreads / 32)
-              join_row<D, QBF>(a, cc.h, cc.qt, c0, c1, slot0, cc.b0, cc.n, lr, cc.first_key() > 0);
+              join_row<D, QBF, 8>(a, cc.h, cc.qt, c0, c1, slot0, cc.b0, cc.n, lr, cc.first_key() > 0);
           }
         }
       }
@@ -909,6 +905,8 @@ DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
   }
 }
 
+// (Registers keep CTAs that find nothing from passing: 48 blocks over three prefixes, eight at a time 275 us, four 269, twenty 294.)
+constexpr int kJoinTogether = kShared ? 4 : 8;
 // Joins the partials of the units cut between CTAs, where the attention leaves that to a launch of its own.  WAITS: of the
 // kernel for many rows, whose waits may give up.
 template <int D, bool QBF, bool WAITS>
@@ -919,7 +917,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
   if (WAITS && d1.z != 0 && blockIdx.y == 0 && threadIdx.x == 0) flag_run(a, blockIdx.x);
   if (d0.x < 0) return;
   for (int lr = blockIdx.y * 4 + (threadIdx.x >> 5); lr < a.s.rows; lr += 4 * gridDim.y)
-    join_row<D, QBF>(a, d0.y, d0.z, blockIdx.x, d0.w >> 1, d0.w & 1, d1.x, d1.y, lr, d1.w != 0);
+    join_row<D, QBF, kJoinTogether>(a, d0.y, d0.z, blockIdx.x, d0.w >> 1, d0.w & 1, d1.x, d1.y, lr, d1.w != 0);
 }
 
 template <int D, int FMT, int MT, bool QBF>
@@ -997,7 +995,7 @@ cudaError_t LAUNCH_ATTENTION(PagedAttnArgs& a, int head_dim, int fmt, int qtype,
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
   // a row per warp for units of 32 rows (four in turn took 2 to 3 us more) and for a prefix's, which are cut into many pieces
-  // (four in turn 24 us against 12, 64 tokens over 32768); four for the others of 256
+  // (four in turn 118 us against 109, 64 tokens over 32768); four for the others of 256
   const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / (kShared && a.g.first ? 4 : 16));
   auto combine = [&](auto kernel, auto kernel_waits) {
     return launch_ex(a.s.rows == 32 ? kernel : kernel_waits, grid, dim3(128), 0, st, true, a);
