@@ -128,19 +128,20 @@ def dflash2_paged_rope_write(h, rope: RopePlan, cache, q, q_out, k, v, token_beg
     what = "dflash2_paged_rope_write"
     f, torch = _calls(), _b._calls()[0]
     g, hq, n, begin, length, st = _b._paged_check(what, torch, h, cache, token_begin, kv_len, status)
-    dev = cache.device
-    if k.shape != v.shape or k.dtype is not v.dtype:
-        raise _inval(what, "k and v must have one shape and type")
-    rk, rv = (_b._PACK_ROWS.pack(*_rows(what, name, t, f["types"], g[2], g[3], dev)) for name, t in (("k", k), ("v", v)))
+    dev, shape = cache.device, k.shape
+    rk, rv = _pair(what, ("k", "v"), k, v, f["types"], dev)
+    tokens = shape[0]
+    if shape[1:] != g[2:]:
+        raise _inval(what, f"k and v must have {g[2]} heads of {g[3]}")
     rq = ry = None
     if (q is None) != (q_out is None):
         raise _inval(what, "q and q_out come together")
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[1] != hq or q.shape[2] != g[3] or q.dtype is not k.dtype:
+        if q.shape != (tokens, hq, g[3]) or q.dtype is not k.dtype:
             raise _inval(what, f"q must have k's tokens and type, {hq} heads of {g[3]}")
         rq, ry = _pair(what, ("q", "q_out"), q, q_out, f["types"], dev)
-    s = f["write"](h, rope.raw, cache.raw, n, k.shape[0], begin, length,
-                   _vector(what, "positions", positions, torch.int32, k.shape[0], dev), rq, ry, rk, rv, st,
+    s = f["write"](h, rope.raw, cache.raw, n, tokens, begin, length,
+                   _vector(what, "positions", positions, torch.int32, tokens, dev), rq, ry, rk, rv, st,
                    _raw_stream(what, torch, stream, dev))
     if s:
         _check(s, what)
@@ -201,12 +202,12 @@ def _layers(what, h, caches):
     g = _b._paged_cfg.get(h)
     if g is None:
         raise _inval(what, "not a paged handle")
+    geometry, dev = g[0], g[2]
     for c in caches:
-        if c.geometry != g[0]:
-            raise _inval(what, "the pools are not of the handle's format, page size or heads")
-        if c.device != g[2]:
-            raise _inval(what, f"the pools are on device {c.device}, the handle on {g[2]}")
-    return g[0], g[2], b"".join([c.raw for c in caches])
+        if c.geometry != geometry or c.device != dev:
+            raise _inval(what, "the pools are not of the handle's format, page size or heads" if c.device == dev else
+                         f"the pools are on device {c.device}, the handle on {dev}")
+    return geometry, dev, b"".join([c.raw for c in caches])
 
 
 def dflash2_pages_copy(h, caches, copies, status=None, stream=None):
