@@ -136,7 +136,8 @@ dflash2_status dflash2_rope(const dflash2_rotation* rope, int32_t n_tokens, int3
                             const dflash2_rows* x, const dflash2_rows* out, int32_t k_heads, const dflash2_rows* k,
                             const dflash2_rows* k_out, const int32_t* positions, int32_t inverse, void* stream) {
   if (!valid_plan(rope) || n_tokens < 0 || x_heads < 0 || k_heads < 0 || head_dim < 8) return DFLASH2_E_INVAL;
-  if (head_dim % 8 || head_dim > kRopeMaxDim || head_dim < rope->rot_dim || x_heads > kRopeMaxHeads || k_heads > kRopeMaxHeads - x_heads)
+  if (head_dim % 8 || head_dim > kRopeMaxDim || head_dim < rope->rot_dim || x_heads > kRopeMaxHeads || k_heads > kRopeMaxHeads - x_heads ||
+      n_tokens > kRopeMaxTokens)
     return DFLASH2_E_UNSUPPORTED;
   if (n_tokens == 0 || x_heads + k_heads == 0) return DFLASH2_OK;
   if (!positions || (x_heads > 0 && !valid_turn(x, out, n_tokens, x_heads, head_dim)) ||
@@ -168,7 +169,7 @@ dflash2_status dflash2_paged_rope_write(dflash2_paged_handle* h, const dflash2_r
   const dflash2_status s = check_cache(h, cache, n_req);
   if (s != DFLASH2_OK) return s;
   if (!valid_plan(rope) || n_tokens < 0 || !k || !v || (n_req > 0 && (!token_begin || !kv_len))) return DFLASH2_E_INVAL;
-  if (rope->rot_dim > h->cfg.head_dim) return DFLASH2_E_UNSUPPORTED;
+  if (rope->rot_dim > h->cfg.head_dim || n_tokens > kRopeMaxTokens) return DFLASH2_E_UNSUPPORTED;
   if (n_tokens == 0 || n_req == 0) return DFLASH2_OK;
   if (!valid_rows(*k) || !valid_rows(*v) || k->type != v->type) return DFLASH2_E_INVAL;
   if (q && (!valid_turn(q, q_out, n_tokens, h->cfg.n_q_heads, h->cfg.head_dim) || q->type != k->type)) return DFLASH2_E_INVAL;

@@ -7,6 +7,7 @@ namespace df2 {
 
 constexpr int kRopeMaxPairs = 128;
 constexpr int kRopeMaxDim = 1024, kRopeMaxHeads = 1024;  // of a row, and of a token in all: at most 2^16 items of 16 channels
+constexpr int kRopeMaxTokens = 0x7FFFFFF0;                // (a CTA's last token is numbered in 32 bits)
 
 struct RopePlan {
   int rot;              // channels that are turned

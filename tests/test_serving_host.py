@@ -119,7 +119,7 @@ def test_rope_refuses_bad_arguments():
         assert _call_rope(_rotation(**kw), x=x, out=y) == b.E_INVAL, kw
     for kw in (dict(n=-1), dict(dim=0), dict(heads=-1), dict(k_heads=-1), dict(positions=None)):
         assert _call_rope(ok, **{**dict(x=x, out=y), **kw}) == b.E_INVAL, kw
-    for kw in (dict(dim=100), dict(dim=2048), dict(dim=56), dict(heads=1025), dict(heads=600, k_heads=500)):
+    for kw in (dict(dim=100), dict(dim=2048), dict(dim=56), dict(heads=1025), dict(heads=600, k_heads=500), dict(n=2 ** 31 - 15)):
         assert _call_rope(ok, **{**dict(x=x, out=y, k=x, k_out=y), **kw}) == b.E_UNSUPPORTED, kw
     for kw in BAD_ROWS:
         assert _call_rope(ok, x=_rows(**kw), out=y) == b.E_INVAL, kw
@@ -156,6 +156,7 @@ def test_rope_write_refuses_bad_arguments():
     assert _call_write(h.p, _rotation(rot_dim=24), c, k=r, v=r) == b.E_INVAL
     assert _call_write(h.p, _rotation(rot_dim=144), c, k=r, v=r) == b.E_UNSUPPORTED       # above head_dim
     assert _call_write(h.p, plan, c, n_req=5, k=r, v=r) == b.E_UNSUPPORTED
+    assert _call_write(h.p, plan, c, n=2 ** 31 - 15, k=r, v=r) == b.E_UNSUPPORTED
     for kw in (dict(n=-1), dict(n_req=-1), dict(begin=None), dict(kv=None), dict(k=None), dict(v=None), dict(v=_rows(type=b.T_F16)),
                dict(q=q), dict(q=q, q_out=_rows(p=far, token_stride=1024, type=b.T_F16)),
                dict(q=_rows(token_stride=1024, type=b.T_F16), q_out=_rows(p=far, token_stride=1024, type=b.T_F16)),
