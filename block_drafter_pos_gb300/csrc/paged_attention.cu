@@ -905,7 +905,8 @@ DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
   }
 }
 
-// (Registers keep CTAs that find nothing from passing: 48 blocks over three prefixes, eight at a time 275 us, four 269, twenty 294.)
+// (Registers keep CTAs that find nothing from passing: 48 blocks over three prefixes, eight at a time 275 us, four 270,
+// twenty 294.)
 constexpr int kJoinTogether = kShared ? 4 : 8;
 // Joins the partials of the units cut between CTAs, where the attention leaves that to a launch of its own.  WAITS: of the
 // kernel for many rows, whose waits may give up.

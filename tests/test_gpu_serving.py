@@ -642,6 +642,87 @@ def test_rows_far_apart_in_the_two_parts():
 
 # ----------------------------------------------------------------------------- streams and graphs
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_pools_past_32_bits(fmt, new):
+    """Pools of more than 2^32 elements, the used pages at both ends: attention against the oracle; what the other calls leave is
+    bit for bit what they leave in a small pool."""
+    page, hk, dim, prefix = 64, 8, 128, 200
+    s = SharedSetup([new] * 3, [prefix + new + 50 * r for r in range(3)], hq=32, hk=hk, dim=dim, page=page, fmt=fmt, order="pch",
+                    seed=new).share([3], [prefix])
+    n_pages = (1 << 32) // (page * hk * dim) + 40
+    small = [t for t in (s.gk, s.gv, s.gks, s.gvs) if t is not None]
+    large = [torch.empty((n_pages,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in small]
+    where = torch.tensor([i if i % 2 else n_pages - 1 - i for i in range(s.gk.shape[0])], device="cuda")
+    small_cache = s.cache
+    table = torch.where(s.gtable >= 0, where[s.gtable.clamp_min(0).long()].int(), s.gtable)
+    s.cache = bd.paged_cache(large[0], large[1], table, *large[2:])
+
+    def same(move=False):
+        torch.cuda.synchronize()
+        for a, b in zip(small, large):
+            if move:
+                b[where] = a
+            assert torch.equal(a.contiguous().view(torch.uint8), b[where].view(torch.uint8))
+
+    same(move=True)
+    q = s.queries("bf16")
+    for how in ("together", "apart"):
+        check_shared(s, q, *s.attend_shared(q, how=how))
+    s.gtable[1:, :prefix // page] = s.gtable[0, :prefix // page]
+    table[1:, :prefix // page] = table[0, :prefix // page]
+    x = torch.randn(s.tokens, hk, dim, generator=torch.Generator().manual_seed(2)).cuda()
+    copies = [[3, 0], [4, 5], [page, 7]]
+    keep, n_keep = i32([[0] if new == 1 else [1, 5, 39]] * 3), i32([1 if new == 1 else 3] * 3)
+    for cache, ids in ((small_cache, torch.arange(len(where), device="cuda")), (s.cache, where)):
+        bd.dflash2_paged_rope_write(s.handle, bd.make_rope(dim), cache, None, None, x, x, s.begin, s.kv_len)
+        bd.dflash2_paged_keep(s.handle, [cache], s.begin, s.kv_len, keep, n_keep)
+        moved = torch.stack([ids[torch.tensor(c, device="cuda")].int() for c in copies[:2]] + [i32(copies[2])])
+        bd.dflash2_pages_copy(s.handle, [cache], moved)
+    same()
+    s.close()
+
+
+def test_rows_past_32_bits():
+    stride = (1 << 31) + 64
+    far = torch.empty(2 * stride + 256, dtype=torch.bfloat16, device="cuda").as_strided((3, 2, 64), (stride, 128, 1))
+    x, plan, pos = torch.randn(3, 2, 64, device="cuda").bfloat16(), bd.make_rope(64), i32([3, 70000, 5])
+    out, back = torch.empty_like(x), torch.empty_like(x)
+    bd.dflash2_rope(plan, x, out, pos)
+    bd.dflash2_rope(plan, x, far, pos)
+    assert torch.equal(far, out)
+    far.copy_(x)
+    bd.dflash2_rope(plan, far, back, pos)
+    assert torch.equal(back, out)
+
+
+@pytest.mark.parametrize("how", ["together", "apart"])
+@pytest.mark.parametrize("sizes,new", [([2] * 265, 1), ([1] * 530, 5), ([530], 1)])
+def test_shared_attention_of_many_requests(sizes, new, how):
+    """More groups, or more requests, than a block has threads, with host bounds far above what there is."""
+    g = np.random.default_rng(len(sizes))
+    prefix = (30 + g.integers(0, 90, len(sizes))).tolist()
+    pre = [p for size, p in zip(sizes, prefix) for _ in range(size)]
+    s = SharedSetup([new] * 530, [p + new + int(x) for p, x in zip(pre, g.integers(0, 40, 530))], hq=4, hk=1, dim=64, seed=6).share(sizes, prefix)
+    s.max_group = s.tokens
+    q = s.queries("bf16")
+    status = torch.zeros(530, dtype=torch.int32, device="cuda")
+    out, lse = s.attend_shared(q, how=how, status=status, max_prefix=1 << 20)
+    assert not status.any()
+    check_shared(s, q, out, lse, skip=[r for r in range(530) if r % 7 and r < 520])
+    assert torch.isfinite(out.float()).all()
+    s.close()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_shared_attention_of_prompts(fmt):
+    """Thousands of new rows a group: prompts that go on from a common beginning."""
+    s = SharedSetup([1100, 0, 515], [900 + 1100, 900, 900 + 700], hq=8, hk=1, dim=64, page=32, fmt=fmt, seed=4).share([3], [900])
+    q = s.queries("bf16")
+    check_shared(s, q, *s.attend_shared(q))
+    s.close()
+
+
 def test_captured_calls_replay_on_new_contents():
     """Two graphs with a handle and workspaces of their own, replayed in turn on lengths, tables and tokens that changed since."""
     graphs = []
