@@ -897,7 +897,7 @@ DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
   };
   long long T = 0, first = 0;
   for (int r = 0; r < a.rq.n_req; ++r) T += tiles(r);
-  const long long C = T < gridDim.x ? T : gridDim.x;
+  const long long C = T < a.ctas ? T : a.ctas;
   for (int r = 0; r < a.rq.n_req; ++r) {
     const long long next = first + tiles(r);
     if (paged_in_run(first, next, paged_run_begin(c, C, T), paged_run_begin(c + 1, C, T))) paged_flag<kShared>(a, r, 3);  // DFLASH2_E_CUDA
@@ -905,9 +905,7 @@ DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
   }
 }
 
-// (Registers keep CTAs that find nothing from passing: 48 blocks over three prefixes, eight at a time 275 us, four 270,
-// twenty 294.)
-constexpr int kJoinTogether = kShared ? 4 : 8;
+constexpr int kJoinTogether = kShared ? 4 : 8;  // (verify blocks: 1.5 us)
 // Joins the partials of the units cut between CTAs, where the attention leaves that to a launch of its own.  WAITS: of the
 // kernel for many rows, whose waits may give up.
 template <int D, bool QBF, bool WAITS>
@@ -920,6 +918,58 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
   for (int lr = blockIdx.y * 4 + (threadIdx.x >> 5); lr < a.s.rows; lr += 4 * gridDim.y)
     join_row<D, QBF, kJoinTogether>(a, d0.y, d0.z, blockIdx.x, d0.w >> 1, d0.w & 1, d1.x, d1.y, lr, d1.w != 0);
 }
+
+#if DF2_SHARED_PREFIX
+// The same for a prefix's units, few and cut into many pieces: their rows are dealt to a grid that is on the SMs as a whole, so
+// that the second launch begins beside it (64 tokens over 32768 98 us, 48 blocks over 30001 262; a CTA for every four rows of
+// every CTA's description 108 and 270).
+constexpr int kJoinCtas = 4;  // of an SM (with two or eight 99 us; 64 registers leave room for a CTA of the second)
+constexpr int kJoinEach = 4, kJoinDesc = 128 * kJoinEach;
+template <int D, bool QBF, bool WAITS>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+  __shared__ int4 cut[kJoinDesc][2];  // the descriptions of cut units, in one order in all CTAs
+  __shared__ int count[kJoinEach][4];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  int4 d0[kJoinEach], d1[kJoinEach];
+#pragma unroll
+  for (int e = 0; e < kJoinEach; ++e) {
+    const int c = e * 128 + tid;
+    d0[e] = c < a.ctas ? __ldcg(reinterpret_cast<const int4*>(a.desc + 8 * c)) : make_int4(-1, 0, 0, 0);
+    d1[e] = c < a.ctas ? __ldcg(reinterpret_cast<const int4*>(a.desc + 8 * c + 4)) : make_int4(0, 0, 0, 0);
+  }
+  uint32_t is_cut[kJoinEach];
+#pragma unroll
+  for (int e = 0; e < kJoinEach; ++e) {
+    is_cut[e] = __ballot_sync(0xffffffffu, d0[e].x >= 0);
+    if (lane == 0) count[e][wid] = __popc(is_cut[e]);
+  }
+  __syncthreads();
+  int n_cut = 0;
+#pragma unroll
+  for (int e = 0; e < kJoinEach; ++e)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w == wid && d0[e].x >= 0) {
+        const int i = n_cut + __popc(is_cut[e] & ((1u << lane) - 1u));
+        d0[e].x = e * 128 + tid;
+        cut[i][0] = d0[e];
+        cut[i][1] = d1[e];
+      }
+      n_cut += count[e][w];
+    }
+  __syncthreads();
+  const int R = a.s.rows, n = n_cut * R;
+  for (int i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n; i += 4 * gridDim.x) {
+    const int4 d = cut[i / R][0], x = cut[i / R][1];
+    join_row<D, QBF, kJoinTogether>(a, d.y, d.z, d.x, d.w >> 1, d.w & 1, x.x, x.y, i % R, false);
+  }
+  if (WAITS && blockIdx.x == 0)
+    for (int c = tid; c < a.ctas; c += 128)
+      if (__ldcg(a.desc + 8 * c + 6) != 0) flag_run(a, c);
+}
+#endif
 
 template <int D, int FMT, int MT, bool QBF>
 cudaError_t launch_rows(PagedAttnArgs& a, int num_sms, cudaStream_t st) {
@@ -995,17 +1045,27 @@ cudaError_t LAUNCH_ATTENTION(PagedAttnArgs& a, int head_dim, int fmt, int qtype,
   else if (rows > kChunkMinRows) e = LAUNCH_CHUNK(a, head_dim, fmt, qtype, num_sms, st);
   else e = head_dim == 64 ? launch_dim<64>(a, fmt, qtype, num_sms, st) : launch_dim<128>(a, fmt, qtype, num_sms, st);
   if (e != cudaSuccess || a.s.rows == 16) return e;  // (one row tile: joined by the kernel itself)
-  // a row per warp for units of 32 rows (four in turn took 2 to 3 us more) and for a prefix's, which are cut into many pieces
-  // (four in turn 118 us against 109, 64 tokens over 32768); four for the others of 256
-  const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / (kShared && a.g.first ? 4 : 16));
-  auto combine = [&](auto kernel, auto kernel_waits) {
+  auto join = [&](auto kernel, auto kernel_waits, dim3 grid) {
     return launch_ex(a.s.rows == 32 ? kernel : kernel_waits, grid, dim3(128), 0, st, true, a);
   };
+#if DF2_SHARED_PREFIX
+  if (a.g.first) {
+    if (a.ctas > kJoinDesc) return cudaErrorInvalidValue;
+    const dim3 grid(std::min(a.ctas * (a.s.rows / 4), num_sms * kJoinCtas));
+    if (head_dim == 64)
+      return qtype == kTBf16 ? join(paged_join_kernel<64, true, false>, paged_join_kernel<64, true, true>, grid)
+                             : join(paged_join_kernel<64, false, false>, paged_join_kernel<64, false, true>, grid);
+    return qtype == kTBf16 ? join(paged_join_kernel<128, true, false>, paged_join_kernel<128, true, true>, grid)
+                           : join(paged_join_kernel<128, false, false>, paged_join_kernel<128, false, true>, grid);
+  }
+#endif
+  // a row per warp for units of 32 rows (four in turn took 2 to 3 us more), four for those of 256
+  const dim3 grid(a.ctas, a.s.rows == 32 ? 8 : a.s.rows / 16);
   if (head_dim == 64)
-    return qtype == kTBf16 ? combine(paged_combine_kernel<64, true, false>, paged_combine_kernel<64, true, true>)
-                           : combine(paged_combine_kernel<64, false, false>, paged_combine_kernel<64, false, true>);
-  return qtype == kTBf16 ? combine(paged_combine_kernel<128, true, false>, paged_combine_kernel<128, true, true>)
-                         : combine(paged_combine_kernel<128, false, false>, paged_combine_kernel<128, false, true>);
+    return qtype == kTBf16 ? join(paged_combine_kernel<64, true, false>, paged_combine_kernel<64, true, true>, grid)
+                           : join(paged_combine_kernel<64, false, false>, paged_combine_kernel<64, false, true>, grid);
+  return qtype == kTBf16 ? join(paged_combine_kernel<128, true, false>, paged_combine_kernel<128, true, true>, grid)
+                         : join(paged_combine_kernel<128, false, false>, paged_combine_kernel<128, false, true>, grid);
 }
 
 }  // namespace df2
