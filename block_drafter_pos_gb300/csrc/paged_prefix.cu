@@ -5,8 +5,8 @@
 // value scales have one reference for all rows.  A unit is 256 rows of one KV head (two tiles of 128) against key tiles of
 // 128, with tensor memory, warps and products as in the kernel for prompt chunks; without what that one keeps for rows
 // that see different keys, a row's 128 scores stay in registers beside 8-bit caches' scales, too.  The page table is read
-// two tiles ahead of the copies.  Units, runs and cut units are dealt and described as there, so the same kernel joins the
-// partials.  Every wait is bounded.
+// two tiles ahead of the copies.  Units, runs and cut units are dealt and described as there; the partials are joined by a
+// launch of their own.  Every wait is bounded.
 //
 // Measured: 64 tokens of 32 query heads over 32768 bf16 positions of 8 KV heads of 128 (134 MB, 34 GFLOP) 43 us, 3700 clocks a
 // tile of 128 keys, of which the products of the two row tiles take 1500 to 1750 each; 11 us pass before the first scores, 4 after the
