@@ -87,7 +87,7 @@ struct Geo {
   static constexpr int kKG = 4 / MT;                   // key groups (a warp: one row tile, one group)
   static constexpr int kWK = kBN / kKG;                // keys of a warp
   static constexpr int kNT = D / 8;                    // output column tiles
-  static_assert((kKG - 1) * MT * kNT * 4 * 32 * 4 <= kStage, "the key groups are joined in a tile's buffer");
+  static_assert(4 * kNT * 32 * 16 <= kStage, "the key groups are joined in a tile's buffer");
   static constexpr int kStat = 4 * 32 * 16;
   static constexpr int kOff = (kStages + 1) * kBN * 8 + (kStages + 1) * 16 + 64;
   static constexpr int kFixed = kStages * kStage + kStat + kOff;
@@ -733,6 +733,100 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         l0 += __shfl_xor_sync(0xffffffffu, l0, of);
         l1 += __shfl_xor_sync(0xffffffffu, l1, of);
       }
+      const int rows = cc.n * a.s.group;
+      const bool whole = cc.unit_t >= t_begin && cc.unit_ends();
+      const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
+      if (MT > 1 && !whole && tid == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
+        const long long tl = cc.unit_t + cc.u.nt;
+        long long cb = (tl * C - 1) / T;  // the CTA of the unit's last tile
+        int* dd = a.desc + 8 * c;
+        dd[1] = cc.h;
+        dd[2] = cc.qt;
+        dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
+        dd[4] = cc.b0;
+        dd[5] = cc.n;
+        if constexpr (kShared) dd[7] = cc.from > 0;
+        dd[0] = cc.r;
+      }
+      // Rows of column tiles t0, t0 + 1, ...; this thread's columns: 8 (t0 + t) + 2 q + e, of codes (D / 8) (2 q + e) + t0 + t.
+      auto write = [&](auto& sum, const int t0) {
+        constexpr int NO = sizeof(sum) / sizeof(sum[0]);
+        [[maybe_unused]] constexpr int kWide = NO % 4 == 0 ? 4 : 2;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int lr = rg * 16 + g + 8 * hf, row = cc.qt * G::kRows + lr;
+          if (row >= rows) continue;
+          const float l = hf ? l1 : l0, m = hf ? m1 : m0;
+          if (whole && !(kShared && a.g.first)) {
+            float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (a NaN sum stays NaN)
+            const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
+            float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+            if constexpr (kShared) {
+              if (cc.from > 0) {  // the prefix's part
+                const JointParts p(m, l, *joint_stat<D>(a, cc.b0 + i, head));
+                const float* const j = joint_row<D>(a, cc.b0 + i, head);
+#pragma unroll
+                for (int t = 0; t < NO; ++t)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    sum[t][2 * hf + e] =
+                        sum[t][2 * hf + e] * p.mine + j[kQuant ? NT * (2 * q + e) + t0 + t : 8 * (t0 + t) + 2 * q + e] * p.other;
+                inv = 1.f;
+                lse = p.lse();
+              }
+            }
+            char* po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
+            if constexpr (!kQuant) {
+#pragma unroll
+              for (int t = 0; t < NO; ++t)
+                *reinterpret_cast<uint32_t*>(po + (8 * (t0 + t) + 2 * q) * 2) = pack2<QBF>(sum[t][2 * hf] * inv, sum[t][2 * hf + 1] * inv);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int t = 0; t < NO; t += kWide) {
+                  uint32_t w[kWide / 2];
+#pragma unroll
+                  for (int x = 0; x < kWide / 2; ++x)
+                    w[x] = pack2<QBF>(sum[t + 2 * x][2 * hf + e] * inv, sum[t + 2 * x + 1][2 * hf + e] * inv);
+                  char* const to = po + (NT * (2 * q + e) + t0 + t) * 2;
+                  if constexpr (kWide == 4) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+                  else *reinterpret_cast<uint32_t*>(to) = w[0];
+                }
+            }
+            if (a.lse && q == 0 && kg == 0)
+              a.lse[static_cast<long long>(cc.b0 + i) * (a.c.n_kv * a.s.group) + head] = lse;
+          } else {
+            float* pp = a.part + slot * (G::kRows * (D + 2)) + lr * D;
+            float2* ps = reinterpret_cast<float2*>(a.part + slot * (G::kRows * (D + 2)) + G::kRows * D + 2 * lr);
+            if constexpr (kShared) {
+              if (whole) {
+                const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
+                pp = joint_row<D>(a, cc.b0 + i, head);
+                ps = joint_stat<D>(a, cc.b0 + i, head);
+              }
+            }
+            if constexpr (!kQuant) {
+#pragma unroll
+              for (int t = 0; t < NO; ++t)
+                *reinterpret_cast<float2*>(pp + 8 * (t0 + t) + 2 * q) = make_float2(sum[t][2 * hf], sum[t][2 * hf + 1]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int t = 0; t < NO; t += kWide) {
+                  float* const to = pp + NT * (2 * q + e) + t0 + t;
+                  if constexpr (kWide == 4)
+                    *reinterpret_cast<float4*>(to) =
+                        make_float4(sum[t][2 * hf + e], sum[t + 1][2 * hf + e], sum[t + 2][2 * hf + e], sum[t + 3][2 * hf + e]);
+                  else
+                    *reinterpret_cast<float2*>(to) = make_float2(sum[t][2 * hf + e], sum[t + 1][2 * hf + e]);
+                }
+            }
+            if (q == 0 && kg == 0) *ps = make_float2(m, l);
+          }
+        }
+      };
       {
         stat[wid * 32 + lane] = make_float4(m0, m1, l0, l1);
         __syncthreads();
@@ -761,108 +855,37 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
         m0 = y0;
         m1 = y1;
-        // (through the tile's own buffer, which all have read)
-        float* const merge = reinterpret_cast<float*>(sm + st_read * G::kStage);
-        if (kg > 0) {
+        // Through the tile's own buffer, which all have read, in the order of the groups.  Four groups: each warp joins a
+        // share of the columns (one with all of them 1.1 us a unit, 64 tokens of ragged 1024 positions 42.5 us against 40); two:
+        // the first joins all (shares 265 to 270 us against 261, 48 blocks over 30001, for want of registers).
+        float4* const merge = reinterpret_cast<float4*>(sm + st_read * G::kStage) + lane;
+        if (KG == 4 || kg > 0) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) merge[((((kg - 1) * MT + rg) * NT + t) * 4 + e) * 32 + lane] = o[t][e];
+          for (int t = 0; t < NT; ++t) merge[(wid * NT + t) * 32] = make_float4(o[t][0], o[t][1], o[t][2], o[t][3]);
         }
         __syncthreads();
-        if (kg == 0) {
+        if constexpr (KG == 4) {
+          float sum[NT / 4][4];
 #pragma unroll
-          for (int i = 0; i < KG - 1; ++i)
+          for (int t = 0; t < NT / 4; ++t) {
+            float4 v = merge[(kg * (NT / 4) + t) * 32];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[t][e] += merge[(((i * MT + rg) * NT + t) * 4 + e) * 32 + lane];
-        }
-        // the buffer is next written after the next tile's barrier
-      }
-      if (kg == 0) {
-        const int rows = cc.n * a.s.group;
-        const bool whole = cc.unit_t >= t_begin && cc.unit_ends();
-        const long long slot = 2 * c + (cc.unit_t <= t_begin ? 0 : 1);
-        if (MT > 1 && !whole && tid == 0 && cc.unit_t >= t_begin) {  // the cut unit begins here: tell the combine
-          const long long tl = cc.unit_t + cc.u.nt;
-          long long cb = (tl * C - 1) / T;  // the CTA of the unit's last tile
-          int* dd = a.desc + 8 * c;
-          dd[1] = cc.h;
-          dd[2] = cc.qt;
-          dd[3] = static_cast<int>(cb) * 2 + (cc.unit_t == t_begin ? 0 : 1);
-          dd[4] = cc.b0;
-          dd[5] = cc.n;
-          if constexpr (kShared) dd[7] = cc.from > 0;
-          dd[0] = cc.r;
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int lr = rg * 16 + g + 8 * hf, row = cc.qt * G::kRows + lr;
-          if (row >= rows) continue;
-          const float l = hf ? l1 : l0, m = hf ? m1 : m0;
-          if (whole && !(kShared && a.g.first)) {
-            float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (a NaN sum stays NaN)
-            const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
-            float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
-            if constexpr (kShared) {
-              if (cc.from > 0) {  // the prefix's part
-                const JointParts p(m, l, *joint_stat<D>(a, cc.b0 + i, head));
-                const float* const j = joint_row<D>(a, cc.b0 + i, head);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    o[t][2 * hf + e] = o[t][2 * hf + e] * p.mine + j[kQuant ? NT * (2 * q + e) + t : 8 * t + 2 * q + e] * p.other;
-                inv = 1.f;
-                lse = p.lse();
-              }
+            for (int x = 1; x < KG; ++x) {
+              const float4 w = merge[(x * NT + kg * (NT / 4) + t) * 32];
+              v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
             }
-            char* po = a.out.p + ((cc.b0 + i) * a.out.token_stride + head * a.out.head_stride) * 2;
-            if constexpr (!kQuant) {
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-                *reinterpret_cast<uint32_t*>(po + (8 * t + 2 * q) * 2) =
-                    pack2<QBF>(o[t][2 * hf] * inv, o[t][2 * hf + 1] * inv);
-            } else {
-              // this thread's columns: (D / 8) (2 q + e) + t
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int t = 0; t < NT; t += 8)
-                  *reinterpret_cast<uint4*>(po + (NT * (2 * q + e) + t) * 2) = make_uint4(
-                      pack2<QBF>(o[t][2 * hf + e] * inv, o[t + 1][2 * hf + e] * inv),
-                      pack2<QBF>(o[t + 2][2 * hf + e] * inv, o[t + 3][2 * hf + e] * inv),
-                      pack2<QBF>(o[t + 4][2 * hf + e] * inv, o[t + 5][2 * hf + e] * inv),
-                      pack2<QBF>(o[t + 6][2 * hf + e] * inv, o[t + 7][2 * hf + e] * inv));
-            }
-            if (a.lse && q == 0)
-              a.lse[static_cast<long long>(cc.b0 + i) * (a.c.n_kv * a.s.group) + head] = lse;
-          } else {
-            float* pp = a.part + slot * (G::kRows * (D + 2)) + lr * D;
-            float2* ps = reinterpret_cast<float2*>(a.part + slot * (G::kRows * (D + 2)) + G::kRows * D + 2 * lr);
-            if constexpr (kShared) {
-              if (whole) {
-                const int i = row / a.s.group, head = cc.h * a.s.group + row % a.s.group;
-                pp = joint_row<D>(a, cc.b0 + i, head);
-                ps = joint_stat<D>(a, cc.b0 + i, head);
-              }
-            }
-            if constexpr (!kQuant) {
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-                *reinterpret_cast<float2*>(pp + 8 * t + 2 * q) = make_float2(o[t][2 * hf], o[t][2 * hf + 1]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int t = 0; t < NT; t += 4)
-                  *reinterpret_cast<float4*>(pp + NT * (2 * q + e) + t) =
-                      make_float4(o[t][2 * hf + e], o[t + 1][2 * hf + e], o[t + 2][2 * hf + e], o[t + 3][2 * hf + e]);
-            }
-            if (q == 0) *ps = make_float2(m, l);
+            sum[t][0] = v.x, sum[t][1] = v.y, sum[t][2] = v.z, sum[t][3] = v.w;
           }
+          write(sum, kg * (NT / 4));
+        } else if (kg == 0) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float4 w = merge[((MT + rg) * NT + t) * 32];
+            o[t][0] += w.x, o[t][1] += w.y, o[t][2] += w.z, o[t][3] += w.w;
+          }
+          write(o, 0);
         }
+        // (the buffer is next written after the next tile's barrier)
       }
       if constexpr (MT == 1) {
         // one row tile: the CTA that brings a cut unit's last partial joins them (up to four rows a warp), which saves a
