@@ -944,8 +944,8 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
 
 #if DF2_SHARED_PREFIX
 // The same for a prefix's units, few and cut into many pieces: their rows are dealt to a grid that is on the SMs as a whole, so
-// that the second launch begins beside it (64 tokens over 32768 98 us, 48 blocks over 30001 262; a CTA for every four rows of
-// every CTA's description 108 and 270).
+// that the second launch begins beside it (64 tokens over 32768 98 us, 48 blocks over 30001 262, where a CTA for every four
+// rows of every CTA's description took 108 and 270).
 constexpr int kJoinCtas = 4;  // of an SM (with two or eight 99 us; 64 registers leave room for a CTA of the second)
 constexpr int kJoinEach = 4, kJoinDesc = 128 * kJoinEach;
 template <int D, bool QBF, bool WAITS>
