@@ -90,7 +90,8 @@ struct ResizeShared {
   int tail[kResizeThreads];       // the last page, partly filled, of a row that grows; -1: none
   int what[kResizeThreads];       // bits below
   int served;                     // pages that rows take
-  int key[kSlots], same[kSlots], least[kSlots];  // rows with the tail `key`: how many, and the first
+  int key[kSlots], same[kSlots];  // rows with the tail `key`: how many,
+  unsigned long long keeper[kSlots];  // and which of them has most positions there (the first of those): positions, 1023 - row
 };
 constexpr int kGood = 1, kRenews = 2, kServed = 4;
 
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_
   cluster_arrive();  // (its shared memory may be written once a CTA has begun)
   // ---- what row tid wants
   int want = 0, what = 0, col = 0, tail = -1, holders = 0;
+  unsigned long long place = 0;
   if (tid < p.n_rows) {
     const int old = a.kv_len[tid], len = __ldg(a.new_len + tid);
     const int have = pages_of(old, p.page_size), need = pages_of(len, p.page_size);
@@ -118,15 +120,17 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_
           tail = p.table[tid * p.table_stride + have - 1];
           holders = in_pool(p, tail) ? p.ref[tail] : 0;
           if (holders < 1) tail = -1, want = 0, what = 0;
+          place = static_cast<unsigned long long>(old % p.page_size) * kResizeThreads + (kResizeThreads - 1 - tid);
         }
       }
     }
   }
   s.tail[tid] = tail;
-  for (int i = tid; i < kSlots; i += kResizeThreads) s.key[i] = -1, s.same[i] = 0, s.least[i] = kResizeThreads;
+  for (int i = tid; i < kSlots; i += kResizeThreads) s.key[i] = -1, s.same[i] = 0, s.keeper[i] = 0;
   if (tid == 0) s.served = 0;
   __syncthreads();
-  // rows with one tail meet in a slot of a small table, where they are counted
+  // Rows with one tail meet in a slot of a small table, where they are counted.  If all holders grow, the one that has most
+  // positions in the page keeps it: what it writes lies behind all others' positions, whether or not those are served.
   int slot = -1;
   if (tail >= 0 && holders > 1) {
     slot = static_cast<int>((static_cast<uint32_t>(tail) * 2654435761u) >> 21);
@@ -135,10 +139,10 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_
       if (k == -1 || k == tail) break;
     }
     atomicAdd(&s.same[slot], 1);
-    atomicMin(&s.least[slot], tid);
+    atomicMax(&s.keeper[slot], place);
   }
   __syncthreads();
-  if (slot >= 0 && (s.least[slot] != tid || s.same[slot] < holders)) what |= kRenews, ++want, --col;
+  if (slot >= 0 && (s.keeper[slot] != place || s.same[slot] < holders)) what |= kRenews, ++want, --col;
   long long total;
   const long long before = block_scan(want, s.tmp, total);
   s.first[tid] = static_cast<int>(min(before, 1ll << 30));

@@ -687,8 +687,8 @@ typedef struct dflash2_page_pool {
  * A shorter row gives the pages past its end back (their columns become -1; a page without holders is free to the
  * next call, not to this one).  A longer one takes pages, by row and then by column, the lowest free ids first.  Where
  * it would write to a page that other rows hold too (its last page, partly filled), it takes a page in that one's
- * place, gives that one back, and notes the copy; but if all holders of the page grow in this call, the first
- * row keeps it.
+ * place, gives that one back, and notes the copy; but if all holders of the page grow in this call, the one with most
+ * positions in it (the first of those) keeps it, and writes behind what the others hold, whether or not they are served.
  *   copies int32 [3][n_rows], written: the page to copy from, the page to copy to, and how many of its first
  *     positions (-1, -1, 0: none), for dflash2_pages_copy, which every layer's pools need before the next change.
  *   status int32 [n_rows] or NULL, set to an error, never cleared: DFLASH2_E_INVAL (a negative length, one past

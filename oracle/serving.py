@@ -45,7 +45,7 @@ def rope(x, positions, rates, amplitude=1.0, interleaved=False, inverse=False):
 
 def pages_resize(table, ref, kv_len, new_len, page):
     """Changes the state; returns copies (a triple per row) and statuses (1: out of bounds, 5: too few free pages)."""
-    before, n, width = list(ref), len(table), len(table[0])
+    before, lengths, n, width = list(ref), list(kv_len), len(table), len(table[0])
     pages = lambda t: -(-t // page)  # noqa: E731
     good = [o >= 0 and m >= 0 and pages(o) <= width and pages(m) <= width for o, m in zip(kv_len, new_len)]
     tail = [None] * n
@@ -78,7 +78,8 @@ def pages_resize(table, ref, kv_len, new_len, page):
         renew = False
         if tail[r] is not None and before[tail[r]] > 1:
             growing = [x for x in range(n) if tail[x] == tail[r]]
-            renew = not (len(growing) >= before[tail[r]] and growing[0] == r)
+            keeper = max(growing, key=lambda x: (lengths[x] % page, -x))   # writes behind what the others hold
+            renew = not (len(growing) >= before[tail[r]] and keeper == r)
         want = need - have + renew
         if want and (full or want > len(free)):
             full = True
