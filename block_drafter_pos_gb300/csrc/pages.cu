@@ -32,8 +32,8 @@ DF2_DEV bool give_back(const PagePool& p, int page) {
 // A cluster of 16 CTAs (of 8: 256 samples freed, forked and grown 43 us against 41).  Every CTA works out what each row
 // wants (a thread per row).  The counts are read in chunks of 1024 pages, a warp each, dealt to the CTAs in turn; each keeps its
 // chunks' free pages as bits and tells all CTAs how many they are.  After the cluster's barrier nothing is read any more that
-// the call changes: each warp hands its chunks' free pages to the rows that their ranks fall to, and rows give back what
-// they no longer hold.
+// the call changes: rows give back what they no longer hold, and each warp hands its chunks' free pages to the rows that
+// their ranks fall to.
 constexpr int kCluster = 16, kResizeThreads = 1024, kChunk = 1024;
 
 DF2_DEV uint32_t cluster_rank() {
@@ -107,12 +107,14 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_
   cluster_arrive();  // (its shared memory may be written once a CTA has begun)
   // ---- what row tid wants
   int want = 0, what = 0, col = 0, tail = -1, holders = 0;
+  bool cut = false;
   unsigned long long place = 0;
   if (tid < p.n_rows) {
     const int old = a.kv_len[tid], len = __ldg(a.new_len + tid);
     const int have = pages_of(old, p.page_size), need = pages_of(len, p.page_size);
     if (old >= 0 && len >= 0 && have <= p.max_pages && need <= p.max_pages) {
       what = kGood;
+      cut = have > need;
       if (len > old) {
         want = need - have;
         col = have;
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_
     atomicAdd(&s.same[slot], 1);
     atomicMax(&s.keeper[slot], place);
   }
-  __syncthreads();
+  const bool cuts = __syncthreads_or(cut);  // (the same in every CTA)
   if (slot >= 0 && (s.keeper[slot] != place || s.same[slot] < holders)) what |= kRenews, ++want, --col;
   long long total;
   const long long before = block_scan(want, s.tmp, total);
@@ -199,37 +201,6 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_
   s.what[tid] = what;
   __syncthreads();
 
-  // ---- pages to rows
-  const int served = s.served;
-  if (served > 0) {
-    for (int k = cta + kCluster * wid; k < chunks; k += kCluster * (kResizeThreads / 32)) {
-      int j = count[k];
-      if (j >= served) break;
-      uint32_t word = bits[(k / kCluster) * 32 + lane];
-      int x = __popc(word);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      j += x - __popc(word);
-      if (word == 0 || j >= served) continue;
-      int r = 0, hi = kResizeThreads;  // the last row whose first page's rank is at most j (those that take none are passed over)
-      while (hi - r > 1) {
-        const int mid = (r + hi) >> 1;
-        if (s.first[mid] <= j) r = mid;
-        else hi = mid;
-      }
-      for (; word != 0 && j < served; word &= word - 1, ++j) {
-        while (j >= s.first[r + 1]) ++r;
-        const int page = k * kChunk + lane * 32 + __ffs(word) - 1, i = j - s.first[r];
-        p.table[r * p.table_stride + s.col[r] + i] = page;
-        p.ref[page] = 1;
-        if (i == 0 && (s.what[r] & kRenews)) a.copies[p.n_rows + r] = page;
-      }
-    }
-  }
-
   // ---- what rows no longer hold, and their lengths (a warp per row)
   for (int r = cta + kCluster * wid; r < p.n_rows; r += kCluster * (kResizeThreads / 32)) {
     const int w = s.what[r], old = a.kv_len[r], len = __ldg(a.new_len + r);
@@ -265,6 +236,42 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const __grid_
       if (done) a.kv_len[r] = len;
       if (!(w & kGood) || !fine) flag(a.status, r, kInval);
       else if (!done) flag(a.status, r, kNoPages);
+    }
+  }
+
+  // ---- pages to rows.  Not before all pages are given back: one that a row lists and does not hold may be among the free ones, and
+  // its count would be taken for that row's.
+  const int served = s.served;
+  if (cuts && served > 0) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (served > 0) {
+    for (int k = cta + kCluster * wid; k < chunks; k += kCluster * (kResizeThreads / 32)) {
+      int j = count[k];
+      if (j >= served) break;
+      uint32_t word = bits[(k / kCluster) * 32 + lane];
+      int x = __popc(word);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      j += x - __popc(word);
+      if (word == 0 || j >= served) continue;
+      int r = 0, hi = kResizeThreads;  // the last row whose first page's rank is at most j (those that take none are passed over)
+      while (hi - r > 1) {
+        const int mid = (r + hi) >> 1;
+        if (s.first[mid] <= j) r = mid;
+        else hi = mid;
+      }
+      for (; word != 0 && j < served; word &= word - 1, ++j) {
+        while (j >= s.first[r + 1]) ++r;
+        const int page = k * kChunk + lane * 32 + __ffs(word) - 1, i = j - s.first[r];
+        p.table[r * p.table_stride + s.col[r] + i] = page;
+        p.ref[page] = 1;
+        if (i == 0 && (s.what[r] & kRenews)) a.copies[p.n_rows + r] = page;
+      }
     }
   }
 }

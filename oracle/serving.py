@@ -58,23 +58,24 @@ def pages_resize(table, ref, kv_len, new_len, page):
                 tail[r] = t
     free = [p for p, h in enumerate(before) if h == 0]
     copies, status, full = [(-1, -1, 0)] * n, [0] * n, False
-    # what rows take is settled first, by what was held before the call
+    # what rows take is settled by what was held before the call; pages are given back before any is taken
     for r in range(n):
-        old, new = kv_len[r], new_len[r]
         if not good[r]:
             status[r] = 1
-            continue
-        have, need = pages(old), pages(new)
-        if new <= old:
-            for c in range(need, have):
+        elif new_len[r] <= lengths[r]:
+            for c in range(pages(new_len[r]), pages(lengths[r])):
                 t = table[r][c]
                 table[r][c] = -1
                 if 0 <= t < len(ref) and ref[t] > 0:
                     ref[t] -= 1
                 else:
                     status[r] = 1
-            kv_len[r] = new
+            kv_len[r] = new_len[r]
+    for r in range(n):
+        old, new = lengths[r], new_len[r]
+        if not good[r] or new <= old:
             continue
+        have, need = pages(old), pages(new)
         renew = False
         if tail[r] is not None and before[tail[r]] > 1:
             growing = [x for x in range(n) if tail[x] == tail[r]]

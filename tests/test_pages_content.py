@@ -142,3 +142,26 @@ def test_no_row_writes_what_another_holds(make, rows, width, n_pages, page, seed
         c.resize(np.where(g.random(rows) < 0.4, 0, kv).tolist())
     assert met > 0
     c.resize([0] * rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cut", [0, 4])
+@pytest.mark.parametrize("rows", [2, 9, 200])
+def test_a_page_that_a_row_does_not_hold_is_not_given_back_under_its_new_holder(rows, cut):
+    """The first half's tables name free pages (of no holder); they are cut, and so flagged, while the second half takes those
+    pages: every taken page has its one holder."""
+    half, page = rows // 2, 4
+    d = Device(rows, 4, 8 * rows, page)
+    d.table[:half, :2] = torch.arange(2 * half, dtype=torch.int32, device="cuda").view(half, 2)
+    d.kv[:half] = 8
+    for _ in range(3):
+        copies, status = d.resize([cut] * half + [11] * (rows - half))
+        table, ref, kv = d.look()
+        assert status == [1] * half + [0] * (rows - half) and kv == [cut] * half + [11] * (rows - half)
+        taken = [t for row in table[half:] for t in row[:3]]
+        assert taken == list(range(3 * (rows - half))) and [t for t, h in enumerate(ref) if h] == taken and set(ref) <= {0, 1}
+        assert all(t == -1 for row in table[:half] for t in row[-(-cut // page):])
+        # as before: the taken pages given back, the first half's tables broken again
+        d.resize([cut] * half + [0] * (rows - half))
+        d.table[:half, :2] = torch.arange(2 * half, dtype=torch.int32, device="cuda").view(half, 2)
+        d.kv[:half] = 8
