@@ -1041,7 +1041,8 @@ cudaError_t launch_shared_attention(PagedAttnArgs& a, int head_dim, int fmt, int
   const long long position = 2ll * a.c.n_kv * (bits16 ? 2 * head_dim : head_dim + 4);
   const long long again = static_cast<long long>(a.g.n_req - a.g.n_groups) * a.g.max_prefix * position;
   const long long most = static_cast<long long>(a.rq.max_new) * a.s.group <= 16 ? kApartBytes : 2 * kApartBytes;
-  a.g.apart = a.g.max_prefix == 0 || a.g.apart == kSharedApart || (a.g.apart == kSharedAuto && again <= most);
+  // (without a prefix, or a row of a group, within the bounds there is no first launch)
+  a.g.apart = a.g.max_prefix == 0 || a.g.max_group == 0 || a.g.apart == kSharedApart || (a.g.apart == kSharedAuto && again <= most);
   if (!a.g.apart) {
     PagedAttnArgs p = a;
     p.g.first = 1;
