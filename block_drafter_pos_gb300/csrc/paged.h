@@ -119,6 +119,34 @@ DF2_HD inline bool paged_in_run(long long first, long long next, long long t0, l
   return first < next && first < t1 && next > t0;
 }
 
+// Calls see(r, first, next, t0, t1) for each request, whose tiles are [first, next), beside CTA c's run [t0, t1) of a launch of
+// `ctas` CTAs; tiles(r): request r's tiles.
+#ifdef __CUDACC__
+#pragma nv_exec_check_disable
+#endif
+template <typename Tiles, typename See>
+DF2_HD inline void paged_beside_run(int n_req, long long ctas, long long c, const Tiles& tiles, const See& see) {
+  long long T = 0, first = 0;
+  for (int r = 0; r < n_req; ++r) T += tiles(r);
+  const long long C = T < ctas ? T : ctas;
+  if (c >= C) return;
+  for (int r = 0; r < n_req; ++r) {
+    const long long next = first + tiles(r);
+    see(r, first, next, paged_run_begin(c, C, T), paged_run_begin(c + 1, C, T));
+    first = next;
+  }
+}
+
+// Every `step`th of the rows (token, query head) of tokens b0 .. b0 + n - 1, from the `first` on.
+#ifdef __CUDACC__
+#pragma nv_exec_check_disable
+#endif
+template <typename Row>
+DF2_HD inline void paged_each_row(int b0, int n, int heads, int first, int step, const Row& row) {
+  const long long rows = static_cast<long long>(n) * heads;
+  for (long long i = first; i < rows; i += step) row(b0 + static_cast<int>(i / heads), static_cast<int>(i % heads));
+}
+
 // Requests in groups that share a prefix: two launches.  In the first the call's "requests" are the groups of more than one: their
 // rows see all of the prefix, and each row's result (outputs not divided by the sum, and maximum and sum) goes to the
 // workspace.  In the second they are the requests, with the keys behind the prefix, and what they write has the prefix's

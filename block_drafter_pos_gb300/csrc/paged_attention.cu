@@ -911,21 +911,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   }
 }
 
-// Flags every request with a tile in CTA c's run (a wait of that CTA gave up).
-DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
-  if (!a.rq.status) return;
+// Calls found(r) for every request with a tile in CTA c's run (a wait of that CTA gave up), and flags them.
+template <typename Found>
+DF2_DEV void each_of_run(const PagedAttnArgs& a, long long c, const Found& found) {
   auto tiles = [&](int r) {
     PagedWork w;
     return paged_work<kShared>(a, r, w) && w.n > 0 ? a.c.n_kv * paged_head_tiles(a.s, w.n, w.len, w.from) : 0ll;
   };
-  long long T = 0, first = 0;
-  for (int r = 0; r < a.rq.n_req; ++r) T += tiles(r);
-  const long long C = T < a.ctas ? T : a.ctas;
-  for (int r = 0; r < a.rq.n_req; ++r) {
-    const long long next = first + tiles(r);
-    if (paged_in_run(first, next, paged_run_begin(c, C, T), paged_run_begin(c + 1, C, T))) paged_flag<kShared>(a, r, 3);  // DFLASH2_E_CUDA
-    first = next;
-  }
+  paged_beside_run(a.rq.n_req, a.ctas, c, tiles, [&](int r, long long first, long long next, long long t0, long long t1) {
+    if (paged_in_run(first, next, t0, t1)) found(r);
+  });
+}
+DF2_DEV void flag_run(const PagedAttnArgs& a, long long c) {
+  if (!a.rq.status) return;
+  each_of_run(a, c, [&](int r) { paged_flag<kShared>(a, r, 3); });  // DFLASH2_E_CUDA
 }
 
 constexpr int kJoinTogether = kShared ? 4 : 8;  // (verify blocks: 1.5 us)
@@ -962,6 +961,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     d0[e] = c < a.ctas ? __ldcg(reinterpret_cast<const int4*>(a.desc + 8 * c)) : make_int4(-1, 0, 0, 0);
     d1[e] = c < a.ctas ? __ldcg(reinterpret_cast<const int4*>(a.desc + 8 * c + 4)) : make_int4(0, 0, 0, 0);
   }
+  bool gave_up = false;
+#pragma unroll
+  for (int e = 0; e < kJoinEach; ++e) gave_up |= d1[e].z != 0;
   uint32_t is_cut[kJoinEach];
 #pragma unroll
   for (int e = 0; e < kJoinEach; ++e) {
@@ -988,9 +990,19 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const int4 d = cut[i / R][0], x = cut[i / R][1];
     join_row<D, QBF, kJoinTogether>(a, d.y, d.z, d.x, d.w >> 1, d.w & 1, x.x, x.y, i % R, false);
   }
-  if (WAITS && blockIdx.x == 0)
-    for (int c = tid; c < a.ctas; c += 128)
-      if (__ldcg(a.desc + 8 * c + 6) != 0) flag_run(a, c);
+  // A CTA whose wait gave up: its groups are flagged, and their rows' parts are NaN, so that the second launch joins nothing that the
+  // workspace held before.
+  if (WAITS && blockIdx.x == 0 && __syncthreads_or(gave_up))
+    for (int c = 0; c < a.ctas; ++c)
+      if (__ldcg(a.desc + 8 * c + 6) != 0) {
+        if (tid == 0) flag_run(a, c);
+        each_of_run(a, c, [&](int r) {
+          PagedWork w;
+          paged_work<true>(a, r, w);
+          paged_each_row(w.b0, w.n, a.c.n_kv * a.s.group, tid, 128,
+                         [&](int token, int head) { *joint_stat<D>(a, token, head) = make_float2(NAN, NAN); });
+        });
+      }
 }
 #endif
 

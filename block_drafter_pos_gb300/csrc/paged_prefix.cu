@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prefix_kernel(const __grid_
   if (tid == 0) a.desc[8 * c] = -1, a.desc[8 * c + 6] = 0;
   if (c >= C) return;
   const long long t_begin = paged_run_begin(c, C, T), t_end = paged_run_begin(c + 1, C, T);
-  // Partials that never come (a wait that gives up) leave NaN in the rows they are joined into.
+  // Partials that never come (a wait that gives up) leave NaN in the rows they are joined into; the joining kernel sees to the
+  // whole units' rows.
   for (int i = tid; i < 2 * kChunkRows; i += kThreads) {
     float* const p = a.part + (2 * c + i / kChunkRows) * (kChunkRows * (D + 2)) + kChunkRows * D;
     reinterpret_cast<float2*>(p)[i % kChunkRows] = make_float2(NAN, NAN);
