@@ -582,12 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         fence_after();
 #pragma unroll
         for (int x = kBN / 32; x < kBN / 16; ++x) mma_ts(go, o, p + 8 * x, v + 128 * x, id_o, 1);
-        mma_commit(go, o_done + 8 * t);
+        mma_commit(go & fine, o_done + 8 * t);
         if (t == 1 || !two) mma_commit(go, empty + 8 * slot);
         if (t) ++pn1;
         else ++pn0;
       };
-      // (a failed wait ends the loop at the tile's end: the others' waits run out in turn)
+      // (a failed wait ends the loop at the tile's end, and no output is announced after it: the others' waits run out in turn)
       for (int n = -1; n < total; ++n) {
         const bool more = n + 1 < total;
         if (n >= 0 && more) {
