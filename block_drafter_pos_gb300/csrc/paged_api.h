@@ -2,6 +2,7 @@
 #pragma once
 
 #include <math.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
@@ -29,6 +30,19 @@ inline bool stride16(int64_t elements, int size) { return (elements * size) % 16
 inline bool valid_rows(const dflash2_rows& r) {
   return r.p && aligned16(r.p) && r.type >= DFLASH2_T_BF16 && r.type <= DFLASH2_T_F32 &&
          stride16(r.token_stride, t_size(r.type)) && stride16(r.head_stride, t_size(r.type));
+}
+
+// Whether no two of the rows share a channel: the step between two of them (dt tokens, dh heads) never comes to less than a row.
+inline bool rows_apart(const dflash2_rows& r, int64_t tokens, int64_t heads, int64_t dim) {
+  const int64_t t = std::abs(r.token_stride), h = std::abs(r.head_stride);
+  if ((heads == 1 || h >= dim) && (tokens == 1 || t >= (heads - 1) * h + dim)) return true;   // heads within tokens
+  if ((tokens == 1 || t >= dim) && (heads == 1 || h >= (tokens - 1) * t + dim)) return true;  // tokens within heads
+  for (int64_t dh = 0; dh < heads; ++dh) {  // any other order: the tokens that come nearest to dh heads
+    const int64_t near = t > 0 ? std::min(dh * h / t, tokens - 1) : 0;
+    for (int64_t dt = near; dt <= near + 1; ++dt)
+      if (dt < tokens && dt + dh > 0 && std::abs(dt * t - dh * h) < dim) return false;
+  }
+  return true;
 }
 
 inline PagedRows rows_of(const dflash2_rows& r) {

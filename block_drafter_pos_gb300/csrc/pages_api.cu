@@ -48,9 +48,9 @@ void span_of(const dflash2_rows& r, int64_t tokens, int64_t heads, int64_t dim, 
   *hi = static_cast<const char*>(r.p) + (std::max<int64_t>(t, 0) + std::max<int64_t>(h, 0) + dim) * size;
 }
 
-// Rows that may be turned from x to y: of one type, and apart from each other or the same.
+// Rows that may be turned from x to y: of one type, and apart from each other or the same; no two of y's overlap.
 bool valid_turn(const dflash2_rows* x, const dflash2_rows* y, int64_t tokens, int64_t heads, int64_t dim) {
-  if (!x || !y || !valid_rows(*x) || !valid_rows(*y) || x->type != y->type) return false;
+  if (!x || !y || !valid_rows(*x) || !valid_rows(*y) || x->type != y->type || !rows_apart(*y, tokens, heads, dim)) return false;
   if (x->p == y->p && x->token_stride == y->token_stride && x->head_stride == y->head_stride) return true;
   const char *x0, *x1, *y0, *y1;
   span_of(*x, tokens, heads, dim, &x0, &x1);

@@ -650,8 +650,8 @@ dflash2_status dflash2_rope_plan(const dflash2_rope_config* cfg, dflash2_rotatio
  * k_out (k_heads 0: none).  positions int32 [n_tokens], any value.  inverse != 0: by the opposite angle with the same
  * amplitude, which takes the gradient of out back to that of x.  head_dim: a multiple of 8 from rot_dim to 1024.
  * n_tokens: at most 2^31 - 16.  Each output is x, cosine and sine in fp32, rounded once.  x and out have one type; out may be x
- * itself (the same address and strides), any other overlap of their address ranges is refused; out is apart from k
- * and k_out from x. */
+ * itself (the same address and strides), any other overlap of their address ranges is refused, and so are rows of out that
+ * overlap each other (a stride of 0); out is apart from k and k_out from x. */
 dflash2_status dflash2_rope(const dflash2_rotation* rope, int32_t n_tokens, int32_t head_dim, int32_t x_heads,
                             const dflash2_rows* x, const dflash2_rows* out, int32_t k_heads, const dflash2_rows* k,
                             const dflash2_rows* k_out, const int32_t* positions, int32_t inverse, void* stream);
@@ -659,7 +659,7 @@ dflash2_status dflash2_rope(const dflash2_rotation* rope, int32_t n_tokens, int3
 /* dflash2_paged_write of the turned keys, and the turned queries (n_q_heads heads) into q_out: k is turned in fp32
  * and rounded once, to the cache's format; v is written as it is.  Tokens are turned by their positions in the
  * cache, or by positions[row] (int32 [n_tokens]; a draft tree's nodes by their depths).  q NULL: keys and values
- * only.  q, k, v, q_out have one type; q_out may be q itself and is apart from k and v.
+ * only.  q, k, v, q_out have one type; q_out may be q itself, its rows do not overlap, and it is apart from k and v.
  * n_tokens: at most 2^31 - 16.  rot_dim at most head_dim.  Rows of a request that is
  * out of bounds keep what they held, q_out's too; a bad page's queries are turned. */
 dflash2_status dflash2_paged_rope_write(dflash2_paged_handle* h, const dflash2_rotation* rope,

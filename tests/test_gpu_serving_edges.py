@@ -25,3 +25,30 @@ def test_groups_of_no_new_tokens_at_most(how, n, new):
     assert not status.any()
     check_shared(s, q, out, lse)
     s.close()
+
+
+def test_rope_of_rows_in_any_order_but_onto_each_other():
+    """Expanded rows are read, never written; rows of out may lie in any order in which they do not overlap."""
+    plan, n, heads, dim = bd.make_rope(32), 3, 4, 32
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, pos = torch.randn(n, heads, dim, generator=g, device="cuda"), i32([5, 0, 1000])
+    want = torch.empty_like(x)
+    bd.dflash2_rope(plan, x, want, pos)
+    for t, h in ((heads * dim, dim), (dim, n * dim), (160, 96), (40, 160), (96, 320), (dim, 3 * dim + 16)):
+        room = torch.full((2000,), 7.0, device="cuda")
+        out = room.as_strided((n, heads, dim), (t, h, 1))
+        bd.dflash2_rope(plan, x, out, pos)
+        assert torch.equal(out, want) and int((room != 7).sum()) <= x.numel()
+        out.copy_(x)
+        bd.dflash2_rope(plan, out, out, pos)
+        assert torch.equal(out, want)
+    one = x[:1].expand(n, heads, dim)
+    bd.dflash2_rope(plan, one, want, pos)
+    bd.dflash2_rope(plan, one.contiguous(), x, pos)
+    assert torch.equal(x, want)
+    for bad in (one, x[:, :1].expand(n, heads, dim), torch.zeros(500, device="cuda").as_strided((n, heads, dim), (64, 16, 1))):
+        for source in (x, bad):
+            with pytest.raises(bd.Dflash2Error):
+                bd.dflash2_rope(plan, source, bad, pos)
+        with pytest.raises(bd.Dflash2Error):
+            bd.dflash2_rope(plan, x, want, pos, k=bad, k_out=bad)

@@ -11,6 +11,10 @@ def test_what_a_prefix_launch_spoils(tmp_path):
     _host_check(tmp_path, "paged_give_up_check.cpp", "-fsanitize=undefined", "-fno-sanitize-recover")
 
 
+def test_rows_that_overlap(tmp_path):
+    _host_check(tmp_path, "rows_apart_check.cpp")
+
+
 @pytest.mark.parametrize("name", ["paged_chunk.cu", "paged_prefix.cu"])
 def test_no_output_is_announced_after_a_failed_wait(name):
     """The products' warp: the one commit on which a unit's rows are written hangs on all of its waits so far, and comes after
