@@ -154,10 +154,17 @@ class PagePool:
     __slots__ = ("raw", "n_rows", "device", "_keep")
 
 
-def page_pool(page_table, ref, page_size: int) -> PagePool:
-    """page_table int32 [rows, pages of a row], ref int32 [pages] (zeros at the start): the pool's state, which the calls change."""
+def page_pool(page_table, ref, page_size: int, h: Optional[int] = None) -> PagePool:
+    """page_table int32 [rows, pages of a row], ref int32 [pages] (zeros at the start): the pool's state, which the calls change.
+    h: the paged handle whose caches go by the table, to have its page size and device compared."""
     what = "page_pool"
     torch = _b._calls()[0]
+    if h is not None:
+        g = _b._paged_cfg.get(h)
+        if g is None:
+            raise _inval(what, "not a paged handle")
+        if g[0][1] != page_size or g[2] != page_table.get_device():
+            raise _inval(what, f"the handle's pages have {g[0][1]} positions, on device {g[2]}")
     dev = page_table.get_device()
     if page_table.dtype is not torch.int32 or page_table.dim() != 2 or dev < 0 or page_table.stride(1) != 1:
         raise _inval(what, "page_table must be an int32 CUDA tensor [rows, pages], with contiguous rows")

@@ -36,7 +36,7 @@ class Target:
         i32 = lambda *s, v=0: torch.full(s, v, dtype=torch.int32, device="cuda")  # noqa: E731
         self.table, self.ref, self.kv_len = i32(rows, width, v=-1), i32(n_pages), i32(rows)
         self.copies, self.status = i32(3, rows), i32(rows)
-        self.pages = bd.page_pool(self.table, self.ref, page)
+        self.pages = bd.page_pool(self.table, self.ref, page, self.handle)
         kv = lambda: torch.zeros(n_pages, page, hk, dim, dtype=torch.bfloat16, device="cuda")  # noqa: E731
         self.pools = [(kv(), kv()) for _ in range(layers)]
         self.caches = self.caches_of(0, rows)

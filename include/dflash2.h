@@ -680,7 +680,7 @@ typedef struct dflash2_page_pool {
   int32_t n_pages;      /* at most DFLASH2_PAGES_MAX */
   int32_t n_rows;       /* at most DFLASH2_PAGED_MAX_REQUESTS */
   int32_t max_pages;
-  int32_t page_size;
+  int32_t page_size;    /* that of the paged handle whose pools go by these ids (nothing here compares them) */
 } dflash2_page_pool;
 
 /* Brings every row from kv_len[r] to new_len[r] positions (int32 [n_rows]) and kv_len[r] to new_len[r].

@@ -2,7 +2,8 @@
 import pytest
 
 import block_drafter_pos_gb300 as bd
-from test_serving_host import _call_rope, _call_write, _rotation
+from test_serving_host import I32, _call_rope, _call_write, _rotation, calls  # noqa: F401
+from test_target_calls import Stub
 from test_target_host import FakeHandle, P, _cache, _rows
 
 b = bd.binding
@@ -21,3 +22,12 @@ def test_rows_turned_onto_each_other_are_refused(kw):
     h, r = FakeHandle(), _rows(p=FAR)
     q = _rows(**{"token_stride": 1024, **kw})
     assert _call_write(h.p, _rotation(), _cache(), q=q, q_out=q, k=r, v=r) == b.E_INVAL
+
+
+def test_a_pool_of_another_page_size_than_the_handles_is_refused(calls):  # noqa: F811
+    """The handle's pages have 16 positions, on device 0."""
+    table, ref = Stub(0, I32, 3, 4), Stub(0, I32, 9)
+    assert bd.page_pool(table, ref, 16, 4096).raw == bd.page_pool(table, ref, 16).raw
+    for size, h, t in ((24, 4096, table), (8, 4096, table), (16, 4097, table), (16, 4096, Stub(1, I32, 3, 4))):
+        with pytest.raises(bd.Dflash2Error):
+            bd.page_pool(t, ref, size, h)
