@@ -169,6 +169,12 @@ enum { kSharedAuto = 0, kSharedTogether = 1, kSharedApart = 2 };
 // 35 / 50; e4m3 4 over 16384 38 / 37, 16 over 2048 31 / 26, over 4096 33 / 38, 64 over 512 41 / 36, over 1024 42 / 45.  Blocks of 8:
 // bf16 16 over 2048 42 / 35, over 4096 51 / 56, 64 over 1024 64 / 64; e4m3 16 over 4096 60 / 53, over 8192 70 / 88, 64 over 1024
 // 80 / 66, over 2048 88 / 99.
+// Other shapes go by the same border, which is then off on either side (us, together / apart, MiB read again; states in turn).  One KV
+// head of 128, bf16: tokens 16 over 16384 (120) 36 / 28, 64 over 4096 (126) 28 / 30; blocks 16 over 16384 (120) 48 / 35, 64 over 4096 (126)
+// 35 / 36.  Eight of 64: tokens 16 over 4096 (120) 22 / 37, e4m3 (64) 25 / 32; blocks 16 over 4096 (120) 34 / 41, 64 over 1024 (126) 50 / 47.
+// Above 32 rows a unit, where products count and not bytes: trees of 33 nodes bf16 16 over 4096 (240) 93 / 88, 64 over 1024 (252) 154 /
+// 122, over 4096 (1008) 231 / 280, e4m3 16 over 4096 (124) 100 / 118; chunks of 128 tokens bf16 16 over 4096 (240) 211 / 173, 64 over 1024
+// (252) 366 / 250; of 301 tokens 8 over 16384 (448) 551 / 604.
 constexpr long long kApartBytes = 100ll << 20;
 
 // Whether group g's requests [g0, g1) follow those of the group before and, the last's, end at the last request.  (Where one

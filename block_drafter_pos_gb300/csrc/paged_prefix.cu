@@ -11,7 +11,8 @@
 // Measured: 64 tokens of 32 query heads over 32768 bf16 positions of 8 KV heads of 128 (134 MB, 34 GFLOP) 43 us, 3700 clocks a
 // tile of 128 keys, of which the products of the two row tiles take 1500 to 1750 each; 11 us pass before the first scores, 4 after the
 // last.  48 blocks of 8 over three e4m3 prefixes to 30001 positions (164 GFLOP) 165 us, 1.0 PFLOP/s, 4500 clocks a tile: a row
-// tile's softmax takes 2600 there, its scales and value factors 1000 of them.
+// tile's softmax takes 2600 there, its scales and value factors 1000 of them.  Under the launch's 128 registers 16-bit caches spill 104
+// bytes a thread, 8-bit ones 2.
 #include "common.cuh"
 #include "paged_mma.cuh"
 #include "paged_sched.cuh"

@@ -735,7 +735,9 @@ dflash2_status dflash2_paged_keep(dflash2_paged_handle* h, int32_t n_caches, con
  *   workspace: dflash2_paged_shared_bytes(h, x.n_tokens) bytes, 32-byte aligned, used by one call at a time.
  *   how: TOGETHER reads a prefix once for its group, in a launch of its own; APART lets each request read it, in one
  *     launch, which is faster while what is read again is little (and stays in the L2 cache).  AUTO chooses by the bytes that
- *     x.n_req - n_groups requests read again of max_prefix positions.
+ *     x.n_req - n_groups requests read again of max_prefix positions: by the bound, not by the prefixes, so that a captured
+ *     call with a generous bound takes two launches for short prefixes too.  The border is that of single tokens and
+ *     blocks of 8 heads of 128; for prompts and trees behind prefixes of a few thousand positions APART is mostly the faster.
  * A group whose prefix or rows break these bounds is skipped and all its requests are flagged, as they are for a bad page of
  * its prefix (which is masked); a request that does is skipped and flagged alone.  A row that two good ranges hold is
  * not valid.  The largest group's rows (max_group times query heads per KV head) end at 2^31 - 512. */
